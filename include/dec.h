@@ -357,6 +357,163 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
                           int n_kv_heads, int head_dim, int ctx_stride, int n, float* o,
                           dec_stream_t stream);
 
+/* ---- A paged key/value cache of many sequences --------------------------------
+ *
+ * Source: "Kernel fusion and block bridging", section "Fusion" (k and v written
+ * into pages), carried to what a serving program keeps: one pool of pages for
+ * many sequences, pages that sequences share, 4-bit pages, and attention over
+ * them with a sliding window.  The pages describe no such calls; they are an
+ * addition of this library.
+ *
+ * All memory is the caller's: the calls below allocate nothing, keep nothing
+ * between calls, wait for nothing and read no device value on the host, so
+ * they can be captured into a CUDA graph.  They run on the current device, to
+ * which the memory must belong, in stream order on `stream`.
+ *
+ *   page    rows [i * page_rows, (i + 1) * page_rows) of one sequence, in one
+ *           layer: K, then V, each [n_kv_heads][page_rows][head_dim].  A page
+ *           number names the same page in every layer.
+ *           DEC_KV_BF16: bf16 values.
+ *           DEC_KV_Q4B32: per K or V and head, first page_rows rows of
+ *           head_dim / 2 bytes of codes, then page_rows rows of head_dim / 32
+ *           fp16 scales.  A row is cut into B = head_dim / 32 blocks of 32
+ *           dimensions; dimension 32 b + 4 g + i (block b, 0 <= g < 8,
+ *           0 <= i < 4) is nibble (g * B + b) * 4 + i of the row, low nibble of
+ *           a byte first, and stands for (nibble - 8) * scale[b].
+ *   pool    [n_layers][n_pages][page_bytes] (dec_kv_sizes), 16-byte aligned
+ *   table   [n_seqs][max_pages]: page of each run of rows, or -1 (none)
+ *   lens    [n_seqs]: rows of each sequence
+ *   refs    [n_pages]: how many table entries name the page; 0 = free
+ *   status  one word of enum dec_kv_bits, OR-ed by the kernels
+ *   scratch dec_kv_sizes ints, used by extend, fork and compact within a call
+ *
+ * An empty cache is table = -1 (all bytes 0xFF), lens = refs = status = 0.
+ * Calls on one cache run one after another (one stream, or ordered by the
+ * caller); attention, read and append touch no table, length or count, and
+ * calls of these may overlap as long as none reads rows that another writes
+ * and each attention has a workspace of its own.
+ *
+ * Lists of sequences are device int32; a negative entry is padding and is
+ * skipped, and what belongs to it is neither read nor written.  A list given
+ * as NULL is 0, 1, ..., n - 1.  What the host cannot see is checked on the
+ * device: an index out of range is skipped and sets DEC_KV_BAD_INDEX. */
+enum dec_kv_format {
+  DEC_KV_BF16 = 0,  /* bf16 rows */
+  DEC_KV_Q4B32 = 1  /* 4-bit codes in blocks of 32 dimensions with an fp16 scale */
+};
+
+enum dec_kv_type { /* of the caller's q, o, k, v */
+  DEC_IO_F32 = 0,
+  DEC_IO_BF16 = 1
+};
+
+enum dec_kv_bits {
+  DEC_KV_BAD_INDEX = 1, /* a sequence, position, length or page out of range: skipped (extend and
+                           fork: nothing done) */
+  DEC_KV_NO_PAGES = 2,  /* extend or fork: not enough free pages, or a sequence longer than its
+                           table: nothing done */
+  DEC_KV_BAD_LIST = 4   /* extend: a sequence twice; fork: a child twice, not empty, or also a
+                           parent: nothing done */
+};
+
+typedef struct dec_kv_cache {
+  int32_t n_layers, n_kv_heads;
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t page_rows;  /* a multiple of 16, 16..1024 */
+  int32_t n_pages;    /* 1..2^20 */
+  int32_t n_seqs;     /* 1..65536 */
+  int32_t max_pages;  /* pages a sequence can have; max_pages * page_rows <= 2^30 */
+  int32_t format;     /* enum dec_kv_format */
+  void* pool;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t* status;
+  int32_t* scratch;
+} dec_kv_cache;
+
+/* Source: none on the pages (see above), as for every dec_kv_ call.
+ * The bytes of a page and the ints of the scratch of a cache of this shape
+ * (its pointers are not looked at). */
+int dec_kv_sizes(const dec_kv_cache* c, size_t* page_bytes, size_t* scratch_ints);
+
+/* Writes n rows into one layer: row t of k and of v ([n_kv_heads][head_dim] of
+ * `type`, rows row_stride elements apart, keys already rotated) becomes row
+ * positions[t] of sequence seqs[t], whose table must have a page for it.
+ * positions NULL: each sequence's last row, lens[seqs[t]] - 1 (a decode step,
+ * after dec_kv_extend).  bf16 pages round to nearest even.  4-bit pages take
+ * per block the scale s = fp16(max |x| / 7) (the quotient in fp32, at most
+ * 65504) and the codes nearest to x / s (exactly, ties to even, within
+ * [-8, 7]; 0 where s is 0); a block with a NaN or an infinity gets a NaN
+ * scale.  k, v and row_stride * size must be multiples of 16 bytes.  A row
+ * must not be named twice in one call, nor lie in a shared page. */
+int dec_kv_append(const dec_kv_cache* c, int layer, const void* k, const void* v, int type,
+                  int64_t row_stride, const int32_t* seqs, const int32_t* positions, int n,
+                  dec_stream_t stream);
+
+/* The reverse: rows positions[t] of sequences seqs[t] of one layer, as values
+ * of `type` (4-bit: code * scale, exact in fp32), into rows of k and v.  Rows
+ * that are skipped are left as they were. */
+int dec_kv_read(const dec_kv_cache* c, int layer, void* k, void* v, int type, int64_t row_stride,
+                const int32_t* seqs, const int32_t* positions, int n, dec_stream_t stream);
+
+/* Attention of one query per entry of seqs over its sequence's rows in one
+ * layer.  q and o: [n][n_q_heads][head_dim] of `type`, rows q_stride and
+ * o_stride elements apart.  With L = lens[seq] and W = window, the query sees
+ * the rows j with j >= L - W and, of those before, the first `sinks` ones
+ * (j < sinks); window 0: every row.  o = sum over them of softmax(scale *
+ * q . k_j) v_j, query head h reading KV head floor(h * n_kv_heads /
+ * n_q_heads), n_q_heads any multiple of n_kv_heads; scale 0 means
+ * 1 / sqrt(head_dim).  No visible row: o = 0.  Rows not visible are not looked
+ * at (whatever they hold); those visible must hold finite values.  Scores,
+ * sums and weights are fp32; the same call gives the same bits.  A visible row
+ * without a valid page is left out and sets DEC_KV_BAD_INDEX.  q, o and their
+ * strides are multiples of 16 bytes; o must not overlap q.
+ * workspace: device memory of dec_kv_attention_workspace bytes, 16-byte
+ * aligned, for this call alone (its content does not matter before or after,
+ * and calls that may overlap need one each). */
+int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q, void* o, int type,
+                     int64_t q_stride, int64_t o_stride, const int32_t* seqs, int n, int n_q_heads,
+                     int window, int sinks, float scale, void* workspace, size_t workspace_bytes,
+                     dec_stream_t stream);
+
+/* The workspace bytes of a dec_kv_attention call on the current device, for
+ * any n up to this one. */
+int dec_kv_attention_workspace(const dec_kv_cache* c, int n, int n_q_heads, size_t* bytes);
+
+/* Makes each listed sequence n_new[i] rows longer (NULL: one), and gives it
+ * the pages that the new rows need: in list order, the free pages from the
+ * lowest number up.  All or nothing: on an error bit no sequence changes.
+ * n <= n_seqs.  The new rows hold nothing until dec_kv_append writes them. */
+int dec_kv_extend(const dec_kv_cache* c, const int32_t* seqs, const int32_t* n_new, int n,
+                  dec_stream_t stream);
+
+/* Makes sequence children[i], which must be empty, a copy of parents[i]: the
+ * full pages are shared, a partly filled last page is copied, in every layer,
+ * into a free page (in list order, from the lowest number up), so that both
+ * can grow.  A parent may be listed many times.  All or nothing, as above;
+ * n <= n_seqs. */
+int dec_kv_fork(const dec_kv_cache* c, const int32_t* parents, const int32_t* children, int n,
+                dec_stream_t stream);
+
+/* window 0: empties each listed sequence and frees its pages (those that no
+ * other sequence shares).  window > 0: frees only the pages that no later
+ * query with this window and these sinks can see, whose rows lie at or past
+ * `sinks` and before lens - window; the lengths stay. */
+int dec_kv_release(const dec_kv_cache* c, const int32_t* seqs, int n, int window, int sinks,
+                   dec_stream_t stream);
+
+/* Moves live pages so that they are the lowest numbers: with L live pages, the
+ * live pages numbered L and up move, in ascending order, to the free ones
+ * below L, in every layer; tables and refs follow.  The pages from L on are
+ * free afterwards. */
+int dec_kv_compact(const dec_kv_cache* c, dec_stream_t stream);
+
+/* Waits for `stream`, reads and clears the status word: DEC_OK, or
+ * DEC_ERR_DEVICE with the bits in *bits (if not NULL) and in the message of
+ * dec_last_error(NULL). */
+int dec_kv_status(const dec_kv_cache* c, int* bits, dec_stream_t stream);
+
 /* Source: none on the pages (resource lifetime of the C ABI).
  * Frees every device buffer and the graph; accepts NULL and partially
  * created handles.  Waits for the device first. */
@@ -364,7 +521,7 @@ int dec_destroy(dec_handle* h);
 
 /* Source: none on the pages (error reporting of the C ABI).
  * Message of the last failed call on h ("" if none); h may be NULL, in which
- * case the message of the last failed dec_create of this thread is returned. */
+ * case the message of the last failed dec_create (or dec_kv_ call) of this thread is returned. */
 const char* dec_last_error(const dec_handle* h);
 
 #ifdef __cplusplus

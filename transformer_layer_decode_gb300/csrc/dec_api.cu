@@ -14,6 +14,7 @@
 #include "../../include/dec.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "kv.h"
 
 using namespace tld;
 
@@ -152,6 +153,24 @@ int fail(dec_handle* h, int code, const char* fmt, ...) {
   else g_create_error = buf;
   return code;
 }
+
+}  // namespace
+
+// Failure of a call without a handle (message in dec_last_error(NULL)).
+int tld::fail_no_handle(int code, const char* fmt, ...) noexcept {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  try {
+    g_create_error = buf;
+  } catch (...) {  // no memory for the message: the code still says what happened
+  }
+  return code;
+}
+
+namespace {
 
 int cuda_fail(dec_handle* h, cudaError_t e, const char* what) {
   return fail(h, DEC_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));

@@ -1,0 +1,49 @@
+// The paged key/value cache of many sequences: layout and the view its kernels take.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/dec.h"
+
+namespace tld {
+
+// Records a message for dec_last_error(NULL) and returns `code`.
+int fail_no_handle(int code, const char* fmt, ...) noexcept;
+
+// One layer of a cache, as a kernel argument.
+struct KvView {
+  uint8_t* pool;  // the layer's pages
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t* status;
+  int32_t* scratch;
+  int64_t page_bytes;
+  int64_t half_bytes;  // of K (or V) in a page
+  int64_t head_bytes;  // of K (or V) of one head in a page
+  int n_pages, n_seqs, max_pages, page_rows, nkv;
+};
+
+// Bytes of one row of K or V of one head, scales included.
+__host__ __device__ inline int kv_row_bytes(int head_dim, bool q4) {
+  return q4 ? head_dim / 2 + head_dim / 16 : 2 * head_dim;
+}
+
+// The scratch of extend, fork and compact, in ints: a few words, the new names
+// of pages (compact) or the free pages found (extend, fork), the page copies
+// (source, destination), and where each list entry's pages start.
+constexpr int kKvScratchHead = 32;
+__host__ __device__ inline int64_t kv_scratch_moves(int64_t n_pages) { return kKvScratchHead + n_pages; }
+__host__ __device__ inline int64_t kv_scratch_offsets(int64_t n_pages, int64_t n_seqs) {
+  return kv_scratch_moves(n_pages) + n_pages + 2 * n_seqs;
+}
+__host__ __device__ inline int64_t kv_scratch_ints(int64_t n_pages, int64_t n_seqs) {
+  return kv_scratch_offsets(n_pages, n_seqs) + n_seqs + 1;
+}
+
+// Checks a cache (its pointers too, with `memory`); DEC_OK or the error, recorded.
+int kv_check(const dec_kv_cache* c, bool memory);
+KvView kv_view(const dec_kv_cache& c, int layer);
+
+}  // namespace tld

@@ -1,0 +1,356 @@
+// dec_kv_extend, dec_kv_fork, dec_kv_release and dec_kv_compact: the pages of a
+// paged key/value cache, counted and copied on the device.
+//
+// Each call that allocates or moves pages plans in one CTA (its work is a scan
+// over refs, a few ints per page), which checks everything and changes nothing
+// on an error, and carries the plan out in a second launch over the whole GPU.
+// All choices are by rank (the k-th page needed gets the k-th lowest free one),
+// so results do not depend on the order in which threads run.
+#include "common.cuh"
+#include "kv.h"
+
+using namespace tld;
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kCopyThreads = 256;
+
+// Words of the scratch head.
+enum { SC_OK = 0, SC_MOVES = 1, SC_LIVE = 2 };
+
+// Exclusive prefix sum over the CTA's kPlanThreads threads; *total gets the sum.
+__device__ int block_scan(int x, int* total) {
+  __shared__ int warp_sums[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // the sums of the previous call have been read
+  if (lane == 31) warp_sums[w] = incl;
+  __syncthreads();
+  int s = warp_sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  const int before = w ? __shfl_sync(0xffffffffu, s, w - 1) : 0;
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  return before + incl - x;
+}
+
+__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// A sequence's length, or -1 if it is not one the table can hold.
+__device__ __forceinline__ int kv_len(const KvView& c, int s) {
+  const int n = c.lens[s];
+  return n >= 0 && n <= c.max_pages * c.page_rows ? n : -1;
+}
+
+// Lists the `need` lowest free pages in the scratch; false if there are fewer.
+__device__ bool find_free(const KvView& c, int need) {
+  int32_t* list = c.scratch + kKvScratchHead;
+  int found = 0;
+  for (int base = 0; base < c.n_pages && found < need; base += kPlanThreads) {
+    const int p = base + threadIdx.x;
+    const int f = p < c.n_pages && c.refs[p] <= 0;
+    int total;
+    const int at = found + block_scan(f, &total);
+    if (f && at < need) list[at] = p;
+    found += total;
+  }
+  __syncthreads();
+  return found >= need;
+}
+
+// FORK: a = parents, b = children.  Otherwise extend: a = sequences, b = rows to add.
+template <bool FORK>
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_alloc(KvView c, const int32_t* a, const int32_t* b, int n) {
+  __shared__ uint32_t seen[65536 / 32];
+  __shared__ int bad_bits;
+  const int tid = threadIdx.x;
+  int32_t* offsets = c.scratch + kv_scratch_offsets(c.n_pages, c.n_seqs);
+  int32_t* moves = c.scratch + kv_scratch_moves(c.n_pages);
+  for (int i = tid; i < (c.n_seqs + 31) / 32; i += kPlanThreads) seen[i] = 0;
+  if (tid == 0) bad_bits = 0;
+  __syncthreads();
+
+  int total = 0;  // pages needed, at most n_pages + 1
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int i = base + tid;
+    int need = 0, bad = 0;
+    if (i < n) {
+      const int s = a ? a[i] : i;
+      const int x = b ? b[i] : 1;  // child, or rows to add
+      if (s >= 0 && (!FORK || x >= 0)) {
+        if (s >= c.n_seqs || (FORK ? x >= c.n_seqs : x < 0)) {
+          bad = DEC_KV_BAD_INDEX;
+        } else {
+          const int mark = FORK ? x : s;
+          if (atomicOr(&seen[mark >> 5], 1u << (mark & 31)) >> (mark & 31) & 1) bad = DEC_KV_BAD_LIST;
+          const int len = kv_len(c, s);
+          if (len < 0) {
+            bad |= DEC_KV_BAD_INDEX;
+          } else if (FORK) {
+            if (c.lens[x] != 0) bad |= DEC_KV_BAD_LIST;
+            need = len % c.page_rows != 0;
+            if (need) {
+              const int tail = c.table[(int64_t)s * c.max_pages + len / c.page_rows];
+              if (tail < 0 || tail >= c.n_pages) bad |= DEC_KV_BAD_INDEX;
+            }
+          } else if (x > c.max_pages * c.page_rows - len) {
+            bad |= DEC_KV_NO_PAGES;
+          } else {
+            need = div_up(len + x, c.page_rows) - div_up(len, c.page_rows);
+          }
+        }
+      }
+    }
+    if (bad) {
+      atomicOr(&bad_bits, bad);
+      need = 0;
+    }
+    int sum;
+    const int at = total + block_scan(min(need, c.n_pages + 1), &sum);
+    if (i < n) offsets[i] = at;
+    total = min(total + sum, c.n_pages + 1);
+  }
+  if (tid == 0) offsets[n] = total;
+  __syncthreads();
+  if (FORK) {  // a parent that is also a child would be copied before or after it changes
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int s = a[i], x = b[i];
+      if (s >= 0 && s < c.n_seqs && x >= 0 && (seen[s >> 5] >> (s & 31) & 1)) atomicOr(&bad_bits, DEC_KV_BAD_LIST);
+    }
+    __syncthreads();
+  }
+  int bad = bad_bits;  // the same in every thread, as are total and find_free's answer
+  if (!bad && (total > c.n_pages || !find_free(c, total))) bad = DEC_KV_NO_PAGES;
+  if (bad) {
+    if (tid == 0) {
+      atomicOr(c.status, bad);
+      c.scratch[SC_OK] = 0;
+      c.scratch[SC_MOVES] = 0;
+    }
+    return;
+  }
+
+  const int32_t* list = c.scratch + kKvScratchHead;
+  if (FORK) {
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int at = offsets[i];
+      if (offsets[i + 1] > at) {
+        const int s = a[i];
+        moves[2 * at] = c.table[(int64_t)s * c.max_pages + c.lens[s] / c.page_rows];
+        moves[2 * at + 1] = list[at];
+      }
+    }
+  } else {
+    for (int k = tid; k < total; k += kPlanThreads) {  // page k belongs to the last entry starting at or before it
+      int lo = 0, hi = n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (offsets[mid] <= k) lo = mid;
+        else hi = mid;
+      }
+      const int s = a ? a[lo] : lo;
+      c.table[(int64_t)s * c.max_pages + div_up(c.lens[s], c.page_rows) + k - offsets[lo]] = list[k];
+      c.refs[list[k]] = 1;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int s = a ? a[i] : i;
+      if (s >= 0) c.lens[s] += b ? b[i] : 1;
+    }
+  }
+  if (tid == 0) {
+    c.scratch[SC_OK] = 1;
+    c.scratch[SC_MOVES] = total;
+  }
+}
+
+// Ranks the live pages from `live` on against the free pages below it, renames
+// them in refs and lists the copies.
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_compact(KvView c) {
+  const int tid = threadIdx.x;
+  int32_t* name = c.scratch + kKvScratchHead;
+  int32_t* moves = c.scratch + kv_scratch_moves(c.n_pages);
+  int live = 0;
+  for (int base = 0; base < c.n_pages; base += kPlanThreads) {
+    const int p = base + tid;
+    int total;
+    block_scan(p < c.n_pages && c.refs[p] > 0, &total);
+    live += total;
+  }
+  int holes = 0, movers = 0;
+  for (int base = 0; base < c.n_pages; base += kPlanThreads) {
+    const int p = base + tid;
+    const bool used = p < c.n_pages && c.refs[p] > 0;
+    const int hole = p < live && !used, mover = p >= live && used;  // (p < live <= n_pages)
+    int total;
+    const int at = block_scan(hole | mover << 16, &total);
+    if (hole) moves[2 * (holes + (at & 0xffff)) + 1] = p;
+    if (mover) moves[2 * (movers + (at >> 16))] = p;
+    if (p < c.n_pages) name[p] = used && !mover ? p : -1;
+    holes += total & 0xffff;
+    movers += total >> 16;
+  }
+  __syncthreads();
+  for (int k = tid; k < movers; k += kPlanThreads) {
+    const int from = moves[2 * k], to = moves[2 * k + 1];
+    c.refs[to] = c.refs[from];
+    c.refs[from] = 0;
+    name[from] = to;
+  }
+  if (tid == 0) {
+    c.scratch[SC_OK] = 1;
+    c.scratch[SC_MOVES] = movers;
+    c.scratch[SC_LIVE] = live;
+  }
+}
+
+// Carries out a plan: copies the listed pages in every layer; FORK: writes the
+// children's table rows and counts; otherwise (compact) renames the pages in
+// every table.
+template <bool FORK>
+__global__ void __launch_bounds__(kCopyThreads) kv_apply(KvView c, const int32_t* parents, const int32_t* children,
+                                                         int n, int n_layers) {
+  if (!c.scratch[SC_OK]) return;
+  const int64_t thread = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
+  const int64_t threads = (int64_t)gridDim.x * kCopyThreads;
+  if (FORK) {
+    const int32_t* offsets = c.scratch + kv_scratch_offsets(c.n_pages, c.n_seqs);
+    const int32_t* list = c.scratch + kKvScratchHead;
+    for (int64_t e = thread; e < (int64_t)n * c.max_pages; e += threads) {
+      const int i = (int)(e / c.max_pages), at = (int)(e % c.max_pages);
+      const int p = parents[i], ch = children[i];
+      if (p < 0 || ch < 0) continue;
+      const int len = c.lens[p];
+      int page = c.table[(int64_t)p * c.max_pages + at];
+      if (len % c.page_rows && at == len / c.page_rows) {
+        page = list[offsets[i]];
+        c.refs[page] = 1;
+      } else if (page >= 0 && page < c.n_pages) {
+        atomicAdd(c.refs + page, 1);
+      }
+      c.table[(int64_t)ch * c.max_pages + at] = page;
+      if (at == 0) c.lens[ch] = len;
+    }
+  } else {
+    const int32_t* name = c.scratch + kKvScratchHead;
+    for (int64_t e = thread; e < (int64_t)c.n_seqs * c.max_pages; e += threads) {
+      const int page = c.table[e];
+      if (page < 0) continue;
+      const int now = page < c.n_pages ? name[page] : -1;
+      if (now < 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
+      else if (now != page) c.table[e] = now;
+    }
+  }
+  const int32_t* moves = c.scratch + kv_scratch_moves(c.n_pages);
+  const int64_t words = c.page_bytes / 16, total = (int64_t)c.scratch[SC_MOVES] * n_layers * words;
+  for (int64_t e = thread; e < total; e += threads) {
+    const int64_t w = e % words, r = e / words;
+    const int64_t layer = r % n_layers, m = r / n_layers;
+    const int from = moves[2 * m], to = moves[2 * m + 1];
+    uint8_t* base = c.pool + layer * c.n_pages * c.page_bytes;
+    reinterpret_cast<uint4*>(base + to * c.page_bytes)[w] = reinterpret_cast<const uint4*>(base + from * c.page_bytes)[w];
+  }
+}
+
+// One CTA per list entry: takes the sequence's pages out of its table.
+__global__ void __launch_bounds__(kCopyThreads) kv_release(KvView c, const int32_t* seqs, int window, int sinks) {
+  const int s = seqs ? seqs[blockIdx.x] : blockIdx.x;
+  if (s < 0) return;
+  const int len = s < c.n_seqs ? kv_len(c, s) : -1;
+  if (len < 0) {
+    if (threadIdx.x == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
+    return;
+  }
+  int first = 0, last = c.max_pages;
+  if (window) {
+    first = sinks / c.page_rows + (sinks % c.page_rows != 0);
+    last = len > window ? (len - window) / c.page_rows : 0;
+  }
+  for (int i = first + threadIdx.x; i < last; i += kCopyThreads) {
+    int32_t* entry = c.table + (int64_t)s * c.max_pages + i;
+    if (*entry < 0) continue;
+    const int page = atomicExch(entry, -1);  // a sequence listed twice gives each page back once
+    if (page < 0) continue;
+    if (page < c.n_pages) atomicSub(c.refs + page, 1);
+    else atomicOr(c.status, DEC_KV_BAD_INDEX);
+  }
+  if (!window && threadIdx.x == 0) c.lens[s] = 0;
+}
+
+cudaLaunchConfig_t config(int64_t ctas, int threads, dec_stream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  return cfg;
+}
+
+int sm_count(int* n) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail_no_handle(DEC_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+  return DEC_OK;
+}
+
+int launched(cudaError_t e) {
+  return e == cudaSuccess ? DEC_OK : fail_no_handle(DEC_ERR_CUDA, "page kernel launch: %s", cudaGetErrorString(e));
+}
+
+int check_list(const dec_kv_cache* c, int n) {
+  if (int rc = kv_check(c, true)) return rc;
+  if (n < 0 || n > c->n_seqs) return fail_no_handle(DEC_ERR_ARG, "a list of %d of %d sequences", n, c->n_seqs);
+  return DEC_OK;
+}
+
+}  // namespace
+
+extern "C" int dec_kv_extend(const dec_kv_cache* c, const int32_t* seqs, const int32_t* n_new, int n,
+                             dec_stream_t stream) {
+  if (int rc = check_list(c, n)) return rc;
+  if (n == 0) return DEC_OK;
+  const cudaLaunchConfig_t cfg = config(1, kPlanThreads, stream);
+  return launched(cudaLaunchKernelEx(&cfg, kv_plan_alloc<false>, kv_view(*c, 0), seqs, n_new, n));
+}
+
+extern "C" int dec_kv_fork(const dec_kv_cache* c, const int32_t* parents, const int32_t* children, int n,
+                           dec_stream_t stream) {
+  if (int rc = check_list(c, n)) return rc;
+  if (n == 0) return DEC_OK;
+  if (!parents || !children) return fail_no_handle(DEC_ERR_ARG, "parents or children is NULL");
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  const KvView v = kv_view(*c, 0);
+  const cudaLaunchConfig_t plan = config(1, kPlanThreads, stream), apply = config(8 * sms, kCopyThreads, stream);
+  if (int rc = launched(cudaLaunchKernelEx(&plan, kv_plan_alloc<true>, v, parents, children, n))) return rc;
+  return launched(cudaLaunchKernelEx(&apply, kv_apply<true>, v, parents, children, n, c->n_layers));
+}
+
+extern "C" int dec_kv_release(const dec_kv_cache* c, const int32_t* seqs, int n, int window, int sinks,
+                              dec_stream_t stream) {
+  if (int rc = check_list(c, n)) return rc;
+  if (window < 0 || sinks < 0) return fail_no_handle(DEC_ERR_ARG, "window %d, sinks %d", window, sinks);
+  if (n == 0) return DEC_OK;
+  const cudaLaunchConfig_t cfg = config(n, kCopyThreads, stream);
+  return launched(cudaLaunchKernelEx(&cfg, kv_release, kv_view(*c, 0), seqs, window, sinks));
+}
+
+extern "C" int dec_kv_compact(const dec_kv_cache* c, dec_stream_t stream) {
+  if (int rc = kv_check(c, true)) return rc;
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  const KvView v = kv_view(*c, 0);
+  const cudaLaunchConfig_t plan = config(1, kPlanThreads, stream), apply = config(8 * sms, kCopyThreads, stream);
+  if (int rc = launched(cudaLaunchKernelEx(&plan, kv_plan_compact, v))) return rc;
+  return launched(cudaLaunchKernelEx(&apply, kv_apply<false>, v, (const int32_t*)nullptr, (const int32_t*)nullptr, 0,
+                                     c->n_layers));
+}

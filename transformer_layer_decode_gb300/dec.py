@@ -40,7 +40,10 @@ EXPORTED = ("dec_create", "dec_load_weights", "dec_load_kv", "dec_read_kv", "dec
             "dec_load_lm_head", "dec_set_token_out", "dec_set_page_table",
             "dec_set_tap", "dec_set_dot_tap", "dec_set_timeline", "dec_sync_status",
             "dec_check_guards", "dec_get_info", "dec_launch_kernel",
-            "dec_destroy", "dec_last_error", "dec_attention_noalloc")
+            "dec_destroy", "dec_last_error", "dec_attention_noalloc",
+            "dec_kv_sizes", "dec_kv_append", "dec_kv_read", "dec_kv_attention",
+            "dec_kv_attention_workspace", "dec_kv_extend", "dec_kv_fork", "dec_kv_release",
+            "dec_kv_compact", "dec_kv_status")
 
 
 class DecError(RuntimeError):
@@ -80,6 +83,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "(run transformer_layer_decode_gb300.build.build())")
     L = ctypes.CDLL(path)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    i64, f32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "dec_create": [ctypes.POINTER(ModelDesc), ctypes.POINTER(vp)],
         "dec_load_weights": [vp, i32, i32, vp, sz],
@@ -99,6 +103,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dec_launch_kernel": [vp, i32, i32, i32, vp],
         "dec_destroy": [vp],
         "dec_attention_noalloc": [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp],
+        # a paged cache of many sequences (bound in kv.py)
+        "dec_kv_sizes": [vp, vp, vp],
+        "dec_kv_append": [vp, i32, vp, vp, i32, i64, vp, vp, i32, vp],
+        "dec_kv_read": [vp, i32, vp, vp, i32, i64, vp, vp, i32, vp],
+        "dec_kv_attention": [vp, i32, vp, vp, i32, i64, i64, vp, i32, i32, i32, i32, f32, vp, sz, vp],
+        "dec_kv_attention_workspace": [vp, i32, i32, vp],
+        "dec_kv_extend": [vp, vp, vp, i32, vp],
+        "dec_kv_fork": [vp, vp, vp, i32, vp],
+        "dec_kv_release": [vp, vp, i32, i32, i32, vp],
+        "dec_kv_compact": [vp, vp],
+        "dec_kv_status": [vp, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

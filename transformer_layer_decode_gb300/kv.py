@@ -1,0 +1,236 @@
+"""A paged key/value cache of many sequences (the dec_kv_ calls of include/dec.h).
+
+:class:`KVCache` holds the tensors of one cache and marshals the calls: rows
+written and read (bf16 or 4-bit blocks), attention of one query per sequence
+with a sliding window and first rows that stay visible, and pages allocated,
+shared, freed and made dense.  Every call is queued on a stream and waits for
+nothing; :meth:`KVCache.sync_status` reports what the kernels refused.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import dec
+
+DEC_KV_BF16, DEC_KV_Q4B32 = 0, 1
+DEC_IO_F32, DEC_IO_BF16 = 0, 1
+DEC_KV_BAD_INDEX, DEC_KV_NO_PAGES, DEC_KV_BAD_LIST = 1, 2, 4
+
+FORMATS = {"bf16": DEC_KV_BF16, "q4": DEC_KV_Q4B32}
+_TYPES = {torch.float32: DEC_IO_F32, torch.bfloat16: DEC_IO_BF16}
+
+
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("pool", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("status", ctypes.c_void_p), ("scratch", ctypes.c_void_p)]
+
+
+def default_page_rows(head_dim: int) -> int:
+    """Rows of a page unless asked otherwise: those of one attention chunk of the decoder."""
+    return 64 if head_dim == 128 else 128
+
+
+class KVCache:
+    """One cache: a pool of pages for every layer, and the tables of its sequences.
+
+    n_layers, n_kv_heads, head_dim (64 or 128), page_rows (a multiple of 16)
+    and fmt ("bf16" or "q4") fix the shape of a page.  The tensors are made
+    empty here from n_pages, n_seqs and max_pages (pages of one sequence), or
+    taken as they are: pool uint8 [n_layers, n_pages, page_bytes], table int32
+    [n_seqs, max_pages], lens int32 [n_seqs], refs int32 [n_pages].
+    """
+
+    def __init__(self, *, n_layers: int, n_kv_heads: int, head_dim: int, page_rows: int | None = None,
+                 fmt: str = "bf16", n_pages: int | None = None, n_seqs: int | None = None,
+                 max_pages: int | None = None, pool=None, table=None, lens=None, refs=None,
+                 device=None, lib_path: str | None = None):
+        if fmt not in FORMATS:
+            raise ValueError(f"fmt {fmt!r}: one of {sorted(FORMATS)}")
+        self.lib = dec.load_library(lib_path or dec.LIB_PATH)
+        given = [t for t in (pool, table, lens, refs) if t is not None]
+        if given:
+            if len(given) != 4:
+                raise ValueError("pool, table, lens and refs are given together")
+            n_pages, (n_seqs, max_pages) = refs.numel(), table.shape
+            device = pool.device
+        elif None in (n_pages, n_seqs, max_pages):
+            raise ValueError("n_pages, n_seqs and max_pages are needed to make a cache")
+        page_rows = default_page_rows(head_dim) if page_rows is None else page_rows
+        self.desc = KVCacheDesc(n_layers, n_kv_heads, head_dim, page_rows, n_pages, n_seqs, max_pages,
+                                FORMATS[fmt])
+        self._ref = ctypes.byref(self.desc)
+        page_bytes, ints = ctypes.c_size_t(), ctypes.c_size_t()
+        self._check(self.lib.dec_kv_sizes(self._ref, ctypes.byref(page_bytes), ctypes.byref(ints)))
+        self.page_bytes = page_bytes.value
+        if given:
+            self._tensor("pool", pool, torch.uint8, (n_layers, n_pages, self.page_bytes), device)
+            self._tensor("lens", lens, torch.int32, (n_seqs,), device)
+            self._tensor("refs", refs, torch.int32, (n_pages,), device)
+            self._tensor("table", table, torch.int32, (n_seqs, max_pages), device)
+        else:
+            device = torch.device("cuda") if device is None else torch.device(device)
+            pool = torch.empty(n_layers, n_pages, self.page_bytes, dtype=torch.uint8, device=device)
+            table = torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device)
+            lens = torch.zeros(n_seqs, dtype=torch.int32, device=device)
+            refs = torch.zeros(n_pages, dtype=torch.int32, device=device)
+        if pool.device.type != "cuda":
+            raise ValueError("the cache's tensors must be on a CUDA device")
+        self.device = pool.device
+        self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.scratch = torch.empty(ints.value, dtype=torch.int32, device=self.device)
+        for name in ("pool", "table", "lens", "refs", "status", "scratch"):
+            setattr(self.desc, name, getattr(self, name).data_ptr())
+        self._workspaces: dict = {}
+
+    # ---- marshalling ----------------------------------------------------------
+
+    def _check(self, rc: int):
+        if rc != dec.DEC_OK:
+            raise dec.DecError(rc, self.lib.dec_last_error(None).decode())
+
+    @staticmethod
+    def _tensor(name, t, dtype, shape, device):
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on {device} is wanted, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+    def _ints(self, name, t, n=None):
+        """(address, length) of a device int32 list."""
+        if t is None:
+            return None, n
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name}: a contiguous one-dimensional int32 tensor on {self.device} is wanted")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name}: {t.shape[0]} entries for {n}")
+        return t.data_ptr(), t.shape[0]
+
+    def _rows(self, name, t, heads=None):
+        """(address, type, elements from row to row) of a [n, heads, head_dim] tensor with whole rows."""
+        d = self.desc.head_dim
+        if (t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads)
+                or t.dtype not in _TYPES or t.device != self.device
+                or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+            raise ValueError(f"{name}: a float32 or bfloat16 tensor [n, {heads or 'heads'}, {d}] on {self.device} "
+                             "with contiguous rows is wanted")
+        return t.data_ptr(), _TYPES[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+
+    def _call(self, fn, *args, stream=None):
+        if stream is None:
+            handle = torch.cuda.current_stream(self.device).cuda_stream
+        else:
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if torch.cuda.current_device() == self.device.index:
+            self._check(fn(self._ref, *args, handle))
+        else:
+            with torch.cuda.device(self.device):
+                self._check(fn(self._ref, *args, handle))
+
+    # ---- rows -----------------------------------------------------------------
+
+    def append(self, layer: int, k, v, *, seqs=None, positions=None, stream=None):
+        """Writes row t of k and v ([n, n_kv_heads, head_dim], keys already rotated) as row positions[t]
+        of sequence seqs[t]; without positions, as the sequence's last row; without seqs, of sequence t."""
+        kp, kt, ks = self._rows("k", k, self.desc.n_kv_heads)
+        vp, vt, vs = self._rows("v", v, self.desc.n_kv_heads)
+        if k.shape[0] != v.shape[0] or kt != vt or ks != vs:
+            raise ValueError("k and v: the same type, rows and row stride are wanted")
+        n = k.shape[0]
+        sp, _ = self._ints("seqs", seqs, n)
+        pp, _ = self._ints("positions", positions, n)
+        self._call(self.lib.dec_kv_append, layer, kp, vp, kt, ks, sp, pp, n, stream=stream)
+
+    def read(self, layer: int, seqs, positions=None, *, k_out=None, v_out=None, dtype=torch.float32, stream=None):
+        """Rows positions[t] of sequences seqs[t] as values: (k, v), each [n, n_kv_heads, head_dim].
+        Rows of skipped entries keep what k_out and v_out hold (zeros where these are made here)."""
+        sp, n = self._ints("seqs", seqs)
+        pp, _ = self._ints("positions", positions, n)
+        shape = (n, self.desc.n_kv_heads, self.desc.head_dim)
+        if k_out is None:
+            k_out = torch.zeros(shape, dtype=dtype if v_out is None else v_out.dtype, device=self.device)
+        if v_out is None:
+            v_out = torch.zeros(shape, dtype=k_out.dtype, device=self.device)
+        kp, kt, ks = self._rows("k_out", k_out, shape[1])
+        vp, vt, vs = self._rows("v_out", v_out, shape[1])
+        if k_out.shape[0] != n or v_out.shape[0] != n or kt != vt or ks != vs:
+            raise ValueError(f"k_out and v_out: the same type and row stride and {n} rows are wanted")
+        self._call(self.lib.dec_kv_read, layer, kp, vp, kt, ks, sp, pp, n, stream=stream)
+        return k_out, v_out
+
+    # ---- attention ------------------------------------------------------------
+
+    def workspace(self, n: int, n_q_heads: int):
+        """A workspace for attention calls of up to n queries: one call at a time may use it."""
+        size = ctypes.c_size_t()
+        with torch.cuda.device(self.device):
+            self._check(self.lib.dec_kv_attention_workspace(self._ref, n, n_q_heads, ctypes.byref(size)))
+        return torch.empty(size.value, dtype=torch.uint8, device=self.device)
+
+    def attention(self, layer: int, q, *, seqs=None, window: int = 0, sinks: int = 0, scale: float = 0.0,
+                  out=None, workspace=None, stream=None):
+        """softmax(scale q K^T) V of one query per entry of seqs over its sequence's visible rows: the last
+        `window` ones (0: all) and the first `sinks` ones.  q and out: [n, n_q_heads, head_dim].  Rows of
+        skipped entries keep what out holds (zeros where it is made here).  Without a workspace the call
+        takes one from torch's allocator for the current stream, so `stream` needs one of its own."""
+        qp, qt, qs = self._rows("q", q)
+        n, heads = q.shape[0], q.shape[1]
+        sp, _ = self._ints("seqs", seqs, n)
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format) if seqs is None else \
+                torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        op, ot, os_ = self._rows("out", out, heads)
+        if ot != qt or out.shape[0] != n:
+            raise ValueError("out: the type and rows of q are wanted")
+        if workspace is None:
+            if stream is not None:
+                raise ValueError("a call with a stream of its own needs a workspace of its own")
+            size = self._workspaces.get((n, heads))
+            if size is None:
+                workspace = self.workspace(n, heads)
+                self._workspaces[(n, heads)] = workspace.numel()
+            else:
+                workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous memory on {self.device} is wanted")
+        self._call(self.lib.dec_kv_attention, layer, qp, op, qt, qs, os_, sp, n, heads, window, sinks, scale,
+                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+        return out
+
+    # ---- pages ----------------------------------------------------------------
+
+    def extend(self, seqs=None, n_new=None, *, stream=None):
+        """Makes sequences longer (by n_new[i] rows, or one), with the pages that takes: all or nothing."""
+        sp, n = self._ints("seqs", seqs)
+        if seqs is None:
+            n = self.desc.n_seqs if n_new is None else n_new.shape[0]
+        np_, _ = self._ints("n_new", n_new, n)
+        self._call(self.lib.dec_kv_extend, sp, np_, n, stream=stream)
+
+    def fork(self, parents, children, *, stream=None):
+        """Makes the empty sequences `children` copies of `parents`: full pages shared, a partly filled
+        last page copied.  All or nothing."""
+        pp, n = self._ints("parents", parents)
+        cp, _ = self._ints("children", children, n)
+        self._call(self.lib.dec_kv_fork, pp, cp, n, stream=stream)
+
+    def release(self, seqs=None, *, window: int = 0, sinks: int = 0, stream=None):
+        """Empties sequences and frees their pages; with a window, frees only the pages that a query
+        with this window and these sinks no longer sees."""
+        sp, n = self._ints("seqs", seqs)
+        self._call(self.lib.dec_kv_release, sp, self.desc.n_seqs if seqs is None else n, window, sinks,
+                   stream=stream)
+
+    def compact(self, *, stream=None):
+        """Moves live pages to the lowest numbers; tables and counts follow."""
+        self._call(self.lib.dec_kv_compact, stream=stream)
+
+    def sync_status(self, stream=None):
+        """Waits for the stream and raises DecError if a kernel refused something since the last call."""
+        bits = ctypes.c_int()
+        self._call(self.lib.dec_kv_status, ctypes.byref(bits), stream=stream)
