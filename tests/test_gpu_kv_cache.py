@@ -81,6 +81,8 @@ class Filled:
             n = self.k[s].shape[1]
             ds = (self.pages.d + 8) * 2.0 ** -24 * np.abs(dots)[:, None]
             tol = size * (2 * ds + 2 * n * 2.0 ** -24 + 2.0 ** -19)
+            if self.pages.fmt == "q4" and n:
+                tol = tol + n * 2.0 ** -31 * np.abs(self.v[s]).max() / 7
             tol = tol + (np.abs(o) + tol) * (2.0 ** -8 if bf16 else 2.0 ** -24) + 1e-37
             bad = np.abs(got[r] - o) > tol
             assert not bad.any(), (what, r, s, n, np.argwhere(bad)[:4].tolist(), np.abs(got[r] - o)[bad][:4], tol[bad][:4])

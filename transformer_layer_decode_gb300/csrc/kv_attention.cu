@@ -1,6 +1,7 @@
 // dec_kv_attention: attention of one query per sequence over a paged key/value
 // cache, bf16 or in 4-bit blocks, with a sliding window and first rows that
 // stay visible.
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -10,7 +11,36 @@ using namespace tld;
 
 namespace {
 
-constexpr int kSimpleThreads = 128;
+// ---- shape of the launch ------------------------------------------------------
+// A tile is 16 rows of one sequence and KV head; pages hold whole tiles.  A
+// unit is (query, KV head, up to 8 of its query heads).  All visible tiles of
+// all units, in that order, are one line that is cut evenly among the CTAs, by
+// the lengths on the device: a long sequence is spread over many CTAs, short
+// ones share one, and a captured graph follows the lengths.  Within a CTA the
+// warps take tiles in turn, each with its own running softmax.
+constexpr int kTileRows = 16;
+constexpr int kWarps = 4;
+constexpr int kThreadsA = kWarps * 32;
+constexpr int kHeadBlock = 8;      // query heads of a unit: the n of the tensor-core products
+constexpr int kMaxQueries = 65535;
+constexpr int kChunkRows = 128;    // queries whose tiles one warp counts at a time
+constexpr int kMaxChunks = (kMaxQueries + kChunkRows - 1) / kChunkRows;
+// A reference moves only when a score passes it by this (log2 units).
+constexpr float kSlack = 5.f;
+
+template <int D, bool Q4>
+struct Tile {
+  static constexpr int NB = D / 32;                                  // blocks of 32 dimensions
+  static constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;               // codes or values
+  static constexpr int kHalf = kTileRows * (kRowBytes + (Q4 ? 2 * NB : 0));  // K or V, scales after the rows
+  static constexpr int kBytes = 2 * kHalf;
+  static constexpr int kStages = Q4 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 4);
+  static constexpr int kRing = kWarps * kStages * kBytes;
+  static constexpr int kMergeRow = D + 8;                            // floats; heads apart by 8 banks
+  static constexpr int kMerge = kWarps * kHeadBlock * kMergeRow * 4; // the warps' sums, once the ring is drained
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kCtasPerSm = Q4 ? 4 : 3;
+};
 
 struct KvAttnParams {
   KvView c;
@@ -19,106 +49,816 @@ struct KvAttnParams {
   int64_t q_stride, o_stride;
   const int32_t* seqs;
   int n, nq, window, sinks;
-  float scale;
+  int group, head_blocks;  // query heads of a KV head, and blocks of 8 of them
+  float scale;             // times log2(e)
+  float* rec;              // [2 * CTAs][8][D]: sums of units cut between CTAs
+  float2* ref;             // [2 * CTAs][8]: reference and sum of the weights
+  int4* cut;               // [CTAs]: the unit that begins in a CTA and ends in a later one
 };
 
-// Value e of a row of K or V of one head.
+// A query's visible rows: [0, first) and [lo, len).
+struct Rows {
+  int seq, len, lo, first;
+  int sink_tiles, win_tile0, tiles;
+};
+
+__device__ __forceinline__ Rows query_rows(const KvAttnParams& p, int r, bool* bad) {
+  Rows v{-1, 0, 0, 0, 0, 0, 0};
+  const int s = p.seqs ? p.seqs[r] : r;
+  if (s < 0) return v;
+  const int len = s < p.c.n_seqs ? p.c.lens[s] : -1;
+  if (len < 0 || len > p.c.max_pages * p.c.page_rows) {
+    *bad = true;
+    return v;
+  }
+  v.seq = s;
+  v.len = len;
+  v.lo = p.window && len > p.window ? len - p.window : 0;
+  v.first = min(p.sinks, v.lo);
+  v.sink_tiles = (v.first + kTileRows - 1) / kTileRows;
+  v.win_tile0 = max(v.lo / kTileRows, v.sink_tiles);
+  v.tiles = v.sink_tiles + (len + kTileRows - 1) / kTileRows - v.win_tile0;
+  return v;
+}
+
+__device__ __forceinline__ int tile_row(const Rows& v, int t) {
+  return kTileRows * (t < v.sink_tiles ? t : v.win_tile0 + t - v.sink_tiles);
+}
+
+// ---- tensor-core products and conversions ---------------------------------------
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+
+// Takes the next piece off (x, y): the pair rounded to 16 bits, leaving the rest.
+__device__ __forceinline__ uint32_t take_bf16(float& x, float& y) {
+  const uint32_t w = pack_bf16(x, y);
+  x -= bf16lo(w);
+  y -= bf16hi(w);
+  return w;
+}
+__device__ __forceinline__ uint32_t take_f16(float& x, float& y) {
+  const uint32_t w = pack_f16(x, y);
+  const float2 f = unpack_f16(w);
+  x -= f.x;
+  y -= f.y;
+  return w;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Byte of 16-byte piece `piece` of row `row` within K or V of a staged tile.
+// The pieces are placed so that the reads below touch every bank once: the K
+// reads of 8 lanes (rows 2i, 2i + 1, four neighbouring pieces each) and the V
+// reads (rows 0, 2, 4, 6 or 1, 3, 5, 7, the same pieces of each).
 template <int D, bool Q4>
-__device__ __forceinline__ float kv_value(const KvView& c, const uint8_t* head, int row, int e) {
-  if constexpr (!Q4) {
-    return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(head)[row * D + e] << 16);
-  } else {
-    constexpr int NB = D / 32;
-    const int b = e / 32, nib = ((e % 32) / 4 * NB + b) * 4 + e % 4;
-    const int byte = head[(int64_t)row * (D / 2) + nib / 2];
-    const float s = __half2float(reinterpret_cast<const __half*>(head + (int64_t)c.page_rows * (D / 2))[row * NB + b]);
-    return (float)((byte >> (4 * (nib & 1)) & 15) - 8) * s;
+__device__ __forceinline__ int staged(int row, int piece) {
+  const int j = row & 7, t = j >> 1;
+  if constexpr (!Q4) {  // rows of 128 or 256 bytes
+    return row * (2 * D) + ((piece ^ ((t ^ ((j & 1) << 1)) << 1)) << 4);
+  } else if constexpr (D == 128) {  // rows of 64 bytes, two to a line of banks
+    return (row >> 1) * 128 + (((j & 1) ^ (t & 1)) << 6) + ((piece ^ (t & 2)) << 4);
+  } else {  // rows of 32 bytes, four to a line
+    return (row >> 3) * 256 + ((j & 1) << 7) + ((t ^ ((j & 1) << 1)) << 5) + (piece << 4);
   }
 }
 
-// One CTA per (query head, query): chunks of 128 visible rows, a thread per
-// row for the scores, a thread per dimension for the sums.
+// ---- the warp's part: tiles of one unit -------------------------------------------
+// For one tile the scores are computed as S[head][row] = q K^T: q is the
+// 16-row operand (its 8 heads in rows 0-7; rows 8-15 hold the next piece of the
+// same heads, so that 16-bit products add up to fp32 ones), K the other, 8 rows
+// of the tile at a time.  Lane (g, t) = (lane / 4, lane % 4) then has head g and
+// rows 2t, 2t + 1 of each half, which is exactly the operand P^T of the second
+// product, O^T[dim][head] = V^T P^T: no value changes lanes.  The order of the
+// dimensions within a product and of O's rows is free, and chosen so that a
+// lane's operands are whole words of the staged rows.
 template <int D, bool Q4, class T>
-__global__ void __launch_bounds__(kSimpleThreads) kv_attn_simple(KvAttnParams p) {
-  __shared__ float q_s[D], w_s[kSimpleThreads], red[kSimpleThreads / 32];
-  __shared__ const uint8_t* base_s[kSimpleThreads];
-  __shared__ int row_s[kSimpleThreads];
-  const KvView& c = p.c;
-  const int tid = threadIdx.x, h = blockIdx.x, r = blockIdx.y;
-  const int s = p.seqs ? p.seqs[r] : r;
-  if (s < 0) return;
-  const int len = s < c.n_seqs ? c.lens[s] : -1;
-  if (len < 0 || len > c.max_pages * c.page_rows) {
-    if (tid == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
-    return;
+struct WarpState {
+  static constexpr int NB = D / 32;
+  // pieces of q: bf16 q is exact in one; fp32 q in three of bf16 (24 bits) or,
+  // scaled to fp16's range, in two of fp16 (22 bits)
+  static constexpr int kQ = Q4 ? 2 : (sizeof(T) == 4 ? 3 : 1);
+  // pieces of the weights: 22 bits (two of fp16), or 24 (three of bf16) for
+  // fp32 results and 16 for bf16 ones
+  static constexpr int kP = Q4 ? 2 : (sizeof(T) == 4 ? 3 : 2);
+  uint32_t a[2 * NB][4];                    // q: pieces one and two
+  uint32_t a3[kQ == 3 ? 2 * NB : 1][2];     // piece three
+  float bias[Q4 ? NB : 1];                  // -8 sum of q over a block (codes are stored plus 8)
+  float f;                                  // score = f * product, in log2 units
+  float acc[NB][2][4];                      // O^T; see out_dim
+  float ref, l;                             // head g: reference of the weights 2^(score - ref), and their sum
+  float lim, top;                           // a score passes at ref + lim; scales of V seen are below top (Q4)
+
+  // acc[x][y][0..1]: dimension out_dim(x, y, g) of heads 2t, 2t + 1; [2..3]: the next dimension.
+  __device__ static int out_dim(int x, int y, int g) {
+    return Q4 ? 32 * x + 4 * g + 2 * y : 64 * (x >> 1) + 8 * g + 4 * (x & 1) + 2 * y;
   }
-  const int lo = p.window ? max(len - p.window, 0) : 0, first = min(p.sinks, lo), count = first + len - lo;
-  const int head = h / (p.nq / c.nkv);
-  const T* q = static_cast<const T*>(p.q) + r * p.q_stride + (int64_t)h * D;
-  for (int e = tid; e < D; e += kSimpleThreads) {
-    if constexpr (sizeof(T) == 4) q_s[e] = q[e];
-    else q_s[e] = __uint_as_float((uint32_t)q[e] << 16);
-  }
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int j0 = 0; j0 < count; j0 += kSimpleThreads) {
-    __syncthreads();
-    const int j = j0 + tid;
-    const uint8_t* base = nullptr;
-    int row = 0;
-    float score = -INFINITY;
-    if (j < count) {
-      const int pos = j < first ? j : lo + j - first;
-      const int page = c.table[(int64_t)s * c.max_pages + pos / c.page_rows];
-      row = pos % c.page_rows;
-      if (page >= 0 && page < c.n_pages) {
-        base = c.pool + page * c.page_bytes + head * c.head_bytes;
-        float dot = 0.f;
-        for (int e = 0; e < D; ++e) dot = fmaf(q_s[e], kv_value<D, Q4>(c, base, row, e), dot);
-        score = dot * p.scale;
+
+  __device__ __forceinline__ void load_q(const T* q, bool valid, int t, float scale) {
+    float x[NB][8];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (!valid) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
+      } else if constexpr (sizeof(T) == 4) {
+        const float4* p = reinterpret_cast<const float4*>(q + 32 * b + 8 * t);
+        const float4 u = p[0], w = p[1];
+        x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w;
+        x[b][4] = w.x, x[b][5] = w.y, x[b][6] = w.z, x[b][7] = w.w;
       } else {
-        atomicOr(c.status, DEC_KV_BAD_INDEX);
+        const uint4 u = *reinterpret_cast<const uint4*>(q + 32 * b + 8 * t);
+        x[b][0] = bf16lo(u.x), x[b][1] = bf16hi(u.x), x[b][2] = bf16lo(u.y), x[b][3] = bf16hi(u.y);
+        x[b][4] = bf16lo(u.z), x[b][5] = bf16hi(u.z), x[b][6] = bf16lo(u.w), x[b][7] = bf16hi(u.w);
       }
     }
-    float top = warp_max(score);
-    if ((tid & 31) == 0) red[tid >> 5] = top;
-    base_s[tid] = base;
-    row_s[tid] = row;
-    __syncthreads();
-    for (int w = 0; w < kSimpleThreads / 32; ++w) top = fmaxf(top, red[w]);
-    const float m_new = fmaxf(m, top);
-    const float keep = m_new == -INFINITY ? 1.f : expf(m - m_new);
-    const float w = base ? expf(score - m_new) : 0.f;
-    w_s[tid] = w;
-    __syncthreads();
-    m = m_new;
+    if constexpr (!Q4) {
+      f = scale;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t(&w)[4] = a[2 * b + h];
+          float(&y)[8] = x[b];
+          w[0] = take_bf16(y[4 * h], y[4 * h + 1]);
+          w[2] = take_bf16(y[4 * h + 2], y[4 * h + 3]);
+          if constexpr (kQ == 3) {
+            w[1] = take_bf16(y[4 * h], y[4 * h + 1]);
+            w[3] = take_bf16(y[4 * h + 2], y[4 * h + 3]);
+            a3[2 * b + h][0] = pack_bf16(y[4 * h], y[4 * h + 1]);
+            a3[2 * b + h][1] = pack_bf16(y[4 * h + 2], y[4 * h + 3]);
+          } else {
+            w[1] = w[3] = 0;
+          }
+        }
+    } else {
+      // to [2^13, 2^14) by a power of two: the codes enter as fp16 numbers
+      // n 2^-24 (nibble as it lies) and n 2^-20 (four bits up), the second
+      // against q / 16
+      float mx = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[b][i]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = (int)(__float_as_uint(mx) >> 23) - 126;  // mx < 2^e
+      const int sh = min(14 - e, 120);
+      const float up = __uint_as_float((uint32_t)(127 + max(sh, -120)) << 23);
+      f = scale * __uint_as_float((uint32_t)(127 + min(24 - sh, 127)) << 23);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t(&w)[4] = a[2 * b + h];
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+            const float unit = odd ? 1.f / 16 : 1.f;
+            float y0 = x[b][2 * h + odd] * up * unit, y1 = x[b][4 + 2 * h + odd] * up * unit;
+            w[2 * odd] = take_f16(y0, y1);
+            w[2 * odd + 1] = pack_f16(y0, y1);
+            const float2 u = unpack_f16(w[2 * odd]), r = unpack_f16(w[2 * odd + 1]);
+            sum += ((u.x + r.x) + (u.y + r.y)) * (odd ? 16.f : 1.f);
+          }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        bias[b] = sum * (-8.f / (1 << 24));
+      }
+    }
+#pragma unroll
+    for (int x_ = 0; x_ < NB; ++x_)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[x_][y][i] = 0.f;
+    ref = -3e38f;
+    l = 0.f;
+    lim = kSlack;
+    top = 0.f;
+  }
+
+  // Moves every head's reference to its largest score so far (mx: of this
+  // lane's rows) and, Q4, makes room for V scales up to `s`: weight * scale
+  // stays below 2^15, and the smallest scale that matters well above fp16's
+  // smallest number.
+  __device__ __forceinline__ void raise(float mx, float s) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    float m = fmaxf(ref + (lim - kSlack), mx);
+    if constexpr (Q4) {
+      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
+      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
+      if (s >= top && s > 0.f) {
+        const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s < 2^e
+        top = __uint_as_float((uint32_t)(127 + e) << 23);
+        lim = kSlack + (float)(10 - e);
+      }
+    }
+    const float now = fmaxf(m - (lim - kSlack), -3e38f);
+    const float keep = exp2_approx(ref - now);
+    ref = now;
     l *= keep;
-    acc *= keep;
-    for (int i = 0; i < kSimpleThreads; ++i) {
-      l += w_s[i];
-      if (base_s[i] && tid < D) acc = fmaf(w_s[i], kv_value<D, Q4>(c, base_s[i] + c.half_bytes, row_s[i], tid), acc);
+    const int t = threadIdx.x & 3;
+    const float k0 = __shfl_sync(0xffffffffu, keep, 8 * t), k1 = __shfl_sync(0xffffffffu, keep, 8 * t + 4);
+#pragma unroll
+    for (int x = 0; x < NB; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) acc[x][y][0] *= k0, acc[x][y][1] *= k1, acc[x][y][2] *= k0, acc[x][y][3] *= k1;
+  }
+
+  // One staged tile.  seen: bit i = row (i & 1) + 2t + 8 (i >> 1) is visible; edge: some row is not.
+  __device__ __forceinline__ void tile(const uint8_t* st, int lane, bool edge, uint32_t seen) {
+    using L = Tile<D, Q4>;
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* sv = st + L::kHalf;
+    float s[4];
+    __half2 vs[Q4 ? 4 : 1][Q4 ? NB / 2 : 1];  // V's scales of the lane's four rows
+    if constexpr (!Q4) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const uint4 w = *reinterpret_cast<const uint4*>(st + staged<D, Q4>(8 * b + g, 4 * j + t));
+          mma_bf16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], w.x, w.y);
+          if constexpr (kQ == 3) mma_bf16(c, a3[2 * j][0], 0, a3[2 * j][1], 0, w.x, w.y);
+          mma_bf16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], w.z, w.w);
+          if constexpr (kQ == 3) mma_bf16(c, a3[2 * j + 1][0], 0, a3[2 * j + 1][1], 0, w.z, w.w);
+        }
+        s[2 * b] = (c[0] + c[2]) * f;
+        s[2 * b + 1] = (c[1] + c[3]) * f;
+      }
+    } else {
+      const uint8_t* ks_at = st + kTileRows * L::kRowBytes;
+      const uint8_t* vs_at = sv + kTileRows * L::kRowBytes;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        __half2 ks[2][NB / 2];
+        uint32_t w[NB];  // the row's words: blocks 0, 1 (and 2, 3) of dimension groups 2t, then of 2t + 1
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(st + staged<D, Q4>(8 * b + g, t));
+          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+          *reinterpret_cast<uint4*>(ks) = *reinterpret_cast<const uint4*>(ks_at + 64 * b + 16 * t);
+          *reinterpret_cast<uint4*>(vs[2 * b]) = *reinterpret_cast<const uint4*>(vs_at + 64 * b + 16 * t);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(st + staged<D, Q4>(8 * b + g, t >> 1) + 8 * (t & 1));
+          w[0] = u.x, w[1] = u.y;
+          *reinterpret_cast<uint2*>(ks) = *reinterpret_cast<const uint2*>(ks_at + 32 * b + 8 * t);
+          *reinterpret_cast<uint2*>(vs[2 * b]) = *reinterpret_cast<const uint2*>(vs_at + 32 * b + 8 * t);
+        }
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          float c[4] = {bias[j], bias[j], 0.f, 0.f};
+          const uint32_t x = __byte_perm(w[j >> 1], w[NB / 2 + (j >> 1)], j & 1 ? 0x7632 : 0x5410);
+          mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], x & 0x000f000fu, x & 0x00f000f0u);
+          const uint32_t y = x >> 8;
+          mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], y & 0x000f000fu,
+                  y & 0x00f000f0u);
+          const __half k0 = j & 1 ? __high2half(ks[0][j >> 1]) : __low2half(ks[0][j >> 1]);
+          const __half k1 = j & 1 ? __high2half(ks[1][j >> 1]) : __low2half(ks[1][j >> 1]);
+          s0 = fmaf(__half2float(k0), c[0] + c[2], s0);
+          s1 = fmaf(__half2float(k1), c[1] + c[3], s1);
+        }
+        s[2 * b] = s0 * f;
+        s[2 * b + 1] = s1 * f;
+      }
+    }
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(seen >> i & 1)) {
+          s[i] = -INFINITY;
+          if constexpr (Q4) {
+#pragma unroll
+            for (int j = 0; j < NB / 2; ++j) vs[i][j] = __float2half2_rn(0.f);
+          }
+        }
+    }
+    const float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+    bool past = mx > ref + lim;
+    float big = 0.f;
+    if constexpr (Q4) {
+      __half2 h = vs[0][0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NB / 2; ++j) h = __hmax2(h, vs[i][j]);
+      big = fmaxf(__low2float(h), __high2float(h));
+      past = past || big >= top;
+    }
+    if (__any_sync(0xffffffffu, past)) raise(mx, big);
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = exp2_approx(s[i] - ref);
+    l += (w[0] + w[1]) + (w[2] + w[3]);
+
+    if constexpr (!Q4) {
+      uint32_t pw[kP][2];
+#pragma unroll
+      for (int k = 0; k < kP; ++k) pw[k][0] = take_bf16(w[0], w[1]), pw[k][1] = take_bf16(w[2], w[3]);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = *reinterpret_cast<const uint4*>(sv + staged<D, Q4>((i & 1) + 2 * t + 8 * (i >> 1), 8 * c + g));
+          if (edge && !(seen >> i & 1)) v[i] = make_uint4(0, 0, 0, 0);  // 0 * NaN would be NaN
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = k == 0 ? v[i].x : k == 1 ? v[i].y : k == 2 ? v[i].z : v[i].w;
+          const uint32_t a0 = __byte_perm(r[0], r[1], 0x5410), a1 = __byte_perm(r[0], r[1], 0x7632);
+          const uint32_t a2 = __byte_perm(r[2], r[3], 0x5410), a3_ = __byte_perm(r[2], r[3], 0x7632);
+#pragma unroll
+          for (int i = 0; i < kP; ++i) mma_bf16(acc[2 * c + (k >> 1)][k & 1], a0, a1, a2, a3_, pw[i][0], pw[i][1]);
+        }
+      }
+    } else {
+      uint32_t v[4][NB / 2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = (i & 1) + 2 * t + 8 * (i >> 1);
+        if constexpr (D == 128) {
+          const uint2 u = *reinterpret_cast<const uint2*>(sv + staged<D, Q4>(row, g >> 1) + 8 * (g & 1));
+          v[i][0] = u.x, v[i][1] = u.y;
+        } else {
+          v[i][0] = *reinterpret_cast<const uint32_t*>(sv + staged<D, Q4>(row, g >> 2) + 4 * (g & 3));
+        }
+      }
+      const __half2 m1032 = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f),
+                    m72 = __float2half2_rn(-72.f);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        uint32_t pw[2][2];  // weight * scale: [piece][rows 2t, 2t + 1 of each half]
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const __half h0 = j & 1 ? __high2half(vs[2 * b][j >> 1]) : __low2half(vs[2 * b][j >> 1]);
+          const __half h1 = j & 1 ? __high2half(vs[2 * b + 1][j >> 1]) : __low2half(vs[2 * b + 1][j >> 1]);
+          float y0 = w[2 * b] * __half2float(h0), y1 = w[2 * b + 1] * __half2float(h1);
+          if constexpr (kP == 2) {
+            pw[0][b] = take_f16(y0, y1);
+            pw[1][b] = pack_f16(y0, y1);
+          } else {
+            pw[0][b] = pack_f16(y0, y1);
+          }
+        }
+        uint32_t z0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], j & 1 ? 0x7632 : 0x5410);
+        uint32_t z1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], j & 1 ? 0x7632 : 0x5410);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          // 1024 + n, and 1024 + 16 n, as fp16; then n - 8, exactly
+          auto low = [&](uint32_t z) {
+            const uint32_t u = (z & 0x000f000fu) | 0x64006400u;
+            const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&u), m1032);
+            return *reinterpret_cast<const uint32_t*>(&r);
+          };
+          auto high = [&](uint32_t z) {
+            const uint32_t u = (z & 0x00f000f0u) | 0x64006400u;
+            const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), sixteenth, m72);
+            return *reinterpret_cast<const uint32_t*>(&r);
+          };
+          const uint32_t a0 = low(z0), a1 = high(z0), a2 = low(z1), a3_ = high(z1);
+#pragma unroll
+          for (int i = 0; i < kP; ++i) mma_f16(acc[j][y], a0, a1, a2, a3_, pw[i][0], pw[i][1]);
+          z0 >>= 8;
+          z1 >>= 8;
+        }
+      }
     }
   }
-  if (tid < D) {
-    const float o = l > 0.f ? acc / l : (l == 0.f ? 0.f : l);
-    T* out = static_cast<T*>(p.o) + r * p.o_stride + (int64_t)h * D;
-    if constexpr (sizeof(T) == 4) out[tid] = o;
-    else out[tid] = f32_to_bf16_bits(o);
+};
+
+// Fills a stage with the tile whose K rows begin at `src` (Q4: codes; the
+// scales of its rows at `scales`), V a fixed distance behind.
+template <int D, bool Q4>
+__device__ __forceinline__ void stage_tile(uint8_t* st, const uint8_t* src, const uint8_t* scales, int64_t half_bytes,
+                                           int lane) {
+  using L = Tile<D, Q4>;
+  constexpr int PPR = L::kRowBytes / 16, N = kTileRows * PPR / 32;
+  const uint32_t dst = smem_u32(st);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int at = i * 32 + lane, to = staged<D, Q4>(at / PPR, at % PPR);
+    cp_async16(dst + to, src + 16 * at);
+    cp_async16(dst + L::kHalf + to, src + half_bytes + 16 * at);
+  }
+  if constexpr (Q4) {
+    constexpr int NS = 2 * L::NB;  // 16-byte pieces of a tile's scales
+    if (lane < 2 * NS) {
+      const int which = lane / NS, at = 16 * (lane % NS);
+      cp_async16(dst + which * L::kHalf + kTileRows * L::kRowBytes + at, scales + which * half_bytes + at);
+    }
   }
 }
 
+template <class T, int N>
+__device__ __forceinline__ void store_out(T* p, const float (&x)[N]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<uint2*>(p + i) = make_uint2(pack_bf16(x[i], x[i + 1]), pack_bf16(x[i + 2], x[i + 3]));
+  }
+}
+
+// The sum over no weight is zero; NaN stays.
+__device__ __forceinline__ float over(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 template <int D, bool Q4, class T>
-cudaError_t launch_simple(const KvAttnParams& p, cudaStream_t s) {
+__global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(const __grid_constant__ KvAttnParams p) {
+  using L = Tile<D, Q4>;
+  using W = WarpState<D, Q4, T>;
+  constexpr int ST = L::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t chunk_tiles[kMaxChunks];
+  __shared__ float2 warp_ref[kWarps][kHeadBlock];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const KvView& c = p.c;
+  pdl_trigger();
+
+  // ---- this CTA's share of the line of tiles
+  const int chunks = (p.n + kChunkRows - 1) / kChunkRows;
+  const int units = c.nkv * p.head_blocks;
+  bool bad = false, empty = false;
+  int mine[4];  // tiles of queries 32 i + lane of a chunk
+  auto count = [&](int chunk) {
+    int64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = chunk * kChunkRows + 32 * i + lane;
+      Rows v{-1, 0, 0, 0, 0, 0, 0};
+      if (r < p.n) v = query_rows(p, r, &bad);
+      mine[i] = v.tiles;
+      sum += v.tiles;
+      empty |= v.seq >= 0 && v.tiles == 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+  };
+  int64_t tiles = 0;
+  if (chunks == 1) {
+    tiles = count(0);  // every warp for itself
+  } else {
+    for (int k = warp; k < chunks; k += kWarps) {
+      const int64_t sum = count(k);
+      if (lane == 0) chunk_tiles[k] = sum;
+    }
+    __syncthreads();
+    for (int k = 0; k < chunks; ++k) tiles += chunk_tiles[k];
+  }
+  if (bad && blockIdx.x == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
+  if (__syncthreads_or(empty)) {  // queries that see no row
+    for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
+      const Rows v = query_rows(p, r, &bad);
+      if (v.seq < 0 || v.tiles) continue;
+      T* out = static_cast<T*>(p.o) + r * p.o_stride;
+      for (int64_t e = tid; e < (int64_t)p.nq * D; e += kThreadsA) out[e] = 0;
+    }
+  }
+  const int64_t total = tiles * units;
+  const int64_t parts = min((int64_t)gridDim.x, (total + kWarps - 1) / kWarps);
+  int4 cut = make_int4(0, 0, 0, 0);
+  if (blockIdx.x < parts) {
+    int64_t pos = total * blockIdx.x / parts;
+    const int64_t end = total * (blockIdx.x + 1) / parts;
+    // the query that holds tile `pos`
+    int64_t before = 0;  // tiles of the queries before r
+    int r = 0;
+    {
+      const int64_t want = pos / units;
+      int k = 0;
+      if (chunks > 1) {
+        while (before + chunk_tiles[k] <= want) before += chunk_tiles[k++];
+        count(k);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int64_t incl = mine[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + incl > want);
+        if (past) {
+          const int at = __ffs(past) - 1;
+          before += __shfl_sync(0xffffffffu, incl - mine[i], at);
+          r = k * kChunkRows + 32 * i + at;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    Rows v = query_rows(p, r, &bad);
+
+    while (pos < end) {
+      const int64_t rel = pos - before * units;
+      // (not so only if lengths change while the call runs: then leave, in bounds)
+      if (rel < 0 || rel >= (int64_t)v.tiles * units) break;
+      const int u = (int)(rel / v.tiles), t0 = (int)(rel - (int64_t)u * v.tiles);
+      const int t1 = (int)min((int64_t)v.tiles, t0 + (end - pos));
+      const int head = u / p.head_blocks, h0 = (u % p.head_blocks) * kHeadBlock;
+      const int n_heads = min(kHeadBlock, p.group - h0);
+      const int64_t col = ((int64_t)head * p.group + h0) * D;
+
+      W st;
+      st.load_q(static_cast<const T*>(p.q) + r * p.q_stride + col + (int64_t)min(g, n_heads - 1) * D, g < n_heads, t,
+                p.scale);
+
+      // ---- the warp's tiles t0 + warp, + kWarps, ...
+      const int nt = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
+      uint8_t* ring = smem + warp * ST * L::kBytes;
+      const int32_t* table = c.table + (int64_t)v.seq * c.max_pages;
+      const uint8_t* cur_base = nullptr;
+      const uint8_t* nxt_base = nullptr;
+      int cur_row = -1, nxt_row = -1;  // row within the page; -1: no page
+      auto fetch = [&](int i0) {       // where tiles i0 .. i0 + 31 lie, one per lane
+        const int i = i0 + lane;
+        nxt_row = -1;
+        if (i < nt) {
+          const int row = tile_row(v, t0 + warp + i * kWarps), page = table[row / c.page_rows];
+          if (page >= 0 && page < c.n_pages) {
+            nxt_base = c.pool + page * c.page_bytes + head * c.head_bytes;
+            nxt_row = row % c.page_rows;
+          } else {
+            atomicOr(c.status, DEC_KV_BAD_INDEX);
+          }
+        }
+      };
+      uint32_t staged_ok = 0;  // bit per stage
+      auto issue = [&](int i) {
+        if ((i & 31) == 0) {
+          cur_base = nxt_base;
+          cur_row = nxt_row;
+          fetch(i + 32);
+        }
+        if (i < nt) {
+          const uint8_t* base = reinterpret_cast<const uint8_t*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cur_base), i & 31));
+          const int row = __shfl_sync(0xffffffffu, cur_row, i & 31);
+          const int slot = i % ST;
+          if (row >= 0) {
+            stage_tile<D, Q4>(ring + slot * L::kBytes, base + (int64_t)row * L::kRowBytes,
+                              base + (int64_t)c.page_rows * L::kRowBytes + row * (2 * L::NB), c.half_bytes, lane);
+            staged_ok |= 1u << slot;
+          } else {
+            staged_ok &= ~(1u << slot);
+          }
+        }
+        cp_async_commit();
+      };
+      fetch(0);
+#pragma unroll 1
+      for (int i = 0; i < ST; ++i) issue(i);
+#pragma unroll 1
+      for (int i = 0; i < nt; ++i) {
+        cp_async_wait<ST - 1>();
+        __syncwarp();
+        const int slot = i % ST;
+        if (staged_ok >> slot & 1) {
+          const int row = tile_row(v, t0 + warp + i * kWarps);
+          const bool edge = !((row >= v.lo && row + kTileRows <= v.len) || row + kTileRows <= v.first);
+          uint32_t seen = 0xf;
+          if (edge) {
+            seen = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int at = row + (k & 1) + 2 * t + 8 * (k >> 1);
+              if (at < v.first || (at >= v.lo && at < v.len)) seen |= 1u << k;
+            }
+          }
+          st.tile(ring + slot * L::kBytes, lane, edge, seen);
+        }
+        __syncwarp();
+        issue(i + ST);
+      }
+      cp_async_wait<0>();
+
+      // ---- the warps' sums, brought to one reference
+      float lsum = st.l;
+      lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+      lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+      if (t == 0) warp_ref[warp][g] = make_float2(st.ref, lsum);
+      __syncthreads();  // every warp is through with its ring
+      float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int h = 2 * t + hh;
+        float m = warp_ref[0][h].x;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, warp_ref[w][h].x);
+        const float k = exp2_approx(warp_ref[warp][h].x - m);
+        float* row = sums + (warp * kHeadBlock + h) * L::kMergeRow;
+#pragma unroll
+        for (int x = 0; x < W::NB; ++x)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            *reinterpret_cast<float2*>(row + W::out_dim(x, y, g)) =
+                make_float2(st.acc[x][y][hh] * k, st.acc[x][y][2 + hh] * k);
+      }
+      __syncthreads();
+      {
+        constexpr int N = D / 16;
+        const int h = tid / 16, e = (tid % 16) * N;
+        float m = warp_ref[0][h].x, ls = 0.f, x[N];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, warp_ref[w][h].x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          ls += warp_ref[w][h].y * exp2_approx(warp_ref[w][h].x - m);
+#pragma unroll
+          for (int i = 0; i < N; i += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(sums + (w * kHeadBlock + h) * L::kMergeRow + e + i);
+            x[i] += y.x, x[i + 1] += y.y, x[i + 2] += y.z, x[i + 3] += y.w;
+          }
+        }
+        if (t0 == 0 && t1 == v.tiles) {
+          if (h < n_heads) {
+            const float k = over(ls);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] *= k;
+            store_out(static_cast<T*>(p.o) + r * p.o_stride + col + h * D + e, x);
+          }
+        } else {  // a part: slot 1 where the unit begins here, slot 0 where it began before
+          const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0);
+          store_out(p.rec + (slot * kHeadBlock + h) * D + e, x);
+          if (e == 0) p.ref[slot * kHeadBlock + h] = make_float2(m, ls);
+          if (t0 == 0) {
+            const int64_t last = (before * units + (int64_t)(u + 1) * v.tiles) - 1;
+            cut = make_int4(r, u, (int)(((last + 1) * parts - 1) / total - blockIdx.x), 0);
+          }
+        }
+      }
+      __syncthreads();
+      pos += t1 - t0;
+      if (pos < end && t1 == v.tiles && u == units - 1 && r + 1 < p.n) {
+        before += v.tiles;
+        do v = query_rows(p, ++r, &bad);
+        while (v.tiles == 0 && r + 1 < p.n);
+      }
+    }
+  }
+  if (tid == 0) p.cut[blockIdx.x] = cut;
+}
+
+// Joins the parts of the unit that begins in CTA blockIdx.x of kv_attn, in
+// their order; a warp per query head.
+template <int D, class T>
+__global__ void __launch_bounds__(kHeadBlock * 32) kv_attn_join(const __grid_constant__ KvAttnParams p) {
+  pdl_wait();
+  const int4 cut = p.cut[blockIdx.x];
+  const int h = threadIdx.x >> 5, lane = threadIdx.x & 31, n = cut.z + 1;
+  if (cut.z == 0) return;
+  const int head = cut.y / p.head_blocks, h0 = (cut.y % p.head_blocks) * kHeadBlock;
+  if (h0 + h >= p.group) return;
+  auto slot = [&](int i) { return (i == 0 ? 2 * blockIdx.x + 1 : 2 * ((int64_t)blockIdx.x + i)) * kHeadBlock + h; };
+  float m = -3e38f;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.ref[slot(i)].x);
+  m = warp_max(m);
+  constexpr int N = D / 32;
+  float x[N], l = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float w = 0.f;
+    if (i0 + lane < n) {
+      const float2 rl = p.ref[slot(i0 + lane)];
+      w = exp2_approx(rl.x - m);
+      l += w * rl.y;
+    }
+    const int here = min(32, n - i0);
+#pragma unroll 4
+    for (int i = 0; i < here; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* src = p.rec + slot(i0 + i) * D + lane * N;
+      if constexpr (N == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        x[0] = fmaf(wi, y.x, x[0]), x[1] = fmaf(wi, y.y, x[1]), x[2] = fmaf(wi, y.z, x[2]), x[3] = fmaf(wi, y.w, x[3]);
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(src);
+        x[0] = fmaf(wi, y.x, x[0]), x[1] = fmaf(wi, y.y, x[1]);
+      }
+    }
+  }
+  l = warp_sum(l);
+  const float k = over(l);
+  T* out = static_cast<T*>(p.o) + cut.x * p.o_stride + ((int64_t)head * p.group + h0 + h) * D + lane * N;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (sizeof(T) == 4) out[i] = x[i] * k;
+    else out[i] = f32_to_bf16_bits(x[i] * k);
+  }
+}
+
+constexpr int kMaxDevices = 64;
+
+// SMs of the current device (they do not change: looked up once).
+int device_sms(int* dev, int* sms) {
+  static std::atomic<int> known[kMaxDevices];
+  cudaError_t e = cudaGetDevice(dev);
+  if (e == cudaSuccess && (*dev < 0 || *dev >= kMaxDevices)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess && (*sms = known[*dev].load(std::memory_order_relaxed)) == 0) {
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e == cudaSuccess) known[*dev].store(*sms, std::memory_order_relaxed);
+  }
+  if (e != cudaSuccess) return fail_no_handle(DEC_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+  return DEC_OK;
+}
+
+// CTAs of a launch: one round of what fits on the GPU.
+int attn_ctas(const dec_kv_cache& c, int sms) {
+  const bool q4 = c.format == DEC_KV_Q4B32;
+  if (c.head_dim == 128) return sms * (q4 ? Tile<128, true>::kCtasPerSm : Tile<128, false>::kCtasPerSm);
+  return sms * (q4 ? Tile<64, true>::kCtasPerSm : Tile<64, false>::kCtasPerSm);
+}
+
+struct Workspace {
+  size_t rec, ref, cut, bytes;
+};
+Workspace workspace_of(int ctas, int head_dim) {
+  Workspace w;
+  w.rec = 0;
+  w.ref = w.rec + (size_t)2 * ctas * kHeadBlock * head_dim * sizeof(float);
+  w.cut = w.ref + (size_t)2 * ctas * kHeadBlock * sizeof(float2);
+  w.bytes = w.cut + (size_t)ctas * sizeof(int4);
+  return w;
+}
+
+template <int D, bool Q4, class T>
+cudaError_t launch_attn_kv(const KvAttnParams& p, int dev, int ctas, cudaStream_t s) {
+  static std::atomic<bool> ready[kMaxDevices];  // the kernel's shared-memory limit has been set on the device
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(kv_attn<D, Q4, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Tile<D, Q4>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.nq, p.n);
-  cfg.blockDim = dim3(kSimpleThreads);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreadsA);
+  cfg.dynamicSmemBytes = Tile<D, Q4>::kSmem;
   cfg.stream = s;
-  return cudaLaunchKernelEx(&cfg, kv_attn_simple<D, Q4, T>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn<D, Q4, T>, p);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute pdl = {};
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kHeadBlock * 32);
+  cfg.dynamicSmemBytes = 0;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T>, p);
 }
 
 int check_attention(const dec_kv_cache* c, int n, int n_q_heads) {
-  if (n < 0 || n > 65535) return fail_no_handle(DEC_ERR_ARG, "%d queries (0..65535)", n);
+  if (n < 0 || n > kMaxQueries) return fail_no_handle(DEC_ERR_ARG, "%d queries (0..%d)", n, kMaxQueries);
   if (n_q_heads < 1 || n_q_heads % c->n_kv_heads || n_q_heads > 65536)
     return fail_no_handle(DEC_ERR_SHAPE, "%d query heads: a multiple of the %d KV heads", n_q_heads, c->n_kv_heads);
+  if ((int64_t)n * n_q_heads > 1 << 24)
+    return fail_no_handle(DEC_ERR_SHAPE, "%d queries of %d heads (at most 2^24 in all)", n, n_q_heads);
   return DEC_OK;
 }
 
@@ -136,7 +876,9 @@ extern "C" int dec_kv_attention_workspace(const dec_kv_cache* c, int n, int n_q_
   if (int rc = kv_check(c, false)) return rc;
   if (int rc = check_attention(c, n, n_q_heads)) return rc;
   if (!bytes) return fail_no_handle(DEC_ERR_ARG, "bytes is NULL");
-  *bytes = 16;
+  int dev = 0, sms = 0;
+  if (int rc = device_sms(&dev, &sms)) return rc;
+  *bytes = workspace_of(attn_ctas(*c, sms), c->head_dim).bytes;
   return DEC_OK;
 }
 
@@ -161,10 +903,12 @@ extern "C" int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q,
   if (rows_overlap(reinterpret_cast<uintptr_t>(q), q_stride * size, reinterpret_cast<uintptr_t>(o), o_stride * size,
                    width * size, n))
     return fail_no_handle(DEC_ERR_ARG, "o overlaps q");
-  size_t need = 0;
-  if (int rc = dec_kv_attention_workspace(c, n, n_q_heads, &need)) return rc;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) || workspace_bytes < need)
-    return fail_no_handle(DEC_ERR_ARG, "the workspace must be 16-byte aligned and of %zu bytes", need);
+  int dev = 0, sms = 0;
+  if (int rc = device_sms(&dev, &sms)) return rc;
+  const int ctas = attn_ctas(*c, sms);
+  const Workspace ws = workspace_of(ctas, c->head_dim);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) || workspace_bytes < ws.bytes)
+    return fail_no_handle(DEC_ERR_ARG, "the workspace must be 16-byte aligned and of %zu bytes", ws.bytes);
 
   KvAttnParams p;
   p.c = kv_view(*c, layer);
@@ -177,11 +921,18 @@ extern "C" int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q,
   p.nq = n_q_heads;
   p.window = window;
   p.sinks = sinks;
-  p.scale = scale != 0.f ? scale : (float)(1.0 / std::sqrt((double)c->head_dim));
+  p.group = n_q_heads / c->n_kv_heads;
+  p.head_blocks = (p.group + kHeadBlock - 1) / kHeadBlock;
+  p.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)c->head_dim)) * 1.4426950408889634);
+  p.rec = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.rec);
+  p.ref = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ws.ref);
+  p.cut = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + ws.cut);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool q4 = c->format == DEC_KV_Q4B32, f32 = type == DEC_IO_F32;
-#define TLD_ATTN(D, Q) e = f32 ? launch_simple<D, Q, float>(p, s) : launch_simple<D, Q, uint16_t>(p, s)
+#define TLD_ATTN(D, Q)                                       \
+  e = f32 ? launch_attn_kv<D, Q, float>(p, dev, ctas, s)     \
+          : launch_attn_kv<D, Q, uint16_t>(p, dev, ctas, s)
   if (c->head_dim == 128) {
     if (q4) TLD_ATTN(128, true);
     else TLD_ATTN(128, false);
