@@ -2,7 +2,9 @@
 // cache, bf16 or in 4-bit blocks, with a sliding window and first rows that
 // stay visible.
 #include <atomic>
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv.h"
@@ -34,12 +36,14 @@ struct Tile {
   static constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;               // codes or values
   static constexpr int kHalf = kTileRows * (kRowBytes + (Q4 ? 2 * NB : 0));  // K or V, scales after the rows
   static constexpr int kBytes = 2 * kHalf;
-  static constexpr int kStages = Q4 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 4);
-  static constexpr int kRing = kWarps * kStages * kBytes;
+  static constexpr int kStep = Q4 ? 2 : 1;                           // tiles a warp takes at a time
+  static constexpr int kStages = Q4 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 4);  // steps in its ring
+  static constexpr int kSlot = kStep * kBytes;
+  static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kMergeRow = D + 8;                            // floats; heads apart by 8 banks
   static constexpr int kMerge = kWarps * kHeadBlock * kMergeRow * 4; // the warps' sums, once the ring is drained
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kCtasPerSm = Q4 ? 4 : 3;
+  static constexpr int kCtasPerSm = 3;
 };
 
 struct KvAttnParams {
@@ -53,7 +57,9 @@ struct KvAttnParams {
   float scale;             // times log2(e)
   float* rec;              // [2 * CTAs][8][D]: sums of units cut between CTAs
   float2* ref;             // [2 * CTAs][8]: reference and sum of the weights
-  int4* cut;               // [CTAs]: the unit that begins in a CTA and ends in a later one
+  int4* cut;               // [CTAs]: query, unit, CTA where it begins, CTAs that it goes on for
+  int ctas;
+  int cut_by_unit;         // cut is indexed by unit (there are no more of them than CTAs), not by CTA
 };
 
 // A query's visible rows: [0, first) and [lo, len).
@@ -165,299 +171,408 @@ __device__ __forceinline__ int staged(int row, int piece) {
 // product, O^T[dim][head] = V^T P^T: no value changes lanes.  The order of the
 // dimensions within a product and of O's rows is free, and chosen so that a
 // lane's operands are whole words of the staged rows.
-template <int D, bool Q4, class T>
-struct WarpState {
+//
+// The softmax runs on a reference that moves only when a score passes it by
+// kSlack: the weights are 2^(score - ref), their sum l and the outputs follow
+// it, and o / l does not depend on it.
+template <int D>
+struct WarpSums {
   static constexpr int NB = D / 32;
-  // pieces of q: bf16 q is exact in one; fp32 q in three of bf16 (24 bits) or,
-  // scaled to fp16's range, in two of fp16 (22 bits)
-  static constexpr int kQ = Q4 ? 2 : (sizeof(T) == 4 ? 3 : 1);
-  // pieces of the weights: 22 bits (two of fp16), or 24 (three of bf16) for
-  // fp32 results and 16 for bf16 ones
-  static constexpr int kP = Q4 ? 2 : (sizeof(T) == 4 ? 3 : 2);
-  uint32_t a[2 * NB][4];                    // q: pieces one and two
-  uint32_t a3[kQ == 3 ? 2 * NB : 1][2];     // piece three
-  float bias[Q4 ? NB : 1];                  // -8 sum of q over a block (codes are stored plus 8)
-  float f;                                  // score = f * product, in log2 units
-  float acc[NB][2][4];                      // O^T; see out_dim
-  float ref, l;                             // head g: reference of the weights 2^(score - ref), and their sum
-  float lim, top;                           // a score passes at ref + lim; scales of V seen are below top (Q4)
+  float acc[NB][2][4];  // O^T: [0..1] a dimension (out_dim) of heads 2t, 2t + 1; [2..3] the next dimension
+  float ref, l;         // head g's
 
-  // acc[x][y][0..1]: dimension out_dim(x, y, g) of heads 2t, 2t + 1; [2..3]: the next dimension.
-  __device__ static int out_dim(int x, int y, int g) {
-    return Q4 ? 32 * x + 4 * g + 2 * y : 64 * (x >> 1) + 8 * g + 4 * (x & 1) + 2 * y;
-  }
-
-  __device__ __forceinline__ void load_q(const T* q, bool valid, int t, float scale) {
-    float x[NB][8];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if (!valid) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
-      } else if constexpr (sizeof(T) == 4) {
-        const float4* p = reinterpret_cast<const float4*>(q + 32 * b + 8 * t);
-        const float4 u = p[0], w = p[1];
-        x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w;
-        x[b][4] = w.x, x[b][5] = w.y, x[b][6] = w.z, x[b][7] = w.w;
-      } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(q + 32 * b + 8 * t);
-        x[b][0] = bf16lo(u.x), x[b][1] = bf16hi(u.x), x[b][2] = bf16lo(u.y), x[b][3] = bf16hi(u.y);
-        x[b][4] = bf16lo(u.z), x[b][5] = bf16hi(u.z), x[b][6] = bf16lo(u.w), x[b][7] = bf16hi(u.w);
-      }
-    }
-    if constexpr (!Q4) {
-      f = scale;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t(&w)[4] = a[2 * b + h];
-          float(&y)[8] = x[b];
-          w[0] = take_bf16(y[4 * h], y[4 * h + 1]);
-          w[2] = take_bf16(y[4 * h + 2], y[4 * h + 3]);
-          if constexpr (kQ == 3) {
-            w[1] = take_bf16(y[4 * h], y[4 * h + 1]);
-            w[3] = take_bf16(y[4 * h + 2], y[4 * h + 3]);
-            a3[2 * b + h][0] = pack_bf16(y[4 * h], y[4 * h + 1]);
-            a3[2 * b + h][1] = pack_bf16(y[4 * h + 2], y[4 * h + 3]);
-          } else {
-            w[1] = w[3] = 0;
-          }
-        }
-    } else {
-      // to [2^13, 2^14) by a power of two: the codes enter as fp16 numbers
-      // n 2^-24 (nibble as it lies) and n 2^-20 (four bits up), the second
-      // against q / 16
-      float mx = 0.f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[b][i]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = (int)(__float_as_uint(mx) >> 23) - 126;  // mx < 2^e
-      const int sh = min(14 - e, 120);
-      const float up = __uint_as_float((uint32_t)(127 + max(sh, -120)) << 23);
-      f = scale * __uint_as_float((uint32_t)(127 + min(24 - sh, 127)) << 23);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float sum = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t(&w)[4] = a[2 * b + h];
-#pragma unroll
-          for (int odd = 0; odd < 2; ++odd) {
-            const float unit = odd ? 1.f / 16 : 1.f;
-            float y0 = x[b][2 * h + odd] * up * unit, y1 = x[b][4 + 2 * h + odd] * up * unit;
-            w[2 * odd] = take_f16(y0, y1);
-            w[2 * odd + 1] = pack_f16(y0, y1);
-            const float2 u = unpack_f16(w[2 * odd]), r = unpack_f16(w[2 * odd + 1]);
-            sum += ((u.x + r.x) + (u.y + r.y)) * (odd ? 16.f : 1.f);
-          }
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        bias[b] = sum * (-8.f / (1 << 24));
-      }
-    }
-#pragma unroll
-    for (int x_ = 0; x_ < NB; ++x_)
+    for (int x = 0; x < NB; ++x)
 #pragma unroll
       for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[x_][y][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[x][y][i] = 0.f;
     ref = -3e38f;
     l = 0.f;
-    lim = kSlack;
-    top = 0.f;
   }
 
-  // Moves every head's reference to its largest score so far (mx: of this
-  // lane's rows) and, Q4, makes room for V scales up to `s`: weight * scale
-  // stays below 2^15, and the smallest scale that matters well above fp16's
-  // smallest number.
-  __device__ __forceinline__ void raise(float mx, float s) {
+  // Moves every head's reference so that its largest score (mx: the largest of
+  // this lane's new ones) has the weight 2^lift; scales the outputs by `unit` besides.
+  __device__ __forceinline__ void raise(float mx, float lift, float unit) {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    float m = fmaxf(ref + (lim - kSlack), mx);
-    if constexpr (Q4) {
-      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
-      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
-      if (s >= top && s > 0.f) {
-        const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s < 2^e
-        top = __uint_as_float((uint32_t)(127 + e) << 23);
-        lim = kSlack + (float)(10 - e);
-      }
-    }
-    const float now = fmaxf(m - (lim - kSlack), -3e38f);
+    const float now = fmaxf(ref, mx - lift);
     const float keep = exp2_approx(ref - now);
     ref = now;
     l *= keep;
     const int t = threadIdx.x & 3;
-    const float k0 = __shfl_sync(0xffffffffu, keep, 8 * t), k1 = __shfl_sync(0xffffffffu, keep, 8 * t + 4);
+    const float k0 = __shfl_sync(0xffffffffu, keep, 8 * t) * unit;
+    const float k1 = __shfl_sync(0xffffffffu, keep, 8 * t + 4) * unit;
 #pragma unroll
     for (int x = 0; x < NB; ++x)
 #pragma unroll
       for (int y = 0; y < 2; ++y) acc[x][y][0] *= k0, acc[x][y][1] *= k1, acc[x][y][2] *= k0, acc[x][y][3] *= k1;
   }
+};
+
+// Eight dimensions 32 b + 8 t .. of a query as fp32.
+template <int NB, class T>
+__device__ __forceinline__ void load_query(const T* q, bool valid, int t, float (&x)[NB][8]) {
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (!valid) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
+    } else if constexpr (sizeof(T) == 4) {
+      const float4* p = reinterpret_cast<const float4*>(q + 32 * b + 8 * t);
+      const float4 u = p[0], w = p[1];
+      x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w;
+      x[b][4] = w.x, x[b][5] = w.y, x[b][6] = w.z, x[b][7] = w.w;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(q + 32 * b + 8 * t);
+      x[b][0] = bf16lo(u.x), x[b][1] = bf16hi(u.x), x[b][2] = bf16lo(u.y), x[b][3] = bf16hi(u.y);
+      x[b][4] = bf16lo(u.z), x[b][5] = bf16hi(u.z), x[b][6] = bf16lo(u.w), x[b][7] = bf16hi(u.w);
+    }
+  }
+}
+
+// bf16 pages.  fp32 calls take q and the weights in three bf16 pieces (24
+// bits); bf16 calls take q as it is and the weights in two (16 bits, against
+// the 8 of their results).
+template <int D, class T>
+struct WarpBf16 : WarpSums<D> {
+  using Sums = WarpSums<D>;
+  static constexpr int NB = Sums::NB, kPieces = sizeof(T) == 4 ? 3 : 2;
+  static constexpr bool kWhole = sizeof(T) == 2;  // q is one piece
+  uint32_t a[2 * NB][4];                // q: the first two pieces
+  uint32_t a3[kWhole ? 1 : 2 * NB][2];  // the third
+  float f;                              // score = f * product, in log2 units
+
+  __device__ static int out_dim(int x, int y, int g) { return 64 * (x >> 1) + 8 * g + 4 * (x & 1) + 2 * y; }
+  __device__ __forceinline__ float out_unit() const { return 1.f; }
+
+  __device__ __forceinline__ void load_q(const T* q, bool valid, int t, float scale) {
+    float x[NB][8];
+    load_query<NB>(q, valid, t, x);
+    f = scale;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t(&w)[4] = a[2 * b + h];
+        float(&y)[8] = x[b];
+        w[0] = take_bf16(y[4 * h], y[4 * h + 1]);
+        w[2] = take_bf16(y[4 * h + 2], y[4 * h + 3]);
+        if constexpr (kWhole) {
+          w[1] = w[3] = 0;
+        } else {
+          w[1] = take_bf16(y[4 * h], y[4 * h + 1]);
+          w[3] = take_bf16(y[4 * h + 2], y[4 * h + 3]);
+          a3[2 * b + h][0] = pack_bf16(y[4 * h], y[4 * h + 1]);
+          a3[2 * b + h][1] = pack_bf16(y[4 * h + 2], y[4 * h + 3]);
+        }
+      }
+    this->clear();
+  }
 
   // One staged tile.  seen: bit i = row (i & 1) + 2t + 8 (i >> 1) is visible; edge: some row is not.
-  __device__ __forceinline__ void tile(const uint8_t* st, int lane, bool edge, uint32_t seen) {
-    using L = Tile<D, Q4>;
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t seen) {
+    using L = Tile<D, false>;
     const int g = lane >> 2, t = lane & 3;
     const uint8_t* sv = st + L::kHalf;
     float s[4];
-    __half2 vs[Q4 ? 4 : 1][Q4 ? NB / 2 : 1];  // V's scales of the lane's four rows
-    if constexpr (!Q4) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int b = 0; b < 2; ++b) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const uint4 w = *reinterpret_cast<const uint4*>(st + staged<D, Q4>(8 * b + g, 4 * j + t));
-          mma_bf16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], w.x, w.y);
-          if constexpr (kQ == 3) mma_bf16(c, a3[2 * j][0], 0, a3[2 * j][1], 0, w.x, w.y);
-          mma_bf16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], w.z, w.w);
-          if constexpr (kQ == 3) mma_bf16(c, a3[2 * j + 1][0], 0, a3[2 * j + 1][1], 0, w.z, w.w);
-        }
-        s[2 * b] = (c[0] + c[2]) * f;
-        s[2 * b + 1] = (c[1] + c[3]) * f;
+      for (int j = 0; j < NB; ++j) {
+        const uint4 w = *reinterpret_cast<const uint4*>(st + staged<D, false>(8 * b + g, 4 * j + t));
+        mma_bf16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], w.x, w.y);
+        if constexpr (!kWhole) mma_bf16(c, a3[2 * j][0], 0, a3[2 * j][1], 0, w.x, w.y);
+        mma_bf16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], w.z, w.w);
+        if constexpr (!kWhole) mma_bf16(c, a3[2 * j + 1][0], 0, a3[2 * j + 1][1], 0, w.z, w.w);
       }
-    } else {
-      const uint8_t* ks_at = st + kTileRows * L::kRowBytes;
-      const uint8_t* vs_at = sv + kTileRows * L::kRowBytes;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        __half2 ks[2][NB / 2];
-        uint32_t w[NB];  // the row's words: blocks 0, 1 (and 2, 3) of dimension groups 2t, then of 2t + 1
-        if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(st + staged<D, Q4>(8 * b + g, t));
-          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-          *reinterpret_cast<uint4*>(ks) = *reinterpret_cast<const uint4*>(ks_at + 64 * b + 16 * t);
-          *reinterpret_cast<uint4*>(vs[2 * b]) = *reinterpret_cast<const uint4*>(vs_at + 64 * b + 16 * t);
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(st + staged<D, Q4>(8 * b + g, t >> 1) + 8 * (t & 1));
-          w[0] = u.x, w[1] = u.y;
-          *reinterpret_cast<uint2*>(ks) = *reinterpret_cast<const uint2*>(ks_at + 32 * b + 8 * t);
-          *reinterpret_cast<uint2*>(vs[2 * b]) = *reinterpret_cast<const uint2*>(vs_at + 32 * b + 8 * t);
-        }
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          float c[4] = {bias[j], bias[j], 0.f, 0.f};
-          const uint32_t x = __byte_perm(w[j >> 1], w[NB / 2 + (j >> 1)], j & 1 ? 0x7632 : 0x5410);
-          mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], x & 0x000f000fu, x & 0x00f000f0u);
-          const uint32_t y = x >> 8;
-          mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], y & 0x000f000fu,
-                  y & 0x00f000f0u);
-          const __half k0 = j & 1 ? __high2half(ks[0][j >> 1]) : __low2half(ks[0][j >> 1]);
-          const __half k1 = j & 1 ? __high2half(ks[1][j >> 1]) : __low2half(ks[1][j >> 1]);
-          s0 = fmaf(__half2float(k0), c[0] + c[2], s0);
-          s1 = fmaf(__half2float(k1), c[1] + c[3], s1);
-        }
-        s[2 * b] = s0 * f;
-        s[2 * b + 1] = s1 * f;
-      }
+      s[2 * b] = (kWhole ? c[0] : c[0] + c[2]) * f;
+      s[2 * b + 1] = (kWhole ? c[1] : c[1] + c[3]) * f;
     }
     if (edge) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (!(seen >> i & 1)) {
-          s[i] = -INFINITY;
-          if constexpr (Q4) {
-#pragma unroll
-            for (int j = 0; j < NB / 2; ++j) vs[i][j] = __float2half2_rn(0.f);
-          }
-        }
+        if (!(seen >> i & 1)) s[i] = -INFINITY;
     }
     const float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-    bool past = mx > ref + lim;
-    float big = 0.f;
-    if constexpr (Q4) {
-      __half2 h = vs[0][0];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < NB / 2; ++j) h = __hmax2(h, vs[i][j]);
-      big = fmaxf(__low2float(h), __high2float(h));
-      past = past || big >= top;
-    }
-    if (__any_sync(0xffffffffu, past)) raise(mx, big);
+    if (__any_sync(0xffffffffu, mx > this->ref + kSlack)) this->raise(mx, 0.f, 1.f);
     float w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = exp2_approx(s[i] - ref);
-    l += (w[0] + w[1]) + (w[2] + w[3]);
+    for (int i = 0; i < 4; ++i) w[i] = exp2_approx(s[i] - this->ref);
+    this->l += (w[0] + w[1]) + (w[2] + w[3]);
+    uint32_t pw[kPieces][2];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) pw[k][0] = take_bf16(w[0], w[1]), pw[k][1] = take_bf16(w[2], w[3]);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = *reinterpret_cast<const uint4*>(sv + staged<D, false>((i & 1) + 2 * t + 8 * (i >> 1), 8 * c + g));
+        if (edge && !(seen >> i & 1)) v[i] = make_uint4(0, 0, 0, 0);  // 0 * NaN would be NaN
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = k == 0 ? v[i].x : k == 1 ? v[i].y : k == 2 ? v[i].z : v[i].w;
+        const uint32_t a0 = __byte_perm(r[0], r[1], 0x5410), a1 = __byte_perm(r[0], r[1], 0x7632);
+        const uint32_t a2 = __byte_perm(r[2], r[3], 0x5410), a3_ = __byte_perm(r[2], r[3], 0x7632);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          mma_bf16(this->acc[2 * c + (k >> 1)][k & 1], a0, a1, a2, a3_, pw[i][0], pw[i][1]);
+      }
+    }
+  }
+};
 
-    if constexpr (!Q4) {
-      uint32_t pw[kP][2];
+// 4-bit pages.  What bounds it is the number of instructions, not HBM: a row of
+// 128 dimensions is 144 bytes for K and V, 1/3.6 of the bf16 row with the same
+// number of values.  So the codes enter the products with as little unpacking
+// as can be exact.
+//  - K: a nibble n where it lies in a 16-bit word is the fp16 number n 2^-24,
+//    or n 2^-20 four bits up (against q / 16): an AND, no conversion.  The
+//    8 that codes are stored with is taken off by one more product per 8 rows,
+//    of the block scales with -8 * (sum of q over the block).
+//  - V: 1024 + n or 1024 + 16 n by an OR, and n - 8 by one addition or FMA.
+//  - K's block scales multiply the fp32 sums over a block, V's the weights.
+// q is scaled by a power of two and taken in two fp16 pieces (22 bits; bf16 q
+// needs one), and so are weight * scale for fp32 results; for bf16 results
+// these are one fp16 number (11 bits, against the 8 of the results).
+template <int D, class T>
+struct WarpQ4 : WarpSums<D> {
+  using Sums = WarpSums<D>;
+  using L = Tile<D, true>;
+  static constexpr int NB = Sums::NB, kTiles = L::kStep;
+  static constexpr bool kWhole = sizeof(T) == 2;  // q, and the weights, are one piece
+  static constexpr float kLift = 9.f;             // weights reach 2^(9 + 5), products with scales below 2: 2^15
+  uint32_t a[2 * NB][kWhole ? 2 : 4];  // q
+  uint32_t bias[2];                    // -8 sum of q per block, in three pieces: operand of one product
+  float f;                             // score = f * product, in log2 units
+  float top, unit;                     // V scales seen are below top, and enter times `unit`
+
+  __device__ static int out_dim(int x, int y, int g) { return 32 * x + 4 * g + 2 * y; }
+  __device__ __forceinline__ float out_unit() const { return 1.f / unit; }
+
+  __device__ __forceinline__ void load_q(const T* q, bool valid, int t, float scale) {
+    float x[NB][8];
+    load_query<NB>(q, valid, t, x);
+    float mx = 0.f;
 #pragma unroll
-      for (int k = 0; k < kP; ++k) pw[k][0] = take_bf16(w[0], w[1]), pw[k][1] = take_bf16(w[2], w[3]);
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint4 v[4];
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[b][i]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // q to below 2^14
+    const int e = (int)(__float_as_uint(mx) >> 23) - 126;  // mx < 2^e
+    const int sh = min(14 - e, 120);
+    const float up = __uint_as_float((uint32_t)(127 + max(sh, -120)) << 23);
+    f = scale * __uint_as_float((uint32_t)(127 + min(24 - sh, 127)) << 23);
+    uint32_t piece[3][NB / 2];
+    float sums[NB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = *reinterpret_cast<const uint4*>(sv + staged<D, Q4>((i & 1) + 2 * t + 8 * (i >> 1), 8 * c + g));
-          if (edge && !(seen >> i & 1)) v[i] = make_uint4(0, 0, 0, 0);  // 0 * NaN would be NaN
-        }
+    for (int b = 0; b < NB; ++b) {
+      float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t r[4];
+      for (int h = 0; h < 2; ++h) {
+        uint32_t(&w)[kWhole ? 2 : 4] = a[2 * b + h];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) r[i] = k == 0 ? v[i].x : k == 1 ? v[i].y : k == 2 ? v[i].z : v[i].w;
-          const uint32_t a0 = __byte_perm(r[0], r[1], 0x5410), a1 = __byte_perm(r[0], r[1], 0x7632);
-          const uint32_t a2 = __byte_perm(r[2], r[3], 0x5410), a3_ = __byte_perm(r[2], r[3], 0x7632);
-#pragma unroll
-          for (int i = 0; i < kP; ++i) mma_bf16(acc[2 * c + (k >> 1)][k & 1], a0, a1, a2, a3_, pw[i][0], pw[i][1]);
+        for (int odd = 0; odd < 2; ++odd) {
+          const float part = odd ? 1.f / 16 : 1.f;
+          float y0 = x[b][2 * h + odd] * up * part, y1 = x[b][4 + 2 * h + odd] * up * part;
+          const uint32_t hi = take_f16(y0, y1), lo = pack_f16(y0, y1);
+          const float2 u = unpack_f16(hi), r = unpack_f16(lo);
+          if constexpr (kWhole) {
+            w[odd] = hi;
+            sum += (u.x + u.y) * (odd ? 16.f : 1.f);
+          } else {
+            w[2 * odd] = hi;
+            w[2 * odd + 1] = lo;
+            sum += ((u.x + r.x) + (u.y + r.y)) * (odd ? 16.f : 1.f);
+          }
         }
       }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sums[b] = sum * (-8.f / (1 << 10));  // (times 2^14: the codes' 2^-24 in fp16's range)
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int j = 0; j < NB / 2; ++j) piece[k][j] = take_f16(sums[2 * j], sums[2 * j + 1]);
+    // the 16 entries of a row of the operand: piece by piece, the blocks in order; then zeros
+    if constexpr (NB == 4) {
+      bias[0] = t == 0 ? piece[0][0] : t == 1 ? piece[0][NB / 2 - 1] : t == 2 ? piece[1][0] : piece[1][NB / 2 - 1];
+      bias[1] = t == 0 ? piece[2][0] : t == 1 ? piece[2][NB / 2 - 1] : 0;
     } else {
+      bias[0] = t == 0 ? piece[0][0] : t == 1 ? piece[1][0] : t == 2 ? piece[2][0] : 0;
+      bias[1] = 0;
+    }
+    this->clear();
+    top = 1e-30f;
+    unit = 1.f;
+  }
+
+  // Makes room for V scales up to s (of this lane's rows) and for the scores up to mx.
+  __device__ __forceinline__ void make_room(float mx, float s) {
+    s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
+    s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
+    float change = 1.f;
+    if (s >= top) {
+      const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s < 2^e, -23 <= e <= 16
+      top = __uint_as_float((uint32_t)(127 + e) << 23);
+      const float now = __uint_as_float((uint32_t)(127 - max(e, -14)) << 23);  // 2^-e, as far as fp16 goes
+      change = now / unit;
+      unit = now;
+    }
+    this->raise(mx, kLift, change);
+  }
+
+  // kTiles staged tiles.  seen: bit 4 k + i = row (i & 1) + 2t + 8 (i >> 1) of tile k is visible; edge: some row is not.
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t seen) {
+    const int g = lane >> 2, t = lane & 3;
+    float s[4 * kTiles];
+    __half2 vs[4 * kTiles][NB / 2];  // V's scales of the lane's rows
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+      const uint8_t* sk = st + k * L::kBytes;
+      const uint8_t* ks_at = sk + kTileRows * L::kRowBytes;
+      const uint8_t* vs_at = ks_at + L::kHalf;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        __half2 ks[2][NB / 2];
+        uint32_t w[NB];  // the row's words: blocks 0, 1 (and 2, 3) of dimension groups 2t, then of 2t + 1
+        uint32_t row_scales;
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + staged<D, true>(8 * b + g, t));
+          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+          *reinterpret_cast<uint4*>(ks) = *reinterpret_cast<const uint4*>(ks_at + 64 * b + 16 * t);
+          *reinterpret_cast<uint4*>(vs[4 * k + 2 * b]) = *reinterpret_cast<const uint4*>(vs_at + 64 * b + 16 * t);
+          row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 64 * b + 8 * g + 4 * (t & 1));
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(sk + staged<D, true>(8 * b + g, t >> 1) + 8 * (t & 1));
+          w[0] = u.x, w[1] = u.y;
+          *reinterpret_cast<uint2*>(ks) = *reinterpret_cast<const uint2*>(ks_at + 32 * b + 8 * t);
+          *reinterpret_cast<uint2*>(vs[4 * k + 2 * b]) = *reinterpret_cast<const uint2*>(vs_at + 32 * b + 8 * t);
+          row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 32 * b + 4 * g);
+        }
+        float z[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(z, bias[0], 0, bias[1], 0, row_scales, row_scales);
+        float s0 = z[0] * (1.f / (1 << 14)), s1 = z[1] * (1.f / (1 << 14));
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t x = __byte_perm(w[j >> 1], w[NB / 2 + (j >> 1)], j & 1 ? 0x7632 : 0x5410);
+          const uint32_t y = x >> 8;
+          if constexpr (kWhole) {
+            mma_f16(c, a[2 * j][0], 0, a[2 * j][1], 0, x & 0x000f000fu, x & 0x00f000f0u);
+            mma_f16(c, a[2 * j + 1][0], 0, a[2 * j + 1][1], 0, y & 0x000f000fu, y & 0x00f000f0u);
+          } else {
+            mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], x & 0x000f000fu, x & 0x00f000f0u);
+            mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], y & 0x000f000fu,
+                    y & 0x00f000f0u);
+          }
+          const float k0 = __half2float(j & 1 ? __high2half(ks[0][j >> 1]) : __low2half(ks[0][j >> 1]));
+          const float k1 = __half2float(j & 1 ? __high2half(ks[1][j >> 1]) : __low2half(ks[1][j >> 1]));
+          s0 = fmaf(k0, kWhole ? c[0] : c[0] + c[2], s0);
+          s1 = fmaf(k1, kWhole ? c[1] : c[1] + c[3], s1);
+        }
+        s[4 * k + 2 * b] = s0 * f;
+        s[4 * k + 2 * b + 1] = s1 * f;
+      }
+    }
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 4 * kTiles; ++i)
+        if (!(seen >> i & 1)) {
+          s[i] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < NB / 2; ++j) vs[i][j] = __float2half2_rn(0.f);
+        }
+    }
+    float mx = s[0];
+    __half2 h = vs[0][0];
+#pragma unroll
+    for (int i = 0; i < 4 * kTiles; ++i) {
+      mx = fmaxf(mx, s[i]);
+#pragma unroll
+      for (int j = 0; j < NB / 2; ++j) h = __hmax2(h, vs[i][j]);
+    }
+    const float big = fmaxf(__low2float(h), __high2float(h));
+    if (__any_sync(0xffffffffu, mx > this->ref + (kLift + kSlack) || big >= top)) make_room(mx, big);
+    float w[4 * kTiles];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4 * kTiles; ++i) {
+      w[i] = exp2_approx(s[i] - this->ref);
+      sum += w[i];
+    }
+    this->l += sum;
+
+    const __half2 m1032 = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);
+    const __half2 unit2 = __float2half2_rn(unit);
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+      const uint8_t* sv = st + k * L::kBytes + L::kHalf;
       uint32_t v[4][NB / 2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = (i & 1) + 2 * t + 8 * (i >> 1);
         if constexpr (D == 128) {
-          const uint2 u = *reinterpret_cast<const uint2*>(sv + staged<D, Q4>(row, g >> 1) + 8 * (g & 1));
+          const uint2 u = *reinterpret_cast<const uint2*>(sv + staged<D, true>(row, g >> 1) + 8 * (g & 1));
           v[i][0] = u.x, v[i][1] = u.y;
         } else {
-          v[i][0] = *reinterpret_cast<const uint32_t*>(sv + staged<D, Q4>(row, g >> 2) + 4 * (g & 3));
+          v[i][0] = *reinterpret_cast<const uint32_t*>(sv + staged<D, true>(row, g >> 2) + 4 * (g & 3));
         }
       }
-      const __half2 m1032 = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f),
-                    m72 = __float2half2_rn(-72.f);
+      uint32_t ph[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if constexpr (kWhole) {
+          ph[b] = pack_f16(w[4 * k + 2 * b], w[4 * k + 2 * b + 1]);
+        } else {
+          w[4 * k + 2 * b] *= unit;
+          w[4 * k + 2 * b + 1] *= unit;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        uint32_t pw[2][2];  // weight * scale: [piece][rows 2t, 2t + 1 of each half]
+        constexpr int kPieces = kWhole ? 1 : 2;
+        uint32_t pw[kPieces][2];  // weight * scale: rows 2t, 2t + 1 of each half
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const __half h0 = j & 1 ? __high2half(vs[2 * b][j >> 1]) : __low2half(vs[2 * b][j >> 1]);
-          const __half h1 = j & 1 ? __high2half(vs[2 * b + 1][j >> 1]) : __low2half(vs[2 * b + 1][j >> 1]);
-          float y0 = w[2 * b] * __half2float(h0), y1 = w[2 * b + 1] * __half2float(h1);
-          if constexpr (kP == 2) {
+          const __half2 h0 = vs[4 * k + 2 * b][j >> 1], h1 = vs[4 * k + 2 * b + 1][j >> 1];
+          if constexpr (kWhole) {
+            const __half2 both = __hmul2(j & 1 ? __highs2half2(h0, h1) : __lows2half2(h0, h1), unit2);
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&ph[b]), both);
+            pw[0][b] = *reinterpret_cast<const uint32_t*>(&y);
+          } else {
+            float y0 = w[4 * k + 2 * b] * (j & 1 ? __high2float(h0) : __low2float(h0));
+            float y1 = w[4 * k + 2 * b + 1] * (j & 1 ? __high2float(h1) : __low2float(h1));
             pw[0][b] = take_f16(y0, y1);
             pw[1][b] = pack_f16(y0, y1);
-          } else {
-            pw[0][b] = pack_f16(y0, y1);
           }
         }
         uint32_t z0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], j & 1 ? 0x7632 : 0x5410);
         uint32_t z1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], j & 1 ? 0x7632 : 0x5410);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          // 1024 + n, and 1024 + 16 n, as fp16; then n - 8, exactly
           auto low = [&](uint32_t z) {
-            const uint32_t u = (z & 0x000f000fu) | 0x64006400u;
+            const uint32_t u = (z & 0x000f000fu) | 0x64006400u;  // 1024 + n
             const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&u), m1032);
             return *reinterpret_cast<const uint32_t*>(&r);
           };
           auto high = [&](uint32_t z) {
-            const uint32_t u = (z & 0x00f000f0u) | 0x64006400u;
+            const uint32_t u = (z & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
             const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), sixteenth, m72);
             return *reinterpret_cast<const uint32_t*>(&r);
           };
-          const uint32_t a0 = low(z0), a1 = high(z0), a2 = low(z1), a3_ = high(z1);
+          const uint32_t a0 = low(z0), a1 = high(z0), a2 = low(z1), a3 = high(z1);
 #pragma unroll
-          for (int i = 0; i < kP; ++i) mma_f16(acc[j][y], a0, a1, a2, a3_, pw[i][0], pw[i][1]);
+          for (int i = 0; i < kPieces; ++i) mma_f16(this->acc[j][y], a0, a1, a2, a3, pw[i][0], pw[i][1]);
           z0 >>= 8;
           z1 >>= 8;
         }
@@ -466,25 +581,26 @@ struct WarpState {
   }
 };
 
-// Fills a stage with the tile whose K rows begin at `src` (Q4: codes; the
-// scales of its rows at `scales`), V a fixed distance behind.
+// Fills a stage with a tile: K's rows (Q4: codes) begin at `src`, their scales
+// `scales` bytes behind, V's half_bytes behind K's.
 template <int D, bool Q4>
-__device__ __forceinline__ void stage_tile(uint8_t* st, const uint8_t* src, const uint8_t* scales, int64_t half_bytes,
-                                           int lane) {
+__device__ __forceinline__ void stage_tile(uint32_t dst, const uint8_t* src, int scales, int64_t half_bytes, int lane) {
   using L = Tile<D, Q4>;
   constexpr int PPR = L::kRowBytes / 16, N = kTileRows * PPR / 32;
-  const uint32_t dst = smem_u32(st);
+  const uint8_t* k = src + 16 * lane;
+  const uint8_t* v = k + half_bytes;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int at = i * 32 + lane, to = staged<D, Q4>(at / PPR, at % PPR);
-    cp_async16(dst + to, src + 16 * at);
-    cp_async16(dst + L::kHalf + to, src + half_bytes + 16 * at);
+    cp_async16(dst + to, k + 512 * i);
+    cp_async16(dst + L::kHalf + to, v + 512 * i);
   }
   if constexpr (Q4) {
-    constexpr int NS = 2 * L::NB;  // 16-byte pieces of a tile's scales
+    constexpr int NS = 2 * L::NB;  // 16-byte pieces of the scales of K, and of V
     if (lane < 2 * NS) {
-      const int which = lane / NS, at = 16 * (lane % NS);
-      cp_async16(dst + which * L::kHalf + kTileRows * L::kRowBytes + at, scales + which * half_bytes + at);
+      const bool second = lane >= NS;
+      cp_async16(dst + kTileRows * L::kRowBytes + 16 * lane + (second ? L::kHalf - 16 * NS : 0),
+                 (second ? v - 16 * NS : k) + scales);
     }
   }
 }
@@ -507,7 +623,7 @@ __device__ __forceinline__ float over(float l) { return l == 0.f ? 0.f : 1.f / l
 template <int D, bool Q4, class T>
 __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(const __grid_constant__ KvAttnParams p) {
   using L = Tile<D, Q4>;
-  using W = WarpState<D, Q4, T>;
+  using W = std::conditional_t<Q4, WarpQ4<D, T>, WarpBf16<D, T>>;
   constexpr int ST = L::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t chunk_tiles[kMaxChunks];
@@ -530,7 +646,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       if (r < p.n) v = query_rows(p, r, &bad);
       mine[i] = v.tiles;
       sum += v.tiles;
-      empty |= v.seq >= 0 && v.tiles == 0;
+      empty |= r < p.n && v.tiles == 0;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -548,16 +664,19 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
     for (int k = 0; k < chunks; ++k) tiles += chunk_tiles[k];
   }
   if (bad && blockIdx.x == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
-  if (__syncthreads_or(empty)) {  // queries that see no row
+  if (__syncthreads_or(empty)) {  // queries that see no row, or are skipped
     for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
       const Rows v = query_rows(p, r, &bad);
-      if (v.seq < 0 || v.tiles) continue;
+      if (v.tiles) continue;
+      if (p.cut_by_unit)
+        for (int u = tid; u < units; u += kThreadsA) p.cut[r * units + u] = make_int4(0, 0, 0, 0);
+      if (v.seq < 0) continue;
       T* out = static_cast<T*>(p.o) + r * p.o_stride;
       for (int64_t e = tid; e < (int64_t)p.nq * D; e += kThreadsA) out[e] = 0;
     }
   }
   const int64_t total = tiles * units;
-  const int64_t parts = min((int64_t)gridDim.x, (total + kWarps - 1) / kWarps);
+  const int64_t parts = min((int64_t)gridDim.x, (total + kWarps * L::kStep - 1) / (kWarps * L::kStep));
   int4 cut = make_int4(0, 0, 0, 0);
   if (blockIdx.x < parts) {
     int64_t pos = total * blockIdx.x / parts;
@@ -606,72 +725,85 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       st.load_q(static_cast<const T*>(p.q) + r * p.q_stride + col + (int64_t)min(g, n_heads - 1) * D, g < n_heads, t,
                 p.scale);
 
-      // ---- the warp's tiles t0 + warp, + kWarps, ...
-      const int nt = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
-      uint8_t* ring = smem + warp * ST * L::kBytes;
+      // ---- the warp's tiles: kStep from t0 + warp * kStep, again kWarps * kStep further on, ...
+      constexpr int kRound = kWarps * L::kStep;
+      const int nt = (t1 - t0) / kRound * L::kStep + min(max((t1 - t0) % kRound - warp * L::kStep, 0), L::kStep);
+      const uint32_t ring = smem_u32(smem) + warp * ST * L::kSlot;
       const int32_t* table = c.table + (int64_t)v.seq * c.max_pages;
-      const uint8_t* cur_base = nullptr;
-      const uint8_t* nxt_base = nullptr;
-      int cur_row = -1, nxt_row = -1;  // row within the page; -1: no page
-      auto fetch = [&](int i0) {       // where tiles i0 .. i0 + 31 lie, one per lane
+      unsigned long long cur_src = 0, nxt_src = 0;  // K rows of a tile; 0: no page
+      int cur_scales = 0, nxt_scales = 0;
+      auto tile_no = [&](int i) { return t0 + warp * L::kStep + i / L::kStep * kRound + i % L::kStep; };
+      auto fetch = [&](int i0) {  // where the warp's tiles i0 .. i0 + 31 lie, one per lane
         const int i = i0 + lane;
-        nxt_row = -1;
+        nxt_src = 0;
         if (i < nt) {
-          const int row = tile_row(v, t0 + warp + i * kWarps), page = table[row / c.page_rows];
+          const int at = tile_row(v, tile_no(i)), page = table[at / c.page_rows], row = at % c.page_rows;
           if (page >= 0 && page < c.n_pages) {
-            nxt_base = c.pool + page * c.page_bytes + head * c.head_bytes;
-            nxt_row = row % c.page_rows;
+            nxt_src = reinterpret_cast<unsigned long long>(c.pool + page * c.page_bytes + head * c.head_bytes +
+                                                           row * L::kRowBytes);
+            nxt_scales = (c.page_rows - row) * L::kRowBytes + row * 2 * L::NB;
           } else {
             atomicOr(c.status, DEC_KV_BAD_INDEX);
           }
         }
       };
-      uint32_t staged_ok = 0;  // bit per stage
-      auto issue = [&](int i) {
-        if ((i & 31) == 0) {
-          cur_base = nxt_base;
-          cur_row = nxt_row;
-          fetch(i + 32);
+      uint32_t held = 0;  // a bit per tile of the ring: it holds rows
+      auto issue = [&](int j, int slot) {
+        if ((j & (32 / L::kStep - 1)) == 0) {
+          cur_src = nxt_src;
+          cur_scales = nxt_scales;
+          fetch(j * L::kStep + 32);
         }
-        if (i < nt) {
-          const uint8_t* base = reinterpret_cast<const uint8_t*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cur_base), i & 31));
-          const int row = __shfl_sync(0xffffffffu, cur_row, i & 31);
-          const int slot = i % ST;
-          if (row >= 0) {
-            stage_tile<D, Q4>(ring + slot * L::kBytes, base + (int64_t)row * L::kRowBytes,
-                              base + (int64_t)c.page_rows * L::kRowBytes + row * (2 * L::NB), c.half_bytes, lane);
-            staged_ok |= 1u << slot;
-          } else {
-            staged_ok &= ~(1u << slot);
+#pragma unroll
+        for (int k = 0; k < L::kStep; ++k) {
+          const int i = j * L::kStep + k, bit = slot * L::kStep + k;
+          held &= ~(1u << bit);
+          if (i < nt) {
+            const unsigned long long src = __shfl_sync(0xffffffffu, cur_src, i & 31);
+            const int scales = Q4 ? __shfl_sync(0xffffffffu, cur_scales, i & 31) : 0;
+            if (src) {
+              stage_tile<D, Q4>(ring + slot * L::kSlot + k * L::kBytes, reinterpret_cast<const uint8_t*>(src), scales,
+                                c.half_bytes, lane);
+              held |= 1u << bit;
+            }
           }
         }
         cp_async_commit();
       };
+      // tiles of which every row is visible
+      const int sinks_full = v.first / kTileRows;
+      const int win_full0 = v.sink_tiles + (v.win_tile0 * kTileRows < v.lo);
+      const int win_full1 = v.sink_tiles + v.len / kTileRows - v.win_tile0;
       fetch(0);
 #pragma unroll 1
-      for (int i = 0; i < ST; ++i) issue(i);
+      for (int j = 0; j < ST; ++j) issue(j, j);
+      int slot = 0;
 #pragma unroll 1
-      for (int i = 0; i < nt; ++i) {
+      for (int j = 0; j * L::kStep < nt; ++j) {
         cp_async_wait<ST - 1>();
         __syncwarp();
-        const int slot = i % ST;
-        if (staged_ok >> slot & 1) {
-          const int row = tile_row(v, t0 + warp + i * kWarps);
-          const bool edge = !((row >= v.lo && row + kTileRows <= v.len) || row + kTileRows <= v.first);
-          uint32_t seen = 0xf;
-          if (edge) {
-            seen = 0;
+        constexpr uint32_t kAll = (1u << L::kStep) - 1;
+        const uint32_t have = held >> (slot * L::kStep) & kAll;
+        const int first_no = tile_no(j * L::kStep), last_no = first_no + L::kStep - 1;
+        const bool edge =
+            have != kAll || !(last_no < sinks_full || (first_no >= win_full0 && last_no < win_full1));
+        uint32_t seen = 0;
+        if (edge) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int at = row + (k & 1) + 2 * t + 8 * (k >> 1);
-              if (at < v.first || (at >= v.lo && at < v.len)) seen |= 1u << k;
+          for (int k = 0; k < L::kStep; ++k) {
+            if (!(have >> k & 1)) continue;
+            const int row = tile_row(v, first_no + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = row + (i & 1) + 2 * t + 8 * (i >> 1);
+              if (at < v.first || (at >= v.lo && at < v.len)) seen |= 1u << (4 * k + i);
             }
           }
-          st.tile(ring + slot * L::kBytes, lane, edge, seen);
         }
+        st.step(smem + warp * ST * L::kSlot + slot * L::kSlot, lane, edge, seen);
         __syncwarp();
-        issue(i + ST);
+        issue(j + ST, slot);
+        slot = slot + 1 == ST ? 0 : slot + 1;
       }
       cp_async_wait<0>();
 
@@ -688,7 +820,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
         float m = warp_ref[0][h].x;
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) m = fmaxf(m, warp_ref[w][h].x);
-        const float k = exp2_approx(warp_ref[warp][h].x - m);
+        const float k = exp2_approx(warp_ref[warp][h].x - m) * st.out_unit();
         float* row = sums + (warp * kHeadBlock + h) * L::kMergeRow;
 #pragma unroll
         for (int x = 0; x < W::NB; ++x)
@@ -726,11 +858,14 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
           const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0);
           store_out(p.rec + (slot * kHeadBlock + h) * D + e, x);
           if (e == 0) p.ref[slot * kHeadBlock + h] = make_float2(m, ls);
-          if (t0 == 0) {
-            const int64_t last = (before * units + (int64_t)(u + 1) * v.tiles) - 1;
-            cut = make_int4(r, u, (int)(((last + 1) * parts - 1) / total - blockIdx.x), 0);
-          }
         }
+      }
+      if (t0 == 0) {  // the unit begins here
+        const int64_t last = before * units + (int64_t)(u + 1) * v.tiles - 1;
+        cut = make_int4(r, u, blockIdx.x, (int)(((last + 1) * parts - 1) / total - blockIdx.x));
+        if (p.cut_by_unit && tid == 0) p.cut[r * units + u] = cut;
+      } else {
+        cut.w = 0;
       }
       __syncthreads();
       pos += t1 - t0;
@@ -741,49 +876,74 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       }
     }
   }
-  if (tid == 0) p.cut[blockIdx.x] = cut;
+  if (tid == 0 && !p.cut_by_unit) p.cut[blockIdx.x] = cut;
 }
 
-// Joins the parts of the unit that begins in CTA blockIdx.x of kv_attn, in
-// their order; a warp per query head.
-template <int D, class T>
-__global__ void __launch_bounds__(kHeadBlock * 32) kv_attn_join(const __grid_constant__ KvAttnParams p) {
+// Joins the parts of the units that are cut, in their order.  WARPS warps take
+// the parts of one query head in turn; with one, a CTA joins all 8 heads of a
+// unit, with 8 blockIdx.y is the head (few units, cut into many parts).
+template <int D, class T, int WARPS>
+__global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAttnParams p) {
+  constexpr int N = D / 32;
+  __shared__ float sums[WARPS][D + 1];
   pdl_wait();
   const int4 cut = p.cut[blockIdx.x];
-  const int h = threadIdx.x >> 5, lane = threadIdx.x & 31, n = cut.z + 1;
-  if (cut.z == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = cut.w + 1;
+  // (the bounds hold unless lengths changed while kv_attn ran)
+  if (cut.w <= 0 || cut.x >= p.n || cut.y >= p.c.nkv * p.head_blocks || cut.z + cut.w >= p.ctas) return;
+  const int h = WARPS == 1 ? warp : blockIdx.y, first = WARPS == 1 ? 0 : warp;
   const int head = cut.y / p.head_blocks, h0 = (cut.y % p.head_blocks) * kHeadBlock;
   if (h0 + h >= p.group) return;
-  auto slot = [&](int i) { return (i == 0 ? 2 * blockIdx.x + 1 : 2 * ((int64_t)blockIdx.x + i)) * kHeadBlock + h; };
+  auto slot = [&](int i) { return (2 * (int64_t)(cut.z + i) + (i == 0)) * kHeadBlock + h; };
   float m = -3e38f;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, p.ref[slot(i)].x);
-  m = warp_max(m);
-  constexpr int N = D / 32;
   float x[N], l = 0.f;
 #pragma unroll
   for (int k = 0; k < N; ++k) x[k] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane < n) {
-      const float2 rl = p.ref[slot(i0 + lane)];
-      w = exp2_approx(rl.x - m);
-      l += w * rl.y;
-    }
-    const int here = min(32, n - i0);
-#pragma unroll 4
-    for (int i = 0; i < here; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.rec + slot(i0 + i) * D + lane * N;
-      if constexpr (N == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src);
-        x[0] = fmaf(wi, y.x, x[0]), x[1] = fmaf(wi, y.y, x[1]), x[2] = fmaf(wi, y.z, x[2]), x[3] = fmaf(wi, y.w, x[3]);
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(src);
-        x[0] = fmaf(wi, y.x, x[0]), x[1] = fmaf(wi, y.y, x[1]);
+  constexpr int kBatch = 8;  // parts whose loads are under way together
+  bool know_m = false;
+  for (int i0 = first; i0 < n; i0 += kBatch * WARPS) {
+    float y[kBatch][N];
+    float2 rl[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * WARPS;
+      rl[b] = make_float2(-3e38f, 0.f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) y[b][k] = 0.f;
+      if (i < n) {
+        rl[b] = p.ref[slot(i)];
+        const float* src = p.rec + slot(i) * D + lane * N;
+        if constexpr (N == 4) *reinterpret_cast<float4*>(y[b]) = *reinterpret_cast<const float4*>(src);
+        else *reinterpret_cast<float2*>(y[b]) = *reinterpret_cast<const float2*>(src);
       }
     }
+    if (!know_m) m = warp_max(m);
+    know_m = true;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const float w = i0 + b * WARPS < n ? exp2_approx(rl[b].x - m) : 0.f;
+      l = fmaf(w, rl[b].y, l);
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] = fmaf(w, y[b][k], x[k]);
+    }
   }
-  l = warp_sum(l);
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) sums[warp][lane * N + k] = x[k];
+    if (lane == 0) sums[warp][D] = l;
+    __syncthreads();
+    if (warp) return;
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      l += sums[w][D];
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] += sums[w][lane * N + k];
+    }
+  }
   const float k = over(l);
   T* out = static_cast<T*>(p.o) + cut.x * p.o_stride + ((int64_t)head * p.group + h0 + h) * D + lane * N;
 #pragma unroll
@@ -846,11 +1006,18 @@ cudaError_t launch_attn_kv(const KvAttnParams& p, int dev, int ctas, cudaStream_
   cudaLaunchAttribute pdl = {};
   pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl.val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kHeadBlock * 32);
+  cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T>, p);
+  if (!p.cut_by_unit) return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T, 1>, p);
+  const int units = p.n * p.c.nkv * p.head_blocks;
+  if (units > ctas / kHeadBlock) {
+    cfg.gridDim = dim3(units);
+    return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T, 1>, p);
+  }
+  cfg.gridDim = dim3(units, std::min(kHeadBlock, p.group));
+  return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T, 8>, p);
 }
 
 int check_attention(const dec_kv_cache* c, int n, int n_q_heads) {
@@ -927,6 +1094,8 @@ extern "C" int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q,
   p.rec = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.rec);
   p.ref = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ws.ref);
   p.cut = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + ws.cut);
+  p.ctas = ctas;
+  p.cut_by_unit = (int64_t)n * c->n_kv_heads * p.head_blocks <= ctas;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool q4 = c->format == DEC_KV_Q4B32, f32 = type == DEC_IO_F32;
