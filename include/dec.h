@@ -477,9 +477,9 @@ int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q, void* o, i
                      int window, int sinks, float scale, void* workspace, size_t workspace_bytes,
                      dec_stream_t stream);
 
-/* The workspace bytes of a dec_kv_attention call on the current device, for
- * any n up to this one. */
-int dec_kv_attention_workspace(const dec_kv_cache* c, int n, int n_q_heads, size_t* bytes);
+/* The workspace bytes of dec_kv_attention calls on the current device, enough
+ * for any queries (a few MB: the sums of units cut between CTAs). */
+int dec_kv_attention_workspace(const dec_kv_cache* c, size_t* bytes);
 
 /* Makes each listed sequence n_new[i] rows longer (NULL: one), and gives it
  * the pages that the new rows need: in list order, the free pages from the

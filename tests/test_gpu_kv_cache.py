@@ -14,9 +14,10 @@ output by sum_j w_j |v_j| * 2^-10.  These numbers also have a smallest step:
 they are off by at most 2^-25, where the weight that sets the reference is 2^9
 and the scale enters as s / 2^e, 2^e <= 2 s for the largest scale s (of 2^-14 or
 more).  With codes up to 8 and a sum of weights of at least 2^9, n rows are off
-by at most n * 8 * 2^-25 / 2^9 * 2^e <= n * 2^-30 * s.  (It shows only where the
-rows that hold the weight are zero in a dimension.)  A block's largest code is
-7, so s is the largest |v| / 7.
+by at most n * 8 * 2^-25 / 2^9 * 2^e <= n * 2^-30 * s.  (For bf16 results scales
+below one enter as they are, e = 0, so there s counts as at least 1/2.)  It
+shows only where the rows that hold the weight are zero in a dimension.  A
+block's largest code is 7, so s is the largest |v| / 7.
 """
 import numpy as np
 import pytest
@@ -44,11 +45,11 @@ class Filled:
     them) and random rows elsewhere, at shuffled pages."""
 
     def __init__(self, fmt, nkv, hd, R, lens, *, layers=2, layer=1, seed=0, window=0, sinks=0, spare=3,
-                 k_of=None, v_of=None):
+                 k_of=None, v_of=None, room=1):
         rng = np.random.default_rng(seed)
         self.pages = ref.Pages(fmt, nkv, hd, R)
         self.lens, self.layer, self.R = list(lens), layer, R
-        width = max(1, max(-(-n // R) for n in lens))
+        width = max(-(-room // R), max(-(-n // R) for n in lens))
         table = np.full((len(lens), width), -1, np.int32)
         seen = [ref.visible(n, window, sinks) for n in lens]
         wanted = [(s, i) for s, v in enumerate(seen) for i in np.unique(v // R)]
@@ -93,7 +94,8 @@ class Filled:
             ds = (self.pages.d + 8) * 2.0 ** -24 * np.abs(dots)[:, None]
             tol = size * (2 * ds + 2 * n * 2.0 ** -24 + 2.0 ** -19)
             if self.pages.fmt == "q4" and n:
-                tol = tol + n * 2.0 ** -30 * np.abs(self.v[s]).max() / 7 + (size * 2.0 ** -10 if bf16 else 0)
+                tol = tol + n * 2.0 ** -30 * max(np.abs(self.v[s]).max() / 7, 0.5 if bf16 else 0)
+                tol = tol + (size * 2.0 ** -10 if bf16 else 0)
             tol = tol + (np.abs(o) + tol) * (2.0 ** -8 if bf16 else 2.0 ** -24) + 1e-37
             bad = np.abs(got[r] - o) > tol
             assert not bad.any(), (what, r, s, n, np.argwhere(bad)[:4].tolist(), np.abs(got[r] - o)[bad][:4], tol[bad][:4])
@@ -104,12 +106,13 @@ SHAPES = [  # kv heads, group, head_dim, page rows
 ]
 
 
+@pytest.mark.parametrize("room", [1, 40000])  # rows that a table has room for: short ones are not cut between CTAs
 @pytest.mark.parametrize("fmt", ["bf16", "q4"])
 @pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("nkv,group,hd,R", SHAPES)
-def test_attention_all_rows(fmt, io, nkv, group, hd, R):
+def test_attention_all_rows(fmt, io, nkv, group, hd, R, room):
     lens = [0, 1, 15, R, R + 1, 2 * R - 1, 333, 2]
-    f = Filled(fmt, nkv, hd, R, lens, seed=nkv * 100 + hd + R)
+    f = Filled(fmt, nkv, hd, R, lens, seed=nkv * 100 + hd + R, room=room)
     g = torch.Generator(device="cuda").manual_seed(1)
     q = torch.randn(len(lens), nkv * group, hd, device="cuda", generator=g).to(io)
     out = f.cache.attention(f.layer, q)
@@ -255,7 +258,7 @@ def test_attention_in_graphs_and_streams():
     f = Filled("bf16", 2, 64, 16, [100, 260], seed=6)
     q = torch.randn(2, 4, 64, device="cuda")
     out_a, out_b = torch.empty_like(q), torch.empty_like(q)
-    ws_a, ws_b = f.cache.workspace(2, 4), f.cache.workspace(2, 4)
+    ws_a, ws_b = f.cache.workspace(), f.cache.workspace()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -531,7 +534,7 @@ def test_a_run_of_all_calls(fmt):
     q = torch.zeros(2, n_seqs, nkv * group, hd, device="cuda")
     out = torch.zeros_like(q)
     lst = ints([-1] * n_seqs)
-    ws = c.workspace(n_seqs, nkv * group)
+    ws = c.workspace()
     graph = torch.cuda.CUDAGraph()
 
     def step():

@@ -40,7 +40,7 @@ def test_bad_shapes_are_refused_by_every_call(lib, kw, code):
     assert lib.dec_kv_append(c, 0, MEM, MEM, 0, 512, None, None, 1, None) == code
     assert lib.dec_kv_read(c, 0, MEM, MEM, 0, 512, None, None, 1, None) == code
     assert lib.dec_kv_attention(c, 0, MEM, 2 * MEM, 0, 1024, 1024, None, 1, 8, 0, 0, 0.0, MEM, 1 << 40, None) == code
-    assert lib.dec_kv_attention_workspace(c, 1, 8, ctypes.byref(n)) == code
+    assert lib.dec_kv_attention_workspace(c, ctypes.byref(n)) == code
     assert lib.dec_kv_extend(c, None, None, 1, None) == code
     assert lib.dec_kv_fork(c, MEM, MEM, 1, None) == code
     assert lib.dec_kv_release(c, None, 1, 0, 0, None) == code
@@ -114,9 +114,7 @@ def test_bad_attention_calls_are_refused(lib):
     args[8] = 0
     assert lib.dec_kv_attention(*args) == OK
     n = ctypes.c_size_t()
-    assert lib.dec_kv_attention_workspace(c, 1, 8, None) == ARG
-    assert lib.dec_kv_attention_workspace(c, -1, 8, ctypes.byref(n)) == ARG
-    assert lib.dec_kv_attention_workspace(c, 1, 7, ctypes.byref(n)) == SHAPE
+    assert lib.dec_kv_attention_workspace(c, None) == ARG
 
 
 def test_bad_page_calls_are_refused(lib):

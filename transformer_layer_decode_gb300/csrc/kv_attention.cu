@@ -2,6 +2,7 @@
 // cache, bf16 or in 4-bit blocks, with a sliding window and first rows that
 // stay visible.
 #include <atomic>
+#include <cstdlib>
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -58,7 +59,7 @@ struct KvAttnParams {
   float* rec;              // [2 * CTAs][8][D]: sums of units cut between CTAs
   float2* ref;             // [2 * CTAs][8]: reference and sum of the weights
   int4* cut;               // [CTAs]: query, unit, CTA where it begins, CTAs that it goes on for
-  int ctas;
+  int ctas, grain;
   int cut_by_unit;         // cut is indexed by unit (there are no more of them than CTAs), not by CTA
 };
 
@@ -138,8 +139,12 @@ __device__ __forceinline__ uint32_t take_f16(float& x, float& y) {
   return w;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Copies `bytes` (16, or 0: then zeros are written) where `on`.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes, bool on = true) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"((int)on)
+      : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -211,6 +216,12 @@ struct WarpSums {
   }
 };
 
+// Of a tile's 16 rows the lane's four: bit i is row (i & 1) + 2t + 8 (i >> 1).
+__device__ __forceinline__ uint32_t rows_of_lane(uint32_t rows, int t) {
+  const uint32_t r = rows >> (2 * t);
+  return (r & 3) | (r >> 6 & 12);
+}
+
 // Eight dimensions 32 b + 8 t .. of a query as fp32.
 template <int NB, class T>
 __device__ __forceinline__ void load_query(const T* q, bool valid, int t, float (&x)[NB][8]) {
@@ -271,10 +282,11 @@ struct WarpBf16 : WarpSums<D> {
     this->clear();
   }
 
-  // One staged tile.  seen: bit i = row (i & 1) + 2t + 8 (i >> 1) is visible; edge: some row is not.
-  __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t seen) {
+  // One staged tile.  edge: some row is not visible; rows_seen: a bit for each that is.
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t rows_seen) {
     using L = Tile<D, false>;
     const int g = lane >> 2, t = lane & 3;
+    const uint32_t seen = rows_of_lane(rows_seen, t);
     const uint8_t* sv = st + L::kHalf;
     float s[4];
 #pragma unroll
@@ -347,14 +359,18 @@ struct WarpQ4 : WarpSums<D> {
   using L = Tile<D, true>;
   static constexpr int NB = Sums::NB, kTiles = L::kStep;
   static constexpr bool kWhole = sizeof(T) == 2;  // q, and the weights, are one piece
-  static constexpr float kLift = 9.f;             // weights reach 2^(9 + 5), products with scales below 2: 2^15
+  // The largest weight is 2^lift to 2^(lift + kSlack), so that its product with
+  // a scale stays below 2^15 and the others well above fp16's smallest step.
+  static constexpr float kLift = 9.f;
   uint32_t a[2 * NB][kWhole ? 2 : 4];  // q
   uint32_t bias[2];                    // -8 sum of q per block, in three pieces: operand of one product
   float f;                             // score = f * product, in log2 units
-  float top, unit;                     // V scales seen are below top, and enter times `unit`
+  float top;                           // V scales seen are below top = 2^e
+  float unit;                          // fp32 results: they enter times unit = 2^-e (as far as fp16 goes) ...
+  float lift;                          // ... at lift = 9; bf16 results: as they are, at lift = min(9, 9 - e)
 
   __device__ static int out_dim(int x, int y, int g) { return 32 * x + 4 * g + 2 * y; }
-  __device__ __forceinline__ float out_unit() const { return 1.f / unit; }
+  __device__ __forceinline__ float out_unit() const { return kWhole ? 1.f : 1.f / unit; }
 
   __device__ __forceinline__ void load_q(const T* q, bool valid, int t, float scale) {
     float x[NB][8];
@@ -414,33 +430,48 @@ struct WarpQ4 : WarpSums<D> {
     this->clear();
     top = 1e-30f;
     unit = 1.f;
+    lift = kLift;
   }
 
-  // Makes room for V scales up to s (of this lane's rows) and for the scores up to mx.
+  // Makes room for V scales up to s (of this lane) and for the scores up to mx.
   __device__ __forceinline__ void make_room(float mx, float s) {
-    s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
-    s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
+    s = warp_max(s);
     float change = 1.f;
     if (s >= top) {
       const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s < 2^e, -23 <= e <= 16
       top = __uint_as_float((uint32_t)(127 + e) << 23);
-      const float now = __uint_as_float((uint32_t)(127 - max(e, -14)) << 23);  // 2^-e, as far as fp16 goes
-      change = now / unit;
-      unit = now;
+      if constexpr (kWhole) {
+        const float now = kLift - (float)max(e, 0);
+        this->ref += lift - now;  // the references that the heads' largest scores have now
+        const float down = exp2_approx(now - lift);
+        this->l *= down;
+        change = down;
+        lift = now;
+      } else {
+        const float now = __uint_as_float((uint32_t)(127 - max(e, -14)) << 23);
+        change = now / unit;
+        unit = now;
+      }
     }
-    this->raise(mx, kLift, change);
+    this->raise(mx, lift, change);
   }
 
-  // kTiles staged tiles.  seen: bit 4 k + i = row (i & 1) + 2t + 8 (i >> 1) of tile k is visible; edge: some row is not.
-  __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t seen) {
+  // kTiles staged tiles.  edge: some row is not visible; rows_seen: a bit for each that is.
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t rows_seen) {
     const int g = lane >> 2, t = lane & 3;
     float s[4 * kTiles];
     __half2 vs[4 * kTiles][NB / 2];  // V's scales of the lane's rows
+    __half2 most = __float2half2_rn(0.f);  // the largest of all, between the lanes
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) {
       const uint8_t* sk = st + k * L::kBytes;
       const uint8_t* ks_at = sk + kTileRows * L::kRowBytes;
       const uint8_t* vs_at = ks_at + L::kHalf;
+      if (D == 128 || lane < 16) {
+        __half2 h = *reinterpret_cast<const __half2*>(vs_at + 4 * lane);
+        if (edge && !(rows_seen >> (16 * k + lane / (NB / 2)) & 1)) h = __float2half2_rn(0.f);
+        most = __hmax2(most, h);
+      }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         __half2 ks[2][NB / 2];
@@ -486,23 +517,22 @@ struct WarpQ4 : WarpSums<D> {
     }
     if (edge) {
 #pragma unroll
-      for (int i = 0; i < 4 * kTiles; ++i)
-        if (!(seen >> i & 1)) {
-          s[i] = -INFINITY;
+      for (int k = 0; k < kTiles; ++k) {
+        const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
 #pragma unroll
-          for (int j = 0; j < NB / 2; ++j) vs[i][j] = __float2half2_rn(0.f);
-        }
+        for (int i = 0; i < 4; ++i)
+          if (!(seen >> i & 1)) {
+            s[4 * k + i] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < NB / 2; ++j) vs[4 * k + i][j] = __float2half2_rn(0.f);
+          }
+      }
     }
     float mx = s[0];
-    __half2 h = vs[0][0];
 #pragma unroll
-    for (int i = 0; i < 4 * kTiles; ++i) {
-      mx = fmaxf(mx, s[i]);
-#pragma unroll
-      for (int j = 0; j < NB / 2; ++j) h = __hmax2(h, vs[i][j]);
-    }
-    const float big = fmaxf(__low2float(h), __high2float(h));
-    if (__any_sync(0xffffffffu, mx > this->ref + (kLift + kSlack) || big >= top)) make_room(mx, big);
+    for (int i = 1; i < 4 * kTiles; ++i) mx = fmaxf(mx, s[i]);
+    const float big = fmaxf(__low2float(most), __high2float(most));
+    if (__any_sync(0xffffffffu, mx > this->ref + (lift + kSlack) || big >= top)) make_room(mx, big);
     float w[4 * kTiles];
     float sum = 0.f;
 #pragma unroll
@@ -513,7 +543,6 @@ struct WarpQ4 : WarpSums<D> {
     this->l += sum;
 
     const __half2 m1032 = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);
-    const __half2 unit2 = __float2half2_rn(unit);
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) {
       const uint8_t* sv = st + k * L::kBytes + L::kHalf;
@@ -546,7 +575,7 @@ struct WarpQ4 : WarpSums<D> {
         for (int b = 0; b < 2; ++b) {
           const __half2 h0 = vs[4 * k + 2 * b][j >> 1], h1 = vs[4 * k + 2 * b + 1][j >> 1];
           if constexpr (kWhole) {
-            const __half2 both = __hmul2(j & 1 ? __highs2half2(h0, h1) : __lows2half2(h0, h1), unit2);
+            const __half2 both = j & 1 ? __highs2half2(h0, h1) : __lows2half2(h0, h1);
             const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&ph[b]), both);
             pw[0][b] = *reinterpret_cast<const uint32_t*>(&y);
           } else {
@@ -582,9 +611,10 @@ struct WarpQ4 : WarpSums<D> {
 };
 
 // Fills a stage with a tile: K's rows (Q4: codes) begin at `src`, their scales
-// `scales` bytes behind, V's half_bytes behind K's.
+// `scales` bytes behind, V's half_bytes behind K's; bytes 0: with zeros.
 template <int D, bool Q4>
-__device__ __forceinline__ void stage_tile(uint32_t dst, const uint8_t* src, int scales, int64_t half_bytes, int lane) {
+__device__ __forceinline__ void stage_tile(uint32_t dst, const uint8_t* src, int scales, int64_t half_bytes, int lane,
+                                           int bytes) {
   using L = Tile<D, Q4>;
   constexpr int PPR = L::kRowBytes / 16, N = kTileRows * PPR / 32;
   const uint8_t* k = src + 16 * lane;
@@ -592,16 +622,14 @@ __device__ __forceinline__ void stage_tile(uint32_t dst, const uint8_t* src, int
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int at = i * 32 + lane, to = staged<D, Q4>(at / PPR, at % PPR);
-    cp_async16(dst + to, k + 512 * i);
-    cp_async16(dst + L::kHalf + to, v + 512 * i);
+    cp_async16(dst + to, k + 512 * i, bytes);
+    cp_async16(dst + L::kHalf + to, v + 512 * i, bytes);
   }
   if constexpr (Q4) {
     constexpr int NS = 2 * L::NB;  // 16-byte pieces of the scales of K, and of V
-    if (lane < 2 * NS) {
-      const bool second = lane >= NS;
-      cp_async16(dst + kTileRows * L::kRowBytes + 16 * lane + (second ? L::kHalf - 16 * NS : 0),
-                 (second ? v - 16 * NS : k) + scales);
-    }
+    const bool second = lane >= NS;
+    cp_async16(dst + kTileRows * L::kRowBytes + 16 * lane + (second ? L::kHalf - 16 * NS : 0),
+               (second ? v - 16 * NS : k) + scales, bytes, lane < 2 * NS);
   }
 }
 
@@ -620,15 +648,194 @@ __device__ __forceinline__ void store_out(T* p, const float (&x)[N]) {
 // The sum over no weight is zero; NaN stays.
 __device__ __forceinline__ float over(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
+// What a thread holds of a unit's sums over a CTA's tiles: N dimensions from e
+// of head h, relative to the reference m, and the sum of the weights.
+template <int D>
+struct UnitSums {
+  static constexpr int N = D / 16;
+  float x[N], m, l;
+};
+
+// The CTA's sums over tiles t0 .. t1 - 1 of unit u of query r.
+template <int D, bool Q4, class T>
+__device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Rows& v, int r, int u, int t0, int t1,
+                                                 uint8_t* smem) {
+  using L = Tile<D, Q4>;
+  using W = std::conditional_t<Q4, WarpQ4<D, T>, WarpBf16<D, T>>;
+  constexpr int ST = L::kStages, kRound = kWarps * L::kStep;
+  __shared__ float2 warp_ref[kWarps][kHeadBlock];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const KvView& c = p.c;
+  const int head = u / p.head_blocks, h0 = (u % p.head_blocks) * kHeadBlock;
+  const int n_heads = min(kHeadBlock, p.group - h0);
+  __syncthreads();  // the sums of the unit before have been read
+
+  // ---- the warp's tiles: kStep from t0 + warp * kStep, again kWarps * kStep further on, ...
+  const int nt = (t1 - t0) / kRound * L::kStep + min(max((t1 - t0) % kRound - warp * L::kStep, 0), L::kStep);
+  const uint32_t ring = smem_u32(smem) + warp * ST * L::kSlot;
+  const int32_t* table = c.table + (int64_t)v.seq * c.max_pages;
+  unsigned long long cur_src = 0, nxt_src = 0;  // K rows of a tile; 0: none
+  int cur_scales = 0, nxt_scales = 0;
+  bool doubt = false;  // a tile had no page
+  auto tile_no = [&](int i) { return t0 + warp * L::kStep + i / L::kStep * kRound + i % L::kStep; };
+  auto page_of = [&](int row) {
+    const int page = table[row / c.page_rows];
+    return page >= 0 && page < c.n_pages ? page : -1;
+  };
+  auto fetch = [&](int i0) {  // where the warp's tiles i0 .. i0 + 31 lie, one per lane
+    const int i = i0 + lane;
+    nxt_src = 0;
+    if (i < nt) {
+      const int at = tile_row(v, tile_no(i)), page = page_of(at), row = at % c.page_rows;
+      if (page >= 0) {
+        nxt_src = reinterpret_cast<unsigned long long>(c.pool + page * c.page_bytes + head * c.head_bytes +
+                                                       row * L::kRowBytes);
+        nxt_scales = (c.page_rows - row) * L::kRowBytes + row * 2 * L::NB;
+      } else {
+        atomicOr(c.status, DEC_KV_BAD_INDEX);
+        doubt = true;
+      }
+    }
+  };
+  auto issue = [&](int j, uint32_t dst) {
+    if ((j & (32 / L::kStep - 1)) == 0) {
+      cur_src = nxt_src;
+      cur_scales = nxt_scales;
+      fetch(j * L::kStep + 32);
+      doubt = __any_sync(0xffffffffu, doubt);
+    }
+#pragma unroll
+    for (int k = 0; k < L::kStep; ++k) {
+      const int i = (j * L::kStep + k) & 31;
+      const unsigned long long src = __shfl_sync(0xffffffffu, cur_src, i);
+      const int scales = Q4 ? __shfl_sync(0xffffffffu, cur_scales, i) : 0;
+      stage_tile<D, Q4>(dst + k * L::kBytes, src ? reinterpret_cast<const uint8_t*>(src) : c.pool, src ? scales : 0,
+                        src ? c.half_bytes : 0, lane, src ? 16 : 0);
+    }
+    cp_async_commit();
+  };
+  // the steps, from plain0 on for plain_n, whose every row is visible (those of the first rows aside)
+  const int n0 = t0 + warp * L::kStep;
+  const int full0 = v.sink_tiles + (v.win_tile0 * kTileRows < v.lo), full1 = v.sink_tiles + v.len / kTileRows - v.win_tile0;
+  const int plain0 = full0 > n0 ? (full0 - n0 + kRound - 1) / kRound : 0;
+  const int plain_n =
+      min(nt / L::kStep, full1 - L::kStep >= n0 ? (full1 - L::kStep - n0) / kRound + 1 : 0) - plain0;
+  fetch(0);
+#pragma unroll 1
+  for (int j = 0; j < ST; ++j) issue(j, ring + j * L::kSlot);
+  W st;  // (q is read while the first tiles are under way)
+  st.load_q(static_cast<const T*>(p.q) + r * p.q_stride + ((int64_t)head * p.group + h0 + min(g, n_heads - 1)) * D,
+            g < n_heads, t, p.scale);
+  uint32_t slot = warp * ST * L::kSlot;
+#pragma unroll 1
+  for (int j = 0; j * L::kStep < nt; ++j) {
+    cp_async_wait<ST - 1>();
+    __syncwarp();
+    const bool edge = doubt || j < plain0 || j - plain0 >= plain_n;
+    uint32_t rows_seen = 0;  // a bit per row of the step
+    if (edge) {
+#pragma unroll
+      for (int k = 0; k < L::kStep; ++k) {
+        const int i = j * L::kStep + k, row = i < nt ? tile_row(v, tile_no(i)) : 0, at = row + (lane & 15);
+        const bool sees = i < nt && (at < v.first || (at >= v.lo && at < v.len)) && page_of(row) >= 0;
+        rows_seen |= (__ballot_sync(0xffffffffu, sees) & 0xffff) << (16 * k);
+      }
+    }
+    st.step(smem + slot, lane, edge, rows_seen);
+    __syncwarp();
+    issue(j + ST, smem_u32(smem) + slot);
+    slot += L::kSlot;
+    if (slot == (warp + 1) * ST * L::kSlot) slot = warp * ST * L::kSlot;
+  }
+  cp_async_wait<0>();
+
+  // ---- the warps' sums, brought to one reference
+  float lsum = st.l;
+  lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+  lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+  if (t == 0) warp_ref[warp][g] = make_float2(st.ref, lsum);
+  __syncthreads();  // every warp is through with its ring
+  float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    const int h = 2 * t + hh;
+    float m = warp_ref[0][h].x;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, warp_ref[w][h].x);
+    const float k = exp2_approx(warp_ref[warp][h].x - m) * st.out_unit();
+    float* row = sums + (warp * kHeadBlock + h) * L::kMergeRow;
+#pragma unroll
+    for (int x = 0; x < W::NB; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        *reinterpret_cast<float2*>(row + W::out_dim(x, y, g)) =
+            make_float2(st.acc[x][y][hh] * k, st.acc[x][y][2 + hh] * k);
+  }
+  __syncthreads();
+  UnitSums<D> o;
+  constexpr int N = UnitSums<D>::N;
+  const int h = tid / 16, e = (tid % 16) * N;
+  o.m = warp_ref[0][h].x;
+  o.l = 0.f;
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) o.m = fmaxf(o.m, warp_ref[w][h].x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) o.x[i] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    o.l += warp_ref[w][h].y * exp2_approx(warp_ref[w][h].x - o.m);
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(sums + (w * kHeadBlock + h) * L::kMergeRow + e + i);
+      o.x[i] += y.x, o.x[i + 1] += y.y, o.x[i + 2] += y.z, o.x[i + 3] += y.w;
+    }
+  }
+  return o;
+}
+
+// Writes a unit's outputs: thread tid the N dimensions that it holds.
+template <int D, class T>
+__device__ __forceinline__ void write_unit(const KvAttnParams& p, int r, int u, UnitSums<D>& o) {
+  const int head = u / p.head_blocks, h = (u % p.head_blocks) * kHeadBlock + threadIdx.x / 16;
+  if (h >= p.group) return;
+  const float k = over(o.l);
+#pragma unroll
+  for (int i = 0; i < o.N; ++i) o.x[i] *= k;
+  store_out(static_cast<T*>(p.o) + r * p.o_stride + ((int64_t)head * p.group + h) * D + (threadIdx.x % 16) * o.N, o.x);
+}
+
+// Units that are all short: a CTA takes whole units in turn.
+template <int D, bool Q4, class T>
+__global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm)
+    kv_attn_whole(const __grid_constant__ KvAttnParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int units = p.c.nkv * p.head_blocks;
+  for (int id = blockIdx.x; id < p.n * units; id += gridDim.x) {
+    const int r = id / units, u = id % units;
+    bool bad = false;
+    const Rows v = query_rows(p, r, &bad);
+    if (bad && threadIdx.x == 0) atomicOr(p.c.status, DEC_KV_BAD_INDEX);
+    if (v.seq < 0) continue;
+    UnitSums<D> o = unit_sums<D, Q4, T>(p, v, r, u, 0, v.tiles, smem);
+    write_unit<D, T>(p, r, u, o);
+  }
+}
+
+// A CTA's share of the line of tiles and where it stands in it.
+struct Share {
+  int64_t pos, end;      // tile positions, of all units
+  int64_t before;        // tiles of the queries before r
+  int64_t total, parts;  // positions and shares of the whole line
+  int r, u, t0, t1;      // the unit at hand
+  int cut;               // a unit begins here that ends elsewhere
+};
+
 template <int D, bool Q4, class T>
 __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(const __grid_constant__ KvAttnParams p) {
   using L = Tile<D, Q4>;
-  using W = std::conditional_t<Q4, WarpQ4<D, T>, WarpBf16<D, T>>;
-  constexpr int ST = L::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t chunk_tiles[kMaxChunks];
-  __shared__ float2 warp_ref[kWarps][kHeadBlock];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvView& c = p.c;
   pdl_trigger();
 
@@ -676,207 +883,85 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
     }
   }
   const int64_t total = tiles * units;
-  const int64_t parts = min((int64_t)gridDim.x, (total + kWarps * L::kStep - 1) / (kWarps * L::kStep));
-  int4 cut = make_int4(0, 0, 0, 0);
+  // As many shares as there are CTAs, but none without work, and beyond one per
+  // unit only while each keeps all warps busy: a share pays for its queries,
+  // its page numbers and its sums (about 2.5 us a unit) however short it is.
+  constexpr int kRound = kWarps * L::kStep;
+  const int64_t grain = kRound * p.grain;
+  const int64_t parts = min(min((int64_t)gridDim.x, total), max((total + grain - 1) / grain, (int64_t)p.n * units));
+  __shared__ Share share;  // (not in registers: the products need them)
   if (blockIdx.x < parts) {
-    int64_t pos = total * blockIdx.x / parts;
-    const int64_t end = total * (blockIdx.x + 1) / parts;
-    // the query that holds tile `pos`
-    int64_t before = 0;  // tiles of the queries before r
-    int r = 0;
-    {
-      const int64_t want = pos / units;
-      int k = 0;
-      if (chunks > 1) {
-        while (before + chunk_tiles[k] <= want) before += chunk_tiles[k++];
-        count(k);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int64_t incl = mine[i];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, before + incl > want);
-        if (past) {
-          const int at = __ffs(past) - 1;
-          before += __shfl_sync(0xffffffffu, incl - mine[i], at);
-          r = k * kChunkRows + 32 * i + at;
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
-      }
+    // the query that holds the share's first tile
+    const int64_t pos = total * blockIdx.x / parts, want = pos / units;
+    int64_t before = 0;
+    int r = 0, k = 0;
+    if (chunks > 1) {
+      while (before + chunk_tiles[k] <= want) before += chunk_tiles[k++];
+      count(k);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int64_t incl = mine[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + incl > want);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        before += __shfl_sync(0xffffffffu, incl - mine[i], at);
+        r = k * kChunkRows + 32 * i + at;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (tid == 0) share = Share{pos, total * (blockIdx.x + 1) / parts, before, total, parts, r, 0, 0, 0, 0};
+    __syncthreads();
     Rows v = query_rows(p, r, &bad);
 
-    while (pos < end) {
-      const int64_t rel = pos - before * units;
+    while (share.pos < share.end) {
+      const int64_t rel = share.pos - share.before * units;
       // (not so only if lengths change while the call runs: then leave, in bounds)
       if (rel < 0 || rel >= (int64_t)v.tiles * units) break;
       const int u = (int)(rel / v.tiles), t0 = (int)(rel - (int64_t)u * v.tiles);
-      const int t1 = (int)min((int64_t)v.tiles, t0 + (end - pos));
-      const int head = u / p.head_blocks, h0 = (u % p.head_blocks) * kHeadBlock;
-      const int n_heads = min(kHeadBlock, p.group - h0);
-      const int64_t col = ((int64_t)head * p.group + h0) * D;
-
-      W st;
-      st.load_q(static_cast<const T*>(p.q) + r * p.q_stride + col + (int64_t)min(g, n_heads - 1) * D, g < n_heads, t,
-                p.scale);
-
-      // ---- the warp's tiles: kStep from t0 + warp * kStep, again kWarps * kStep further on, ...
-      constexpr int kRound = kWarps * L::kStep;
-      const int nt = (t1 - t0) / kRound * L::kStep + min(max((t1 - t0) % kRound - warp * L::kStep, 0), L::kStep);
-      const uint32_t ring = smem_u32(smem) + warp * ST * L::kSlot;
-      const int32_t* table = c.table + (int64_t)v.seq * c.max_pages;
-      unsigned long long cur_src = 0, nxt_src = 0;  // K rows of a tile; 0: no page
-      int cur_scales = 0, nxt_scales = 0;
-      auto tile_no = [&](int i) { return t0 + warp * L::kStep + i / L::kStep * kRound + i % L::kStep; };
-      auto fetch = [&](int i0) {  // where the warp's tiles i0 .. i0 + 31 lie, one per lane
-        const int i = i0 + lane;
-        nxt_src = 0;
-        if (i < nt) {
-          const int at = tile_row(v, tile_no(i)), page = table[at / c.page_rows], row = at % c.page_rows;
-          if (page >= 0 && page < c.n_pages) {
-            nxt_src = reinterpret_cast<unsigned long long>(c.pool + page * c.page_bytes + head * c.head_bytes +
-                                                           row * L::kRowBytes);
-            nxt_scales = (c.page_rows - row) * L::kRowBytes + row * 2 * L::NB;
-          } else {
-            atomicOr(c.status, DEC_KV_BAD_INDEX);
-          }
-        }
-      };
-      uint32_t held = 0;  // a bit per tile of the ring: it holds rows
-      auto issue = [&](int j, int slot) {
-        if ((j & (32 / L::kStep - 1)) == 0) {
-          cur_src = nxt_src;
-          cur_scales = nxt_scales;
-          fetch(j * L::kStep + 32);
-        }
-#pragma unroll
-        for (int k = 0; k < L::kStep; ++k) {
-          const int i = j * L::kStep + k, bit = slot * L::kStep + k;
-          held &= ~(1u << bit);
-          if (i < nt) {
-            const unsigned long long src = __shfl_sync(0xffffffffu, cur_src, i & 31);
-            const int scales = Q4 ? __shfl_sync(0xffffffffu, cur_scales, i & 31) : 0;
-            if (src) {
-              stage_tile<D, Q4>(ring + slot * L::kSlot + k * L::kBytes, reinterpret_cast<const uint8_t*>(src), scales,
-                                c.half_bytes, lane);
-              held |= 1u << bit;
-            }
-          }
-        }
-        cp_async_commit();
-      };
-      // tiles of which every row is visible
-      const int sinks_full = v.first / kTileRows;
-      const int win_full0 = v.sink_tiles + (v.win_tile0 * kTileRows < v.lo);
-      const int win_full1 = v.sink_tiles + v.len / kTileRows - v.win_tile0;
-      fetch(0);
-#pragma unroll 1
-      for (int j = 0; j < ST; ++j) issue(j, j);
-      int slot = 0;
-#pragma unroll 1
-      for (int j = 0; j * L::kStep < nt; ++j) {
-        cp_async_wait<ST - 1>();
-        __syncwarp();
-        constexpr uint32_t kAll = (1u << L::kStep) - 1;
-        const uint32_t have = held >> (slot * L::kStep) & kAll;
-        const int first_no = tile_no(j * L::kStep), last_no = first_no + L::kStep - 1;
-        const bool edge =
-            have != kAll || !(last_no < sinks_full || (first_no >= win_full0 && last_no < win_full1));
-        uint32_t seen = 0;
-        if (edge) {
-#pragma unroll
-          for (int k = 0; k < L::kStep; ++k) {
-            if (!(have >> k & 1)) continue;
-            const int row = tile_row(v, first_no + k);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = row + (i & 1) + 2 * t + 8 * (i >> 1);
-              if (at < v.first || (at >= v.lo && at < v.len)) seen |= 1u << (4 * k + i);
-            }
-          }
-        }
-        st.step(smem + warp * ST * L::kSlot + slot * L::kSlot, lane, edge, seen);
-        __syncwarp();
-        issue(j + ST, slot);
-        slot = slot + 1 == ST ? 0 : slot + 1;
+      const int t1 = (int)min((int64_t)v.tiles, t0 + (share.end - share.pos));
+      if (tid == 0) share.u = u, share.t0 = t0, share.t1 = t1;  // (read after the barriers within unit_sums)
+      UnitSums<D> o = unit_sums<D, Q4, T>(p, v, share.r, u, t0, t1, smem);
+      const bool begins = share.t0 == 0, ends = share.t1 == v.tiles;
+      if (begins && ends) {
+        write_unit<D, T>(p, share.r, share.u, o);
+      } else {  // a part: slot 1 where the unit begins here, slot 0 where it began before
+        const int64_t slot = (2 * (int64_t)blockIdx.x + begins) * kHeadBlock + tid / 16;
+        store_out(p.rec + slot * D + (tid % 16) * o.N, o.x);
+        if (tid % 16 == 0) p.ref[slot] = make_float2(o.m, o.l);
       }
-      cp_async_wait<0>();
-
-      // ---- the warps' sums, brought to one reference
-      float lsum = st.l;
-      lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
-      lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
-      if (t == 0) warp_ref[warp][g] = make_float2(st.ref, lsum);
-      __syncthreads();  // every warp is through with its ring
-      float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int h = 2 * t + hh;
-        float m = warp_ref[0][h].x;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, warp_ref[w][h].x);
-        const float k = exp2_approx(warp_ref[warp][h].x - m) * st.out_unit();
-        float* row = sums + (warp * kHeadBlock + h) * L::kMergeRow;
-#pragma unroll
-        for (int x = 0; x < W::NB; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            *reinterpret_cast<float2*>(row + W::out_dim(x, y, g)) =
-                make_float2(st.acc[x][y][hh] * k, st.acc[x][y][2 + hh] * k);
+      if (begins && tid == 0) {
+        const int64_t after = share.before * units + (int64_t)(share.u + 1) * v.tiles;  // the next unit's first tile
+        const int more = (int)((after * share.parts - 1) / share.total - blockIdx.x);
+        if (p.cut_by_unit) p.cut[share.r * units + share.u] = make_int4(share.r, share.u, blockIdx.x, more);
+        else if (more) p.cut[blockIdx.x] = make_int4(share.r, share.u, blockIdx.x, more);
+        share.cut |= more;
+      }
+      const bool next = ends && share.u == units - 1;
+      const int64_t now = share.pos + share.t1 - share.t0;
+      int at = share.r;
+      const int64_t past = share.before + v.tiles;
+      if (next && now < share.end && at + 1 < p.n) {
+        do v = query_rows(p, ++at, &bad);
+        while (v.tiles == 0 && at + 1 < p.n);
       }
       __syncthreads();
-      {
-        constexpr int N = D / 16;
-        const int h = tid / 16, e = (tid % 16) * N;
-        float m = warp_ref[0][h].x, ls = 0.f, x[N];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, warp_ref[w][h].x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          ls += warp_ref[w][h].y * exp2_approx(warp_ref[w][h].x - m);
-#pragma unroll
-          for (int i = 0; i < N; i += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(sums + (w * kHeadBlock + h) * L::kMergeRow + e + i);
-            x[i] += y.x, x[i + 1] += y.y, x[i + 2] += y.z, x[i + 3] += y.w;
-          }
-        }
-        if (t0 == 0 && t1 == v.tiles) {
-          if (h < n_heads) {
-            const float k = over(ls);
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] *= k;
-            store_out(static_cast<T*>(p.o) + r * p.o_stride + col + h * D + e, x);
-          }
-        } else {  // a part: slot 1 where the unit begins here, slot 0 where it began before
-          const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0);
-          store_out(p.rec + (slot * kHeadBlock + h) * D + e, x);
-          if (e == 0) p.ref[slot * kHeadBlock + h] = make_float2(m, ls);
-        }
-      }
-      if (t0 == 0) {  // the unit begins here
-        const int64_t last = before * units + (int64_t)(u + 1) * v.tiles - 1;
-        cut = make_int4(r, u, blockIdx.x, (int)(((last + 1) * parts - 1) / total - blockIdx.x));
-        if (p.cut_by_unit && tid == 0) p.cut[r * units + u] = cut;
-      } else {
-        cut.w = 0;
+      if (tid == 0) {
+        share.pos = now;
+        if (next) share.before = past, share.r = at;
       }
       __syncthreads();
-      pos += t1 - t0;
-      if (pos < end && t1 == v.tiles && u == units - 1 && r + 1 < p.n) {
-        before += v.tiles;
-        do v = query_rows(p, ++r, &bad);
-        while (v.tiles == 0 && r + 1 < p.n);
-      }
     }
+    if (!p.cut_by_unit && tid == 0 && !share.cut) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  } else if (!p.cut_by_unit && tid == 0) {
+    p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  if (tid == 0 && !p.cut_by_unit) p.cut[blockIdx.x] = cut;
 }
 
 // Joins the parts of the units that are cut, in their order.  WARPS warps take
@@ -987,20 +1072,37 @@ Workspace workspace_of(int ctas, int head_dim) {
   return w;
 }
 
+// The longest unit, in tiles, of a cache of this shape.
+int64_t longest_unit(const KvAttnParams& p) {
+  const int64_t rows = (int64_t)p.c.max_pages * p.c.page_rows;
+  return p.window ? std::min(rows, (int64_t)p.window + p.sinks) / kTileRows + 3 : (rows + kTileRows - 1) / kTileRows;
+}
+
 template <int D, bool Q4, class T>
-cudaError_t launch_attn_kv(const KvAttnParams& p, int dev, int ctas, cudaStream_t s) {
-  static std::atomic<bool> ready[kMaxDevices];  // the kernel's shared-memory limit has been set on the device
+cudaError_t launch_attn_kv(KvAttnParams p, int dev, int ctas, cudaStream_t s) {
+  static std::atomic<bool> ready[kMaxDevices];  // the kernels' shared-memory limits have been set on the device
   if (!ready[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv_attn<D, Q4, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Tile<D, Q4>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kv_attn<D, Q4, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Tile<D, Q4>::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kv_attn_whole<D, Q4, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Tile<D, Q4>::kSmem);
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
+  const int64_t units = (int64_t)p.n * p.c.nkv * p.head_blocks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreadsA);
   cfg.dynamicSmemBytes = Tile<D, Q4>::kSmem;
   cfg.stream = s;
+  const char* ev = getenv("KV_WHOLE");
+  const int wr = ev ? atoi(ev) : 8;
+  p.grain = getenv("KV_GRAIN") ? atoi(getenv("KV_GRAIN")) : 1;
+  if (longest_unit(p) <= wr * kWarps * Tile<D, Q4>::kStep) {
+    cfg.gridDim = dim3((unsigned)std::min(units, (int64_t)ctas));
+    return cudaLaunchKernelEx(&cfg, kv_attn_whole<D, Q4, T>, p);
+  }
+  cfg.gridDim = dim3(ctas);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn<D, Q4, T>, p);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute pdl = {};
@@ -1011,12 +1113,11 @@ cudaError_t launch_attn_kv(const KvAttnParams& p, int dev, int ctas, cudaStream_
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
   if (!p.cut_by_unit) return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T, 1>, p);
-  const int units = p.n * p.c.nkv * p.head_blocks;
   if (units > ctas / kHeadBlock) {
-    cfg.gridDim = dim3(units);
+    cfg.gridDim = dim3((unsigned)units);
     return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T, 1>, p);
   }
-  cfg.gridDim = dim3(units, std::min(kHeadBlock, p.group));
+  cfg.gridDim = dim3((unsigned)units, std::min(kHeadBlock, p.group));
   return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T, 8>, p);
 }
 
@@ -1039,9 +1140,8 @@ bool rows_overlap(uintptr_t a, int64_t sa, uintptr_t b, int64_t sb, int64_t widt
 
 }  // namespace
 
-extern "C" int dec_kv_attention_workspace(const dec_kv_cache* c, int n, int n_q_heads, size_t* bytes) {
+extern "C" int dec_kv_attention_workspace(const dec_kv_cache* c, size_t* bytes) {
   if (int rc = kv_check(c, false)) return rc;
-  if (int rc = check_attention(c, n, n_q_heads)) return rc;
   if (!bytes) return fail_no_handle(DEC_ERR_ARG, "bytes is NULL");
   int dev = 0, sms = 0;
   if (int rc = device_sms(&dev, &sms)) return rc;

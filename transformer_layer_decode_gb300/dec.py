@@ -108,7 +108,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dec_kv_append": [vp, i32, vp, vp, i32, i64, vp, vp, i32, vp],
         "dec_kv_read": [vp, i32, vp, vp, i32, i64, vp, vp, i32, vp],
         "dec_kv_attention": [vp, i32, vp, vp, i32, i64, i64, vp, i32, i32, i32, i32, f32, vp, sz, vp],
-        "dec_kv_attention_workspace": [vp, i32, i32, vp],
+        "dec_kv_attention_workspace": [vp, vp],
         "dec_kv_extend": [vp, vp, vp, i32, vp],
         "dec_kv_fork": [vp, vp, vp, i32, vp],
         "dec_kv_release": [vp, vp, i32, i32, i32, vp],

@@ -21,6 +21,12 @@ DEC_KV_BAD_INDEX, DEC_KV_NO_PAGES, DEC_KV_BAD_LIST = 1, 2, 4
 FORMATS = {"bf16": DEC_KV_BF16, "q4": DEC_KV_Q4B32}
 _TYPES = {torch.float32: DEC_IO_F32, torch.bfloat16: DEC_IO_BF16}
 
+# what torch.cuda.current_stream(), current_device() and is_current_stream_capturing() ask, without their
+# objects: a decode step makes a few short calls per layer, and the host has to keep ahead of them
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+
 
 class KVCacheDesc(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
@@ -82,12 +88,13 @@ class KVCache:
         if pool.device.type != "cuda":
             raise ValueError("the cache's tensors must be on a CUDA device")
         self.device = pool.device
+        self._index, self._d = pool.device.index, head_dim
         self.pool, self.table, self.lens, self.refs = pool, table, lens, refs
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.scratch = torch.empty(ints.value, dtype=torch.int32, device=self.device)
         for name in ("pool", "table", "lens", "refs", "status", "scratch"):
             setattr(self.desc, name, getattr(self, name).data_ptr())
-        self._workspaces: dict = {}
+        self._workspaces: dict = {}  # of a stream's attention calls, which run one after another
 
     # ---- marshalling ----------------------------------------------------------
 
@@ -113,24 +120,24 @@ class KVCache:
 
     def _rows(self, name, t, heads=None):
         """(address, type, elements from row to row) of a [n, heads, head_dim] tensor with whole rows."""
-        d = self.desc.head_dim
-        if (t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads)
-                or t.dtype not in _TYPES or t.device != self.device
-                or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
-            raise ValueError(f"{name}: a float32 or bfloat16 tensor [n, {heads or 'heads'}, {d}] on {self.device} "
-                             "with contiguous rows is wanted")
-        return t.data_ptr(), _TYPES[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+        shape, d = t.shape, self._d
+        if len(shape) == 3 and shape[2] == d and (heads is None or shape[1] == heads) and t.device == self.device:
+            step, type_ = t.stride(), _TYPES.get(t.dtype)
+            if type_ is not None and step[2] == 1 and (step[1] == d or shape[1] == 1):
+                return t.data_ptr(), type_, step[0] if shape[0] > 1 else shape[1] * d
+        raise ValueError(f"{name}: a float32 or bfloat16 tensor [n, {heads or 'heads'}, {d}] on {self.device} "
+                         "with contiguous rows is wanted")
 
     def _call(self, fn, *args, stream=None):
-        if stream is None:
-            handle = torch.cuda.current_stream(self.device).cuda_stream
-        else:
-            handle = stream if isinstance(stream, int) else stream.cuda_stream
-        if torch.cuda.current_device() == self.device.index:
-            self._check(fn(self._ref, *args, handle))
+        handle = _raw_stream(self._index) if stream is None else \
+            stream if isinstance(stream, int) else stream.cuda_stream
+        if _current_device() == self._index:
+            rc = fn(self._ref, *args, handle)
         else:
             with torch.cuda.device(self.device):
-                self._check(fn(self._ref, *args, handle))
+                rc = fn(self._ref, *args, handle)
+        if rc:
+            self._check(rc)
 
     # ---- rows -----------------------------------------------------------------
 
@@ -165,19 +172,19 @@ class KVCache:
 
     # ---- attention ------------------------------------------------------------
 
-    def workspace(self, n: int, n_q_heads: int):
-        """A workspace for attention calls of up to n queries: one call at a time may use it."""
+    def workspace(self):
+        """A workspace for attention calls on this cache: one call at a time may use it."""
         size = ctypes.c_size_t()
         with torch.cuda.device(self.device):
-            self._check(self.lib.dec_kv_attention_workspace(self._ref, n, n_q_heads, ctypes.byref(size)))
+            self._check(self.lib.dec_kv_attention_workspace(self._ref, ctypes.byref(size)))
         return torch.empty(size.value, dtype=torch.uint8, device=self.device)
 
     def attention(self, layer: int, q, *, seqs=None, window: int = 0, sinks: int = 0, scale: float = 0.0,
                   out=None, workspace=None, stream=None):
         """softmax(scale q K^T) V of one query per entry of seqs over its sequence's visible rows: the last
         `window` ones (0: all) and the first `sinks` ones.  q and out: [n, n_q_heads, head_dim].  Rows of
-        skipped entries keep what out holds (zeros where it is made here).  Without a workspace the call
-        takes one from torch's allocator for the current stream, so `stream` needs one of its own."""
+        skipped entries keep what out holds (zeros where it is made here).  Without a workspace the calls of
+        the current stream share one, and a captured call gets its own; `stream` needs one to be given."""
         qp, qt, qs = self._rows("q", q)
         n, heads = q.shape[0], q.shape[1]
         sp, _ = self._ints("seqs", seqs, n)
@@ -190,12 +197,12 @@ class KVCache:
         if workspace is None:
             if stream is not None:
                 raise ValueError("a call with a stream of its own needs a workspace of its own")
-            size = self._workspaces.get((n, heads))
-            if size is None:
-                workspace = self.workspace(n, heads)
-                self._workspaces[(n, heads)] = workspace.numel()
+            if _capturing():  # a graph keeps its own: it may be replayed beside other calls
+                workspace = self.workspace()
             else:
-                workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+                workspace = self._workspaces.get(_raw_stream(self._index))
+                if workspace is None:
+                    workspace = self._workspaces[_raw_stream(self._index)] = self.workspace()
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"workspace: contiguous memory on {self.device} is wanted")
         self._call(self.lib.dec_kv_attention, layer, qp, op, qt, qs, os_, sp, n, heads, window, sinks, scale,
