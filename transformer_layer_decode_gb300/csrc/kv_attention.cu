@@ -2,7 +2,6 @@
 // cache, bf16 or in 4-bit blocks, with a sliding window and first rows that
 // stay visible.
 #include <atomic>
-#include <cstdlib>
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -59,7 +58,7 @@ struct KvAttnParams {
   float* rec;              // [2 * CTAs][8][D]: sums of units cut between CTAs
   float2* ref;             // [2 * CTAs][8]: reference and sum of the weights
   int4* cut;               // [CTAs]: query, unit, CTA where it begins, CTAs that it goes on for
-  int ctas, grain;
+  int ctas;
   int cut_by_unit;         // cut is indexed by unit (there are no more of them than CTAs), not by CTA
 };
 
@@ -345,14 +344,14 @@ struct WarpBf16 : WarpSums<D> {
 // number of values.  So the codes enter the products with as little unpacking
 // as can be exact.
 //  - K: a nibble n where it lies in a 16-bit word is the fp16 number n 2^-24,
-//    or n 2^-20 four bits up (against q / 16): an AND, no conversion.  The
-//    8 that codes are stored with is taken off by one more product per 8 rows,
+//    or n 2^-20 four bits up (against q / 16): an AND, no conversion.  The 8
+//    that codes are stored with is taken off by one more product per 8 rows,
 //    of the block scales with -8 * (sum of q over the block).
 //  - V: 1024 + n or 1024 + 16 n by an OR, and n - 8 by one addition or FMA.
 //  - K's block scales multiply the fp32 sums over a block, V's the weights.
 // q is scaled by a power of two and taken in two fp16 pieces (22 bits; bf16 q
-// needs one), and so are weight * scale for fp32 results; for bf16 results
-// these are one fp16 number (11 bits, against the 8 of the results).
+// needs one), and so is weight * scale for fp32 results; for bf16 results it
+// is one fp16 number (11 bits, against the 8 of the results).
 template <int D, class T>
 struct WarpQ4 : WarpSums<D> {
   using Sums = WarpSums<D>;
@@ -362,7 +361,10 @@ struct WarpQ4 : WarpSums<D> {
   // The largest weight is 2^lift to 2^(lift + kSlack), so that its product with
   // a scale stays below 2^15 and the others well above fp16's smallest step.
   static constexpr float kLift = 9.f;
-  uint32_t a[2 * NB][kWhole ? 2 : 4];  // q
+  // q: both pieces, whole operands of the products as they lie in registers (for
+  // bf16 q the second is zero, which must not be known: zeros would be moved
+  // into place before every product)
+  uint32_t a[2 * NB][4];
   uint32_t bias[2];                    // -8 sum of q per block, in three pieces: operand of one product
   float f;                             // score = f * product, in log2 units
   float top;                           // V scales seen are below top = 2^e
@@ -382,33 +384,30 @@ struct WarpQ4 : WarpSums<D> {
       for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[b][i]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // q to below 2^14
     const int e = (int)(__float_as_uint(mx) >> 23) - 126;  // mx < 2^e
-    const int sh = min(14 - e, 120);
+    const int sh = min(14 - e, 120);                       // q to below 2^14
     const float up = __uint_as_float((uint32_t)(127 + max(sh, -120)) << 23);
     f = scale * __uint_as_float((uint32_t)(127 + min(24 - sh, 127)) << 23);
+    if (!(mx < INFINITY)) f = __uint_as_float(0x7fffffffu);  // an infinity in q: NaN
     uint32_t piece[3][NB / 2];
     float sums[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float sum = 0.f;
 #pragma unroll
+      for (int i = 0; i < 8; ++i) x[b][i] *= up;
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t(&w)[kWhole ? 2 : 4] = a[2 * b + h];
+        uint32_t(&w)[4] = a[2 * b + h];
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {
           const float part = odd ? 1.f / 16 : 1.f;
-          float y0 = x[b][2 * h + odd] * up * part, y1 = x[b][4 + 2 * h + odd] * up * part;
+          float y0 = x[b][2 * h + odd] * part, y1 = x[b][4 + 2 * h + odd] * part;
           const uint32_t hi = take_f16(y0, y1), lo = pack_f16(y0, y1);
           const float2 u = unpack_f16(hi), r = unpack_f16(lo);
-          if constexpr (kWhole) {
-            w[odd] = hi;
-            sum += (u.x + u.y) * (odd ? 16.f : 1.f);
-          } else {
-            w[2 * odd] = hi;
-            w[2 * odd + 1] = lo;
-            sum += ((u.x + r.x) + (u.y + r.y)) * (odd ? 16.f : 1.f);
-          }
+          w[2 * odd] = hi;
+          w[2 * odd + 1] = lo;
+          sum += ((u.x + r.x) + (u.y + r.y)) * (odd ? 16.f : 1.f);
         }
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -460,7 +459,6 @@ struct WarpQ4 : WarpSums<D> {
   __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t rows_seen) {
     const int g = lane >> 2, t = lane & 3;
     float s[4 * kTiles];
-    __half2 vs[4 * kTiles][NB / 2];  // V's scales of the lane's rows
     __half2 most = __float2half2_rn(0.f);  // the largest of all, between the lanes
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) {
@@ -481,31 +479,24 @@ struct WarpQ4 : WarpSums<D> {
           const uint4 u = *reinterpret_cast<const uint4*>(sk + staged<D, true>(8 * b + g, t));
           w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
           *reinterpret_cast<uint4*>(ks) = *reinterpret_cast<const uint4*>(ks_at + 64 * b + 16 * t);
-          *reinterpret_cast<uint4*>(vs[4 * k + 2 * b]) = *reinterpret_cast<const uint4*>(vs_at + 64 * b + 16 * t);
           row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 64 * b + 8 * g + 4 * (t & 1));
         } else {
           const uint2 u = *reinterpret_cast<const uint2*>(sk + staged<D, true>(8 * b + g, t >> 1) + 8 * (t & 1));
           w[0] = u.x, w[1] = u.y;
           *reinterpret_cast<uint2*>(ks) = *reinterpret_cast<const uint2*>(ks_at + 32 * b + 8 * t);
-          *reinterpret_cast<uint2*>(vs[4 * k + 2 * b]) = *reinterpret_cast<const uint2*>(vs_at + 32 * b + 8 * t);
           row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 32 * b + 4 * g);
         }
         float z[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(z, bias[0], 0, bias[1], 0, row_scales, row_scales);
+        mma_f16(z, bias[0], bias[0], bias[1], bias[1], row_scales, row_scales);  // (rows 8-15 are not used)
         float s0 = z[0] * (1.f / (1 << 14)), s1 = z[1] * (1.f / (1 << 14));
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
           const uint32_t x = __byte_perm(w[j >> 1], w[NB / 2 + (j >> 1)], j & 1 ? 0x7632 : 0x5410);
           const uint32_t y = x >> 8;
-          if constexpr (kWhole) {
-            mma_f16(c, a[2 * j][0], 0, a[2 * j][1], 0, x & 0x000f000fu, x & 0x00f000f0u);
-            mma_f16(c, a[2 * j + 1][0], 0, a[2 * j + 1][1], 0, y & 0x000f000fu, y & 0x00f000f0u);
-          } else {
-            mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], x & 0x000f000fu, x & 0x00f000f0u);
-            mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], y & 0x000f000fu,
-                    y & 0x00f000f0u);
-          }
+          mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], x & 0x000f000fu, x & 0x00f000f0u);
+          mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], y & 0x000f000fu,
+                  y & 0x00f000f0u);
           const float k0 = __half2float(j & 1 ? __high2half(ks[0][j >> 1]) : __low2half(ks[0][j >> 1]));
           const float k1 = __half2float(j & 1 ? __high2half(ks[1][j >> 1]) : __low2half(ks[1][j >> 1]));
           s0 = fmaf(k0, kWhole ? c[0] : c[0] + c[2], s0);
@@ -521,11 +512,7 @@ struct WarpQ4 : WarpSums<D> {
         const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!(seen >> i & 1)) {
-            s[4 * k + i] = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < NB / 2; ++j) vs[4 * k + i][j] = __float2half2_rn(0.f);
-          }
+          if (!(seen >> i & 1)) s[4 * k + i] = -INFINITY;
       }
     }
     float mx = s[0];
@@ -546,6 +533,23 @@ struct WarpQ4 : WarpSums<D> {
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) {
       const uint8_t* sv = st + k * L::kBytes + L::kHalf;
+      const uint8_t* vs_at = sv + kTileRows * L::kRowBytes;
+      __half2 vs[4][NB / 2];  // V's scales of the lane's rows
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if constexpr (D == 128)
+          *reinterpret_cast<uint4*>(vs[2 * b]) = *reinterpret_cast<const uint4*>(vs_at + 64 * b + 16 * t);
+        else *reinterpret_cast<uint2*>(vs[2 * b]) = *reinterpret_cast<const uint2*>(vs_at + 32 * b + 8 * t);
+      }
+      if (edge) {  // 0 * NaN would be NaN
+        const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!(seen >> i & 1)) {
+#pragma unroll
+            for (int j = 0; j < NB / 2; ++j) vs[i][j] = __float2half2_rn(0.f);
+          }
+      }
       uint32_t v[4][NB / 2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -573,7 +577,7 @@ struct WarpQ4 : WarpSums<D> {
         uint32_t pw[kPieces][2];  // weight * scale: rows 2t, 2t + 1 of each half
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const __half2 h0 = vs[4 * k + 2 * b][j >> 1], h1 = vs[4 * k + 2 * b + 1][j >> 1];
+          const __half2 h0 = vs[2 * b][j >> 1], h1 = vs[2 * b + 1][j >> 1];
           if constexpr (kWhole) {
             const __half2 both = j & 1 ? __highs2half2(h0, h1) : __lows2half2(h0, h1);
             const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&ph[b]), both);
@@ -648,6 +652,11 @@ __device__ __forceinline__ void store_out(T* p, const float (&x)[N]) {
 // The sum over no weight is zero; NaN stays.
 __device__ __forceinline__ float over(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
+// What a unit costs a CTA besides its tiles (page numbers, q, the sums of the
+// warps: about 2.5 us, a few rounds of the warps), in rounds; and the rounds up
+// to which a unit is not cut.
+constexpr int kUnitRounds = 3, kShortRounds = 5;
+
 // What a thread holds of a unit's sums over a CTA's tiles: N dimensions from e
 // of head h, relative to the reference m, and the sum of the weights.
 template <int D>
@@ -674,8 +683,9 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
   const int nt = (t1 - t0) / kRound * L::kStep + min(max((t1 - t0) % kRound - warp * L::kStep, 0), L::kStep);
   const uint32_t ring = smem_u32(smem) + warp * ST * L::kSlot;
   const int32_t* table = c.table + (int64_t)v.seq * c.max_pages;
-  unsigned long long cur_src = 0, nxt_src = 0;  // K rows of a tile; 0: none
-  int cur_scales = 0, nxt_scales = 0;
+  // K rows of a tile, and how far behind its scales are; -1: there is none
+  unsigned long long cur_src = 0, nxt_src = 0;
+  int cur_scales = -1, nxt_scales = -1;
   bool doubt = false;  // a tile had no page
   auto tile_no = [&](int i) { return t0 + warp * L::kStep + i / L::kStep * kRound + i % L::kStep; };
   auto page_of = [&](int row) {
@@ -684,7 +694,8 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
   };
   auto fetch = [&](int i0) {  // where the warp's tiles i0 .. i0 + 31 lie, one per lane
     const int i = i0 + lane;
-    nxt_src = 0;
+    nxt_src = reinterpret_cast<unsigned long long>(c.pool);
+    nxt_scales = -1;
     if (i < nt) {
       const int at = tile_row(v, tile_no(i)), page = page_of(at), row = at % c.page_rows;
       if (page >= 0) {
@@ -704,13 +715,15 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
       fetch(j * L::kStep + 32);
       doubt = __any_sync(0xffffffffu, doubt);
     }
+    if (j * L::kStep < nt) {
 #pragma unroll
-    for (int k = 0; k < L::kStep; ++k) {
-      const int i = (j * L::kStep + k) & 31;
-      const unsigned long long src = __shfl_sync(0xffffffffu, cur_src, i);
-      const int scales = Q4 ? __shfl_sync(0xffffffffu, cur_scales, i) : 0;
-      stage_tile<D, Q4>(dst + k * L::kBytes, src ? reinterpret_cast<const uint8_t*>(src) : c.pool, src ? scales : 0,
-                        src ? c.half_bytes : 0, lane, src ? 16 : 0);
+      for (int k = 0; k < L::kStep; ++k) {
+        const int i = (j * L::kStep + k) & 31;
+        const unsigned long long src = __shfl_sync(0xffffffffu, cur_src, i);
+        const int scales = __shfl_sync(0xffffffffu, cur_scales, i);
+        stage_tile<D, Q4>(dst + k * L::kBytes, reinterpret_cast<const uint8_t*>(src), max(scales, 0), c.half_bytes, lane,
+                          scales < 0 ? 0 : 16);
+      }
     }
     cp_async_commit();
   };
@@ -821,11 +834,13 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm)
   }
 }
 
-// A CTA's share of the line of tiles and where it stands in it.
+// A CTA's share of the line and where it stands in it.  The line is all units
+// in order, each as long as its tiles and kUnitRounds rounds more, which come
+// first.
 struct Share {
-  int64_t pos, end;      // tile positions, of all units
-  int64_t before;        // tiles of the queries before r
-  int64_t total, parts;  // positions and shares of the whole line
+  int64_t pos, end;      // positions in the line
+  int64_t before;        // the length of one unit each of the queries before r
+  int64_t total, parts;  // length and shares of the whole line
   int r, u, t0, t1;      // the unit at hand
   int cut;               // a unit begins here that ends elsewhere
 };
@@ -839,11 +854,12 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
   const KvView& c = p.c;
   pdl_trigger();
 
-  // ---- this CTA's share of the line of tiles
+  // ---- this CTA's share of the line
+  constexpr int kRound = kWarps * L::kStep, kUnit = kUnitRounds * kRound;
   const int chunks = (p.n + kChunkRows - 1) / kChunkRows;
   const int units = c.nkv * p.head_blocks;
   bool bad = false, empty = false;
-  int mine[4];  // tiles of queries 32 i + lane of a chunk
+  int mine[4];  // the lengths of units of queries 32 i + lane of a chunk
   auto count = [&](int chunk) {
     int64_t sum = 0;
 #pragma unroll
@@ -851,24 +867,24 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       const int r = chunk * kChunkRows + 32 * i + lane;
       Rows v{-1, 0, 0, 0, 0, 0, 0};
       if (r < p.n) v = query_rows(p, r, &bad);
-      mine[i] = v.tiles;
-      sum += v.tiles;
+      mine[i] = v.tiles ? v.tiles + kUnit : 0;
+      sum += mine[i];
       empty |= r < p.n && v.tiles == 0;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
   };
-  int64_t tiles = 0;
+  int64_t length = 0;
   if (chunks == 1) {
-    tiles = count(0);  // every warp for itself
+    length = count(0);  // every warp for itself
   } else {
     for (int k = warp; k < chunks; k += kWarps) {
       const int64_t sum = count(k);
       if (lane == 0) chunk_tiles[k] = sum;
     }
     __syncthreads();
-    for (int k = 0; k < chunks; ++k) tiles += chunk_tiles[k];
+    for (int k = 0; k < chunks; ++k) length += chunk_tiles[k];
   }
   if (bad && blockIdx.x == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
   if (__syncthreads_or(empty)) {  // queries that see no row, or are skipped
@@ -882,50 +898,73 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       for (int64_t e = tid; e < (int64_t)p.nq * D; e += kThreadsA) out[e] = 0;
     }
   }
-  const int64_t total = tiles * units;
-  // As many shares as there are CTAs, but none without work, and beyond one per
-  // unit only while each keeps all warps busy: a share pays for its queries,
-  // its page numbers and its sums (about 2.5 us a unit) however short it is.
-  constexpr int kRound = kWarps * L::kStep;
-  const int64_t grain = kRound * p.grain;
-  const int64_t parts = min(min((int64_t)gridDim.x, total), max((total + grain - 1) / grain, (int64_t)p.n * units));
+  const int64_t total = length * units;
+  // One share per CTA; small ones of whole rounds, so that every warp has as much.
+  const int64_t rounds = (total + (int64_t)gridDim.x * kRound - 1) / ((int64_t)gridDim.x * kRound);
+  const int64_t parts = rounds > 3 ? gridDim.x : total / (max(rounds, (int64_t)1) * kRound);
   __shared__ Share share;  // (not in registers: the products need them)
   if (blockIdx.x < parts) {
-    // the query that holds the share's first tile
-    const int64_t pos = total * blockIdx.x / parts, want = pos / units;
-    int64_t before = 0;
-    int r = 0, k = 0;
-    if (chunks > 1) {
-      while (before + chunk_tiles[k] <= want) before += chunk_tiles[k++];
-      count(k);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int64_t incl = mine[i];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+    // The border between two shares is moved to the nearer end of a unit that
+    // is short, in itself or beside a share, and to an end of a long one that
+    // is less than a round off.
+    const int64_t shortest = max((int64_t)kShortRounds * kRound, total / parts / 16) + kUnit;
+    int64_t before;
+    int r, r_len;
+    auto locate = [&](int64_t want) {  // the query with position `want` of the line
+      want /= units;
+      before = 0;
+      r = r_len = 0;
+      int k = 0;
+      if (chunks > 1) {
+        while (k + 1 < chunks && before + chunk_tiles[k] <= want) before += chunk_tiles[k++];
+        count(k);
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + incl > want);
-      if (past) {
-        const int at = __ffs(past) - 1;
-        before += __shfl_sync(0xffffffffu, incl - mine[i], at);
-        r = k * kChunkRows + 32 * i + at;
-        break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int64_t incl = mine[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + incl > want);
+        if (past) {
+          const int at = __ffs(past) - 1;
+          r_len = __shfl_sync(0xffffffffu, mine[i], at);
+          before += __shfl_sync(0xffffffffu, incl, at) - r_len;
+          r = k * kChunkRows + 32 * i + at;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
       }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (tid == 0) share = Share{pos, total * (blockIdx.x + 1) / parts, before, total, parts, r, 0, 0, 0, 0};
+    };
+    auto border = [&](int64_t part) {  // where share `part` begins
+      int64_t pos = total * part / parts;
+      if (pos < total) {
+        locate(pos);
+        if (r_len > 0) {
+          const int in = (int)((pos - before * units) % r_len);
+          if (r_len <= shortest) pos += 2 * in < r_len ? -in : r_len - in;
+          else if (in < kUnit + kRound) pos -= in;
+          else if (in > r_len - kRound) pos += r_len - in;
+        }
+      }
+      return pos;
+    };
+    const int64_t end = border(blockIdx.x + 1), pos = border(blockIdx.x);
+    if (pos < end && pos >= (before + r_len) * units) locate(pos);  // moved on to the next query
+    if (tid == 0) share = Share{pos, end, before, total, parts, r, 0, 0, 0, 0};
     __syncthreads();
     Rows v = query_rows(p, r, &bad);
 
     while (share.pos < share.end) {
       const int64_t rel = share.pos - share.before * units;
+      const int len = v.tiles + kUnit;
       // (not so only if lengths change while the call runs: then leave, in bounds)
-      if (rel < 0 || rel >= (int64_t)v.tiles * units) break;
-      const int u = (int)(rel / v.tiles), t0 = (int)(rel - (int64_t)u * v.tiles);
-      const int t1 = (int)min((int64_t)v.tiles, t0 + (share.end - share.pos));
+      if (v.tiles == 0 || rel < 0 || rel >= (int64_t)len * units) break;
+      const int u = (int)(rel / len), in = (int)(rel - (int64_t)u * len);
+      const int t0 = max(in - kUnit, 0);
+      const int t1 = max((int)min((int64_t)len, in + (share.end - share.pos)) - kUnit, t0);
       if (tid == 0) share.u = u, share.t0 = t0, share.t1 = t1;  // (read after the barriers within unit_sums)
       UnitSums<D> o = unit_sums<D, Q4, T>(p, v, share.r, u, t0, t1, smem);
       const bool begins = share.t0 == 0, ends = share.t1 == v.tiles;
@@ -937,16 +976,20 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
         if (tid % 16 == 0) p.ref[slot] = make_float2(o.m, o.l);
       }
       if (begins && tid == 0) {
-        const int64_t after = share.before * units + (int64_t)(share.u + 1) * v.tiles;  // the next unit's first tile
-        const int more = (int)((after * share.parts - 1) / share.total - blockIdx.x);
+        int more = 0;  // borders within the unit
+        if (!ends) {
+          const int64_t first = share.before * units + (int64_t)share.u * (v.tiles + kUnit);
+          auto owner = [&](int64_t x) { return ((x + 1) * share.parts - 1) / share.total; };
+          more = (int)(owner(first + v.tiles + kUnit - kRound) - owner(first + kUnit + kRound - 1));
+        }
         if (p.cut_by_unit) p.cut[share.r * units + share.u] = make_int4(share.r, share.u, blockIdx.x, more);
         else if (more) p.cut[blockIdx.x] = make_int4(share.r, share.u, blockIdx.x, more);
         share.cut |= more;
       }
       const bool next = ends && share.u == units - 1;
-      const int64_t now = share.pos + share.t1 - share.t0;
+      const int64_t now = share.before * units + (int64_t)share.u * (v.tiles + kUnit) + kUnit + share.t1;
+      const int64_t past = share.before + v.tiles + kUnit;
       int at = share.r;
-      const int64_t past = share.before + v.tiles;
       if (next && now < share.end && at + 1 < p.n) {
         do v = query_rows(p, ++at, &bad);
         while (v.tiles == 0 && at + 1 < p.n);
@@ -1039,6 +1082,8 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 }
 
 constexpr int kMaxDevices = 64;
+// Where no unit can be longer than so many rounds of a CTA's warps, each is left to one CTA.
+constexpr int kWholeRounds = 6;
 
 // SMs of the current device (they do not change: looked up once).
 int device_sms(int* dev, int* sms) {
@@ -1095,10 +1140,7 @@ cudaError_t launch_attn_kv(KvAttnParams p, int dev, int ctas, cudaStream_t s) {
   cfg.blockDim = dim3(kThreadsA);
   cfg.dynamicSmemBytes = Tile<D, Q4>::kSmem;
   cfg.stream = s;
-  const char* ev = getenv("KV_WHOLE");
-  const int wr = ev ? atoi(ev) : 8;
-  p.grain = getenv("KV_GRAIN") ? atoi(getenv("KV_GRAIN")) : 1;
-  if (longest_unit(p) <= wr * kWarps * Tile<D, Q4>::kStep) {
+  if (longest_unit(p) <= kWholeRounds * kWarps * Tile<D, Q4>::kStep) {
     cfg.gridDim = dim3((unsigned)std::min(units, (int64_t)ctas));
     return cudaLaunchKernelEx(&cfg, kv_attn_whole<D, Q4, T>, p);
   }
