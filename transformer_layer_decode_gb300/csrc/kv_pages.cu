@@ -15,6 +15,8 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;
+constexpr int kCopyPiece = kCopyThreads * 16 * kCopyUnroll;  // 16 KB
 
 // Words of the scratch head.
 enum { SC_OK = 0, SC_MOVES = 1, SC_LIVE = 2 };
@@ -51,20 +53,44 @@ __device__ __forceinline__ int kv_len(const KvView& c, int s) {
   return n >= 0 && n <= c.max_pages * c.page_rows ? n : -1;
 }
 
+// Calls f(page, k-th of its kind, k-th of its kind) ... for every page in order:
+// kind(page) puts a page into neither, the first or the second of two kinds (0,
+// 1, 2), and f(page, kind, rank) gets its rank among those of its kind.  Four
+// pages a thread at a time; stops once `enough` of the first kind are found.
+// The counts of both kinds are returned to every thread.
+template <class Kind, class F>
+__device__ int2 rank_pages(int n_pages, int enough, Kind kind, F f) {
+  int2 found = make_int2(0, 0);
+  for (int base = 0; base < n_pages && found.x < enough; base += 4 * kPlanThreads) {
+    int kinds[4], mine = 0;  // counts of both kinds in 16 bits each (at most 4096)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = base + 4 * threadIdx.x + i;
+      kinds[i] = p < n_pages ? kind(p) : 0;
+      mine += kinds[i] == 1 ? 1 : kinds[i] == 2 ? 1 << 16 : 0;
+    }
+    int total;
+    int at = block_scan(mine, &total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = base + 4 * threadIdx.x + i;
+      if (p < n_pages) f(p, kinds[i], kinds[i] == 1 ? found.x + (at & 0xffff) : found.y + (at >> 16));
+      at += kinds[i] == 1 ? 1 : kinds[i] == 2 ? 1 << 16 : 0;
+    }
+    found.x += total & 0xffff;
+    found.y += total >> 16;
+  }
+  __syncthreads();
+  return found;
+}
+
 // Lists the `need` lowest free pages in the scratch; false if there are fewer.
 __device__ bool find_free(const KvView& c, int need) {
   int32_t* list = c.scratch + kKvScratchHead;
-  int found = 0;
-  for (int base = 0; base < c.n_pages && found < need; base += kPlanThreads) {
-    const int p = base + threadIdx.x;
-    const int f = p < c.n_pages && c.refs[p] <= 0;
-    int total;
-    const int at = found + block_scan(f, &total);
-    if (f && at < need) list[at] = p;
-    found += total;
-  }
-  __syncthreads();
-  return found >= need;
+  return rank_pages(c.n_pages, need, [&](int p) { return c.refs[p] <= 0 ? 1 : 0; },
+                    [&](int p, int kind, int rank) {
+                      if (kind && rank < need) list[rank] = p;
+                    }).x >= need;
 }
 
 // FORK: a = parents, b = children.  Otherwise extend: a = sequences, b = rows to add.
@@ -72,6 +98,7 @@ template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_alloc(KvView c, const int32_t* a, const int32_t* b, int n) {
   __shared__ uint32_t seen[65536 / 32];
   __shared__ int bad_bits;
+  if (FORK) pdl_trigger();
   const int tid = threadIdx.x;
   int32_t* offsets = c.scratch + kv_scratch_offsets(c.n_pages, c.n_seqs);
   int32_t* moves = c.scratch + kv_scratch_moves(c.n_pages);
@@ -176,30 +203,22 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_alloc(KvView c, const in
 // Ranks the live pages from `live` on against the free pages below it, renames
 // them in refs and lists the copies.
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_compact(KvView c) {
+  pdl_trigger();
   const int tid = threadIdx.x;
   int32_t* name = c.scratch + kKvScratchHead;
   int32_t* moves = c.scratch + kv_scratch_moves(c.n_pages);
-  int live = 0;
-  for (int base = 0; base < c.n_pages; base += kPlanThreads) {
-    const int p = base + tid;
-    int total;
-    block_scan(p < c.n_pages && c.refs[p] > 0, &total);
-    live += total;
-  }
-  int holes = 0, movers = 0;
-  for (int base = 0; base < c.n_pages; base += kPlanThreads) {
-    const int p = base + tid;
-    const bool used = p < c.n_pages && c.refs[p] > 0;
-    const int hole = p < live && !used, mover = p >= live && used;  // (p < live <= n_pages)
-    int total;
-    const int at = block_scan(hole | mover << 16, &total);
-    if (hole) moves[2 * (holes + (at & 0xffff)) + 1] = p;
-    if (mover) moves[2 * (movers + (at >> 16))] = p;
-    if (p < c.n_pages) name[p] = used && !mover ? p : -1;
-    holes += total & 0xffff;
-    movers += total >> 16;
-  }
-  __syncthreads();
+  const int all = 0x7fffffff;
+  const int live = rank_pages(c.n_pages, all, [&](int p) { return c.refs[p] > 0 ? 1 : 0; }, [](int, int, int) {}).x;
+  const int movers = rank_pages(
+      c.n_pages, all,
+      [&](int p) {
+        const bool used = c.refs[p] > 0;
+        return p < live ? (used ? 0 : 1) : (used ? 2 : 0);
+      },
+      [&](int p, int kind, int rank) {
+        if (kind) moves[2 * rank + (kind == 1)] = p;
+        name[p] = kind == 0 && p < live ? p : -1;  // (those that move get theirs below)
+      }).y;
   for (int k = tid; k < movers; k += kPlanThreads) {
     const int from = moves[2 * k], to = moves[2 * k + 1];
     c.refs[to] = c.refs[from];
@@ -219,6 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_compact(KvView c) {
 template <bool FORK>
 __global__ void __launch_bounds__(kCopyThreads) kv_apply(KvView c, const int32_t* parents, const int32_t* children,
                                                          int n, int n_layers) {
+  pdl_wait();
   if (!c.scratch[SC_OK]) return;
   const int64_t thread = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
   const int64_t threads = (int64_t)gridDim.x * kCopyThreads;
@@ -250,14 +270,25 @@ __global__ void __launch_bounds__(kCopyThreads) kv_apply(KvView c, const int32_t
       else if (now != page) c.table[e] = now;
     }
   }
+  // Pieces of kCopyPiece bytes of a page, in turn: 64 bytes a thread under way.
   const int32_t* moves = c.scratch + kv_scratch_moves(c.n_pages);
-  const int64_t words = c.page_bytes / 16, total = (int64_t)c.scratch[SC_MOVES] * n_layers * words;
-  for (int64_t e = thread; e < total; e += threads) {
-    const int64_t w = e % words, r = e / words;
-    const int64_t layer = r % n_layers, m = r / n_layers;
-    const int from = moves[2 * m], to = moves[2 * m + 1];
-    uint8_t* base = c.pool + layer * c.n_pages * c.page_bytes;
-    reinterpret_cast<uint4*>(base + to * c.page_bytes)[w] = reinterpret_cast<const uint4*>(base + from * c.page_bytes)[w];
+  const uint32_t pieces = (uint32_t)((c.page_bytes + kCopyPiece - 1) / kCopyPiece);
+  const int64_t total = (int64_t)c.scratch[SC_MOVES] * n_layers * pieces;
+  for (int64_t e = blockIdx.x; e < total; e += gridDim.x) {
+    const uint32_t piece = (uint32_t)(e % pieces);
+    const int64_t rest = e / pieces;
+    const int layer = (int)(rest % n_layers), m = (int)(rest / n_layers);
+    uint8_t* pages = c.pool + (int64_t)layer * c.n_pages * c.page_bytes;
+    const int64_t at = (int64_t)piece * kCopyPiece + 16 * threadIdx.x;
+    const uint8_t* from = pages + moves[2 * m] * c.page_bytes + at;
+    uint8_t* to = pages + moves[2 * m + 1] * c.page_bytes + at;
+    uint4 w[kCopyUnroll];
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (at + i * 16 * kCopyThreads < c.page_bytes) w[i] = __ldcs(reinterpret_cast<const uint4*>(from + i * 16 * kCopyThreads));
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (at + i * 16 * kCopyThreads < c.page_bytes) __stcs(reinterpret_cast<uint4*>(to + i * 16 * kCopyThreads), w[i]);
   }
 }
 
@@ -292,6 +323,18 @@ cudaLaunchConfig_t config(int64_t ctas, int threads, dec_stream_t stream) {
   cfg.blockDim = dim3(threads);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   return cfg;
+}
+
+// The launch that carries out a plan: it may begin before the plan's ends, and waits for it.
+template <class... Args>
+cudaError_t launch_after(void (*kernel)(Args...), int64_t ctas, dec_stream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = config(ctas, kCopyThreads, stream);
+  cudaLaunchAttribute pdl = {};
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 int sm_count(int* n) {
@@ -330,9 +373,9 @@ extern "C" int dec_kv_fork(const dec_kv_cache* c, const int32_t* parents, const 
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
   const KvView v = kv_view(*c, 0);
-  const cudaLaunchConfig_t plan = config(1, kPlanThreads, stream), apply = config(8 * sms, kCopyThreads, stream);
+  const cudaLaunchConfig_t plan = config(1, kPlanThreads, stream);
   if (int rc = launched(cudaLaunchKernelEx(&plan, kv_plan_alloc<true>, v, parents, children, n))) return rc;
-  return launched(cudaLaunchKernelEx(&apply, kv_apply<true>, v, parents, children, n, c->n_layers));
+  return launched(launch_after(kv_apply<true>, 8 * sms, stream, v, parents, children, n, (int)c->n_layers));
 }
 
 extern "C" int dec_kv_release(const dec_kv_cache* c, const int32_t* seqs, int n, int window, int sinks,
@@ -349,8 +392,8 @@ extern "C" int dec_kv_compact(const dec_kv_cache* c, dec_stream_t stream) {
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
   const KvView v = kv_view(*c, 0);
-  const cudaLaunchConfig_t plan = config(1, kPlanThreads, stream), apply = config(8 * sms, kCopyThreads, stream);
+  const cudaLaunchConfig_t plan = config(1, kPlanThreads, stream);
   if (int rc = launched(cudaLaunchKernelEx(&plan, kv_plan_compact, v))) return rc;
-  return launched(cudaLaunchKernelEx(&apply, kv_apply<false>, v, (const int32_t*)nullptr, (const int32_t*)nullptr, 0,
-                                     c->n_layers));
+  return launched(launch_after(kv_apply<false>, 8 * sms, stream, v, (const int32_t*)nullptr, (const int32_t*)nullptr, 0,
+                               (int)c->n_layers));
 }

@@ -60,117 +60,161 @@ KvView kv_view(const dec_kv_cache& c, int layer) {
 namespace {
 
 constexpr int kRowWarps = 8;  // warps of a CTA of the row kernels
+constexpr int kRowRounds = 4; // rounds of a warp: rows whose loads are under way together
 
-// Four fp32 values from / to the caller's type.
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-  const float4 w = *reinterpret_cast<const float4*>(p);
-  x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+// Eight fp32 values from / to the caller's type.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 u = reinterpret_cast<const float4*>(p)[0], w = reinterpret_cast<const float4*>(p)[1];
+  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
 }
-__device__ __forceinline__ void load4(const uint16_t* p, float (&x)[4]) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  x[0] = bf16lo(u.x), x[1] = bf16hi(u.x), x[2] = bf16lo(u.y), x[3] = bf16hi(u.y);
+  x[4] = bf16lo(u.z), x[5] = bf16hi(u.z), x[6] = bf16lo(u.w), x[7] = bf16hi(u.w);
 }
-__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-__device__ __forceinline__ void store4(uint16_t* p, const float (&x)[4]) {
-  uint2 w;
-  w.x = f32_to_bf16_bits(x[0]) | (uint32_t)f32_to_bf16_bits(x[1]) << 16;
-  w.y = f32_to_bf16_bits(x[2]) | (uint32_t)f32_to_bf16_bits(x[3]) << 16;
-  *reinterpret_cast<uint2*>(p) = w;
+__device__ __forceinline__ uint32_t pair(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// The code of x for a scale s > 0: the integer nearest to x / s, ties to even.
-// The fp32 quotient can only err where it lands on a half: there the sign of
-// x - (q +- 0.5) s, which one FMA gives exactly, decides.
-__device__ __forceinline__ int q4_code(float x, float s) {
-  float q = rintf(__fdiv_rn(x, s));
-  if (fmaf(-(q + 0.5f), s, x) > 0.f) q += 1.f;
-  else if (fmaf(-(q - 0.5f), s, x) < 0.f) q -= 1.f;
-  return (int)fminf(fmaxf(q, -8.f), 7.f);
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pair(x[0], x[1]), pair(x[2], x[3]), pair(x[4], x[5]), pair(x[6], x[7]));
 }
 
-// The page row a token goes to, or null (with the status bit set where that is an error).
-__device__ __forceinline__ uint8_t* kv_token_row(const KvView& c, const int32_t* seqs,
-                                                 const int32_t* positions, int t, int which, int head,
-                                                 int* row) {
-  const int s = seqs ? seqs[t] : t;
-  if (s < 0) return nullptr;
-  int page = -1;
+// Codes plus 8 of eight values for a scale s > 0, four bits each, lowest first:
+// the integers nearest to x / s, ties to even, within [-8, 7].  r = x * (1 / s)
+// is off by a few 2^-24 of itself, so its nearest integer q is the answer or,
+// next to a half, a neighbour; the remainder e = x - q s is exact (it has no
+// bits below x's and is below s), and |e| against s / 2 decides: past it, or on
+// it with q odd, q moves one on.  EDGE: also for scales so small or so large
+// that |x / s| passes 7.5 (s below fp16's normal numbers, or at its top).
+template <bool EDGE>
+__device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], float s) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+  const float inv = 1.f / s;
+  const int half = __float_as_int(0.5f * s);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float r = x[i] * inv;
+    if (EDGE) r = fminf(fmaxf(r, -8.f), 7.f);
+    const float m = r + kMagic, e = fmaf(-(m - kMagic), s, x[i]);
+    int q = __float_as_int(m) - __float_as_int(kMagic);
+    if (fabsf(e) > __int_as_float(half - (q & 1))) q += e > 0.f ? 1 : -1;
+    if (EDGE) q = min(max(q, -8), 7);
+    w |= (uint32_t)(q + 8) << (4 * i);
+  }
+  return w;
+}
+
+// A warp takes one token and kRowRounds rounds of 256 / D of its rows (K's
+// heads, then V's), so that the token's page is looked up once and the rows'
+// loads are under way together.  A row takes D / 8 lanes, eight dimensions
+// 8 l .. 8 l + 7 each: lane l = 4 b + j has the dimensions of block b that make
+// up groups g = 2 j and 2 j + 1, two whole 16-bit words of the row's codes.
+//
+// What bounds it: reading or writing the caller's rows, by bytes, and writing
+// 4-bit rows the instructions besides (about 14 a value).
+template <int D, bool Q4, class T, bool READ>
+__global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
+                                                          const int32_t* seqs, const int32_t* positions,
+                                                          int n, int warps_per_token) {
+  constexpr int LANES = D / 8, NB = D / 32, RPR = 32 / LANES;  // rows of a round
+  const int lane = threadIdx.x & 31, l = lane % LANES, b = l / 4, j = l % 4;
+  const uint32_t warp = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const uint32_t t = warp / warps_per_token;
+  if (t >= (uint32_t)n) return;
+  const int s = seqs ? seqs[t] : (int)t;
+  if (s < 0) return;
+  int page = -1, row = 0;
   if (s < c.n_seqs) {
     const int pos = positions ? positions[t] : c.lens[s] - 1;
     if (pos >= 0 && pos < c.max_pages * c.page_rows) {
       page = c.table[(int64_t)s * c.max_pages + pos / c.page_rows];
-      *row = pos % c.page_rows;
+      row = pos % c.page_rows;
     }
   }
   if (page < 0 || page >= c.n_pages) {
-    atomicOr(c.status, DEC_KV_BAD_INDEX);
-    return nullptr;
+    if (lane == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
+    return;
   }
-  return c.pool + page * c.page_bytes + which * c.half_bytes + head * c.head_bytes;
-}
-
-// One row of K or V of one head takes D / 4 lanes, four dimensions 4 l .. 4 l + 3
-// each: lane l = 8 b + g of a row holds the four dimensions of block b that
-// share a 16-bit word of the row's codes, so the loads, the block maximum (8
-// lanes) and the stores are all whole.
-template <int D, bool Q4, class T, bool READ>
-__global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
-                                                          const int32_t* seqs, const int32_t* positions,
-                                                          int n) {
-  constexpr int LANES = D / 4, NB = D / 32;
-  const int l = threadIdx.x % LANES, b = l / 8, g = l % 8;
-  const int64_t item = ((int64_t)blockIdx.x * kRowWarps * 32 + threadIdx.x) / LANES;
-  const int per = 2 * c.nkv;
-  const int64_t t = item / per;
-  const bool in = t < n;
-  const int which = (int)(item % per) / c.nkv, head = (int)(item % per) % c.nkv;
-  int row = 0;
-  uint8_t* base = in ? kv_token_row(c, seqs, positions, (int)t, which, head, &row) : nullptr;
-  T* x_ptr = (which ? v : k) + t * stride + (int64_t)head * D + 4 * l;
+  // (no lane of the warp has left)
+  const int first = (warp % warps_per_token) * (kRowRounds * RPR) + lane / LANES;
+  uint8_t* base = c.pool + page * c.page_bytes;
+  const int64_t token = t * stride + 8 * l;
+  float x[kRowRounds][8];
+  if constexpr (!READ || !Q4) {
+#pragma unroll
+    for (int i = 0; i < kRowRounds; ++i) {
+      const int at = first + i * RPR, head = at < c.nkv ? at : at - c.nkv;
+      if (at >= 2 * c.nkv) continue;
+      T* mine = (at < c.nkv ? k : v) + token + (int64_t)head * D;
+      uint16_t* bf = reinterpret_cast<uint16_t*>(base + at * c.head_bytes) + row * D + 8 * l;
+      if constexpr (READ) load8(bf, x[i]);
+      else load8(mine, x[i]);
+    }
+  }
   if constexpr (!Q4) {
-    if (!base) return;
-    uint16_t* p = reinterpret_cast<uint16_t*>(base) + (int64_t)row * D + 4 * l;
-    float x[4];
-    if constexpr (READ) {
-      load4(p, x);
-      store4(x_ptr, x);
-    } else {
-      load4(x_ptr, x);
-      store4(p, x);
+#pragma unroll
+    for (int i = 0; i < kRowRounds; ++i) {
+      const int at = first + i * RPR, head = at < c.nkv ? at : at - c.nkv;
+      if (at >= 2 * c.nkv) continue;
+      T* mine = (at < c.nkv ? k : v) + token + (int64_t)head * D;
+      uint16_t* bf = reinterpret_cast<uint16_t*>(base + at * c.head_bytes) + row * D + 8 * l;
+      if constexpr (READ) store8(mine, x[i]);
+      else store8(bf, x[i]);
+    }
+  } else if constexpr (READ) {
+    uint32_t codes[kRowRounds];
+    __half scale[kRowRounds];
+#pragma unroll
+    for (int i = 0; i < kRowRounds; ++i) {
+      const int at = first + i * RPR;
+      if (at >= 2 * c.nkv) continue;
+      const uint8_t* head = base + at * c.head_bytes;
+      const uint16_t* words = reinterpret_cast<const uint16_t*>(head + row * (D / 2)) + 2 * j * NB + b;
+      codes[i] = words[0] | (uint32_t)words[NB] << 16;
+      scale[i] = reinterpret_cast<const __half*>(head + (int64_t)c.page_rows * (D / 2))[row * NB + b];
+    }
+#pragma unroll
+    for (int i = 0; i < kRowRounds; ++i) {
+      const int at = first + i * RPR, head = at < c.nkv ? at : at - c.nkv;
+      if (at >= 2 * c.nkv) continue;
+      const float f = __half2float(scale[i]);
+#pragma unroll
+      for (int m = 0; m < 8; ++m)  // 2^23 + n, less 2^23 + 8
+        x[i][m] = (__int_as_float(0x4b000000 | (codes[i] >> (4 * m) & 15)) - 8388616.f) * f;
+      store8((at < c.nkv ? k : v) + token + (int64_t)head * D, x[i]);
     }
   } else {
-    uint16_t* code_ptr = reinterpret_cast<uint16_t*>(base + (int64_t)row * (D / 2)) + g * NB + b;
-    __half* scale_ptr = reinterpret_cast<__half*>(base + (int64_t)c.page_rows * (D / 2)) + (int64_t)row * NB + b;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (READ) {
-      if (!base) return;
-      const uint32_t w = *code_ptr;
-      const float s = __half2float(*scale_ptr);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = (float)((int)((w >> (4 * i)) & 15) - 8) * s;
-      store4(x_ptr, x);
-    } else {
-      if (base) load4(x_ptr, x);
-      uint32_t top = 0;  // largest magnitude of the block, as bits: order of the values, NaN and infinity last
+    for (int i = 0; i < kRowRounds; ++i) {
+      const int at = first + i * RPR;
+      const bool on = at < 2 * c.nkv;
+      uint32_t top = 0;  // the block's largest magnitude, as bits: in the order of the values, infinity and NaN last
+      if (on) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (!base) return;
-      const bool finite = top < 0x7f800000u;
-      const __half s = finite ? __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top), 7.f), 65504.f))
-                              : __ushort_as_half(0x7fff);
-      const float sf = __half2float(s);
-      uint32_t w = 0x8888u;
-      if (finite && sf > 0.f) {
-        w = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w |= (uint32_t)(q4_code(x[i], sf) + 8) << (4 * i);
+        for (int m = 0; m < 8; ++m) top = max(top, __float_as_uint(x[i][m]) & 0x7fffffffu);
       }
-      *code_ptr = (uint16_t)w;
-      if (g == 0) *scale_ptr = s;
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if (!on) continue;
+      const bool finite = top < 0x7f800000u;
+      const __half s16 = finite ? __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top), 7.f), 65504.f))
+                                : __ushort_as_half(0x7fff);
+      const float f = __half2float(s16);
+      uint32_t w = 0x88888888u;
+      if (f >= 6.103515625e-5f && f < 65504.f) w = q4_codes<false>(x[i], f);
+      else if (f > 0.f) w = q4_codes<true>(x[i], f);  // (not where f is NaN)
+      uint8_t* head = base + at * c.head_bytes;
+      uint16_t* words = reinterpret_cast<uint16_t*>(head + row * (D / 2)) + 2 * j * NB + b;
+      words[0] = (uint16_t)w;
+      words[NB] = (uint16_t)(w >> 16);
+      if (j == 0) reinterpret_cast<__half*>(head + (int64_t)c.page_rows * (D / 2))[row * NB + b] = s16;
     }
   }
 }
@@ -178,13 +222,15 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
 template <int D, bool Q4, class T, bool READ>
 cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const int32_t* seqs,
                         const int32_t* positions, int n, cudaStream_t s) {
-  const int64_t threads = (int64_t)n * 2 * c.nkv * (D / 4);
+  constexpr int kPerWarp = kRowRounds * (256 / D);
+  const int warps_per_token = (2 * c.nkv + kPerWarp - 1) / kPerWarp;
+  const int64_t warps = (int64_t)n * warps_per_token;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((threads + kRowWarps * 32 - 1) / (kRowWarps * 32)));
+  cfg.gridDim = dim3((unsigned)((warps + kRowWarps - 1) / kRowWarps));
   cfg.blockDim = dim3(kRowWarps * 32);
   cfg.stream = s;
   return cudaLaunchKernelEx(&cfg, kv_rows<D, Q4, T, READ>, c, static_cast<T*>(k), static_cast<T*>(v), stride, seqs,
-                            positions, n);
+                            positions, n, warps_per_token);
 }
 
 template <bool READ>
@@ -203,8 +249,8 @@ int rows_call(const dec_kv_cache* c, int layer, void* k, void* v, int type, int6
                           (long long)width);
   if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) || (row_stride * size) % 16)
     return fail_no_handle(DEC_ERR_ARG, "k, v and their rows must be 16-byte aligned");
-  if ((int64_t)n * 2 * width > (int64_t)1 << 38)
-    return fail_no_handle(DEC_ERR_SHAPE, "%d rows are more than one launch takes", n);
+  if ((int64_t)n * c->n_kv_heads > (int64_t)1 << 30)
+    return fail_no_handle(DEC_ERR_SHAPE, "%d rows of %d heads (at most 2^30 in all)", n, c->n_kv_heads);
   const KvView view = kv_view(*c, layer);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
