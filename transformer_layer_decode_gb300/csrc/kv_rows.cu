@@ -1,6 +1,7 @@
 // dec_kv_append and dec_kv_read: rows of a paged key/value cache from and to
 // plain tensors, bf16 or in 4-bit blocks.  Also the checks shared by the
 // dec_kv_ calls.
+#include <algorithm>
 #include <cstdio>
 
 #include "common.cuh"
@@ -60,7 +61,11 @@ KvView kv_view(const dec_kv_cache& c, int layer) {
 namespace {
 
 constexpr int kRowWarps = 8;  // warps of a CTA of the row kernels
-constexpr int kRowRounds = 4; // rounds of a warp: rows whose loads are under way together
+// Rounds of a warp, rows whose loads are under way together, where there are
+// enough warps to fill the GPU; one otherwise.
+constexpr int kRowRounds = 4;
+constexpr int kFewRounds = 8192;  // (about a GPU full of warps)
+constexpr int kManyCtas = 1200;   // (eight an SM)
 
 // Eight fp32 values from / to the caller's type.
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
@@ -85,136 +90,181 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
       make_uint4(pair(x[0], x[1]), pair(x[2], x[3]), pair(x[4], x[5]), pair(x[6], x[7]));
 }
 
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+
+// 1 / s to a few 2^-24 of itself.
+__device__ __forceinline__ float reciprocal(float s) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  return y;
+}
+
+// The larger magnitude; NaN if either is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+  return y;
+}
+
 // Codes plus 8 of eight values for a scale s > 0, four bits each, lowest first:
 // the integers nearest to x / s, ties to even, within [-8, 7].  r = x * (1 / s)
 // is off by a few 2^-24 of itself, so its nearest integer q is the answer or,
-// next to a half, a neighbour; the remainder e = x - q s is exact (it has no
-// bits below x's and is below s), and |e| against s / 2 decides: past it, or on
-// it with q odd, q moves one on.  EDGE: also for scales so small or so large
-// that |x / s| passes 7.5 (s below fp16's normal numbers, or at its top).
-template <bool EDGE>
+// next to a half, a neighbour.  Where no r is within 2^-19 of a half (r, below
+// 7.01, is off by less) all q are right as they are.  Otherwise the remainder
+// e = x - q s, which is exact (it has no bits below x's and is below s), decides
+// against s / 2: past it, or on it with q odd, q moves one on.  So for scales
+// below fp16's normal numbers, or at its top, where |r| can be larger, too.
+// The codes are put together as digits of a float, 16 bits at a time, to spare
+// the integer pipe.
 __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], float s) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-  const float inv = 1.f / s;
-  const int half = __float_as_int(0.5f * s);
-  uint32_t w = 0;
+  const float inv = reciprocal(s);
+  float q[8], off = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float r = x[i] * inv;
-    if (EDGE) r = fminf(fmaxf(r, -8.f), 7.f);
-    const float m = r + kMagic, e = fmaf(-(m - kMagic), s, x[i]);
-    int q = __float_as_int(m) - __float_as_int(kMagic);
-    if (fabsf(e) > __int_as_float(half - (q & 1))) q += e > 0.f ? 1 : -1;
-    if (EDGE) q = min(max(q, -8), 7);
-    w |= (uint32_t)(q + 8) << (4 * i);
+    const float r = x[i] * inv;
+    q[i] = (r + kMagic) - kMagic;
+    off = fmaxf(off, fabsf(r - q[i]));
   }
-  return w;
+  if (!(off < 0.5f - 1.f / (1 << 19)) || s < 6.103515625e-5f || s >= 65504.f) {
+    const int half = __float_as_int(0.5f * s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float m = fminf(fmaxf(x[i] * inv, -8.f), 7.f) + kMagic, e = fmaf(-(m - kMagic), s, x[i]);
+      const float one = fabsf(e) > __int_as_float(half - (__float_as_int(m) & 1)) ? copysignf(1.f, e) : 0.f;
+      q[i] = fminf(fmaxf((m - kMagic) + one, -8.f), 7.f);
+    }
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float y = fmaf(fmaf(fmaf(q[4 * i + 3], 16.f, q[4 * i + 2]), 16.f, q[4 * i + 1]), 16.f, q[4 * i]);
+    w[i] = __float_as_uint(y + (8388608.f + 8.f * 4369.f));  // 2^23 and 8 in every digit
+  }
+  return __byte_perm(w[0], w[1], 0x5410);
 }
 
-// A warp takes one token and kRowRounds rounds of 256 / D of its rows (K's
-// heads, then V's), so that the token's page is looked up once and the rows'
-// loads are under way together.  A row takes D / 8 lanes, eight dimensions
-// 8 l .. 8 l + 7 each: lane l = 4 b + j has the dimensions of block b that make
-// up groups g = 2 j and 2 j + 1, two whole 16-bit words of the row's codes.
+// x / 7, correctly rounded: the product with the rounded reciprocal and one FMA
+// correction (Markstein's division; the quotient's remainder is exact).
+__device__ __forceinline__ float seventh(float x) {
+  constexpr float y = 1.f / 7;
+  const float q = x * y;
+  return fmaf(fmaf(-7.f, q, x), y, q);
+}
+
+constexpr int kMaxTokens = 32;  // of a CTA
+
+// A CTA takes `tokens` tokens, looks up where each goes (a thread per token),
+// and its warps take them in turn, ROUNDS rounds of 256 / D rows of a token
+// (K's heads, then V's) at a time, so that these rows' loads are under way
+// together.  A row takes D / 8 lanes, eight dimensions 8 l .. 8 l + 7 each:
+// lane l = 4 b + j has the dimensions of block b that make up groups g = 2 j and
+// 2 j + 1, two whole 16-bit words of the row's codes.
 //
-// What bounds it: reading or writing the caller's rows, by bytes, and writing
-// 4-bit rows the instructions besides (about 14 a value).
-template <int D, bool Q4, class T, bool READ>
+// What bounds it: the caller's rows, by bytes; writing 4-bit rows, the integer
+// and float pipes besides (about 10 instructions a value).
+template <int D, bool Q4, class T, bool READ, int ROUNDS>
 __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
                                                           const int32_t* seqs, const int32_t* positions,
-                                                          int n, int warps_per_token) {
+                                                          int n, int tokens, int items_per_token) {
   constexpr int LANES = D / 8, NB = D / 32, RPR = 32 / LANES;  // rows of a round
+  __shared__ uint8_t* token_page[kMaxTokens];
+  __shared__ int token_row[kMaxTokens];
   const int lane = threadIdx.x & 31, l = lane % LANES, b = l / 4, j = l % 4;
-  const uint32_t warp = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const uint32_t t = warp / warps_per_token;
-  if (t >= (uint32_t)n) return;
-  const int s = seqs ? seqs[t] : (int)t;
-  if (s < 0) return;
-  int page = -1, row = 0;
-  if (s < c.n_seqs) {
-    const int pos = positions ? positions[t] : c.lens[s] - 1;
-    if (pos >= 0 && pos < c.max_pages * c.page_rows) {
-      page = c.table[(int64_t)s * c.max_pages + pos / c.page_rows];
-      row = pos % c.page_rows;
-    }
-  }
-  if (page < 0 || page >= c.n_pages) {
-    if (lane == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
-    return;
-  }
-  // (no lane of the warp has left)
-  const int first = (warp % warps_per_token) * (kRowRounds * RPR) + lane / LANES;
-  uint8_t* base = c.pool + page * c.page_bytes;
-  const int64_t token = t * stride + 8 * l;
-  float x[kRowRounds][8];
-  if constexpr (!READ || !Q4) {
-#pragma unroll
-    for (int i = 0; i < kRowRounds; ++i) {
-      const int at = first + i * RPR, head = at < c.nkv ? at : at - c.nkv;
-      if (at >= 2 * c.nkv) continue;
-      T* mine = (at < c.nkv ? k : v) + token + (int64_t)head * D;
-      uint16_t* bf = reinterpret_cast<uint16_t*>(base + at * c.head_bytes) + row * D + 8 * l;
-      if constexpr (READ) load8(bf, x[i]);
-      else load8(mine, x[i]);
-    }
-  }
-  if constexpr (!Q4) {
-#pragma unroll
-    for (int i = 0; i < kRowRounds; ++i) {
-      const int at = first + i * RPR, head = at < c.nkv ? at : at - c.nkv;
-      if (at >= 2 * c.nkv) continue;
-      T* mine = (at < c.nkv ? k : v) + token + (int64_t)head * D;
-      uint16_t* bf = reinterpret_cast<uint16_t*>(base + at * c.head_bytes) + row * D + 8 * l;
-      if constexpr (READ) store8(mine, x[i]);
-      else store8(bf, x[i]);
-    }
-  } else if constexpr (READ) {
-    uint32_t codes[kRowRounds];
-    __half scale[kRowRounds];
-#pragma unroll
-    for (int i = 0; i < kRowRounds; ++i) {
-      const int at = first + i * RPR;
-      if (at >= 2 * c.nkv) continue;
-      const uint8_t* head = base + at * c.head_bytes;
-      const uint16_t* words = reinterpret_cast<const uint16_t*>(head + row * (D / 2)) + 2 * j * NB + b;
-      codes[i] = words[0] | (uint32_t)words[NB] << 16;
-      scale[i] = reinterpret_cast<const __half*>(head + (int64_t)c.page_rows * (D / 2))[row * NB + b];
-    }
-#pragma unroll
-    for (int i = 0; i < kRowRounds; ++i) {
-      const int at = first + i * RPR, head = at < c.nkv ? at : at - c.nkv;
-      if (at >= 2 * c.nkv) continue;
-      const float f = __half2float(scale[i]);
-#pragma unroll
-      for (int m = 0; m < 8; ++m)  // 2^23 + n, less 2^23 + 8
-        x[i][m] = (__int_as_float(0x4b000000 | (codes[i] >> (4 * m) & 15)) - 8388616.f) * f;
-      store8((at < c.nkv ? k : v) + token + (int64_t)head * D, x[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kRowRounds; ++i) {
-      const int at = first + i * RPR;
-      const bool on = at < 2 * c.nkv;
-      uint32_t top = 0;  // the block's largest magnitude, as bits: in the order of the values, infinity and NaN last
-      if (on) {
-#pragma unroll
-        for (int m = 0; m < 8; ++m) top = max(top, __float_as_uint(x[i][m]) & 0x7fffffffu);
+  const int64_t t0 = (int64_t)blockIdx.x * tokens;
+  if (threadIdx.x < tokens) {
+    const int64_t t = t0 + threadIdx.x;
+    uint8_t* at = nullptr;
+    const int s = t < n ? (seqs ? seqs[t] : (int)t) : -1;
+    if (s >= 0) {
+      int page = -1;
+      if (s < c.n_seqs) {
+        const int pos = positions ? positions[t] : c.lens[s] - 1;
+        if (pos >= 0 && pos < c.max_pages * c.page_rows) {
+          page = c.table[(int64_t)s * c.max_pages + pos / c.page_rows];
+          token_row[threadIdx.x] = pos % c.page_rows;
+        }
       }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if (!on) continue;
-      const bool finite = top < 0x7f800000u;
-      const __half s16 = finite ? __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top), 7.f), 65504.f))
-                                : __ushort_as_half(0x7fff);
-      const float f = __half2float(s16);
-      uint32_t w = 0x88888888u;
-      if (f >= 6.103515625e-5f && f < 65504.f) w = q4_codes<false>(x[i], f);
-      else if (f > 0.f) w = q4_codes<true>(x[i], f);  // (not where f is NaN)
-      uint8_t* head = base + at * c.head_bytes;
-      uint16_t* words = reinterpret_cast<uint16_t*>(head + row * (D / 2)) + 2 * j * NB + b;
-      words[0] = (uint16_t)w;
-      words[NB] = (uint16_t)(w >> 16);
-      if (j == 0) reinterpret_cast<__half*>(head + (int64_t)c.page_rows * (D / 2))[row * NB + b] = s16;
+      if (page >= 0 && page < c.n_pages) at = c.pool + page * c.page_bytes;
+      else atomicOr(c.status, DEC_KV_BAD_INDEX);
+    }
+    token_page[threadIdx.x] = at;
+  }
+  __syncthreads();
+  for (int item = threadIdx.x >> 5; item < tokens * items_per_token; item += kRowWarps) {
+    const int token = item / items_per_token;
+    uint8_t* base = token_page[token];
+    if (!base) continue;
+    const int row = token_row[token], page_rows = c.page_rows, nkv = c.nkv;
+    const uint32_t head_bytes = (uint32_t)c.head_bytes;
+    const int first = (item - token * items_per_token) * (ROUNDS * RPR) + lane / LANES;
+    T* k_at = k + (t0 + token) * stride + 8 * l;
+    T* v_at = v + (t0 + token) * stride + 8 * l - nkv * D;
+    auto mine = [&](int at) { return (at < nkv ? k_at : v_at) + at * D; };  // the caller's
+    // in the page: bf16 values, or two words of codes, 2 NB bytes apart, and a scale
+    uint8_t* values = base + row * kv_row_bytes(D, false) + 16 * l;
+    uint8_t* words = base + row * (D / 2) + 4 * j * NB + 2 * b;
+    uint8_t* scales = base + page_rows * (D / 2) + (row * NB + b) * 2;
+    float x[ROUNDS][8];
+    if constexpr (!READ || !Q4) {
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int at = first + i * RPR;
+        if (at >= 2 * nkv) continue;
+        if constexpr (READ) load8(reinterpret_cast<const uint16_t*>(values + at * head_bytes), x[i]);
+        else load8(mine(at), x[i]);
+      }
+    }
+    if constexpr (!Q4) {
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int at = first + i * RPR;
+        if (at >= 2 * nkv) continue;
+        if constexpr (READ) store8(mine(at), x[i]);
+        else store8(reinterpret_cast<uint16_t*>(values + at * head_bytes), x[i]);
+      }
+    } else if constexpr (READ) {
+      uint32_t codes[ROUNDS];
+      __half scale[ROUNDS];
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const uint32_t at = first + i * RPR;
+        if (at >= 2 * nkv) continue;
+        const uint16_t* w = reinterpret_cast<const uint16_t*>(words + at * head_bytes);
+        codes[i] = w[0] | (uint32_t)w[NB] << 16;
+        scale[i] = *reinterpret_cast<const __half*>(scales + at * head_bytes);
+      }
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int at = first + i * RPR;
+        if (at >= 2 * nkv) continue;
+        const float f = __half2float(scale[i]);
+#pragma unroll
+        for (int m = 0; m < 8; ++m)  // 2^23 + n, less 2^23 + 8
+          x[i][m] = (__int_as_float(0x4b000000 | (codes[i] >> (4 * m) & 15)) - 8388616.f) * f;
+        store8(mine(at), x[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int at = first + i * RPR;
+        const bool on = at < 2 * nkv;
+        float top = 0.f;  // the block's largest magnitude
+        if (on) {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) top = larger(top, x[i][m]);
+        }
+        top = larger(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = larger(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (!on) continue;
+        const bool finite = top < INFINITY;
+        const __half s16 = finite ? __float2half_rn(fminf(seventh(top), 65504.f)) : __ushort_as_half(0x7fff);
+        const float f = __half2float(s16);
+        const uint32_t w = f > 0.f ? q4_codes(x[i], f) : 0x88888888u;  // (not where f is NaN)
+        uint16_t* to = reinterpret_cast<uint16_t*>(words + at * head_bytes);
+        to[0] = (uint16_t)w;
+        to[NB] = (uint16_t)(w >> 16);
+        if (j == 0) *reinterpret_cast<__half*>(scales + at * head_bytes) = s16;
+      }
     }
   }
 }
@@ -222,15 +272,18 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
 template <int D, bool Q4, class T, bool READ>
 cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const int32_t* seqs,
                         const int32_t* positions, int n, cudaStream_t s) {
-  constexpr int kPerWarp = kRowRounds * (256 / D);
-  const int warps_per_token = (2 * c.nkv + kPerWarp - 1) / kPerWarp;
-  const int64_t warps = (int64_t)n * warps_per_token;
+  constexpr int kPerRound = 256 / D;
+  const bool few = (int64_t)n * 2 * c.nkv / kPerRound < kFewRounds;
+  const int per_item = kPerRound * (few ? 1 : kRowRounds);
+  const int items = (2 * c.nkv + per_item - 1) / per_item;
+  // enough tokens for every warp of a CTA, and more where there are CTAs enough without
+  const int tokens = std::max((kRowWarps + items - 1) / items, std::min(n / kManyCtas, kMaxTokens));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((warps + kRowWarps - 1) / kRowWarps));
+  cfg.gridDim = dim3((unsigned)((n + tokens - 1) / tokens));
   cfg.blockDim = dim3(kRowWarps * 32);
   cfg.stream = s;
-  return cudaLaunchKernelEx(&cfg, kv_rows<D, Q4, T, READ>, c, static_cast<T*>(k), static_cast<T*>(v), stride, seqs,
-                            positions, n, warps_per_token);
+  return cudaLaunchKernelEx(&cfg, few ? kv_rows<D, Q4, T, READ, 1> : kv_rows<D, Q4, T, READ, kRowRounds>, c,
+                            static_cast<T*>(k), static_cast<T*>(v), stride, seqs, positions, n, tokens, items);
 }
 
 template <bool READ>
