@@ -183,15 +183,31 @@ template <int D>
 struct WarpSums {
   static constexpr int NB = D / 32;
   float acc[NB][2][4];  // O^T: [0..1] a dimension (out_dim) of heads 2t, 2t + 1; [2..3] the next dimension
-  float ref, l;         // head g's
 
-  __device__ __forceinline__ void clear() {
+  __device__ __forceinline__ void clear_acc() {
 #pragma unroll
     for (int x = 0; x < NB; ++x)
 #pragma unroll
       for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[x][y][i] = 0.f;
+  }
+
+  __device__ __forceinline__ void scale_acc(float k0, float k1) {
+#pragma unroll
+    for (int x = 0; x < NB; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) acc[x][y][0] *= k0, acc[x][y][1] *= k1, acc[x][y][2] *= k0, acc[x][y][3] *= k1;
+  }
+};
+
+// The softmax state of a lane that has the scores of head g.
+template <int D>
+struct WarpHead : WarpSums<D> {
+  float ref, l;
+
+  __device__ __forceinline__ void clear() {
+    this->clear_acc();
     ref = -3e38f;
     l = 0.f;
   }
@@ -206,12 +222,49 @@ struct WarpSums {
     ref = now;
     l *= keep;
     const int t = threadIdx.x & 3;
-    const float k0 = __shfl_sync(0xffffffffu, keep, 8 * t) * unit;
-    const float k1 = __shfl_sync(0xffffffffu, keep, 8 * t + 4) * unit;
+    this->scale_acc(__shfl_sync(0xffffffffu, keep, 8 * t) * unit, __shfl_sync(0xffffffffu, keep, 8 * t + 4) * unit);
+  }
+
+  __device__ __forceinline__ void write_refs(float2* to, int lane) {
+    float sum = l;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if ((lane & 3) == 0) to[lane >> 2] = make_float2(ref, sum);
+  }
+};
+
+// The same of a lane that has the scores of heads 2t and 2t + 1.
+template <int D>
+struct WarpHeadPair : WarpSums<D> {
+  float ref[2], l[2];
+
+  __device__ __forceinline__ void clear() {
+    this->clear_acc();
+    ref[0] = ref[1] = -3e38f;
+    l[0] = l[1] = 0.f;
+  }
+
+  __device__ __forceinline__ void raise(float mx0, float mx1, float lift, float unit) {
 #pragma unroll
-    for (int x = 0; x < NB; ++x)
+    for (int o = 4; o < 32; o <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+    }
+    const float now0 = fmaxf(ref[0], mx0 - lift), now1 = fmaxf(ref[1], mx1 - lift);
+    const float keep0 = exp2_approx(ref[0] - now0), keep1 = exp2_approx(ref[1] - now1);
+    ref[0] = now0, ref[1] = now1;
+    l[0] *= keep0, l[1] *= keep1;
+    this->scale_acc(keep0 * unit, keep1 * unit);
+  }
+
+  __device__ __forceinline__ void write_refs(float2* to, int lane) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) acc[x][y][0] *= k0, acc[x][y][1] *= k1, acc[x][y][2] *= k0, acc[x][y][3] *= k1;
+    for (int i = 0; i < 2; ++i) {
+      float sum = l[i];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane < 4) to[2 * lane + i] = make_float2(ref[i], sum);
+    }
   }
 };
 
@@ -246,7 +299,7 @@ __device__ __forceinline__ void load_query(const T* q, bool valid, int t, float 
 // bits); bf16 calls take q as it is and the weights in two (16 bits, against
 // the 8 of their results).
 template <int D, class T>
-struct WarpBf16 : WarpSums<D> {
+struct WarpBf16 : WarpHead<D> {
   using Sums = WarpSums<D>;
   static constexpr int NB = Sums::NB, kPieces = sizeof(T) == 4 ? 3 : 2;
   static constexpr bool kWhole = sizeof(T) == 2;  // q is one piece
@@ -351,9 +404,12 @@ struct WarpBf16 : WarpSums<D> {
 //  - K's block scales multiply the fp32 sums over a block, V's the weights.
 // q is scaled by a power of two and taken in two fp16 pieces (22 bits; bf16 q
 // needs one), and so is weight * scale for fp32 results; for bf16 results it
-// is one fp16 number (11 bits, against the 8 of the results).
+// is one fp16 number (11 bits, against the 8 of the results).  With one piece
+// each, the scores are computed the other way round, S^T = K q^T, 16 rows at a
+// time, which takes half the products and block scales, and the weights, packed
+// in pairs of heads, are turned by movmatrix.
 template <int D, class T>
-struct WarpQ4 : WarpSums<D> {
+struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>> {
   using Sums = WarpSums<D>;
   using L = Tile<D, true>;
   static constexpr int NB = Sums::NB, kTiles = L::kStep;
@@ -361,12 +417,9 @@ struct WarpQ4 : WarpSums<D> {
   // The largest weight is 2^lift to 2^(lift + kSlack), so that its product with
   // a scale stays below 2^15 and the others well above fp16's smallest step.
   static constexpr float kLift = 9.f;
-  // q: both pieces, whole operands of the products as they lie in registers (for
-  // bf16 q the second is zero, which must not be known: zeros would be moved
-  // into place before every product)
-  uint32_t a[2 * NB][4];
+  uint32_t a[2 * NB][kWhole ? 2 : 4];  // q
   uint32_t bias[2];                    // -8 sum of q per block, in three pieces: operand of one product
-  float f;                             // score = f * product, in log2 units
+  float f, f1;                         // score = f * product, in log2 units; kWhole: f of head 2t, f1 of the next
   float top;                           // V scales seen are below top = 2^e
   float unit;                          // fp32 results: they enter times unit = 2^-e (as far as fp16 goes) ...
   float lift;                          // ... at lift = 9; bf16 results: as they are, at lift = min(9, 9 - e)
@@ -398,15 +451,19 @@ struct WarpQ4 : WarpSums<D> {
       for (int i = 0; i < 8; ++i) x[b][i] *= up;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t(&w)[4] = a[2 * b + h];
+        uint32_t(&w)[kWhole ? 2 : 4] = a[2 * b + h];
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {
           const float part = odd ? 1.f / 16 : 1.f;
           float y0 = x[b][2 * h + odd] * part, y1 = x[b][4 + 2 * h + odd] * part;
           const uint32_t hi = take_f16(y0, y1), lo = pack_f16(y0, y1);
           const float2 u = unpack_f16(hi), r = unpack_f16(lo);
-          w[2 * odd] = hi;
-          w[2 * odd + 1] = lo;
+          if constexpr (kWhole) {  // (lo is zero)
+            w[odd] = hi;
+          } else {
+            w[2 * odd] = hi;
+            w[2 * odd + 1] = lo;
+          }
           sum += ((u.x + r.x) + (u.y + r.y)) * (odd ? 16.f : 1.f);
         }
       }
@@ -426,14 +483,18 @@ struct WarpQ4 : WarpSums<D> {
       bias[0] = t == 0 ? piece[0][0] : t == 1 ? piece[1][0] : t == 2 ? piece[2][0] : 0;
       bias[1] = 0;
     }
+    if constexpr (kWhole) {
+      f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+      f = __shfl_sync(0xffffffffu, f, 8 * t);
+    }
     this->clear();
     top = 1e-30f;
     unit = 1.f;
     lift = kLift;
   }
 
-  // Makes room for V scales up to s (of this lane) and for the scores up to mx.
-  __device__ __forceinline__ void make_room(float mx, float s) {
+  // Makes room for V scales up to s (of this lane); what the outputs are to be scaled by.
+  __device__ __forceinline__ float make_room(float s) {
     s = warp_max(s);
     float change = 1.f;
     if (s >= top) {
@@ -441,10 +502,12 @@ struct WarpQ4 : WarpSums<D> {
       top = __uint_as_float((uint32_t)(127 + e) << 23);
       if constexpr (kWhole) {
         const float now = kLift - (float)max(e, 0);
-        this->ref += lift - now;  // the references that the heads' largest scores have now
-        const float down = exp2_approx(now - lift);
-        this->l *= down;
-        change = down;
+        change = exp2_approx(now - lift);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          this->ref[i] += lift - now;  // the references that the heads' largest scores have now
+          this->l[i] *= change;
+        }
         lift = now;
       } else {
         const float now = __uint_as_float((uint32_t)(127 - max(e, -14)) << 23);
@@ -452,82 +515,148 @@ struct WarpQ4 : WarpSums<D> {
         unit = now;
       }
     }
-    this->raise(mx, lift, change);
+    return change;
   }
 
   // kTiles staged tiles.  edge: some row is not visible; rows_seen: a bit for each that is.
   __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t rows_seen) {
     const int g = lane >> 2, t = lane & 3;
+    // scores: of head g, rows 2t, 2t + 1 of each half; kWhole: of heads 2t, 2t + 1, rows g and g + 8
     float s[4 * kTiles];
-    __half2 most = __float2half2_rn(0.f);  // the largest of all, between the lanes
+    __half2 most = __float2half2_rn(0.f);  // the largest of V's scales, between the lanes
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) {
       const uint8_t* sk = st + k * L::kBytes;
       const uint8_t* ks_at = sk + kTileRows * L::kRowBytes;
-      const uint8_t* vs_at = ks_at + L::kHalf;
       if (D == 128 || lane < 16) {
-        __half2 h = *reinterpret_cast<const __half2*>(vs_at + 4 * lane);
+        __half2 h = *reinterpret_cast<const __half2*>(ks_at + L::kHalf + 4 * lane);
         if (edge && !(rows_seen >> (16 * k + lane / (NB / 2)) & 1)) h = __float2half2_rn(0.f);
         most = __hmax2(most, h);
       }
+      uint32_t w[2][NB];  // rows g, g + 8: blocks 0, 1 (and 2, 3) of dimension groups 2t, then of 2t + 1
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        __half2 ks[2][NB / 2];
-        uint32_t w[NB];  // the row's words: blocks 0, 1 (and 2, 3) of dimension groups 2t, then of 2t + 1
-        uint32_t row_scales;
         if constexpr (D == 128) {
           const uint4 u = *reinterpret_cast<const uint4*>(sk + staged<D, true>(8 * b + g, t));
-          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-          *reinterpret_cast<uint4*>(ks) = *reinterpret_cast<const uint4*>(ks_at + 64 * b + 16 * t);
-          row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 64 * b + 8 * g + 4 * (t & 1));
+          w[b][0] = u.x, w[b][1] = u.y, w[b][2] = u.z, w[b][3] = u.w;
         } else {
           const uint2 u = *reinterpret_cast<const uint2*>(sk + staged<D, true>(8 * b + g, t >> 1) + 8 * (t & 1));
-          w[0] = u.x, w[1] = u.y;
-          *reinterpret_cast<uint2*>(ks) = *reinterpret_cast<const uint2*>(ks_at + 32 * b + 8 * t);
-          row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 32 * b + 4 * g);
+          w[b][0] = u.x, w[b][1] = u.y;
         }
+      }
+      auto codes = [&](int b, int j) {  // four of group 2t, four of 2t + 1
+        return __byte_perm(w[b][j >> 1], w[b][NB / 2 + (j >> 1)], j & 1 ? 0x7632 : 0x5410);
+      };
+      if constexpr (kWhole) {
+        uint32_t ks[2][NB / 2];  // K's scales of rows g, g + 8
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if constexpr (D == 128) {
+            const uint2 u = *reinterpret_cast<const uint2*>(ks_at + 64 * b + 8 * g);
+            ks[b][0] = u.x, ks[b][NB / 2 - 1] = u.y;
+          } else {
+            ks[b][0] = *reinterpret_cast<const uint32_t*>(ks_at + 32 * b + 4 * g);
+          }
+        }
+        const uint32_t odd = (uint32_t) - (t & 1);  // the blocks of this lane's part of the bias
+        const uint32_t z0 = (ks[0][0] & ~odd) | (ks[0][NB / 2 - 1] & odd), z1 = (ks[1][0] & ~odd) | (ks[1][NB / 2 - 1] & odd);
         float z[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(z, bias[0], bias[0], bias[1], bias[1], row_scales, row_scales);  // (rows 8-15 are not used)
-        float s0 = z[0] * (1.f / (1 << 14)), s1 = z[1] * (1.f / (1 << 14));
+        mma_f16(z, z0, z1, z0, z1, bias[0], bias[1]);
+        float r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = z[i] * (1.f / (1 << 14));
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint32_t x = __byte_perm(w[j >> 1], w[NB / 2 + (j >> 1)], j & 1 ? 0x7632 : 0x5410);
-          const uint32_t y = x >> 8;
-          mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], x & 0x000f000fu, x & 0x00f000f0u);
-          mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], y & 0x000f000fu,
-                  y & 0x00f000f0u);
-          const float k0 = __half2float(j & 1 ? __high2half(ks[0][j >> 1]) : __low2half(ks[0][j >> 1]));
-          const float k1 = __half2float(j & 1 ? __high2half(ks[1][j >> 1]) : __low2half(ks[1][j >> 1]));
-          s0 = fmaf(k0, kWhole ? c[0] : c[0] + c[2], s0);
-          s1 = fmaf(k1, kWhole ? c[1] : c[1] + c[3], s1);
+          const uint32_t x0 = codes(0, j), x1 = codes(1, j), y0 = x0 >> 8, y1 = x1 >> 8;
+          mma_f16(c, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, a[2 * j][0], a[2 * j][1]);
+          mma_f16(c, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, a[2 * j + 1][0],
+                  a[2 * j + 1][1]);
+          const float2 u0 = unpack_f16(ks[0][j >> 1]), u1 = unpack_f16(ks[1][j >> 1]);
+          const float k0 = j & 1 ? u0.y : u0.x, k1 = j & 1 ? u1.y : u1.x;
+          r[0] = fmaf(k0, c[0], r[0]);
+          r[1] = fmaf(k0, c[1], r[1]);
+          r[2] = fmaf(k1, c[2], r[2]);
+          r[3] = fmaf(k1, c[3], r[3]);
         }
-        s[4 * k + 2 * b] = s0 * f;
-        s[4 * k + 2 * b + 1] = s1 * f;
+        s[4 * k] = r[0] * f;
+        s[4 * k + 1] = r[1] * f1;
+        s[4 * k + 2] = r[2] * f;
+        s[4 * k + 3] = r[3] * f1;
+        if (edge) {
+          if (!(rows_seen >> (16 * k + g) & 1)) s[4 * k] = s[4 * k + 1] = -INFINITY;
+          if (!(rows_seen >> (16 * k + 8 + g) & 1)) s[4 * k + 2] = s[4 * k + 3] = -INFINITY;
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          __half2 ks[2][NB / 2];
+          uint32_t row_scales;
+          if constexpr (D == 128) {
+            *reinterpret_cast<uint4*>(ks) = *reinterpret_cast<const uint4*>(ks_at + 64 * b + 16 * t);
+            row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 64 * b + 8 * g + 4 * (t & 1));
+          } else {
+            *reinterpret_cast<uint2*>(ks) = *reinterpret_cast<const uint2*>(ks_at + 32 * b + 8 * t);
+            row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 32 * b + 4 * g);
+          }
+          float z[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(z, bias[0], bias[0], bias[1], bias[1], row_scales, row_scales);  // (rows 8-15 are not used)
+          float s0 = z[0] * (1.f / (1 << 14)), s1 = z[1] * (1.f / (1 << 14));
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t x = codes(b, j), y = x >> 8;
+            mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], x & 0x000f000fu, x & 0x00f000f0u);
+            mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], y & 0x000f000fu,
+                    y & 0x00f000f0u);
+            const float k0 = __half2float(j & 1 ? __high2half(ks[0][j >> 1]) : __low2half(ks[0][j >> 1]));
+            const float k1 = __half2float(j & 1 ? __high2half(ks[1][j >> 1]) : __low2half(ks[1][j >> 1]));
+            s0 = fmaf(k0, c[0] + c[2], s0);
+            s1 = fmaf(k1, c[1] + c[3], s1);
+          }
+          s[4 * k + 2 * b] = s0 * f;
+          s[4 * k + 2 * b + 1] = s1 * f;
+        }
+        if (edge) {
+          const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(seen >> i & 1)) s[4 * k + i] = -INFINITY;
+        }
       }
     }
-    if (edge) {
-#pragma unroll
-      for (int k = 0; k < kTiles; ++k) {
-        const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!(seen >> i & 1)) s[4 * k + i] = -INFINITY;
-      }
-    }
-    float mx = s[0];
-#pragma unroll
-    for (int i = 1; i < 4 * kTiles; ++i) mx = fmaxf(mx, s[i]);
     const float big = fmaxf(__low2float(most), __high2float(most));
-    if (__any_sync(0xffffffffu, mx > this->ref + (lift + kSlack) || big >= top)) make_room(mx, big);
     float w[4 * kTiles];
-    float sum = 0.f;
+    if constexpr (kWhole) {
+      float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
 #pragma unroll
-    for (int i = 0; i < 4 * kTiles; ++i) {
-      w[i] = exp2_approx(s[i] - this->ref);
-      sum += w[i];
+      for (int i = 4; i < 4 * kTiles; i += 2) mx0 = fmaxf(mx0, s[i]), mx1 = fmaxf(mx1, s[i + 1]);
+      if (__any_sync(0xffffffffu, mx0 > this->ref[0] + (lift + kSlack) || mx1 > this->ref[1] + (lift + kSlack) ||
+                                      big >= top)) {
+        const float change = make_room(big);
+        this->raise(mx0, mx1, lift, change);
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * kTiles; ++i) {
+        w[i] = exp2_approx(s[i] - this->ref[i & 1]);
+        this->l[i & 1] += w[i];
+      }
+    } else {
+      float mx = s[0];
+#pragma unroll
+      for (int i = 1; i < 4 * kTiles; ++i) mx = fmaxf(mx, s[i]);
+      if (__any_sync(0xffffffffu, mx > this->ref + (lift + kSlack) || big >= top)) {
+        const float change = make_room(big);
+        this->raise(mx, lift, change);
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * kTiles; ++i) {
+        w[i] = exp2_approx(s[i] - this->ref);
+        sum += w[i];
+      }
+      this->l += sum;
     }
-    this->l += sum;
 
     const __half2 m1032 = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);
 #pragma unroll
@@ -565,7 +694,9 @@ struct WarpQ4 : WarpSums<D> {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         if constexpr (kWhole) {
-          ph[b] = pack_f16(w[4 * k + 2 * b], w[4 * k + 2 * b + 1]);
+          // row g + 8 b of heads 2t, 2t + 1 to rows 2t, 2t + 1 of that half of head g
+          const uint32_t rows = pack_f16(w[4 * k + 2 * b], w[4 * k + 2 * b + 1]);
+          asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(ph[b]) : "r"(rows));
         } else {
           w[4 * k + 2 * b] *= unit;
           w[4 * k + 2 * b + 1] *= unit;
@@ -763,10 +894,7 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
   cp_async_wait<0>();
 
   // ---- the warps' sums, brought to one reference
-  float lsum = st.l;
-  lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
-  lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
-  if (t == 0) warp_ref[warp][g] = make_float2(st.ref, lsum);
+  st.write_refs(warp_ref[warp], lane);
   __syncthreads();  // every warp is through with its ring
   float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
