@@ -334,8 +334,9 @@ struct WarpBf16 : WarpHead<D> {
     this->clear();
   }
 
-  // One staged tile.  edge: some row is not visible; rows_seen: a bit for each that is.
-  __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t rows_seen) {
+  // One staged tile.  EDGE: some row is not visible; rows_seen: a bit for each that is.
+  template <bool EDGE>
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, uint32_t rows_seen) {
     using L = Tile<D, false>;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t seen = rows_of_lane(rows_seen, t);
@@ -355,7 +356,7 @@ struct WarpBf16 : WarpHead<D> {
       s[2 * b] = (kWhole ? c[0] : c[0] + c[2]) * f;
       s[2 * b + 1] = (kWhole ? c[1] : c[1] + c[3]) * f;
     }
-    if (edge) {
+    if (EDGE) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (!(seen >> i & 1)) s[i] = -INFINITY;
@@ -375,7 +376,7 @@ struct WarpBf16 : WarpHead<D> {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = *reinterpret_cast<const uint4*>(sv + staged<D, false>((i & 1) + 2 * t + 8 * (i >> 1), 8 * c + g));
-        if (edge && !(seen >> i & 1)) v[i] = make_uint4(0, 0, 0, 0);  // 0 * NaN would be NaN
+        if (EDGE && !(seen >> i & 1)) v[i] = make_uint4(0, 0, 0, 0);  // 0 * NaN would be NaN
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -518,8 +519,9 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
     return change;
   }
 
-  // kTiles staged tiles.  edge: some row is not visible; rows_seen: a bit for each that is.
-  __device__ __forceinline__ void step(const uint8_t* st, int lane, bool edge, uint32_t rows_seen) {
+  // kTiles staged tiles.  EDGE: some row is not visible; rows_seen: a bit for each that is.
+  template <bool EDGE>
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, uint32_t rows_seen) {
     const int g = lane >> 2, t = lane & 3;
     // scores: of head g, rows 2t, 2t + 1 of each half; kWhole: of heads 2t, 2t + 1, rows g and g + 8
     float s[4 * kTiles];
@@ -530,7 +532,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       const uint8_t* ks_at = sk + kTileRows * L::kRowBytes;
       if (D == 128 || lane < 16) {
         __half2 h = *reinterpret_cast<const __half2*>(ks_at + L::kHalf + 4 * lane);
-        if (edge && !(rows_seen >> (16 * k + lane / (NB / 2)) & 1)) h = __float2half2_rn(0.f);
+        if (EDGE && !(rows_seen >> (16 * k + lane / (NB / 2)) & 1)) h = __float2half2_rn(0.f);
         most = __hmax2(most, h);
       }
       uint32_t w[2][NB];  // rows g, g + 8: blocks 0, 1 (and 2, 3) of dimension groups 2t, then of 2t + 1
@@ -583,7 +585,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
         s[4 * k + 1] = r[1] * f1;
         s[4 * k + 2] = r[2] * f;
         s[4 * k + 3] = r[3] * f1;
-        if (edge) {
+        if (EDGE) {
           if (!(rows_seen >> (16 * k + g) & 1)) s[4 * k] = s[4 * k + 1] = -INFINITY;
           if (!(rows_seen >> (16 * k + 8 + g) & 1)) s[4 * k + 2] = s[4 * k + 3] = -INFINITY;
         }
@@ -617,7 +619,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
           s[4 * k + 2 * b] = s0 * f;
           s[4 * k + 2 * b + 1] = s1 * f;
         }
-        if (edge) {
+        if (EDGE) {
           const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -670,7 +672,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
           *reinterpret_cast<uint4*>(vs[2 * b]) = *reinterpret_cast<const uint4*>(vs_at + 64 * b + 16 * t);
         else *reinterpret_cast<uint2*>(vs[2 * b]) = *reinterpret_cast<const uint2*>(vs_at + 32 * b + 8 * t);
       }
-      if (edge) {  // 0 * NaN would be NaN
+      if (EDGE) {  // 0 * NaN would be NaN
         const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -875,17 +877,18 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
   for (int j = 0; j * L::kStep < nt; ++j) {
     cp_async_wait<ST - 1>();
     __syncwarp();
-    const bool edge = doubt || j < plain0 || j - plain0 >= plain_n;
-    uint32_t rows_seen = 0;  // a bit per row of the step
-    if (edge) {
+    if (doubt || j < plain0 || j - plain0 >= plain_n) {
+      uint32_t rows_seen = 0;  // a bit per row of the step
 #pragma unroll
       for (int k = 0; k < L::kStep; ++k) {
         const int i = j * L::kStep + k, row = i < nt ? tile_row(v, tile_no(i)) : 0, at = row + (lane & 15);
         const bool sees = i < nt && (at < v.first || (at >= v.lo && at < v.len)) && page_of(row) >= 0;
         rows_seen |= (__ballot_sync(0xffffffffu, sees) & 0xffff) << (16 * k);
       }
+      st.template step<true>(smem + slot, lane, rows_seen);
+    } else {
+      st.template step<false>(smem + slot, lane, 0);
     }
-    st.step(smem + slot, lane, edge, rows_seen);
     __syncwarp();
     issue(j + ST, smem_u32(smem) + slot);
     slot += L::kSlot;
