@@ -138,12 +138,13 @@ __device__ __forceinline__ uint32_t take_f16(float& x, float& y) {
   return w;
 }
 
-// Copies `bytes` (16, or 0: then zeros are written) where `on`.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes, bool on = true) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"((int)on)
-      : "memory");
+// Copies N bytes, of which the first `bytes` (N, or 0) from src and zeros for the rest.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(N) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -748,25 +749,25 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 };
 
 // Fills a stage with a tile: K's rows (Q4: codes) begin at `src`, their scales
-// `scales` bytes behind, V's half_bytes behind K's; bytes 0: with zeros.
+// `scales` bytes behind, V's half_bytes behind K's; not `there`: with zeros.
 template <int D, bool Q4>
 __device__ __forceinline__ void stage_tile(uint32_t dst, const uint8_t* src, int scales, int64_t half_bytes, int lane,
-                                           int bytes) {
+                                           bool there) {
   using L = Tile<D, Q4>;
   constexpr int PPR = L::kRowBytes / 16, N = kTileRows * PPR / 32;
   const uint8_t* k = src + 16 * lane;
-  const uint8_t* v = k + half_bytes;
+  const uint8_t* v = src + (half_bytes + 16 * lane);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int at = i * 32 + lane, to = staged<D, Q4>(at / PPR, at % PPR);
-    cp_async16(dst + to, k + 512 * i, bytes);
-    cp_async16(dst + L::kHalf + to, v + 512 * i, bytes);
+    cp_async<16>(dst + to, k + 512 * i, there ? 16 : 0);
+    cp_async<16>(dst + L::kHalf + to, v + 512 * i, there ? 16 : 0);
   }
-  if constexpr (Q4) {
-    constexpr int NS = 2 * L::NB;  // 16-byte pieces of the scales of K, and of V
-    const bool second = lane >= NS;
-    cp_async16(dst + kTileRows * L::kRowBytes + 16 * lane + (second ? L::kHalf - 16 * NS : 0),
-               (second ? v - 16 * NS : k) + scales, bytes, lane < 2 * NS);
+  if constexpr (Q4) {  // half the lanes K's scales, half V's
+    constexpr int kPart = L::NB * 2;
+    const int64_t from = (lane < 16 ? 0 : half_bytes) + (lane & 15) * kPart;
+    const int to = kTileRows * L::kRowBytes + (lane < 16 ? 0 : L::kHalf) + (lane & 15) * kPart;
+    cp_async<kPart>(dst + to, src + (from + scales), there ? kPart : 0);
   }
 }
 
@@ -855,7 +856,7 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
         const unsigned long long src = __shfl_sync(0xffffffffu, cur_src, i);
         const int scales = __shfl_sync(0xffffffffu, cur_scales, i);
         stage_tile<D, Q4>(dst + k * L::kBytes, reinterpret_cast<const uint8_t*>(src), max(scales, 0), c.half_bytes, lane,
-                          scales < 0 ? 0 : 16);
+                          scales >= 0);
       }
     }
     cp_async_commit();
