@@ -465,10 +465,13 @@ int dec_kv_read(const dec_kv_cache* c, int layer, void* k, void* v, int type, in
  * q . k_j) v_j, query head h reading KV head floor(h * n_kv_heads /
  * n_q_heads), n_q_heads any multiple of n_kv_heads; scale 0 means
  * 1 / sqrt(head_dim).  No visible row: o = 0.  Rows not visible are not looked
- * at (whatever they hold); those visible must hold finite values.  Scores,
- * sums and weights are fp32; the same call gives the same bits.  A visible row
+ * at (whatever they hold); those visible must hold finite values, or the
+ * outputs are NaN.  Scores and sums are fp32.  Weights keep 24 bits (16 for
+ * bf16 results); over 4-bit pages 22 bits (11 for bf16 results), down to about
+ * 2^-30 of the largest.  The same call gives the same bits.  A visible row
  * without a valid page is left out and sets DEC_KV_BAD_INDEX.  q, o and their
- * strides are multiples of 16 bytes; o must not overlap q.
+ * strides are multiples of 16 bytes; o must not overlap q.  n * n_q_heads is
+ * at most 2^24.
  * workspace: device memory of dec_kv_attention_workspace bytes, 16-byte
  * aligned, for this call alone (its content does not matter before or after,
  * and calls that may overlap need one each). */

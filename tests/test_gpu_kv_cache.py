@@ -158,6 +158,34 @@ def test_attention_long_sequences_and_rising_scores(fmt, hd):
     f.check(q[:1], one, [0])
 
 
+@pytest.mark.parametrize("fmt,nkv,io,n", [
+    ("bf16", 1, torch.float32, 140), ("q4", 1, torch.float32, 140), ("bf16", 2, torch.bfloat16, 300),
+    ("q4", 2, torch.bfloat16, 300), ("q4", 3, torch.float32, 700)])
+def test_attention_many_queries(fmt, nkv, io, n):
+    """More queries than are counted at once, fewer and more units than CTAs, long and short and empty
+    sequences and padding among them; with and without the last query of each."""
+    lens = [0, 1, 40, 300, 4000, 17]
+    f = Filled(fmt, nkv, 64, 32, lens, seed=n)
+    rng = np.random.default_rng(n)
+    seqs = rng.choice([-1, 0, 1, 2, 3, 5, 1, 2, 5], n)
+    seqs[[3, n // 2, n - 2]] = 4
+    q = torch.randn(n, 2 * nkv, 64, device="cuda").to(io)
+    out = f.cache.attention(f.layer, q, seqs=ints(seqs))
+    f.cache.sync_status()
+    f.check(q, out, seqs)
+    assert torch.all(out[torch.tensor(seqs < 1)] == 0)
+    seqs[:] = rng.choice([1, 2], n)                      # all short, and hardly any
+    out = f.cache.attention(f.layer, q, seqs=ints(seqs))
+    f.check(q, out, seqs)
+    seqs[:] = -1
+    keep = torch.full_like(q, 3)
+    assert torch.all(f.cache.attention(f.layer, q, seqs=ints(seqs), out=keep) == 3)
+    seqs[n - 1] = 4
+    out = f.cache.attention(f.layer, q, seqs=ints(seqs))
+    f.check(q, out, seqs)
+    f.cache.sync_status()
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "q4"])
 def test_attention_lists_strides_and_padding(fmt):
     """Sequences in any order and twice, padding left as it was, q and out as parts of wider rows."""
@@ -287,6 +315,37 @@ def test_attention_in_graphs_and_streams():
             f.check(q, out, range(2), what=f"window {win}, lengths {lens}")
     with pytest.raises(ValueError, match="workspace"):
         f.cache.attention(f.layer, q, stream=side)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+def test_attention_without_workspaces_on_streams_and_in_graphs(fmt):
+    """Calls that share nothing but the cache: two streams at once, and two graphs replayed beside them."""
+    f = Filled(fmt, 2, 128, 16, [3000, 2500], seed=8)
+    qs = [torch.randn(2, 4, 128, device="cuda") for _ in range(4)]
+    want = [f.cache.attention(f.layer, q).clone() for q in qs]
+    f.check(qs[0], want[0], range(2))
+    outs = [torch.empty_like(q) for q in qs]
+    graphs = []
+    for i in (2, 3):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f.cache.attention(f.layer, qs[i], out=outs[i])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(20):
+        torch.cuda.synchronize()
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if i < 2:
+                    f.cache.attention(f.layer, qs[i], out=outs[i])
+                else:
+                    graphs[i - 2].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    f.cache.sync_status()
 
 
 # ---- rows ------------------------------------------------------------------------

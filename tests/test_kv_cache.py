@@ -1,6 +1,8 @@
 """CPU checks of the paged cache's calls: what is refused before anything is
 queued, the sizes, and the plain statements its GPU tests compare with."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -192,3 +194,12 @@ def test_reference_model_counts_pages():
         named = np.bincount(m.table[m.table >= 0], minlength=40)
         assert np.array_equal(named, m.refs)
     assert m.bits
+
+
+def test_codes_without_divisions(tmp_path):
+    """The quotients behind the 4-bit codes and scales, against IEEE division and 64 bits."""
+    exe = tmp_path / "kv_codes_check"
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "host", "kv_codes_check.cpp")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-ffp-contract=off", src, "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and "OK" in r.stdout, r.stdout

@@ -37,13 +37,18 @@ struct Tile {
   static constexpr int kHalf = kTileRows * (kRowBytes + (Q4 ? 2 * NB : 0));  // K or V, scales after the rows
   static constexpr int kBytes = 2 * kHalf;
   static constexpr int kStep = Q4 ? 2 : 1;                           // tiles a warp takes at a time
-  static constexpr int kStages = Q4 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 4);  // steps in its ring
+  static constexpr int kStages = Q4 ? (D == 128 ? 2 : 4) : (D == 128 ? 2 : 4);  // steps in its ring
   static constexpr int kSlot = kStep * kBytes;
   static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kMergeRow = D + 8;                            // floats; heads apart by 8 banks
   static constexpr int kMerge = kWarps * kHeadBlock * kMergeRow * 4; // the warps' sums, once the ring is drained
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
   static constexpr int kCtasPerSm = 3;
+  // What a unit costs a CTA besides its tiles (page numbers, q, the sums of the
+  // warps: about 2.5 us), in tiles; the tiles up to which a unit is not cut
+  // between CTAs; and those up to which, if none can have more, every unit is
+  // left to one CTA and nothing is counted.
+  static constexpr int kUnit = Q4 ? 24 : 12, kShort = Q4 ? 40 : 20, kWhole = Q4 ? 48 : 24;
 };
 
 struct KvAttnParams {
@@ -337,10 +342,10 @@ struct WarpBf16 : WarpHead<D> {
 
   // One staged tile.  EDGE: some row is not visible; rows_seen: a bit for each that is.
   template <bool EDGE>
-  __device__ __forceinline__ void step(const uint8_t* st, int lane, uint32_t rows_seen) {
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, uint64_t rows_seen) {
     using L = Tile<D, false>;
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t seen = rows_of_lane(rows_seen, t);
+    const uint32_t seen = rows_of_lane((uint32_t)rows_seen, t);
     const uint8_t* sv = st + L::kHalf;
     float s[4];
 #pragma unroll
@@ -522,7 +527,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 
   // kTiles staged tiles.  EDGE: some row is not visible; rows_seen: a bit for each that is.
   template <bool EDGE>
-  __device__ __forceinline__ void step(const uint8_t* st, int lane, uint32_t rows_seen) {
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, uint64_t rows_seen) {
     const int g = lane >> 2, t = lane & 3;
     // scores: of head g, rows 2t, 2t + 1 of each half; kWhole: of heads 2t, 2t + 1, rows g and g + 8
     float s[4 * kTiles];
@@ -534,7 +539,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       if (D == 128 || lane < 16) {
         __half2 h = *reinterpret_cast<const __half2*>(ks_at + L::kHalf + 4 * lane);
         if (EDGE && !(rows_seen >> (16 * k + lane / (NB / 2)) & 1)) h = __float2half2_rn(0.f);
-        most = __hmax2(most, h);
+        most = __hmax2(most, __habs2(h));
       }
       uint32_t w[2][NB];  // rows g, g + 8: blocks 0, 1 (and 2, 3) of dimension groups 2t, then of 2t + 1
 #pragma unroll
@@ -621,7 +626,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
           s[4 * k + 2 * b + 1] = s1 * f;
         }
         if (EDGE) {
-          const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
+          const uint32_t seen = rows_of_lane((uint32_t)(rows_seen >> (16 * k)) & 0xffff, t);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (!(seen >> i & 1)) s[4 * k + i] = -INFINITY;
@@ -674,7 +679,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
         else *reinterpret_cast<uint2*>(vs[2 * b]) = *reinterpret_cast<const uint2*>(vs_at + 32 * b + 8 * t);
       }
       if (EDGE) {  // 0 * NaN would be NaN
-        const uint32_t seen = rows_of_lane(rows_seen >> (16 * k), t);
+        const uint32_t seen = rows_of_lane((uint32_t)(rows_seen >> (16 * k)) & 0xffff, t);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (!(seen >> i & 1)) {
@@ -786,11 +791,6 @@ __device__ __forceinline__ void store_out(T* p, const float (&x)[N]) {
 // The sum over no weight is zero; NaN stays.
 __device__ __forceinline__ float over(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
-// What a unit costs a CTA besides its tiles (page numbers, q, the sums of the
-// warps: about 2.5 us, a few rounds of the warps), in rounds; and the rounds up
-// to which a unit is not cut.
-constexpr int kUnitRounds = 3, kShortRounds = 5;
-
 // What a thread holds of a unit's sums over a CTA's tiles: N dimensions from e
 // of head h, relative to the reference m, and the sum of the weights.
 template <int D>
@@ -879,12 +879,12 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
     cp_async_wait<ST - 1>();
     __syncwarp();
     if (doubt || j < plain0 || j - plain0 >= plain_n) {
-      uint32_t rows_seen = 0;  // a bit per row of the step
+      uint64_t rows_seen = 0;  // a bit per row of the step
 #pragma unroll
       for (int k = 0; k < L::kStep; ++k) {
         const int i = j * L::kStep + k, row = i < nt ? tile_row(v, tile_no(i)) : 0, at = row + (lane & 15);
         const bool sees = i < nt && (at < v.first || (at >= v.lo && at < v.len)) && page_of(row) >= 0;
-        rows_seen |= (__ballot_sync(0xffffffffu, sees) & 0xffff) << (16 * k);
+        rows_seen |= (uint64_t)(__ballot_sync(0xffffffffu, sees) & 0xffff) << (16 * k);
       }
       st.template step<true>(smem + slot, lane, rows_seen);
     } else {
@@ -967,8 +967,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm)
 }
 
 // A CTA's share of the line and where it stands in it.  The line is all units
-// in order, each as long as its tiles and kUnitRounds rounds more, which come
-// first.
+// in order, each as long as its tiles and `unit` more, which come first.
 struct Share {
   int64_t pos, end;      // positions in the line
   int64_t before;        // the length of one unit each of the queries before r
@@ -981,42 +980,47 @@ template <int D, bool Q4, class T>
 __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(const __grid_constant__ KvAttnParams p) {
   using L = Tile<D, Q4>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t chunk_tiles[kMaxChunks];
+  __shared__ int64_t chunk_sum[kMaxChunks];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvView& c = p.c;
   pdl_trigger();
 
   // ---- this CTA's share of the line
-  constexpr int kRound = kWarps * L::kStep, kUnit = kUnitRounds * kRound;
+  constexpr int kRound = kWarps * L::kStep;
   const int chunks = (p.n + kChunkRows - 1) / kChunkRows;
   const int units = c.nkv * p.head_blocks;
   bool bad = false, empty = false;
-  int mine[4];  // the lengths of units of queries 32 i + lane of a chunk
+  int mine[4];  // tiles of a unit of queries 32 i + lane of a chunk
   auto count = [&](int chunk) {
-    int64_t sum = 0;
+    int64_t sum = 0;  // tiles, and the queries that have any from bit 48 up
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = chunk * kChunkRows + 32 * i + lane;
       Rows v{-1, 0, 0, 0, 0, 0, 0};
       if (r < p.n) v = query_rows(p, r, &bad);
-      mine[i] = v.tiles ? v.tiles + kUnit : 0;
-      sum += mine[i];
+      mine[i] = v.tiles;
+      sum += v.tiles + ((int64_t)(v.tiles > 0) << 48);
       empty |= r < p.n && v.tiles == 0;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
   };
-  int64_t length = 0;
+  int64_t tiles = 0;
+  int queries = 0;
+  auto add = [&](int64_t sum) {
+    tiles += sum & ((1ll << 48) - 1);
+    queries += (int)(sum >> 48);
+  };
   if (chunks == 1) {
-    length = count(0);  // every warp for itself
+    add(count(0));  // every warp for itself
   } else {
     for (int k = warp; k < chunks; k += kWarps) {
       const int64_t sum = count(k);
-      if (lane == 0) chunk_tiles[k] = sum;
+      if (lane == 0) chunk_sum[k] = sum;
     }
     __syncthreads();
-    for (int k = 0; k < chunks; ++k) length += chunk_tiles[k];
+    for (int k = 0; k < chunks; ++k) add(chunk_sum[k]);
   }
   if (bad && blockIdx.x == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
   if (__syncthreads_or(empty)) {  // queries that see no row, or are skipped
@@ -1030,16 +1034,23 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       for (int64_t e = tid; e < (int64_t)p.nq * D; e += kThreadsA) out[e] = 0;
     }
   }
-  const int64_t total = length * units;
+  // What a unit counts besides its tiles: what it costs; but where all are long
+  // and the shares short, a share has one unit at most and the cost is the same
+  // for all.
+  const int unit = tiles <= (int64_t)L::kShort * queries
+                       ? L::kUnit
+                       : (int)min((int64_t)L::kUnit, tiles * units / (int64_t)gridDim.x);
+  const int64_t total = (tiles + (int64_t)unit * queries) * units;
   // One share per CTA; small ones of whole rounds, so that every warp has as much.
   const int64_t rounds = (total + (int64_t)gridDim.x * kRound - 1) / ((int64_t)gridDim.x * kRound);
-  const int64_t parts = rounds > 3 ? gridDim.x : total / (max(rounds, (int64_t)1) * kRound);
+  const int64_t parts = rounds > 3 ? gridDim.x : (total + rounds * kRound - 1) / (max(rounds, (int64_t)1) * kRound);
   __shared__ Share share;  // (not in registers: the products need them)
   if (blockIdx.x < parts) {
     // The border between two shares is moved to the nearer end of a unit that
     // is short, in itself or beside a share, and to an end of a long one that
-    // is less than a round off.
-    const int64_t shortest = max((int64_t)kShortRounds * kRound, total / parts / 16) + kUnit;
+    // is less than kLeast tiles off (shares are longer).
+    constexpr int kLeast = kRound / 2;
+    const int64_t shortest = max((int64_t)L::kShort, total / parts / 16) + unit;
     int64_t before;
     int r, r_len;
     auto locate = [&](int64_t want) {  // the query with position `want` of the line
@@ -1048,12 +1059,14 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       r = r_len = 0;
       int k = 0;
       if (chunks > 1) {
-        while (k + 1 < chunks && before + chunk_tiles[k] <= want) before += chunk_tiles[k++];
+        auto length = [&](int at) { return (chunk_sum[at] & ((1ll << 48) - 1)) + unit * (chunk_sum[at] >> 48); };
+        while (k + 1 < chunks && before + length(k) <= want) before += length(k++);
         count(k);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        int64_t incl = mine[i];
+        const int len = mine[i] ? mine[i] + unit : 0;
+        int64_t incl = len;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -1062,7 +1075,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
         const uint32_t past = __ballot_sync(0xffffffffu, before + incl > want);
         if (past) {
           const int at = __ffs(past) - 1;
-          r_len = __shfl_sync(0xffffffffu, mine[i], at);
+          r_len = __shfl_sync(0xffffffffu, len, at);
           before += __shfl_sync(0xffffffffu, incl, at) - r_len;
           r = k * kChunkRows + 32 * i + at;
           break;
@@ -1077,8 +1090,8 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
         if (r_len > 0) {
           const int in = (int)((pos - before * units) % r_len);
           if (r_len <= shortest) pos += 2 * in < r_len ? -in : r_len - in;
-          else if (in < kUnit + kRound) pos -= in;
-          else if (in > r_len - kRound) pos += r_len - in;
+          else if (in < unit + kLeast) pos -= in;
+          else if (in > r_len - kLeast) pos += r_len - in;
         }
       }
       return pos;
@@ -1091,12 +1104,12 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
 
     while (share.pos < share.end) {
       const int64_t rel = share.pos - share.before * units;
-      const int len = v.tiles + kUnit;
+      const int len = v.tiles + unit;
       // (not so only if lengths change while the call runs: then leave, in bounds)
       if (v.tiles == 0 || rel < 0 || rel >= (int64_t)len * units) break;
       const int u = (int)(rel / len), in = (int)(rel - (int64_t)u * len);
-      const int t0 = max(in - kUnit, 0);
-      const int t1 = max((int)min((int64_t)len, in + (share.end - share.pos)) - kUnit, t0);
+      const int t0 = max(in - unit, 0);
+      const int t1 = max((int)min((int64_t)len, in + (share.end - share.pos)) - unit, t0);
       if (tid == 0) share.u = u, share.t0 = t0, share.t1 = t1;  // (read after the barriers within unit_sums)
       UnitSums<D> o = unit_sums<D, Q4, T>(p, v, share.r, u, t0, t1, smem);
       const bool begins = share.t0 == 0, ends = share.t1 == v.tiles;
@@ -1110,17 +1123,17 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       if (begins && tid == 0) {
         int more = 0;  // borders within the unit
         if (!ends) {
-          const int64_t first = share.before * units + (int64_t)share.u * (v.tiles + kUnit);
+          const int64_t first = share.before * units + (int64_t)share.u * (v.tiles + unit);
           auto owner = [&](int64_t x) { return ((x + 1) * share.parts - 1) / share.total; };
-          more = (int)(owner(first + v.tiles + kUnit - kRound) - owner(first + kUnit + kRound - 1));
+          more = (int)(owner(first + v.tiles + unit - kLeast) - owner(first + unit + kLeast - 1));
         }
         if (p.cut_by_unit) p.cut[share.r * units + share.u] = make_int4(share.r, share.u, blockIdx.x, more);
         else if (more) p.cut[blockIdx.x] = make_int4(share.r, share.u, blockIdx.x, more);
         share.cut |= more;
       }
       const bool next = ends && share.u == units - 1;
-      const int64_t now = share.before * units + (int64_t)share.u * (v.tiles + kUnit) + kUnit + share.t1;
-      const int64_t past = share.before + v.tiles + kUnit;
+      const int64_t now = share.before * units + (int64_t)share.u * (v.tiles + unit) + unit + share.t1;
+      const int64_t past = share.before + v.tiles + unit;
       int at = share.r;
       if (next && now < share.end && at + 1 < p.n) {
         do v = query_rows(p, ++at, &bad);
@@ -1214,8 +1227,6 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 }
 
 constexpr int kMaxDevices = 64;
-// Where no unit can be longer than so many rounds of a CTA's warps, each is left to one CTA.
-constexpr int kWholeRounds = 6;
 
 // SMs of the current device (they do not change: looked up once).
 int device_sms(int* dev, int* sms) {
@@ -1272,7 +1283,7 @@ cudaError_t launch_attn_kv(KvAttnParams p, int dev, int ctas, cudaStream_t s) {
   cfg.blockDim = dim3(kThreadsA);
   cfg.dynamicSmemBytes = Tile<D, Q4>::kSmem;
   cfg.stream = s;
-  if (longest_unit(p) <= kWholeRounds * kWarps * Tile<D, Q4>::kStep) {
+  if (longest_unit(p) <= Tile<D, Q4>::kWhole) {
     cfg.gridDim = dim3((unsigned)std::min(units, (int64_t)ctas));
     return cudaLaunchKernelEx(&cfg, kv_attn_whole<D, Q4, T>, p);
   }
