@@ -974,6 +974,7 @@ struct Share {
   int64_t total, parts;  // length and shares of the whole line
   int r, u, t0, t1;      // the unit at hand
   int cut;               // a unit begins here that ends elsewhere
+  int more;              // CTAs that the unit which begins here goes on for; -1: to be worked out
 };
 
 template <int D, bool Q4, class T>
@@ -986,70 +987,96 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
   pdl_trigger();
 
   // ---- this CTA's share of the line
-  constexpr int kRound = kWarps * L::kStep;
+  constexpr int kRound = kWarps * L::kStep, kLeast = kRound / 2;
   const int chunks = (p.n + kChunkRows - 1) / kChunkRows;
   const int units = c.nkv * p.head_blocks;
   bool bad = false, empty = false;
-  int mine[4];  // tiles of a unit of queries 32 i + lane of a chunk
-  auto count = [&](int chunk) {
-    int64_t sum = 0;  // tiles, and the queries that have any from bit 48 up
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = chunk * kChunkRows + 32 * i + lane;
-      Rows v{-1, 0, 0, 0, 0, 0, 0};
-      if (r < p.n) v = query_rows(p, r, &bad);
-      mine[i] = v.tiles;
-      sum += v.tiles + ((int64_t)(v.tiles > 0) << 48);
-      empty |= r < p.n && v.tiles == 0;
+  __shared__ Share share;  // (not in registers: the products need them)
+  Rows v{-1, 0, 0, 0, 0, 0, 0};
+  auto hidden = [&](int r, const Rows& rows) {  // a query that sees no row, or is skipped
+    if (p.cut_by_unit)
+      for (int u = tid; u < units; u += kThreadsA) p.cut[r * units + u] = make_int4(0, 0, 0, 0);
+    if (rows.seq < 0) return;
+    T* out = static_cast<T*>(p.o) + r * p.o_stride;
+    for (int64_t e = tid; e < (int64_t)p.nq * D; e += kThreadsA) out[e] = 0;
+  };
+  int unit = 0;  // what a unit counts besides its tiles
+  if (p.n == 1 && units <= (int)gridDim.x) {
+    // One query: its units are alike, each is cut into as many parts as there are
+    // CTAs for it, of whole rounds if they are small.  (Counting and looking for
+    // borders, below, would take 2.5 us of a short call.)
+    v = query_rows(p, 0, &bad);
+    if (bad && blockIdx.x == 0 && tid == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
+    if (v.tiles == 0) {
+      if (blockIdx.x == 0) hidden(0, v);
+      return;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
-  };
-  int64_t tiles = 0;
-  int queries = 0;
-  auto add = [&](int64_t sum) {
-    tiles += sum & ((1ll << 48) - 1);
-    queries += (int)(sum >> 48);
-  };
-  if (chunks == 1) {
-    add(count(0));  // every warp for itself
-  } else {
-    for (int k = warp; k < chunks; k += kWarps) {
-      const int64_t sum = count(k);
-      if (lane == 0) chunk_sum[k] = sum;
+    const int most = gridDim.x / units, even = (v.tiles + most - 1) / most;
+    const int size = even <= 3 * kRound ? (even + kRound - 1) / kRound * kRound : even;
+    const int cuts = (v.tiles + size - 1) / size;
+    const int u = blockIdx.x / cuts, t0 = (blockIdx.x - u * cuts) * size;
+    if (u >= units) return;
+    if (tid == 0) {
+      const int64_t first = (int64_t)u * v.tiles;
+      share = Share{first + t0, first + min(t0 + size, v.tiles), 0, 0, 0, 0, 0, 0, 0, 0, cuts - 1};
     }
     __syncthreads();
-    for (int k = 0; k < chunks; ++k) add(chunk_sum[k]);
-  }
-  if (bad && blockIdx.x == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
-  if (__syncthreads_or(empty)) {  // queries that see no row, or are skipped
-    for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
-      const Rows v = query_rows(p, r, &bad);
-      if (v.tiles) continue;
-      if (p.cut_by_unit)
-        for (int u = tid; u < units; u += kThreadsA) p.cut[r * units + u] = make_int4(0, 0, 0, 0);
-      if (v.seq < 0) continue;
-      T* out = static_cast<T*>(p.o) + r * p.o_stride;
-      for (int64_t e = tid; e < (int64_t)p.nq * D; e += kThreadsA) out[e] = 0;
+  } else {
+    int mine[4];  // tiles of a unit of queries 32 i + lane of a chunk
+    auto count = [&](int chunk) {
+      int64_t sum = 0;  // tiles, and the queries that have any from bit 48 up
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = chunk * kChunkRows + 32 * i + lane;
+        Rows v{-1, 0, 0, 0, 0, 0, 0};
+        if (r < p.n) v = query_rows(p, r, &bad);
+        mine[i] = v.tiles;
+        sum += v.tiles + ((int64_t)(v.tiles > 0) << 48);
+        empty |= r < p.n && v.tiles == 0;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      return sum;
+    };
+    int64_t tiles = 0;
+    int queries = 0;
+    auto add = [&](int64_t sum) {
+      tiles += sum & ((1ll << 48) - 1);
+      queries += (int)(sum >> 48);
+    };
+    if (chunks == 1) {
+      add(count(0));  // every warp for itself
+    } else {
+      for (int k = warp; k < chunks; k += kWarps) {
+        const int64_t sum = count(k);
+        if (lane == 0) chunk_sum[k] = sum;
+      }
+      __syncthreads();
+      for (int k = 0; k < chunks; ++k) add(chunk_sum[k]);
     }
-  }
-  // What a unit counts besides its tiles: what it costs; but where all are long
-  // and the shares short, a share has one unit at most and the cost is the same
-  // for all.
-  const int unit = tiles <= (int64_t)L::kShort * queries
-                       ? L::kUnit
-                       : (int)min((int64_t)L::kUnit, tiles * units / (int64_t)gridDim.x);
-  const int64_t total = (tiles + (int64_t)unit * queries) * units;
-  // One share per CTA; small ones of whole rounds, so that every warp has as much.
-  const int64_t rounds = (total + (int64_t)gridDim.x * kRound - 1) / ((int64_t)gridDim.x * kRound);
-  const int64_t parts = rounds > 3 ? gridDim.x : (total + rounds * kRound - 1) / (max(rounds, (int64_t)1) * kRound);
-  __shared__ Share share;  // (not in registers: the products need them)
-  if (blockIdx.x < parts) {
+    if (bad && blockIdx.x == 0) atomicOr(c.status, DEC_KV_BAD_INDEX);
+    if (__syncthreads_or(empty)) {
+      for (int r = blockIdx.x; r < p.n; r += gridDim.x) {
+        const Rows rows = query_rows(p, r, &bad);
+        if (rows.tiles == 0) hidden(r, rows);
+      }
+    }
+    // What a unit counts besides its tiles: what it costs; but where all are long
+    // and the shares short, a share has one unit at most and the cost is the same
+    // for all.
+    unit = tiles <= (int64_t)L::kShort * queries ? L::kUnit
+                                                 : (int)min((int64_t)L::kUnit, tiles * units / (int64_t)gridDim.x);
+    const int64_t total = (tiles + (int64_t)unit * queries) * units;
+    // One share per CTA; small ones of whole rounds, so that every warp has as much.
+    const int64_t rounds = (total + (int64_t)gridDim.x * kRound - 1) / ((int64_t)gridDim.x * kRound);
+    const int64_t parts = rounds > 3 ? gridDim.x : (total + rounds * kRound - 1) / (max(rounds, (int64_t)1) * kRound);
+    if (blockIdx.x >= parts) {
+      if (!p.cut_by_unit && tid == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+      return;
+    }
     // The border between two shares is moved to the nearer end of a unit that
     // is short, in itself or beside a share, and to an end of a long one that
     // is less than kLeast tiles off (shares are longer).
-    constexpr int kLeast = kRound / 2;
     const int64_t shortest = max((int64_t)L::kShort, total / parts / 16) + unit;
     int64_t before;
     int r, r_len;
@@ -1098,58 +1125,56 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
     };
     const int64_t end = border(blockIdx.x + 1), pos = border(blockIdx.x);
     if (pos < end && pos >= (before + r_len) * units) locate(pos);  // moved on to the next query
-    if (tid == 0) share = Share{pos, end, before, total, parts, r, 0, 0, 0, 0};
+    if (tid == 0) share = Share{pos, end, before, total, parts, r, 0, 0, 0, 0, -1};
     __syncthreads();
-    Rows v = query_rows(p, r, &bad);
-
-    while (share.pos < share.end) {
-      const int64_t rel = share.pos - share.before * units;
-      const int len = v.tiles + unit;
-      // (not so only if lengths change while the call runs: then leave, in bounds)
-      if (v.tiles == 0 || rel < 0 || rel >= (int64_t)len * units) break;
-      const int u = (int)(rel / len), in = (int)(rel - (int64_t)u * len);
-      const int t0 = max(in - unit, 0);
-      const int t1 = max((int)min((int64_t)len, in + (share.end - share.pos)) - unit, t0);
-      if (tid == 0) share.u = u, share.t0 = t0, share.t1 = t1;  // (read after the barriers within unit_sums)
-      UnitSums<D> o = unit_sums<D, Q4, T>(p, v, share.r, u, t0, t1, smem);
-      const bool begins = share.t0 == 0, ends = share.t1 == v.tiles;
-      if (begins && ends) {
-        write_unit<D, T>(p, share.r, share.u, o);
-      } else {  // a part: slot 1 where the unit begins here, slot 0 where it began before
-        const int64_t slot = (2 * (int64_t)blockIdx.x + begins) * kHeadBlock + tid / 16;
-        store_out(p.rec + slot * D + (tid % 16) * o.N, o.x);
-        if (tid % 16 == 0) p.ref[slot] = make_float2(o.m, o.l);
-      }
-      if (begins && tid == 0) {
-        int more = 0;  // borders within the unit
-        if (!ends) {
-          const int64_t first = share.before * units + (int64_t)share.u * (v.tiles + unit);
-          auto owner = [&](int64_t x) { return ((x + 1) * share.parts - 1) / share.total; };
-          more = (int)(owner(first + v.tiles + unit - kLeast) - owner(first + unit + kLeast - 1));
-        }
-        if (p.cut_by_unit) p.cut[share.r * units + share.u] = make_int4(share.r, share.u, blockIdx.x, more);
-        else if (more) p.cut[blockIdx.x] = make_int4(share.r, share.u, blockIdx.x, more);
-        share.cut |= more;
-      }
-      const bool next = ends && share.u == units - 1;
-      const int64_t now = share.before * units + (int64_t)share.u * (v.tiles + unit) + unit + share.t1;
-      const int64_t past = share.before + v.tiles + unit;
-      int at = share.r;
-      if (next && now < share.end && at + 1 < p.n) {
-        do v = query_rows(p, ++at, &bad);
-        while (v.tiles == 0 && at + 1 < p.n);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        share.pos = now;
-        if (next) share.before = past, share.r = at;
-      }
-      __syncthreads();
-    }
-    if (!p.cut_by_unit && tid == 0 && !share.cut) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
-  } else if (!p.cut_by_unit && tid == 0) {
-    p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    v = query_rows(p, r, &bad);
   }
+
+  while (share.pos < share.end) {
+    const int64_t rel = share.pos - share.before * units;
+    const int len = v.tiles + unit;
+    // (not so only if lengths change while the call runs: then leave, in bounds)
+    if (v.tiles == 0 || rel < 0 || rel >= (int64_t)len * units) break;
+    const int u = (int)(rel / len), in = (int)(rel - (int64_t)u * len);
+    const int t0 = max(in - unit, 0);
+    const int t1 = max((int)min((int64_t)len, in + (share.end - share.pos)) - unit, t0);
+    if (tid == 0) share.u = u, share.t0 = t0, share.t1 = t1;  // (read after the barriers within unit_sums)
+    UnitSums<D> o = unit_sums<D, Q4, T>(p, v, share.r, u, t0, t1, smem);
+    const bool begins = share.t0 == 0, ends = share.t1 == v.tiles;
+    if (begins && ends) {
+      write_unit<D, T>(p, share.r, share.u, o);
+    } else {  // a part: slot 1 where the unit begins here, slot 0 where it began before
+      const int64_t slot = (2 * (int64_t)blockIdx.x + begins) * kHeadBlock + tid / 16;
+      store_out(p.rec + slot * D + (tid % 16) * o.N, o.x);
+      if (tid % 16 == 0) p.ref[slot] = make_float2(o.m, o.l);
+    }
+    if (begins && tid == 0) {
+      int more = ends ? 0 : share.more;  // borders within the unit
+      if (more < 0) {
+        const int64_t first = share.before * units + (int64_t)share.u * (v.tiles + unit);
+        auto owner = [&](int64_t x) { return ((x + 1) * share.parts - 1) / share.total; };
+        more = (int)(owner(first + v.tiles + unit - kLeast) - owner(first + unit + kLeast - 1));
+      }
+      if (p.cut_by_unit) p.cut[share.r * units + share.u] = make_int4(share.r, share.u, blockIdx.x, more);
+      else if (more) p.cut[blockIdx.x] = make_int4(share.r, share.u, blockIdx.x, more);
+      share.cut |= more;
+    }
+    const bool next = ends && share.u == units - 1;
+    const int64_t now = share.before * units + (int64_t)share.u * (v.tiles + unit) + unit + share.t1;
+    const int64_t past = share.before + v.tiles + unit;
+    int at = share.r;
+    if (next && now < share.end && at + 1 < p.n) {
+      do v = query_rows(p, ++at, &bad);
+      while (v.tiles == 0 && at + 1 < p.n);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      share.pos = now;
+      if (next) share.before = past, share.r = at;
+    }
+    __syncthreads();
+  }
+  if (!p.cut_by_unit && tid == 0 && !share.cut) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
 // Joins the parts of the units that are cut, in their order.  WARPS warps take
