@@ -15,8 +15,8 @@ they are off by at most 2^-25, where the weight that sets the reference is 2^9
 and the scale enters as s / 2^e, 2^e <= 2 s for the largest scale s (of 2^-14 or
 more).  With codes up to 8 and a sum of weights of at least 2^9, n rows are off
 by at most n * 8 * 2^-25 / 2^9 * 2^e <= n * 2^-30 * s.  (For bf16 results scales
-below one enter as they are, e = 0, so there s counts as at least 1/2.)  It
-shows only where the rows that hold the weight are zero in a dimension.  A
+between 2^-7 and 1 enter as they are, e = 0, so there s counts as at least 1/2.)
+It shows only where the rows that hold the weight are zero in a dimension.  A
 block's largest code is 7, so s is the largest |v| / 7.
 """
 import numpy as np
@@ -94,7 +94,8 @@ class Filled:
             ds = (self.pages.d + 8) * 2.0 ** -24 * np.abs(dots)[:, None]
             tol = size * (2 * ds + 2 * n * 2.0 ** -24 + 2.0 ** -19)
             if self.pages.fmt == "q4" and n:
-                tol = tol + n * 2.0 ** -30 * max(np.abs(self.v[s]).max() / 7, 0.5 if bf16 else 0)
+                top = np.abs(self.v[s]).max() / 7
+                tol = tol + n * 2.0 ** -30 * max(top, 0.5 if bf16 and top > 2 ** -8 else 2 ** -14)
                 tol = tol + (size * 2.0 ** -10 if bf16 else 0)
             tol = tol + (np.abs(o) + tol) * (2.0 ** -8 if bf16 else 2.0 ** -24) + 1e-37
             bad = np.abs(got[r] - o) > tol
@@ -227,6 +228,20 @@ def test_attention_extreme_queries(fmt):
     for scale in (0.125, -0.02):
         out = f.cache.attention(f.layer, q, scale=scale)
         f.check(q, out, range(5), scale=scale)
+    f.cache.sync_status()
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [(1e5,), (1e-3,), (3e-6,), (1e-4, 1, 1e4), (1e4, 1, 1e-4)])
+def test_attention_value_sizes_over_4_bits(io, sizes):
+    """V scales from fp16's smallest numbers to its largest, rising and falling along a sequence."""
+    def v_of(s, h, pos, rng):
+        return rng.normal(0, 1, 128) * sizes[pos * len(sizes) // 400]
+
+    f = Filled("q4", 1, 128, 32, [400, 130], seed=12, v_of=v_of)
+    q = torch.randn(2, 3, 128, device="cuda").to(io)
+    out = f.cache.attention(f.layer, q)
+    f.check(q, out, range(2), what=str(sizes))
     f.cache.sync_status()
 
 

@@ -421,18 +421,17 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   using L = Tile<D, true>;
   static constexpr int NB = Sums::NB, kTiles = L::kStep;
   static constexpr bool kWhole = sizeof(T) == 2;  // q, and the weights, are one piece
-  // The largest weight is 2^lift to 2^(lift + kSlack), so that its product with
-  // a scale stays below 2^15 and the others well above fp16's smallest step.
+  // The largest weight is 2^9 to 2^(9 + kSlack), so that its product with a scale
+  // below one fits fp16 and the others are well above its smallest step.
   static constexpr float kLift = 9.f;
   uint32_t a[2 * NB][kWhole ? 2 : 4];  // q
   uint32_t bias[2];                    // -8 sum of q per block, in three pieces: operand of one product
   float f, f1;                         // score = f * product, in log2 units; kWhole: f of head 2t, f1 of the next
   float top;                           // V scales seen are below top = 2^e
-  float unit;                          // fp32 results: they enter times unit = 2^-e (as far as fp16 goes) ...
-  float lift;                          // ... at lift = 9; bf16 results: as they are, at lift = min(9, 9 - e)
+  float unit;                          // ... and enter times unit = 2^-e (as far as fp16 goes); kWhole: as they are for e in [-6, 0]
 
   __device__ static int out_dim(int x, int y, int g) { return 32 * x + 4 * g + 2 * y; }
-  __device__ __forceinline__ float out_unit() const { return kWhole ? 1.f : 1.f / unit; }
+  __device__ __forceinline__ float out_unit() const { return 1.f / unit; }
 
   __device__ __forceinline__ void load_q(const T* q, bool valid, int t, float scale) {
     float x[NB][8];
@@ -497,7 +496,6 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
     this->clear();
     top = 1e-30f;
     unit = 1.f;
-    lift = kLift;
   }
 
   // Makes room for V scales up to s (of this lane); what the outputs are to be scaled by.
@@ -507,20 +505,10 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
     if (s >= top) {
       const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s < 2^e, -23 <= e <= 16
       top = __uint_as_float((uint32_t)(127 + e) << 23);
-      if constexpr (kWhole) {
-        const float now = kLift - (float)max(e, 0);
-        change = exp2_approx(now - lift);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          this->ref[i] += lift - now;  // the references that the heads' largest scores have now
-          this->l[i] *= change;
-        }
-        lift = now;
-      } else {
-        const float now = __uint_as_float((uint32_t)(127 - max(e, -14)) << 23);
-        change = now / unit;
-        unit = now;
-      }
+      const bool fits = kWhole && e <= 0 && e >= -6;
+      const float now = __uint_as_float((uint32_t)(127 - (fits ? 0 : max(e, -14))) << 23);
+      change = now / unit;
+      unit = now;
     }
     return change;
   }
@@ -639,10 +627,10 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
 #pragma unroll
       for (int i = 4; i < 4 * kTiles; i += 2) mx0 = fmaxf(mx0, s[i]), mx1 = fmaxf(mx1, s[i + 1]);
-      if (__any_sync(0xffffffffu, mx0 > this->ref[0] + (lift + kSlack) || mx1 > this->ref[1] + (lift + kSlack) ||
+      if (__any_sync(0xffffffffu, mx0 > this->ref[0] + (kLift + kSlack) || mx1 > this->ref[1] + (kLift + kSlack) ||
                                       big >= top)) {
         const float change = make_room(big);
-        this->raise(mx0, mx1, lift, change);
+        this->raise(mx0, mx1, kLift, change);
       }
 #pragma unroll
       for (int i = 0; i < 4 * kTiles; ++i) {
@@ -653,9 +641,9 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       float mx = s[0];
 #pragma unroll
       for (int i = 1; i < 4 * kTiles; ++i) mx = fmaxf(mx, s[i]);
-      if (__any_sync(0xffffffffu, mx > this->ref + (lift + kSlack) || big >= top)) {
+      if (__any_sync(0xffffffffu, mx > this->ref + (kLift + kSlack) || big >= top)) {
         const float change = make_room(big);
-        this->raise(mx, lift, change);
+        this->raise(mx, kLift, change);
       }
       float sum = 0.f;
 #pragma unroll
@@ -686,6 +674,12 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 #pragma unroll
             for (int j = 0; j < NB / 2; ++j) vs[i][j] = __float2half2_rn(0.f);
           }
+      }
+      if (kWhole && unit != 1.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < NB / 2; ++j) vs[i][j] = __hmul2(vs[i][j], __float2half2_rn(unit));
       }
       uint32_t v[4][NB / 2];
 #pragma unroll
