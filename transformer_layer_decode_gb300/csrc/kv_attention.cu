@@ -316,9 +316,7 @@ struct WarpBf16 : WarpHead<D> {
   __device__ static int out_dim(int x, int y, int g) { return 64 * (x >> 1) + 8 * g + 4 * (x & 1) + 2 * y; }
   __device__ __forceinline__ float out_unit() const { return 1.f; }
 
-  __device__ __forceinline__ void load_q(const T* q, bool valid, int t, float scale) {
-    float x[NB][8];
-    load_query<NB>(q, valid, t, x);
+  __device__ __forceinline__ void set_q(float (&x)[NB][8], int, float scale) {
     f = scale;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -433,9 +431,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   __device__ static int out_dim(int x, int y, int g) { return 32 * x + 4 * g + 2 * y; }
   __device__ __forceinline__ float out_unit() const { return 1.f / unit; }
 
-  __device__ __forceinline__ void load_q(const T* q, bool valid, int t, float scale) {
-    float x[NB][8];
-    load_query<NB>(q, valid, t, x);
+  __device__ __forceinline__ void set_q(float (&x)[NB][8], int t, float scale) {
     float mx = 0.f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -861,12 +857,15 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
   const int plain0 = full0 > n0 ? (full0 - n0 + kRound - 1) / kRound : 0;
   const int plain_n =
       min(nt / L::kStep, full1 - L::kStep >= n0 ? (full1 - L::kStep - n0) / kRound + 1 : 0) - plain0;
+  float x[L::NB][8];  // q, read while the page numbers are, and made operands while the first tiles are under way
+  load_query<L::NB>(
+      static_cast<const T*>(p.q) + r * p.q_stride + ((int64_t)head * p.group + h0 + min(g, n_heads - 1)) * D, g < n_heads,
+      t, x);
   fetch(0);
 #pragma unroll 1
   for (int j = 0; j < ST; ++j) issue(j, ring + j * L::kSlot);
-  W st;  // (q is read while the first tiles are under way)
-  st.load_q(static_cast<const T*>(p.q) + r * p.q_stride + ((int64_t)head * p.group + h0 + min(g, n_heads - 1)) * D,
-            g < n_heads, t, p.scale);
+  W st;
+  st.set_q(x, t, p.scale);
   uint32_t slot = warp * ST * L::kSlot;
 #pragma unroll 1
   for (int j = 0; j * L::kStep < nt; ++j) {
@@ -1117,11 +1116,17 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       }
       return pos;
     };
-    const int64_t end = border(blockIdx.x + 1), pos = border(blockIdx.x);
-    if (pos < end && pos >= (before + r_len) * units) locate(pos);  // moved on to the next query
-    if (tid == 0) share = Share{pos, end, before, total, parts, r, 0, 0, 0, 0, -1};
+    if (warp < 2) {  // one looks for each end
+      const int64_t pos = border(blockIdx.x + warp);
+      if (warp == 0 && pos < total && pos >= (before + r_len) * units) locate(pos);  // moved on to the next query
+      if (tid == 0) {
+        share.pos = pos, share.before = before, share.r = r;
+        share.total = total, share.parts = parts, share.cut = 0, share.more = -1;
+      }
+      if (tid == 32) share.end = pos;
+    }
     __syncthreads();
-    v = query_rows(p, r, &bad);
+    if (share.pos < share.end) v = query_rows(p, share.r, &bad);
   }
 
   while (share.pos < share.end) {
@@ -1129,7 +1134,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
     const int len = v.tiles + unit;
     // (not so only if lengths change while the call runs: then leave, in bounds)
     if (v.tiles == 0 || rel < 0 || rel >= (int64_t)len * units) break;
-    const int u = (int)(rel / len), in = (int)(rel - (int64_t)u * len);
+    const int u = rel < 1ll << 31 ? (int)rel / len : (int)(rel / len), in = (int)(rel - (int64_t)u * len);
     const int t0 = max(in - unit, 0);
     const int t1 = max((int)min((int64_t)len, in + (share.end - share.pos)) - unit, t0);
     if (tid == 0) share.u = u, share.t0 = t0, share.t1 = t1;  // (read after the barriers within unit_sums)

@@ -199,14 +199,19 @@ class KVCache:
                 raise ValueError("a call with a stream of its own needs a workspace of its own")
             if _capturing():  # a graph keeps its own: it may be replayed beside other calls
                 workspace = self.workspace()
+                ws = workspace.data_ptr(), workspace.numel()
             else:
-                workspace = self._workspaces.get(_raw_stream(self._index))
-                if workspace is None:
-                    workspace = self._workspaces[_raw_stream(self._index)] = self.workspace()
+                ws = self._workspaces.get(_raw_stream(self._index))
+                if ws is None:
+                    workspace = self.workspace()
+                    ws = workspace.data_ptr(), workspace.numel(), workspace
+                    self._workspaces[_raw_stream(self._index)] = ws
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"workspace: contiguous memory on {self.device} is wanted")
+        else:
+            ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         self._call(self.lib.dec_kv_attention, layer, qp, op, qt, qs, os_, sp, n, heads, window, sinks, scale,
-                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+                   ws[0], ws[1], stream=stream)
         return out
 
     # ---- pages ----------------------------------------------------------------
