@@ -160,8 +160,10 @@ constexpr int kMaxTokens = 32;  // of a CTA
 // lane l = 4 b + j has the dimensions of block b that make up groups g = 2 j and
 // 2 j + 1, two whole 16-bit words of the row's codes.
 //
-// What bounds it: the caller's rows, by bytes; writing 4-bit rows, the integer
-// and float pipes besides (about 10 instructions a value).
+// What bounds it: 8185 rows of 32 heads of 128 in bf16, 172 MB with their 4-bit
+// rows, are written in 52 us (19 instructions a value: amax, quotient, check,
+// digits) and read in 34 (the latency of 2-byte loads), where the bytes take 26.
+// Four rounds: two or eight are 5 to 15 % slower.
 template <int D, bool Q4, class T, bool READ, int ROUNDS>
 __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
                                                           const int32_t* seqs, const int32_t* positions,
