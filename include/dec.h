@@ -367,7 +367,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  *
  * All memory is the caller's: the calls below allocate nothing, keep nothing
  * between calls, wait for nothing and read no device value on the host, so
- * they can be captured into a CUDA graph.  They run on the current device, to
+ * they can be captured into a CUDA graph (dec_kv_status alone waits and reads,
+ * and must not be called while capturing).  They run on the current device, to
  * which the memory must belong, in stream order on `stream`.
  *
  *   page    rows [i * page_rows, (i + 1) * page_rows) of one sequence, in one
@@ -388,6 +389,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  *   scratch dec_kv_sizes ints, used by extend, fork and compact within a call
  *
  * An empty cache is table = -1 (all bytes 0xFF), lens = refs = status = 0.
+ * A caller that takes rows off a sequence's end by itself (lens) must also take
+ * the pages that are then past it out of table and refs.
  * Calls on one cache run one after another (one stream, or ordered by the
  * caller); attention, read and append touch no table, length or count, and
  * calls of these may overlap as long as none reads rows that another writes

@@ -357,6 +357,55 @@ def test_attention_in_graphs_and_streams():
         f.cache.attention(f.layer, q, stream=side)
 
 
+def test_results_made_for_a_stream_are_made_on_it():
+    """A call on a stream of its own while the current one is busy: nothing queued there may touch its results."""
+    f = Filled("q4", 2, 64, 16, [100, 260], seed=9)
+    q = torch.randn(2, 4, 64, device="cuda")
+    seqs, pos, ws = ints([1, -1, 0]), ints([259, 0, 99]), f.cache.workspace()
+    want = f.cache.read(f.layer, seqs, pos)
+    outs = f.cache.attention(f.layer, q), f.cache.attention(f.layer, q, seqs=ints([0, -1]))
+    some = ints([0, -1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)   # about 10 ms
+        got = f.cache.read(f.layer, seqs, pos, stream=stream)
+        got_outs = (f.cache.attention(f.layer, q, workspace=ws, stream=stream),
+                    f.cache.attention(f.layer, q, seqs=some, workspace=ws, stream=stream))
+        torch.cuda.synchronize()
+        for a, b in zip(got + got_outs, want + outs):
+            assert torch.equal(a, b)
+
+
+def test_calls_from_another_device(monkeypatch):
+    """Another device is current: calls go to the cache's, and a capture is noticed there (a graph's own
+    workspace is never kept for other calls)."""
+    f = Filled("bf16", 2, 64, 16, [100, 2600], seed=10)
+    q = torch.randn(2, 4, 64, device="cuda")
+    want = f.cache.attention(f.layer, q)
+    g, out, kept, inside = torch.cuda.CUDAGraph(), torch.empty_like(q), dict(f.cache._workspaces), []
+    here = kv._capturing
+
+    class Entered(torch.cuda.device):
+        def __enter__(self):
+            inside.append(1)
+            return super().__enter__()
+
+        def __exit__(self, *error):
+            inside.pop()
+            return super().__exit__(*error)
+
+    with torch.cuda.graph(g):
+        monkeypatch.setattr(torch.cuda, "device", Entered)
+        monkeypatch.setattr(kv, "_current_device", lambda: f.cache.device.index + (not inside))
+        monkeypatch.setattr(kv, "_capturing", lambda: bool(inside) and here())  # (the other device captures nothing)
+        f.cache.attention(f.layer, q, out=out)
+        monkeypatch.undo()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and f.cache._workspaces == kept
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "q4"])
 def test_attention_without_workspaces_on_streams_and_in_graphs(fmt):
     """Calls that share nothing but the cache: two streams at once, and two graphs replayed beside them."""

@@ -128,6 +128,22 @@ class KVCache:
         raise ValueError(f"{name}: a float32 or bfloat16 tensor [n, {heads or 'heads'}, {d}] on {self.device} "
                          "with contiguous rows is wanted")
 
+    def _captured(self):
+        """Whether the current stream of the cache's device is being captured."""
+        if _current_device() == self._index:
+            return _capturing()
+        with torch.cuda.device(self.device):
+            return _capturing()
+
+    def _new(self, make, shape, dtype, stream):
+        """make(shape) for a call on `stream`: its memory, and what fills it, belong to that stream."""
+        if stream is None:
+            return make(shape, dtype=dtype, device=self.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.stream(stream):
+            return make(shape, dtype=dtype, device=self.device)
+
     def _call(self, fn, *args, stream=None):
         handle = _raw_stream(self._index) if stream is None else \
             stream if isinstance(stream, int) else stream.cuda_stream
@@ -160,9 +176,9 @@ class KVCache:
         pp, _ = self._ints("positions", positions, n)
         shape = (n, self.desc.n_kv_heads, self.desc.head_dim)
         if k_out is None:
-            k_out = torch.zeros(shape, dtype=dtype if v_out is None else v_out.dtype, device=self.device)
+            k_out = self._new(torch.zeros, shape, dtype if v_out is None else v_out.dtype, stream)
         if v_out is None:
-            v_out = torch.zeros(shape, dtype=k_out.dtype, device=self.device)
+            v_out = self._new(torch.zeros, shape, k_out.dtype, stream)
         kp, kt, ks = self._rows("k_out", k_out, shape[1])
         vp, vt, vs = self._rows("v_out", v_out, shape[1])
         if k_out.shape[0] != n or v_out.shape[0] != n or kt != vt or ks != vs:
@@ -189,15 +205,14 @@ class KVCache:
         n, heads = q.shape[0], q.shape[1]
         sp, _ = self._ints("seqs", seqs, n)
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format) if seqs is None else \
-                torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+            out = self._new(torch.empty if seqs is None else torch.zeros, q.shape, q.dtype, stream)
         op, ot, os_ = self._rows("out", out, heads)
         if ot != qt or out.shape[0] != n:
             raise ValueError("out: the type and rows of q are wanted")
         if workspace is None:
             if stream is not None:
                 raise ValueError("a call with a stream of its own needs a workspace of its own")
-            if _capturing():  # a graph keeps its own: it may be replayed beside other calls
+            if self._captured():  # a graph keeps its own: it may be replayed beside other calls
                 workspace = self.workspace()
                 ws = workspace.data_ptr(), workspace.numel()
             else:
