@@ -3,6 +3,7 @@
 // dec_kv_ calls.
 #include <algorithm>
 #include <cstdio>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv.h"
@@ -67,16 +68,74 @@ constexpr int kRowRounds = 4;
 constexpr int kFewRounds = 8192;  // (about a GPU full of warps)
 constexpr int kManyCtas = 1200;   // (eight an SM)
 
-// Eight fp32 values from / to the caller's type.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 u = reinterpret_cast<const float4*>(p)[0], w = reinterpret_cast<const float4*>(p)[1];
-  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+// The largest of three magnitudes; NaN if one is.
+__device__ __forceinline__ float largest(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  x[0] = bf16lo(u.x), x[1] = bf16hi(u.x), x[2] = bf16lo(u.y), x[3] = bf16hi(u.y);
-  x[4] = bf16lo(u.z), x[5] = bf16hi(u.z), x[6] = bf16lo(u.w), x[7] = bf16hi(u.w);
+// The larger magnitudes of two bf16 pairs (with some sign); NaN if either is.
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
 }
+
+// Two fp32 numbers handled by one instruction.
+struct Two {
+  uint64_t w;
+  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
+  __device__ __forceinline__ float2 get() const {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(w));
+    return y;
+  }
+};
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.w) : "l"(b.w), "l"(c.w));
+  return a;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.w) : "l"(b.w));
+  return a;
+}
+
+// Eight values of the caller's type as they are loaded, their fp32 values, and
+// the largest magnitude among them and those of four neighbouring lanes (NaN if
+// one of them is).
+template <class T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 u, w;
+  __device__ __forceinline__ void load(const float* p) {
+    u = reinterpret_cast<const float4*>(p)[0], w = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+  }
+  __device__ __forceinline__ float top() const {
+    float y = largest(largest(largest(u.x, u.y, u.z), u.w, w.x), w.y, w.z);
+    y = largest(y, w.w, __shfl_xor_sync(0xffffffffu, largest(y, w.w, 0.f), 1));
+    return largest(y, __shfl_xor_sync(0xffffffffu, y, 2), 0.f);
+  }
+};
+template <>
+struct Eight<uint16_t> {
+  uint4 u;
+  __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    x[0] = bf16lo(u.x), x[1] = bf16hi(u.x), x[2] = bf16lo(u.y), x[3] = bf16hi(u.y);
+    x[4] = bf16lo(u.z), x[5] = bf16hi(u.z), x[6] = bf16lo(u.w), x[7] = bf16hi(u.w);
+  }
+  __device__ __forceinline__ float top() const {
+    uint32_t y = larger2(larger2(u.x, u.y), larger2(u.z, u.w));
+    y = larger2(y, __shfl_xor_sync(0xffffffffu, y, 1));
+    y = larger2(y, __shfl_xor_sync(0xffffffffu, y, 2));
+    return largest(bf16lo(y), bf16hi(y), 0.f);
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -99,48 +158,45 @@ __device__ __forceinline__ float reciprocal(float s) {
   return y;
 }
 
-// The larger magnitude; NaN if either is.
-__device__ __forceinline__ float larger(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
-  return y;
-}
-
 // Codes plus 8 of eight values for a scale s > 0, four bits each, lowest first:
 // the integers nearest to x / s, ties to even, within [-8, 7].  r = x * (1 / s)
-// is off by a few 2^-24 of itself, so its nearest integer q is the answer or,
-// next to a half, a neighbour.  Where no r is within 2^-19 of a half (r, below
-// 7.01, is off by less) all q are right as they are.  Otherwise the remainder
-// e = x - q s, which is exact (it has no bits below x's and is below s), decides
-// against s / 2: past it, or on it with q odd, q moves one on.  So for scales
-// below fp16's normal numbers, or at its top, where |r| can be larger, too.
-// The codes are put together as digits of a float, 16 bits at a time, to spare
-// the integer pipe.
+// is off by 2^-23 of itself, so its nearest integer q is the answer or, next to a
+// half, a neighbour.  Where no r is within 2^-19 of a half (r, below 7.01, is off
+// by less) all q are right as they are.  Otherwise the remainder e = x - q s, which
+// is exact (it has no bits below x's and is below s), decides against s / 2: past
+// it, or on it with q odd, q moves one on.  So for scales below fp16's normal
+// numbers, or at its top, where |r| can be larger, too.  The codes are put together
+// as digits of a float, 16 bits at a time, to spare the integer pipe; x[i] and
+// x[4 + i], which are the same digit, go through each step in one instruction.
 __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], float s) {
   const float inv = reciprocal(s);
-  float q[8], off = 0.f;
+  Two nq[4] = {Two(0.f), Two(0.f), Two(0.f), Two(0.f)};  // -q
+  float off[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float r = x[i] * inv;
-    q[i] = (r + kMagic) - kMagic;
-    off = fmaxf(off, fabsf(r - q[i]));
+  for (int i = 0; i < 4; ++i) {
+    const Two y(x[i], x[4 + i]);
+    nq[i] = fma2(fma2(y, Two(inv), Two(kMagic)), Two(-1.f), Two(kMagic));
+    const float2 d = fma2(y, Two(inv), nq[i]).get();
+    off[i] = d.x, off[4 + i] = d.y;
   }
-  if (!(off < 0.5f - 1.f / (1 << 19)) || s < 6.103515625e-5f || s >= 65504.f) {
+  const float most = largest(largest(largest(off[0], off[1], off[2]), off[3], off[4]), off[5],
+                             largest(off[6], off[7], 0.f));
+  if (!(most < 0.5f - 1.f / (1 << 19)) || s < 6.103515625e-5f || s >= 65504.f) {
     const int half = __float_as_int(0.5f * s);
+    float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float m = fminf(fmaxf(x[i] * inv, -8.f), 7.f) + kMagic, e = fmaf(-(m - kMagic), s, x[i]);
       const float one = fabsf(e) > __int_as_float(half - (__float_as_int(m) & 1)) ? copysignf(1.f, e) : 0.f;
-      q[i] = fminf(fmaxf((m - kMagic) + one, -8.f), 7.f);
+      q[i] = -fminf(fmaxf((m - kMagic) + one, -8.f), 7.f);
     }
-  }
-  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float y = fmaf(fmaf(fmaf(q[4 * i + 3], 16.f, q[4 * i + 2]), 16.f, q[4 * i + 1]), 16.f, q[4 * i]);
-    w[i] = __float_as_uint(y + (8388608.f + 8.f * 4369.f));  // 2^23 and 8 in every digit
+    for (int i = 0; i < 4; ++i) nq[i] = Two(q[i], q[4 + i]);
   }
-  return __byte_perm(w[0], w[1], 0x5410);
+  const Two digit(16.f);
+  const Two y = fma2(fma2(fma2(nq[3], digit, nq[2]), digit, nq[1]), digit, nq[0]);
+  const float2 w = fma2(y, Two(-1.f), Two(8388608.f + 8.f * 4369.f)).get();  // 2^23 and 8 in every digit
+  return __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x5410);
 }
 
 // x / 7, correctly rounded: the product with the rounded reciprocal and one FMA
@@ -206,14 +262,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
     uint8_t* values = base + row * kv_row_bytes(D, false) + 16 * l;
     uint8_t* words = base + row * (D / 2) + 4 * j * NB + 2 * b;
     uint8_t* scales = base + page_rows * (D / 2) + (row * NB + b) * 2;
-    float x[ROUNDS][8];
+    Eight<std::conditional_t<READ, uint16_t, T>> in[ROUNDS] = {};
     if constexpr (!READ || !Q4) {
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
         const int at = first + i * RPR;
         if (at >= 2 * nkv) continue;
-        if constexpr (READ) load8(reinterpret_cast<const uint16_t*>(values + at * head_bytes), x[i]);
-        else load8(mine(at), x[i]);
+        if constexpr (READ) in[i].load(reinterpret_cast<const uint16_t*>(values + at * head_bytes));
+        else in[i].load(mine(at));
       }
     }
     if constexpr (!Q4) {
@@ -221,8 +277,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
       for (int i = 0; i < ROUNDS; ++i) {
         const int at = first + i * RPR;
         if (at >= 2 * nkv) continue;
-        if constexpr (READ) store8(mine(at), x[i]);
-        else store8(reinterpret_cast<uint16_t*>(values + at * head_bytes), x[i]);
+        float x[8];
+        in[i].values(x);
+        if constexpr (READ) store8(mine(at), x);
+        else store8(reinterpret_cast<uint16_t*>(values + at * head_bytes), x);
       }
     } else if constexpr (READ) {
       uint32_t codes[ROUNDS];
@@ -240,28 +298,24 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
         const int at = first + i * RPR;
         if (at >= 2 * nkv) continue;
         const float f = __half2float(scale[i]);
+        float x[8];
 #pragma unroll
         for (int m = 0; m < 8; ++m)  // 2^23 + n, less 2^23 + 8
-          x[i][m] = (__int_as_float(0x4b000000 | (codes[i] >> (4 * m) & 15)) - 8388616.f) * f;
-        store8(mine(at), x[i]);
+          x[m] = (__int_as_float(0x4b000000 | (codes[i] >> (4 * m) & 15)) - 8388616.f) * f;
+        store8(mine(at), x);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
         const int at = first + i * RPR;
-        const bool on = at < 2 * nkv;
-        float top = 0.f;  // the block's largest magnitude
-        if (on) {
-#pragma unroll
-          for (int m = 0; m < 8; ++m) top = larger(top, x[i][m]);
-        }
-        top = larger(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = larger(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (!on) continue;
+        const float top = in[i].top();  // the block's largest magnitude
+        if (at >= 2 * nkv) continue;    // (whole rows: no other block's lanes)
         const bool finite = top < INFINITY;
         const __half s16 = finite ? __float2half_rn(fminf(seventh(top), 65504.f)) : __ushort_as_half(0x7fff);
         const float f = __half2float(s16);
-        const uint32_t w = f > 0.f ? q4_codes(x[i], f) : 0x88888888u;  // (not where f is NaN)
+        float x[8];
+        in[i].values(x);
+        const uint32_t w = f > 0.f ? q4_codes(x, f) : 0x88888888u;  // (not where f is NaN)
         uint16_t* to = reinterpret_cast<uint16_t*>(words + at * head_bytes);
         to[0] = (uint16_t)w;
         to[NB] = (uint16_t)(w >> 16);
