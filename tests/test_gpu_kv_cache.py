@@ -497,6 +497,42 @@ def test_append_writes_the_documented_bytes(fmt, io, nkv, hd, R):
     c.sync_status()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", [3, 700])
+def test_rows_at_other_alignments(fmt, io, rows):
+    """Rows that begin 16 bytes past a multiple of 32, or are an odd number of 16 bytes apart."""
+    nkv, hd, R = 8, 64, 16
+    c = kv.KVCache(n_layers=1, n_kv_heads=nkv, head_dim=hd, page_rows=R, fmt=fmt, n_pages=-(-rows // R), n_seqs=1,
+                   max_pages=-(-rows // R))
+    c.extend(None, ints([rows]))
+    seqs, pos, step = ints([0] * rows), ints(range(rows)), 16 // (4 if io == torch.float32 else 2)
+
+    def placed(offset, gap):
+        width = nkv * hd + gap
+        flat = torch.full((offset + rows * width,), 7.0, dtype=io, device="cuda")
+        return flat, flat[offset:].view(rows, width)[:, :nkv * hd].view(rows, nkv, hd)
+
+    k, v = (torch.randn(rows, nkv, hd, device="cuda").to(io) for _ in range(2))
+    want = None
+    for offset, gap in ((0, 0), (step, 0), (0, step), (step, step), (0, 2 * step)):
+        (_, kin), (_, vin) = placed(offset, gap), placed(offset, gap)
+        kin.copy_(k)
+        vin.copy_(v)
+        c.pool.fill_(0xFF)
+        c.append(0, kin, vin, seqs=seqs, positions=pos)
+        (kf, ko), (vf, vo) = placed(offset, gap), placed(offset, gap)
+        c.read(0, seqs, pos, k_out=ko, v_out=vo)
+        c.sync_status()
+        want = want or (c.pool.clone(), ko.clone(), vo.clone())
+        assert torch.equal(c.pool, want[0]) and torch.equal(ko, want[1]) and torch.equal(vo, want[2]), (offset, gap)
+        for flat, rest in ((kf, ko), (vf, vo)):   # what lies between the rows stays
+            rest.fill_(7.0)
+            assert (flat == 7.0).all(), (offset, gap)
+    if fmt == "bf16":
+        assert torch.equal(want[1], k.bfloat16().to(io))
+
+
 def test_append_ties_and_extremes():
     """Quotients on and next to a half, at 24 bits; blocks with NaN or infinity; values past fp16's range."""
     hd, R = 64, 16

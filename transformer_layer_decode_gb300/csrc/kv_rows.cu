@@ -66,7 +66,9 @@ constexpr int kRowWarps = 8;  // warps of a CTA of the row kernels
 // enough warps to fill the GPU; one otherwise.
 constexpr int kRowRounds = 4;
 constexpr int kFewRounds = 8192;  // (about a GPU full of warps)
-constexpr int kManyCtas = 1200;   // (eight an SM)
+// CTAs beyond which they take more tokens each: eight an SM where they code (twice as
+// many: 3 to 5 % slower), twice as many where they copy (4 to 7 % faster).
+constexpr int kManyCtas = 1200;
 
 // The largest of three magnitudes; NaN if one is.
 __device__ __forceinline__ float largest(float a, float b, float c) {
@@ -136,15 +138,24 @@ struct Eight<uint16_t> {
     return largest(bf16lo(y), bf16hi(y), 0.f);
   }
 };
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+// wide: p is a multiple of 32 bytes, which one store then writes whole; two
+// stores of half a sector each take longer (8185 rows of 32 heads of 128 read
+// from 4-bit pages: 81 us, against 53).
+__device__ __forceinline__ void store8(float* p, const float (&x)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
 }
 __device__ __forceinline__ uint32_t pair(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8], bool) {
   *reinterpret_cast<uint4*>(p) =
       make_uint4(pair(x[0], x[1]), pair(x[2], x[3]), pair(x[4], x[5]), pair(x[6], x[7]));
 }
@@ -217,13 +228,14 @@ constexpr int kMaxTokens = 32;  // of a CTA
 // 2 j + 1, two whole 16-bit words of the row's codes.
 //
 // What bounds it: 8185 rows of 32 heads of 128 in bf16, 172 MB with their 4-bit
-// rows, are written in 52 us (19 instructions a value: amax, quotient, check,
-// digits) and read in 34 (the latency of 2-byte loads), where the bytes take 26.
-// Four rounds: two or eight are 5 to 15 % slower.
+// rows, are written in 45 us (instructions: amax, quotient, check, digits) and
+// read in 34 (the latency of 2-byte loads), where the bytes take 26; in fp32, 306
+// MB, in 52 and 50 (46); from and to bf16 pages, 268 MB, in 43 (40).  Four rounds:
+// two or eight are 5 to 15 % slower.
 template <int D, bool Q4, class T, bool READ, int ROUNDS>
 __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
                                                           const int32_t* seqs, const int32_t* positions,
-                                                          int n, int tokens, int items_per_token) {
+                                                          int n, int tokens, int items_per_token, bool wide) {
   constexpr int LANES = D / 8, NB = D / 32, RPR = 32 / LANES;  // rows of a round
   __shared__ uint8_t* token_page[kMaxTokens];
   __shared__ int token_row[kMaxTokens];
@@ -279,8 +291,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
         if (at >= 2 * nkv) continue;
         float x[8];
         in[i].values(x);
-        if constexpr (READ) store8(mine(at), x);
-        else store8(reinterpret_cast<uint16_t*>(values + at * head_bytes), x);
+        if constexpr (READ) store8(mine(at), x, wide);
+        else store8(reinterpret_cast<uint16_t*>(values + at * head_bytes), x, false);
       }
     } else if constexpr (READ) {
       uint32_t codes[ROUNDS];
@@ -302,7 +314,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
 #pragma unroll
         for (int m = 0; m < 8; ++m)  // 2^23 + n, less 2^23 + 8
           x[m] = (__int_as_float(0x4b000000 | (codes[i] >> (4 * m) & 15)) - 8388616.f) * f;
-        store8(mine(at), x);
+        store8(mine(at), x, wide);
       }
     } else {
 #pragma unroll
@@ -332,14 +344,17 @@ cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const
   const bool few = (int64_t)n * 2 * c.nkv / kPerRound < kFewRounds;
   const int per_item = kPerRound * (few ? 1 : kRowRounds);
   const int items = (2 * c.nkv + per_item - 1) / per_item;
-  // enough tokens for every warp of a CTA, and more where there are CTAs enough without
-  const int tokens = std::max((kRowWarps + items - 1) / items, std::min(n / kManyCtas, kMaxTokens));
+  const int many = Q4 && !READ ? kManyCtas : 2 * kManyCtas;
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | stride * sizeof(T)) & 31) == 0;
+  // enough tokens for every warp of a CTA, or a multiple where there are CTAs enough
+  const int least = (kRowWarps + items - 1) / items;
+  const int tokens = std::min(std::max((n / many + least - 1) / least, 1) * least, kMaxTokens);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((n + tokens - 1) / tokens));
   cfg.blockDim = dim3(kRowWarps * 32);
   cfg.stream = s;
   return cudaLaunchKernelEx(&cfg, few ? kv_rows<D, Q4, T, READ, 1> : kv_rows<D, Q4, T, READ, kRowRounds>, c,
-                            static_cast<T*>(k), static_cast<T*>(v), stride, seqs, positions, n, tokens, items);
+                            static_cast<T*>(k), static_cast<T*>(v), stride, seqs, positions, n, tokens, items, wide);
 }
 
 template <bool READ>
