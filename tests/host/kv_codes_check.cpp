@@ -1,7 +1,7 @@
 // The divisions that the 4-bit rows are written without (csrc/kv_rows.cu):
-// x / 7 from the rounded reciprocal with one FMA correction, and the integer
-// nearest to x / s from a reciprocal that is a few 2^-24 off, checked against
-// IEEE division and against exact arithmetic in 64 bits.
+// x / 7 from the rounded reciprocal, and the integer nearest to x / s from a
+// reciprocal that is up to 2^-23 off, with one FMA correction each, checked
+// against IEEE division and against exact arithmetic in 64 bits.
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -28,15 +28,9 @@ static float seventh(float x) {
 // As q4_codes, for one value; `inv` is the reciprocal it is given.
 static int code(float x, float s, float inv) {
   const float magic = 12582912.f;
-  float r = x * inv;
-  float q = (r + magic) - magic;
-  if (!(std::fabs(r - q) < 0.5f - 1.f / (1 << 19)) || s < 6.103515625e-5f || s >= 65504.f) {
-    const int half = as_int(0.5f * s);
-    const float m = std::fmin(std::fmax(x * inv, -8.f), 7.f) + magic, e = std::fmaf(-(m - magic), s, x);
-    const float one = std::fabs(e) > bits((uint32_t)(half - (as_int(m) & 1))) ? std::copysign(1.f, e) : 0.f;
-    q = std::fmin(std::fmax((m - magic) + one, -8.f), 7.f);
-  }
-  return (int)q;
+  if (s < 6.103515625e-5f || s >= 65504.f) x = std::fmin(std::fmax(x, -8.f * s), 7.f * s);
+  const float r0 = x * inv, r = std::fmaf(std::fmaf(r0, -s, x), inv, r0);
+  return (int)((r + magic) - magic);
 }
 
 int main() {
@@ -59,7 +53,7 @@ int main() {
       x = (float)(((int)(rng() % 14) - 7 + 0.5) * (double)s);  // (a block's values are within 7.0035 s)
       x = bits((uint32_t)(as_int(x) + (int)(rng() % 5) - 2));
     } else {
-      x = (float)(((double)(rng() >> 11) / 9007199254740992.0 * 2 - 1) * (s >= 65504.f ? 1e6 : 7.0033) * s);
+      x = (float)(((double)(rng() >> 11) / 9007199254740992.0 * 2 - 1) * (s >= 65504.f ? 1e6 : s < 6.103515625e-5f ? 11 : 7.0033) * s);
     }
     if (rng() % 2) x = bits((uint32_t)as_int(x) & 0xffff0000u);
     if (!std::isfinite(x)) continue;

@@ -66,9 +66,9 @@ constexpr int kRowWarps = 8;  // warps of a CTA of the row kernels
 // enough warps to fill the GPU; one otherwise.
 constexpr int kRowRounds = 4;
 constexpr int kFewRounds = 8192;  // (about a GPU full of warps)
-// CTAs beyond which they take more tokens each: eight an SM where they code (twice as
-// many: 3 to 5 % slower), twice as many where they copy (4 to 7 % faster).
-constexpr int kManyCtas = 1200;
+// CTAs beyond which they take more tokens each (half or 1.5 times as many: up to
+// 6 % slower).
+constexpr int kManyCtas = 2400;
 
 // The largest of three magnitudes; NaN if one is.
 __device__ __forceinline__ float largest(float a, float b, float c) {
@@ -170,44 +170,30 @@ __device__ __forceinline__ float reciprocal(float s) {
 }
 
 // Codes plus 8 of eight values for a scale s > 0, four bits each, lowest first:
-// the integers nearest to x / s, ties to even, within [-8, 7].  r = x * (1 / s)
-// is off by 2^-23 of itself, so its nearest integer q is the answer or, next to a
-// half, a neighbour.  Where no r is within 2^-19 of a half (r, below 7.01, is off
-// by less) all q are right as they are.  Otherwise the remainder e = x - q s, which
-// is exact (it has no bits below x's and is below s), decides against s / 2: past
-// it, or on it with q odd, q moves one on.  So for scales below fp16's normal
-// numbers, or at its top, where |r| can be larger, too.  The codes are put together
-// as digits of a float, 16 bits at a time, to spare the integer pipe; x[i] and
-// x[4 + i], which are the same digit, go through each step in one instruction.
-__device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], float s) {
-  const float inv = reciprocal(s);
-  Two nq[4] = {Two(0.f), Two(0.f), Two(0.f), Two(0.f)};  // -q
-  float off[8];
+// the integers nearest to x / s, ties to even, within [-8, 7].  The quotient takes
+// one correction (Markstein's division): with a reciprocal that is off by 2^-23 of
+// itself, r = r0 + (x - r0 s) / s is off from x / s by half a step of r and a
+// millionth of a step.  x has 24 bits and s 11, so x / s is a half exactly, and then
+// so is r, or it is away from every half by half a step and 2^-11 of that or more,
+// and r is on the same side.  Scales below fp16's normal numbers, or at its top, can
+// be too small for their block: there x is clamped.  Adding kMagic leaves
+// the integer in a float's low bits, whose other bits leave the word as it is put
+// together from its digits.  x[i] and x[4 + i], which are the same digit, go through
+// each step in one instruction.
+__device__ __forceinline__ uint32_t q4_codes(float (&x)[8], float s) {
+  if (s < 6.103515625e-5f || s >= 65504.f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const Two y(x[i], x[4 + i]);
-    nq[i] = fma2(fma2(y, Two(inv), Two(kMagic)), Two(-1.f), Two(kMagic));
-    const float2 d = fma2(y, Two(inv), nq[i]).get();
-    off[i] = d.x, off[4 + i] = d.y;
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -8.f * s), 7.f * s);
   }
-  const float most = largest(largest(largest(off[0], off[1], off[2]), off[3], off[4]), off[5],
-                             largest(off[6], off[7], 0.f));
-  if (!(most < 0.5f - 1.f / (1 << 19)) || s < 6.103515625e-5f || s >= 65504.f) {
-    const int half = __float_as_int(0.5f * s);
-    float q[8];
+  const Two inv(reciprocal(s)), minus(-s), magic(kMagic), zero(-0.f);
+  uint32_t y0 = 0, y1 = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float m = fminf(fmaxf(x[i] * inv, -8.f), 7.f) + kMagic, e = fmaf(-(m - kMagic), s, x[i]);
-      const float one = fabsf(e) > __int_as_float(half - (__float_as_int(m) & 1)) ? copysignf(1.f, e) : 0.f;
-      q[i] = -fminf(fmaxf((m - kMagic) + one, -8.f), 7.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) nq[i] = Two(q[i], q[4 + i]);
+  for (int i = 3; i >= 0; --i) {
+    const Two u(x[i], x[4 + i]), r0 = fma2(u, inv, zero), r = fma2(fma2(r0, minus, u), inv, r0);
+    const float2 m = add2(r, i ? magic : Two(kMagic + 34952.f)).get();  // 8 in every digit
+    y0 = y0 * 16 + __float_as_uint(m.x), y1 = y1 * 16 + __float_as_uint(m.y);
   }
-  const Two digit(16.f);
-  const Two y = fma2(fma2(fma2(nq[3], digit, nq[2]), digit, nq[1]), digit, nq[0]);
-  const float2 w = fma2(y, Two(-1.f), Two(8388608.f + 8.f * 4369.f)).get();  // 2^23 and 8 in every digit
-  return __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x5410);
+  return __byte_perm(y0, y1, 0x5410);
 }
 
 // x / 7, correctly rounded: the product with the rounded reciprocal and one FMA
@@ -228,10 +214,10 @@ constexpr int kMaxTokens = 32;  // of a CTA
 // 2 j + 1, two whole 16-bit words of the row's codes.
 //
 // What bounds it: 8185 rows of 32 heads of 128 in bf16, 172 MB with their 4-bit
-// rows, are written in 45 us (instructions: amax, quotient, check, digits) and
-// read in 34 (the latency of 2-byte loads), where the bytes take 26; in fp32, 306
-// MB, in 52 and 50 (46); from and to bf16 pages, 268 MB, in 43 (40).  Four rounds:
-// two or eight are 5 to 15 % slower.
+// rows, are written in 37 us (instructions: amax, scale, quotients, digits) and
+// read in 33 (the latency of 2-byte loads), where the bytes take 26; in fp32, 306
+// MB, in 51 and 51 (46); from and to bf16 pages, 268 MB, in 43 (40).  Four rounds:
+// two are 10 % slower, eight 15 % in fp32.
 template <int D, bool Q4, class T, bool READ, int ROUNDS>
 __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
                                                           const int32_t* seqs, const int32_t* positions,
@@ -260,78 +246,76 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
     token_page[threadIdx.x] = at;
   }
   __syncthreads();
-  for (int item = threadIdx.x >> 5; item < tokens * items_per_token; item += kRowWarps) {
-    const int token = item / items_per_token;
+  const int last = 2 * c.nkv - 1;
+  int token = (threadIdx.x >> 5) / items_per_token, part = (threadIdx.x >> 5) % items_per_token;
+  for (; token < tokens; part += kRowWarps) {
+    if (part >= items_per_token) {
+      token += part / items_per_token, part %= items_per_token;
+      if (token >= tokens) break;
+    }
     uint8_t* base = token_page[token];
     if (!base) continue;
     const int row = token_row[token], page_rows = c.page_rows, nkv = c.nkv;
     const uint32_t head_bytes = (uint32_t)c.head_bytes;
-    const int first = (item - token * items_per_token) * (ROUNDS * RPR) + lane / LANES;
+    const int first = part * (ROUNDS * RPR) + lane / LANES;
+    // (lanes past the last row take it once more: the same bytes to the same place)
+    auto round = [&](int i) { return min(first + i * RPR, last); };
     T* k_at = k + (t0 + token) * stride + 8 * l;
     T* v_at = v + (t0 + token) * stride + 8 * l - nkv * D;
     auto mine = [&](int at) { return (at < nkv ? k_at : v_at) + at * D; };  // the caller's
     // in the page: bf16 values, or two words of codes, 2 NB bytes apart, and a scale
+    auto head = [&](int at) { return (uint64_t)(uint32_t)at * head_bytes; };
     uint8_t* values = base + row * kv_row_bytes(D, false) + 16 * l;
     uint8_t* words = base + row * (D / 2) + 4 * j * NB + 2 * b;
     uint8_t* scales = base + page_rows * (D / 2) + (row * NB + b) * 2;
-    Eight<std::conditional_t<READ, uint16_t, T>> in[ROUNDS] = {};
     if constexpr (!READ || !Q4) {
+      Eight<std::conditional_t<READ, uint16_t, T>> in[ROUNDS];
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
-        const int at = first + i * RPR;
-        if (at >= 2 * nkv) continue;
-        if constexpr (READ) in[i].load(reinterpret_cast<const uint16_t*>(values + at * head_bytes));
+        const int at = round(i);
+        if constexpr (READ) in[i].load(reinterpret_cast<const uint16_t*>(values + head(at)));
         else in[i].load(mine(at));
       }
-    }
-    if constexpr (!Q4) {
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
-        const int at = first + i * RPR;
-        if (at >= 2 * nkv) continue;
+        const int at = round(i);
         float x[8];
         in[i].values(x);
-        if constexpr (READ) store8(mine(at), x, wide);
-        else store8(reinterpret_cast<uint16_t*>(values + at * head_bytes), x, false);
+        if constexpr (READ) {
+          store8(mine(at), x, wide);
+        } else if constexpr (!Q4) {
+          store8(reinterpret_cast<uint16_t*>(values + head(at)), x, false);
+        } else {
+          const float top = in[i].top();  // the block's largest magnitude
+          const bool finite = top < INFINITY;
+          const __half s16 = finite ? __float2half_rn(fminf(seventh(top), 65504.f)) : __ushort_as_half(0x7fff);
+          const float f = __half2float(s16);
+          // (where f is 0 every |x| is far below 1/2)
+          const uint32_t codes = q4_codes(x, f > 0.f ? f : 1.f), w = finite ? codes : 0x88888888u;
+          uint16_t* to = reinterpret_cast<uint16_t*>(words + head(at));
+          to[0] = (uint16_t)w;
+          to[NB] = (uint16_t)(w >> 16);
+          if (j == 0) *reinterpret_cast<__half*>(scales + head(at)) = s16;
+        }
       }
-    } else if constexpr (READ) {
+    } else {
       uint32_t codes[ROUNDS];
       __half scale[ROUNDS];
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
-        const uint32_t at = first + i * RPR;
-        if (at >= 2 * nkv) continue;
-        const uint16_t* w = reinterpret_cast<const uint16_t*>(words + at * head_bytes);
+        const int at = round(i);
+        const uint16_t* w = reinterpret_cast<const uint16_t*>(words + head(at));
         codes[i] = w[0] | (uint32_t)w[NB] << 16;
-        scale[i] = *reinterpret_cast<const __half*>(scales + at * head_bytes);
+        scale[i] = *reinterpret_cast<const __half*>(scales + head(at));
       }
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
-        const int at = first + i * RPR;
-        if (at >= 2 * nkv) continue;
         const float f = __half2float(scale[i]);
         float x[8];
 #pragma unroll
         for (int m = 0; m < 8; ++m)  // 2^23 + n, less 2^23 + 8
           x[m] = (__int_as_float(0x4b000000 | (codes[i] >> (4 * m) & 15)) - 8388616.f) * f;
-        store8(mine(at), x, wide);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < ROUNDS; ++i) {
-        const int at = first + i * RPR;
-        const float top = in[i].top();  // the block's largest magnitude
-        if (at >= 2 * nkv) continue;    // (whole rows: no other block's lanes)
-        const bool finite = top < INFINITY;
-        const __half s16 = finite ? __float2half_rn(fminf(seventh(top), 65504.f)) : __ushort_as_half(0x7fff);
-        const float f = __half2float(s16);
-        float x[8];
-        in[i].values(x);
-        const uint32_t w = f > 0.f ? q4_codes(x, f) : 0x88888888u;  // (not where f is NaN)
-        uint16_t* to = reinterpret_cast<uint16_t*>(words + at * head_bytes);
-        to[0] = (uint16_t)w;
-        to[NB] = (uint16_t)(w >> 16);
-        if (j == 0) *reinterpret_cast<__half*>(scales + at * head_bytes) = s16;
+        store8(mine(round(i)), x, wide);
       }
     }
   }
@@ -344,11 +328,10 @@ cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const
   const bool few = (int64_t)n * 2 * c.nkv / kPerRound < kFewRounds;
   const int per_item = kPerRound * (few ? 1 : kRowRounds);
   const int items = (2 * c.nkv + per_item - 1) / per_item;
-  const int many = Q4 && !READ ? kManyCtas : 2 * kManyCtas;
   const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | stride * sizeof(T)) & 31) == 0;
   // enough tokens for every warp of a CTA, or a multiple where there are CTAs enough
   const int least = (kRowWarps + items - 1) / items;
-  const int tokens = std::min(std::max((n / many + least - 1) / least, 1) * least, kMaxTokens);
+  const int tokens = std::min(std::max((n / kManyCtas + least - 1) / least, 1) * least, kMaxTokens);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((n + tokens - 1) / tokens));
   cfg.blockDim = dim3(kRowWarps * 32);
