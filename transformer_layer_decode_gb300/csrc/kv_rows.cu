@@ -215,7 +215,7 @@ constexpr int kMaxTokens = 32;  // of a CTA
 //
 // What bounds it: 8185 rows of 32 heads of 128 in bf16, 172 MB with their 4-bit
 // rows, are written in 37 us (instructions: amax, scale, quotients, digits) and
-// read in 33 (the latency of 2-byte loads), where the bytes take 26; in fp32, 306
+// read in 33 (instructions, and a CTA's look-up), where the bytes take 26; in fp32, 306
 // MB, in 51 and 51 (46); from and to bf16 pages, 268 MB, in 43 (40).  Four rounds:
 // two are 10 % slower, eight 15 % in fp32.
 template <int D, bool Q4, class T, bool READ, int ROUNDS>
