@@ -295,6 +295,31 @@ def test_attention_long_batch_does_not_drift(fmt):
     assert rms <= (5 * tiles / 3) ** 0.5 * 2.0 ** -24 + 2.0 ** -22, rms
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+def test_attention_scores_keep_fp32(fmt, hd):
+    """Scores of a standard deviation of 4, fp32 results.  A score's errors, as root mean squares: q in pieces
+    of 22 bits, 2^-23 / sqrt(3) of each of its products and so of the score, 2.8e-7; five roundings of 2^-24
+    of a block's sum (below 4), 2e-7; the score in log2 units (of 6) and its difference from the reference,
+    2^-24 each, 4e-7; the exponential, 2^-22 / sqrt(3), 1.4e-7: 5.5e-7 together.  With values of mean 0 the
+    outputs are off by as much of their own size.  (Codes as subnormal numbers: 1.2e-6 to 1.4e-6.)"""
+    n, seqs, heads = 31, 64, 8
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    c = kv.KVCache(n_layers=1, n_kv_heads=heads, head_dim=hd, page_rows=16, fmt=fmt, n_pages=2 * seqs, n_seqs=seqs,
+                   max_pages=2)
+    c.extend(None, ints([n] * seqs))
+    at, pos = ints(np.repeat(range(seqs), n)), ints(np.tile(range(n), seqs))
+    k, v = (torch.randn(n * seqs, heads, hd, device="cuda", generator=gen) for _ in range(2))
+    c.append(0, k, v, seqs=at, positions=pos)
+    k, v = (x.double().view(seqs, n, heads, hd) for x in c.read(0, at, pos))
+    q = 4 * torch.randn(seqs, heads, hd, device="cuda", generator=gen)
+    got = c.attention(0, q).double()
+    c.sync_status()
+    w = torch.softmax(torch.einsum("shd,snhd->shn", q.double(), k) / hd ** 0.5, -1)
+    want = torch.einsum("shn,snhd->shd", w, v)
+    assert ((got - want).norm() / want.norm()).item() <= 5.5e-7
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "q4"])
 def test_attention_offsets_past_32_bits(fmt):
     """Pages whose bytes begin past 2^32, in the second layer too."""

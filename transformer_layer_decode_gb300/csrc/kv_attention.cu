@@ -426,11 +426,14 @@ struct WarpBf16 : WarpHead<D> {
 // 128 dimensions is 144 bytes for K and V, 1/3.6 of the bf16 row with the same
 // number of values.  So the codes enter the products with as little unpacking
 // as can be exact.
-//  - K: a nibble n where it lies in a 16-bit word is the fp16 number n 2^-24,
-//    or n 2^-20 four bits up (against q / 16): an AND, no conversion.  The 8
-//    that codes are stored with is taken off by one more product per 8 or 16 rows,
-//    of the block scales with -8 * (sum of q over the block).
-//  - V: 1024 + n or 1024 + 16 n by an OR, and n - 8 by one addition or FMA.
+//  - K, bf16 results: a nibble n where it lies in a 16-bit word is the fp16 number
+//    n 2^-24, or n 2^-20 four bits up (against q / 16): an AND, no conversion.  The
+//    8 that codes are stored with is taken off by one more product per 16 rows, of
+//    the block scales with -8 * (sum of q over the block).  The tensor cores align
+//    such small numbers by fp16's smallest exponent and cut off what is then below
+//    the sum's last bit: scores are off by 4e-7 of themselves.
+//  - V, and K for fp32 results: 1024 + n or 1024 + 16 n by an OR, and n - 8 by one
+//    addition or FMA.
 //  - K's block scales multiply the fp32 sums over a block, V's the weights.
 // q is scaled by a power of two and taken in two fp16 pieces (22 bits; bf16 q
 // needs one), and so is weight * scale for fp32 results; for bf16 results it
@@ -448,14 +451,18 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   using L = Tile<D, true>;
   static constexpr int NB = Sums::NB, kTiles = L::kStep;
   static constexpr bool kWhole = sizeof(T) == 2;  // q, and the weights, are one piece
-  // The largest weight is 2^9 to 2^(9 + kSlack), so that its product with a scale
-  // below one fits fp16 and the others are well above its smallest step.
-  static constexpr float kLift = 9.f;
+  // The largest weight enters its products as 2^9 to 2^(9 + kSlack), so that they,
+  // with scales below one, fit fp16 and the others are well above its smallest step.
+  // kWhole has these 9 in the exponential; fp32 results have them in `unit`: an
+  // exponent near 9 is good to 2^-21, one near 0 to much more.
+  static constexpr int kRoom = 9;
+  static constexpr float kLift = kWhole ? kRoom : 0;
   uint32_t a[2 * NB][kWhole ? 2 : 4];  // q
-  uint32_t bias[2];                    // -8 sum of q per block, in three pieces: operand of one product
+  uint32_t bias[kWhole ? 2 : 1];       // kWhole: -8 sum of q per block, in three pieces: operand of one product
   float f, f1;                         // score = f * product, in log2 units; kWhole: f of head 2t, f1 of the next
   float top;                           // V scales seen are below top = 2^e
-  float unit;                          // ... and enter times unit = 2^-e (as far as fp16 goes); kWhole: as they are for e in [-6, 0]
+  float unit;                          // ... and enter times unit = 2^(kRoom - e) (as far as fp16 goes); kWhole: 2^-e, or
+                                       // as they are for e in [-6, 0]
 
   __device__ static int out_dim(int x, int y, int g) { return 32 * x + 4 * g + 2 * y; }
   __device__ __forceinline__ float out_unit() const { return 1.f / unit; }
@@ -471,10 +478,9 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
     const int e = (int)(__float_as_uint(mx) >> 23) - 126;  // mx < 2^e
     const int sh = min(14 - e, 120);                       // q to below 2^14
     const float up = __uint_as_float((uint32_t)(127 + max(sh, -120)) << 23);
-    f = scale * __uint_as_float((uint32_t)(127 + min(24 - sh, 127)) << 23);
+    f = scale * __uint_as_float((uint32_t)(127 + (kWhole ? min(24 - sh, 127) : -sh)) << 23);
     if (!(mx < INFINITY)) f = __uint_as_float(0x7fffffffu);  // an infinity in q: NaN
-    uint32_t piece[3][NB / 2];
-    float sums[NB];
+    float sums[NB];  // kWhole: of q
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float sum = 0.f;
@@ -485,36 +491,39 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
         uint32_t(&w)[kWhole ? 2 : 4] = a[2 * b + h];
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {
-          const float part = odd ? 1.f / 16 : 1.f;
+          const float part = kWhole && odd ? 1.f / 16 : 1.f;
           float y0 = x[b][2 * h + odd] * part, y1 = x[b][4 + 2 * h + odd] * part;
           const uint32_t hi = take_f16(y0, y1), lo = pack_f16(y0, y1);
-          const float2 u = unpack_f16(hi), r = unpack_f16(lo);
           if constexpr (kWhole) {  // (lo is zero)
+            const float2 u = unpack_f16(hi);
             w[odd] = hi;
+            sum += (u.x + u.y) * (odd ? 16.f : 1.f);
           } else {
             w[2 * odd] = hi;
             w[2 * odd + 1] = lo;
           }
-          sum += ((u.x + r.x) + (u.y + r.y)) * (odd ? 16.f : 1.f);
         }
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      sums[b] = sum * (-8.f / (1 << 10));  // (times 2^14: the codes' 2^-24 in fp16's range)
-    }
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-      for (int j = 0; j < NB / 2; ++j) piece[k][j] = take_f16(sums[2 * j], sums[2 * j + 1]);
-    // the 16 entries of a row of the operand: piece by piece, the blocks in order; then zeros
-    if constexpr (NB == 4) {
-      bias[0] = t == 0 ? piece[0][0] : t == 1 ? piece[0][NB / 2 - 1] : t == 2 ? piece[1][0] : piece[1][NB / 2 - 1];
-      bias[1] = t == 0 ? piece[2][0] : t == 1 ? piece[2][NB / 2 - 1] : 0;
-    } else {
-      bias[0] = t == 0 ? piece[0][0] : t == 1 ? piece[1][0] : t == 2 ? piece[2][0] : 0;
-      bias[1] = 0;
+      if constexpr (kWhole) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sums[b] = sum * (-8.f / (1 << 10));  // (times 2^14: the codes' 2^-24 in fp16's range)
+      }
     }
     if constexpr (kWhole) {
+      uint32_t piece[3][NB / 2];
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int j = 0; j < NB / 2; ++j) piece[k][j] = take_f16(sums[2 * j], sums[2 * j + 1]);
+      // the 16 entries of a row of the operand: piece by piece, the blocks in order; then zeros
+      if constexpr (NB == 4) {
+        bias[0] = t == 0 ? piece[0][0] : t == 1 ? piece[0][NB / 2 - 1] : t == 2 ? piece[1][0] : piece[1][NB / 2 - 1];
+        bias[1] = t == 0 ? piece[2][0] : t == 1 ? piece[2][NB / 2 - 1] : 0;
+      } else {
+        bias[0] = t == 0 ? piece[0][0] : t == 1 ? piece[1][0] : t == 2 ? piece[2][0] : 0;
+        bias[1] = 0;
+      }
       f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
       f = __shfl_sync(0xffffffffu, f, 8 * t);
     }
@@ -531,7 +540,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s < 2^e, -23 <= e <= 16
       top = __uint_as_float((uint32_t)(127 + e) << 23);
       const bool fits = kWhole && e <= 0 && e >= -6;
-      const float now = __uint_as_float((uint32_t)(127 - (fits ? 0 : max(e, -14))) << 23);
+      const float now = __uint_as_float((uint32_t)(127 + (kWhole ? 0 : kRoom) - (fits ? 0 : max(e, -14))) << 23);
       change = now / unit;
       unit = now;
     }
@@ -542,6 +551,18 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   template <bool EDGE>
   __device__ __forceinline__ void step(const uint8_t* st, int lane, uint64_t rows_seen) {
     const int g = lane >> 2, t = lane & 3;
+    const __half2 m1032 = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);
+    // n - 8 of the nibbles 0 and 4, or 1 and 5, of a word
+    auto low = [&](uint32_t z) {
+      const uint32_t u = (z & 0x000f000fu) | 0x64006400u;  // 1024 + n
+      const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&u), m1032);
+      return *reinterpret_cast<const uint32_t*>(&r);
+    };
+    auto high = [&](uint32_t z) {
+      const uint32_t u = (z & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
+      const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), sixteenth, m72);
+      return *reinterpret_cast<const uint32_t*>(&r);
+    };
     // scores: of head g, rows 2t, 2t + 1 of each half; kWhole: of heads 2t, 2t + 1, rows g and g + 8
     float s[4 * kTiles];
     __half2 most = __float2half2_rn(0.f);  // the largest of V's scales, between the lanes
@@ -612,24 +633,15 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           __half2 ks[2][NB / 2];
-          uint32_t row_scales;
-          if constexpr (D == 128) {
-            *reinterpret_cast<uint4*>(ks) = *reinterpret_cast<const uint4*>(ks_at + 64 * b + 16 * t);
-            row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 64 * b + 8 * g + 4 * (t & 1));
-          } else {
-            *reinterpret_cast<uint2*>(ks) = *reinterpret_cast<const uint2*>(ks_at + 32 * b + 8 * t);
-            row_scales = *reinterpret_cast<const uint32_t*>(ks_at + 32 * b + 4 * g);
-          }
-          float z[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(z, bias[0], bias[0], bias[1], bias[1], row_scales, row_scales);  // (rows 8-15 are not used)
-          float s0 = z[0] * (1.f / (1 << 14)), s1 = z[1] * (1.f / (1 << 14));
+          if constexpr (D == 128) *reinterpret_cast<uint4*>(ks) = *reinterpret_cast<const uint4*>(ks_at + 64 * b + 16 * t);
+          else *reinterpret_cast<uint2*>(ks) = *reinterpret_cast<const uint2*>(ks_at + 32 * b + 8 * t);
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             float c[4] = {0.f, 0.f, 0.f, 0.f};
             const uint32_t x = codes(b, j), y = x >> 8;
-            mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], x & 0x000f000fu, x & 0x00f000f0u);
-            mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], y & 0x000f000fu,
-                    y & 0x00f000f0u);
+            mma_f16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], low(x), high(x));
+            mma_f16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], low(y), high(y));
             const float k0 = __half2float(j & 1 ? __high2half(ks[0][j >> 1]) : __low2half(ks[0][j >> 1]));
             const float k1 = __half2float(j & 1 ? __high2half(ks[1][j >> 1]) : __low2half(ks[1][j >> 1]));
             s0 = fmaf(k0, c[0] + c[2], s0);
@@ -679,7 +691,6 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       this->l += sum;
     }
 
-    const __half2 m1032 = __float2half2_rn(-1032.f), sixteenth = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) {
       const uint8_t* sv = st + k * L::kBytes + L::kHalf;
@@ -751,16 +762,6 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
         uint32_t z1 = __byte_perm(v[2][j >> 1], v[3][j >> 1], j & 1 ? 0x7632 : 0x5410);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          auto low = [&](uint32_t z) {
-            const uint32_t u = (z & 0x000f000fu) | 0x64006400u;  // 1024 + n
-            const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&u), m1032);
-            return *reinterpret_cast<const uint32_t*>(&r);
-          };
-          auto high = [&](uint32_t z) {
-            const uint32_t u = (z & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 n
-            const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), sixteenth, m72);
-            return *reinterpret_cast<const uint32_t*>(&r);
-          };
           const uint32_t a0 = low(z0), a1 = high(z0), a2 = low(z1), a3 = high(z1);
           if constexpr (kWhole) {
             mma_f16(this->acc[j][y], a0, a1, a2, a3, pw[0][0], pw[0][1]);
