@@ -136,6 +136,9 @@ __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
 }
 __device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
 
+// 1 / x of a power of two (2^-126 to 2^126).
+__device__ __forceinline__ float inverse2(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+
 // Takes the next piece off (x, y): the pair rounded to 16 bits, leaving the rest.
 __device__ __forceinline__ uint32_t take_bf16(float& x, float& y) {
   const uint32_t w = pack_bf16(x, y);
@@ -217,6 +220,13 @@ struct WarpSums {
     for (int i = 0; i < 4; ++i) to[i] += o[i];
   }
 
+  __device__ __forceinline__ void scale_block(int x, float k) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[x][y][i] *= k;
+  }
+
   __device__ __forceinline__ void scale_acc(float k0, float k1) {
 #pragma unroll
     for (int x = 0; x < NB; ++x)
@@ -237,8 +247,8 @@ struct WarpHead : WarpSums<D> {
   }
 
   // Moves every head's reference so that its largest score (mx: the largest of
-  // this lane's new ones) has the weight 2^lift; scales the outputs by `unit` besides.
-  __device__ __forceinline__ void raise(float mx, float lift, float unit) {
+  // this lane's new ones) has the weight 2^lift.
+  __device__ __forceinline__ void raise(float mx, float lift) {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float now = fmaxf(ref, mx - lift);
@@ -246,7 +256,7 @@ struct WarpHead : WarpSums<D> {
     ref = now;
     l *= keep;
     const int t = threadIdx.x & 3;
-    this->scale_acc(__shfl_sync(0xffffffffu, keep, 8 * t) * unit, __shfl_sync(0xffffffffu, keep, 8 * t + 4) * unit);
+    this->scale_acc(__shfl_sync(0xffffffffu, keep, 8 * t), __shfl_sync(0xffffffffu, keep, 8 * t + 4));
   }
 
   __device__ __forceinline__ void write_refs(float2* to, int lane) {
@@ -268,7 +278,7 @@ struct WarpHeadPair : WarpSums<D> {
     l[0] = l[1] = 0.f;
   }
 
-  __device__ __forceinline__ void raise(float mx0, float mx1, float lift, float unit) {
+  __device__ __forceinline__ void raise(float mx0, float mx1, float lift) {
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
@@ -278,7 +288,7 @@ struct WarpHeadPair : WarpSums<D> {
     const float keep0 = exp2_approx(ref[0] - now0), keep1 = exp2_approx(ref[1] - now1);
     ref[0] = now0, ref[1] = now1;
     l[0] *= keep0, l[1] *= keep1;
-    this->scale_acc(keep0 * unit, keep1 * unit);
+    this->scale_acc(keep0, keep1);
   }
 
   __device__ __forceinline__ void write_refs(float2* to, int lane) {
@@ -332,7 +342,7 @@ struct WarpBf16 : WarpHead<D> {
   float f;                              // score = f * product, in log2 units
 
   __device__ static int out_dim(int x, int y, int g) { return 64 * (x >> 1) + 8 * g + 4 * (x & 1) + 2 * y; }
-  __device__ __forceinline__ float out_unit() const { return 1.f; }
+  __device__ __forceinline__ float out_unit(int) const { return 1.f; }
 
   __device__ __forceinline__ void set_q(float (&x)[NB][8], int, float scale) {
     f = scale;
@@ -384,7 +394,7 @@ struct WarpBf16 : WarpHead<D> {
         if (!(seen >> i & 1)) s[i] = -INFINITY;
     }
     const float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-    if (__any_sync(0xffffffffu, mx > this->ref + kSlack)) this->raise(mx, 0.f, 1.f);
+    if (__any_sync(0xffffffffu, mx > this->ref + kSlack)) this->raise(mx, 0.f);
     float w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = exp2_approx(s[i] - this->ref);
@@ -454,18 +464,28 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   // The largest weight enters its products as 2^9 to 2^(9 + kSlack), so that they,
   // with scales below one, fit fp16 and the others are well above its smallest step.
   // kWhole has these 9 in the exponential; fp32 results have them in `unit`: an
-  // exponent near 9 is good to 2^-21, one near 0 to much more.
-  static constexpr int kRoom = 9;
+  // exponent near 9 is good to 2^-21, one near 0 to much more.  The scales of a block
+  // are brought below one by a power of two of their own: the blocks of a row can
+  // differ by as much as fp16 does, and a product's step should be that of its block.
+  // The second piece of a product enters times 2^kLow, which comes off its sums: it is
+  // the first one's rounding, 2^-11 of it, and would lose its bits to fp16's smallest
+  // step where the product is below 2^-3.
+  static constexpr int kRoom = 9, kLow = 11;
   static constexpr float kLift = kWhole ? kRoom : 0;
   uint32_t a[2 * NB][kWhole ? 2 : 4];  // q
   uint32_t bias[kWhole ? 2 : 1];       // kWhole: -8 sum of q per block, in three pieces: operand of one product
   float f, f1;                         // score = f * product, in log2 units; kWhole: f of head 2t, f1 of the next
-  float top;                           // V scales seen are below top = 2^e
-  float unit;                          // ... and enter times unit = 2^(kRoom - e) (as far as fp16 goes); kWhole: 2^-e, or
-                                       // as they are for e in [-6, 0]
+  float top0, top1;                    // V scales seen in the two blocks that this lane looks at are below 2^e
+  float unit[kWhole ? 1 : NB];         // a block's enter times 2^(kRoom - e); kWhole: in unit2, as far as fp16 goes 2^-e, or
+  __half2 unit2[kWhole ? NB / 2 : 1];  // as they are for e in [-2, 0] (e = -1 is usual; scaling costs 2 %)
+  bool scaled;                         // kWhole: some block's are not as they are
 
   __device__ static int out_dim(int x, int y, int g) { return 32 * x + 4 * g + 2 * y; }
-  __device__ __forceinline__ float out_unit() const { return 1.f / unit; }
+  __device__ __forceinline__ float unit_of(int x) const {
+    if constexpr (kWhole) return x & 1 ? __high2float(unit2[x >> 1]) : __low2float(unit2[x >> 1]);
+    else return unit[x];
+  }
+  __device__ __forceinline__ float out_unit(int x) const { return inverse2(unit_of(x)); }
 
   __device__ __forceinline__ void set_q(float (&x)[NB][8], int t, float scale) {
     float mx = 0.f;
@@ -528,23 +548,48 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       f = __shfl_sync(0xffffffffu, f, 8 * t);
     }
     this->clear();
-    top = 1e-30f;
-    unit = 1.f;
+    top0 = top1 = 5.9604644775390625e-8f;  // fp16's smallest: a scale that is not 0 reaches it
+    if constexpr (kWhole) {
+#pragma unroll
+      for (int j = 0; j < NB / 2; ++j) unit2[j] = __float2half2_rn(1.f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) unit[j] = 1.f;
+    }
+    scaled = false;
   }
 
-  // Makes room for V scales up to s (of this lane); what the outputs are to be scaled by.
-  __device__ __forceinline__ float make_room(float s) {
-    s = warp_max(s);
-    float change = 1.f;
-    if (s >= top) {
-      const int e = (int)(__float_as_uint(s) >> 23) - 126;  // s < 2^e, -23 <= e <= 16
-      top = __uint_as_float((uint32_t)(127 + e) << 23);
-      const bool fits = kWhole && e <= 0 && e >= -6;
-      const float now = __uint_as_float((uint32_t)(127 + (kWhole ? 0 : kRoom) - (fits ? 0 : max(e, -14))) << 23);
-      change = now / unit;
-      unit = now;
+  // Makes room for V scales up to s0 and s1 in this lane's two blocks, which are 2 i
+  // and 2 i + 1 for i = lane % (NB / 2).
+  __device__ __forceinline__ void make_room(float s0, float s1) {
+#pragma unroll
+    for (int o = NB / 2; o < 32; o <<= 1) {
+      s0 = fmaxf(s0, __shfl_xor_sync(0xffffffffu, s0, o));
+      s1 = fmaxf(s1, __shfl_xor_sync(0xffffffffu, s1, o));
     }
-    return change;
+    auto above = [](float s, float top) {  // the next power of two (-23 <= e <= 16)
+      return s < top ? top : __uint_as_float(((__float_as_uint(s) >> 23) + 1) << 23);
+    };
+    top0 = above(s0, top0);
+    top1 = above(s1, top1);
+    scaled = false;
+    float now[NB];
+#pragma unroll
+    for (int x = 0; x < NB; ++x) {
+      const float top = __shfl_sync(0xffffffffu, x & 1 ? top1 : top0, x >> 1);
+      const int e = (int)(__float_as_uint(top) >> 23) - 127;
+      const bool fits = kWhole && e <= 0 && e >= -2;
+      now[x] = __uint_as_float((uint32_t)(127 + (kWhole ? (fits ? 0 : -max(e, -15)) : kRoom - e)) << 23);
+      scaled |= now[x] != 1.f;
+      this->scale_block(x, now[x] * out_unit(x));
+    }
+    if constexpr (kWhole) {
+#pragma unroll
+      for (int j = 0; j < NB / 2; ++j) unit2[j] = __floats2half2_rn(now[2 * j], now[2 * j + 1]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < NB; ++x) unit[x] = now[x];
+    }
   }
 
   // kTiles staged tiles.  EDGE: some row is not visible; rows_seen: a bit for each that is.
@@ -658,16 +703,17 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
         }
       }
     }
-    const float big = fmaxf(__low2float(most), __high2float(most));
+    const float most0 = __low2float(most), most1 = __high2float(most);
+    const bool over = most0 >= top0 || most1 >= top1;
     float w[4 * kTiles];
     if constexpr (kWhole) {
       float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
 #pragma unroll
       for (int i = 4; i < 4 * kTiles; i += 2) mx0 = fmaxf(mx0, s[i]), mx1 = fmaxf(mx1, s[i + 1]);
-      if (__any_sync(0xffffffffu, mx0 > this->ref[0] + (kLift + kSlack) || mx1 > this->ref[1] + (kLift + kSlack) ||
-                                      big >= top)) {
-        const float change = make_room(big);
-        this->raise(mx0, mx1, kLift, change);
+      if (__any_sync(0xffffffffu,
+                     mx0 > this->ref[0] + (kLift + kSlack) || mx1 > this->ref[1] + (kLift + kSlack) || over)) {
+        make_room(most0, most1);
+        this->raise(mx0, mx1, kLift);
       }
 #pragma unroll
       for (int i = 0; i < 4 * kTiles; ++i) {
@@ -678,9 +724,9 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       float mx = s[0];
 #pragma unroll
       for (int i = 1; i < 4 * kTiles; ++i) mx = fmaxf(mx, s[i]);
-      if (__any_sync(0xffffffffu, mx > this->ref + (kLift + kSlack) || big >= top)) {
-        const float change = make_room(big);
-        this->raise(mx, kLift, change);
+      if (__any_sync(0xffffffffu, mx > this->ref + (kLift + kSlack) || over)) {
+        make_room(most0, most1);
+        this->raise(mx, kLift);
       }
       float sum = 0.f;
 #pragma unroll
@@ -711,11 +757,13 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
             for (int j = 0; j < NB / 2; ++j) vs[i][j] = __float2half2_rn(0.f);
           }
       }
-      if (kWhole && unit != 1.f) {
+      if constexpr (kWhole) {
+        if (scaled) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < NB / 2; ++j) vs[i][j] = __hmul2(vs[i][j], __float2half2_rn(unit));
+            for (int j = 0; j < NB / 2; ++j) vs[i][j] = __hmul2(vs[i][j], unit2[j]);
+        }
       }
       uint32_t v[4][NB / 2];
 #pragma unroll
@@ -729,15 +777,12 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
         }
       }
       uint32_t ph[2];
+      if constexpr (kWhole) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if constexpr (kWhole) {
+        for (int b = 0; b < 2; ++b) {
           // row g + 8 b of heads 2t, 2t + 1 to rows 2t, 2t + 1 of that half of head g
           const uint32_t rows = pack_f16(w[4 * k + 2 * b], w[4 * k + 2 * b + 1]);
           asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(ph[b]) : "r"(rows));
-        } else {
-          w[4 * k + 2 * b] *= unit;
-          w[4 * k + 2 * b + 1] *= unit;
         }
       }
 #pragma unroll
@@ -752,10 +797,10 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
             const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&ph[b]), both);
             pw[0][b] = *reinterpret_cast<const uint32_t*>(&y);
           } else {
-            float y0 = w[4 * k + 2 * b] * (j & 1 ? __high2float(h0) : __low2float(h0));
-            float y1 = w[4 * k + 2 * b + 1] * (j & 1 ? __high2float(h1) : __low2float(h1));
+            float y0 = w[4 * k + 2 * b] * unit[j] * (j & 1 ? __high2float(h0) : __low2float(h0));
+            float y1 = w[4 * k + 2 * b + 1] * unit[j] * (j & 1 ? __high2float(h1) : __low2float(h1));
             pw[0][b] = take_f16(y0, y1);
-            pw[1][b] = pack_f16(y0, y1);
+            pw[1][b] = pack_f16(y0 * (1 << kLow), y1 * (1 << kLow));
           }
         }
         uint32_t z0 = __byte_perm(v[0][j >> 1], v[1][j >> 1], j & 1 ? 0x7632 : 0x5410);
@@ -768,6 +813,8 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
           } else {  // (see add_tile)
             float o[4] = {0.f, 0.f, 0.f, 0.f};
             mma_f16(o, a0, a1, a2, a3, pw[kPieces - 1][0], pw[kPieces - 1][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= 1.f / (1 << kLow);
             mma_f16(o, a0, a1, a2, a3, pw[0][0], pw[0][1]);
             this->add_tile(this->acc[j][y], o);
           }
@@ -936,14 +983,16 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
     float m = warp_ref[0][h].x;
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) m = fmaxf(m, warp_ref[w][h].x);
-    const float k = exp2_approx(warp_ref[warp][h].x - m) * st.out_unit();
+    const float k = exp2_approx(warp_ref[warp][h].x - m);
     float* row = sums + (warp * kHeadBlock + h) * L::kMergeRow;
 #pragma unroll
-    for (int x = 0; x < W::NB; ++x)
+    for (int x = 0; x < W::NB; ++x) {
+      const float kx = k * st.out_unit(x);
 #pragma unroll
       for (int y = 0; y < 2; ++y)
         *reinterpret_cast<float2*>(row + W::out_dim(x, y, g)) =
-            make_float2(st.acc[x][y][hh] * k, st.acc[x][y][2 + hh] * k);
+            make_float2(st.acc[x][y][hh] * kx, st.acc[x][y][2 + hh] * kx);
+    }
   }
   __syncthreads();
   UnitSums<D> o;
