@@ -395,6 +395,9 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  * caller); attention, read and append touch no table, length or count, and
  * calls of these may overlap as long as none reads rows that another writes
  * and each attention has a workspace of its own.
+ * Attention, fork and compact are two launches each, of which the second reads
+ * what the first left in the workspace or the scratch: host threads that queue
+ * calls on one stream must not do so at the same time where these share either.
  *
  * Lists of sequences are device int32; a negative entry is padding and is
  * skipped, and what belongs to it is neither read nor written.  A list given

@@ -1,0 +1,107 @@
+"""Calls of the paged cache in the circumstances that its documentation allows: host threads, streams, captures
+that others begin, the largest sizes, pages and lengths out of range."""
+import threading
+
+import numpy as np
+import pytest
+
+from transformer_layer_decode_gb300 import dec, kv
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+
+def ints(a):
+    return torch.tensor(np.asarray(a, np.int32), dtype=torch.int32, device="cuda")
+
+
+def filled(fmt, nkv, hd, R, lens, *, spare=3, seed=0, layers=1, room=0):
+    """A cache with sequences of these lengths, all rows written."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    width = max(1, -(-room // R), max(-(-n // R) for n in lens))
+    c = kv.KVCache(n_layers=layers, n_kv_heads=nkv, head_dim=hd, page_rows=R, fmt=fmt, n_seqs=len(lens),
+                   n_pages=sum(-(-n // R) for n in lens) + spare, max_pages=width)
+    c.extend(None, ints(lens))
+    seqs = ints([s for s, n in enumerate(lens) for _ in range(n)])
+    pos = ints([j for n in lens for j in range(n)])
+    for layer in range(layers):
+        k, v = (torch.randn(len(seqs), nkv, hd, device="cuda", generator=gen) for _ in range(2))
+        c.append(layer, k, v, seqs=seqs, positions=pos)
+    c.sync_status()
+    return c
+
+
+def in_threads(*works):
+    errors = []
+
+    def run(work):
+        try:
+            work()
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(w,)) for w in works]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if errors:
+        raise errors[0]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+def test_attention_of_threads_on_one_stream(fmt):
+    """Units cut into parts, which the second launch of a call joins: with another call's first launch between
+    the two it would join that one's."""
+    c = filled(fmt, 2, 64, 16, [3000, 2500])
+    n = 6
+    qs = [torch.randn(2, 4, 64, device="cuda") for _ in range(n)]
+    want = [c.attention(0, q).clone() for q in qs]
+    outs = [[] for _ in qs]
+
+    def work(i):
+        for _ in range(300):
+            outs[i].append(c.attention(0, qs[i]))
+
+    torch.cuda.synchronize()
+    in_threads(*(lambda i=i: work(i) for i in range(n)))
+    torch.cuda.synchronize()
+    for i in range(n):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+    c.sync_status()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+def test_pages_of_threads_on_one_stream(fmt):
+    """Threads that fork, extend, release and compact one cache over and over: every plan is carried out by its
+    own call, so at the end the tables name each page as often as it is counted, and the forks hold their
+    parents' rows."""
+    lens = [40, 0, 0, 100, 0, 0, 7, 0, 0]
+    c = filled(fmt, 1, 64, 16, lens, spare=60, room=160, layers=2)
+    torch.cuda.synchronize()
+
+    def work(parent):
+        parents, children = ints([parent, parent]), ints([parent + 1, parent + 2])
+        for i in range(60):
+            c.fork(parents, children)
+            c.extend(children)
+            if i < 59:
+                c.release(children)
+            if i % 7 == parent:
+                c.compact()
+
+    in_threads(*(lambda p=p: work(p) for p in (0, 3, 6)))
+    c.sync_status()
+    assert c.lens.tolist() == [lens[p] + more for p in (0, 3, 6) for more in (0, 1, 1)]
+    table = c.table.cpu().numpy()
+    assert np.array_equal(np.bincount(table[table >= 0], minlength=c.refs.numel()), c.refs.cpu().numpy())
+    for parent in (0, 3, 6):
+        pos = ints(range(lens[parent]))
+        for layer in range(2):
+            rows = [c.read(layer, torch.full_like(pos, s), pos) for s in (parent, parent + 1, parent + 2)]
+            for k, v in rows[1:]:
+                assert torch.equal(k, rows[0][0]) and torch.equal(v, rows[0][1])
+    c.sync_status()

@@ -9,6 +9,7 @@ nothing; :meth:`KVCache.sync_status` reports what the kernels refused.
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -50,6 +51,9 @@ class KVCache:
     empty here from n_pages, n_seqs and max_pages (pages of one sequence), or
     taken as they are: pool uint8 [n_layers, n_pages, page_bytes], table int32
     [n_seqs, max_pages], lens int32 [n_seqs], refs int32 [n_pages].
+
+    Host threads may share a cache: a call's launches are queued without another's
+    between them.  On the GPU the calls keep the order that include/dec.h asks for.
     """
 
     def __init__(self, *, n_layers: int, n_kv_heads: int, head_dim: int, page_rows: int | None = None,
@@ -94,6 +98,7 @@ class KVCache:
         self.scratch = torch.empty(ints.value, dtype=torch.int32, device=self.device)
         for name in ("pool", "table", "lens", "refs", "status", "scratch"):
             setattr(self.desc, name, getattr(self, name).data_ptr())
+        self._lock = threading.Lock()  # of the launches of a call, which hand a workspace or the scratch on
         self._workspaces: dict = {}  # of a stream's attention calls, which run one after another
 
     # ---- marshalling ----------------------------------------------------------
@@ -148,9 +153,10 @@ class KVCache:
         handle = _raw_stream(self._index) if stream is None else \
             stream if isinstance(stream, int) else stream.cuda_stream
         if _current_device() == self._index:
-            rc = fn(self._ref, *args, handle)
+            with self._lock:
+                rc = fn(self._ref, *args, handle)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(self.device), self._lock:
                 rc = fn(self._ref, *args, handle)
         if rc:
             self._check(rc)
