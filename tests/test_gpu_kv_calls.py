@@ -105,3 +105,40 @@ def test_pages_of_threads_on_one_stream(fmt):
             for k, v in rows[1:]:
                 assert torch.equal(k, rows[0][0]) and torch.equal(v, rows[0][1])
     c.sync_status()
+
+
+# ---- pages ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("at", [0, 2, 3, 40])
+def test_fork_refuses_pages_that_are_none(at):
+    """A parent's entry past the pool, at its first page, further on, its partly filled last one or past it:
+    nothing is forked, not even the entry beside it, and the status says so."""
+    R, width = 16, 50
+    c = kv.KVCache(n_layers=1, n_kv_heads=1, head_dim=64, page_rows=R, n_pages=12, n_seqs=5, max_pages=width)
+    c.extend(ints([0, 1]), ints([3 * R + 5, 20]))
+    c.sync_status()
+    good = int(c.table[0, at])
+    for bad in (12, 1 << 20, 2**31 - 1):
+        c.table[0, at] = bad
+        state = [t.clone() for t in (c.table, c.lens, c.refs)]
+        c.fork(ints([1, 0]), ints([2, 3]))
+        with pytest.raises(dec.DecError, match="index"):
+            c.sync_status()
+        assert all(torch.equal(a, b) for a, b in zip(state, (c.table, c.lens, c.refs)))
+    c.table[0, at] = good
+    c.fork(ints([1, 0, -1]), ints([2, 3, 4]))
+    c.sync_status()
+    assert c.lens.tolist() == [3 * R + 5, 20, 20, 3 * R + 5, 0]
+
+
+def test_fork_of_a_windowed_parent():
+    """Entries without a page (freed behind a window) are copied as they are."""
+    c = kv.KVCache(n_layers=1, n_kv_heads=1, head_dim=64, page_rows=16, n_pages=12, n_seqs=2, max_pages=8)
+    c.extend(ints([0]), ints([100]))
+    c.release(ints([0]), window=20, sinks=3)
+    c.fork(ints([0]), ints([1]))
+    c.sync_status()
+    a, b = c.table.cpu().numpy()
+    assert list(a >= 0) == list(b >= 0) == [True, False, False, False, False, True, True, False]
+    assert list(a == b) == [True, True, True, True, True, True, False, True]
+    assert c.refs.cpu().numpy()[a[[0, 5]]].tolist() == [2, 2] and c.refs.cpu().numpy()[[a[6], b[6]]].tolist() == [1, 1]
