@@ -386,7 +386,7 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  *   lens    [n_seqs]: rows of each sequence
  *   refs    [n_pages]: how many table entries name the page; 0 = free
  *   status  one word of enum dec_kv_bits, OR-ed by the kernels
- *   scratch dec_kv_sizes ints, used by extend, fork and compact within a call
+ *   scratch dec_kv_sizes ints, used by extend, fork, compact and status within a call
  *
  * An empty cache is table = -1 (all bytes 0xFF), lens = refs = status = 0.
  * A caller that takes rows off a sequence's end by itself (lens) must also take
@@ -526,7 +526,8 @@ int dec_kv_compact(const dec_kv_cache* c, dec_stream_t stream);
 
 /* Waits for `stream`, reads and clears the status word: DEC_OK, or
  * DEC_ERR_DEVICE with the bits in *bits (if not NULL) and in the message of
- * dec_last_error(NULL). */
+ * dec_last_error(NULL).  A bit that a call on another stream sets meanwhile is
+ * reported by this call or by the next. */
 int dec_kv_status(const dec_kv_cache* c, int* bits, dec_stream_t stream);
 
 /* Source: none on the pages (resource lifetime of the C ABI).

@@ -107,6 +107,44 @@ def test_pages_of_threads_on_one_stream(fmt):
     c.sync_status()
 
 
+# ---- the status ---------------------------------------------------------------------
+
+def test_status_of_other_streams_calls_is_not_lost():
+    """While a thread reads a status that has a bit of its own, appends on another stream are refused one at a
+    time: every refusal is reported by a reading that began before or by the first one that begins after it."""
+    c = filled("bf16", 1, 64, 16, [20, 0])
+    x = torch.zeros(1, 1, 64, device="cuda")
+    bad, at = ints([1]), ints([99])
+    side, reader = torch.cuda.Stream(), torch.cuda.Stream()
+    rng = np.random.default_rng(0)
+
+    def bits(stream):
+        try:
+            c.sync_status(stream)
+        except dec.DecError as e:
+            return ("index" in str(e)) + 2 * ("bad list" in str(e))
+        return 0
+
+    for i in range(400):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(reader):
+            c.extend(ints([1, 1]))                      # refused: the reading below has something to clear
+        got = []
+        t = threading.Thread(target=lambda: got.append(bits(reader)))
+        torch.cuda.synchronize()
+        torch.cuda._sleep(1)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(int(rng.integers(1, 400_000)))  # up to 0.2 ms
+            c.append(0, x, x, seqs=bad, positions=at)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        got.append(bits(reader))
+        assert got[0] & 2 and (got[0] | got[1]) & 1, (i, got)
+    c.sync_status()
+
+
 # ---- pages ------------------------------------------------------------------------
 
 @pytest.mark.parametrize("at", [0, 2, 3, 40])

@@ -34,6 +34,7 @@ __host__ __device__ inline int kv_row_bytes(int head_dim, bool q4) {
 // of pages (compact) or the free pages found (extend, fork), the page copies
 // (source, destination), and where each list entry's pages start.
 constexpr int kKvScratchHead = 32;
+constexpr int kKvScratchStatus = kKvScratchHead - 1;  // of the head's words: the status as dec_kv_status found it
 __host__ __device__ inline int64_t kv_scratch_moves(int64_t n_pages) { return kKvScratchHead + n_pages; }
 __host__ __device__ inline int64_t kv_scratch_offsets(int64_t n_pages, int64_t n_seqs) {
   return kv_scratch_moves(n_pages) + n_pages + 2 * n_seqs;

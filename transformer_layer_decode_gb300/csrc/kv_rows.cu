@@ -321,6 +321,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
   }
 }
 
+// Reads and clears the status in one step: bits that calls on other streams set in
+// the meantime are in this answer or in the next.
+__global__ void kv_take_status(int32_t* status, int32_t* taken) { *taken = atomicExch(status, 0); }
+
 template <int D, bool Q4, class T, bool READ>
 cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const int32_t* seqs,
                         const int32_t* positions, int n, cudaStream_t s) {
@@ -403,12 +407,13 @@ extern "C" int dec_kv_status(const dec_kv_cache* c, int* bits, dec_stream_t stre
   if (int rc = kv_check(c, true)) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int flag = 0;
-  cudaError_t e = cudaMemcpyAsync(&flag, c->status, sizeof flag, cudaMemcpyDeviceToHost, s);
+  int32_t* taken = c->scratch + kKvScratchStatus;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = cfg.blockDim = dim3(1);
+  cfg.stream = s;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_take_status, c->status, taken);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&flag, taken, sizeof flag, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && flag) {
-    e = cudaMemsetAsync(c->status, 0, sizeof flag, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  }
   if (e != cudaSuccess) return fail_no_handle(DEC_ERR_CUDA, "reading the cache's status: %s", cudaGetErrorString(e));
   if (bits) *bits = flag;
   if (flag)
