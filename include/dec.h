@@ -423,7 +423,8 @@ enum dec_kv_bits {
 };
 
 typedef struct dec_kv_cache {
-  int32_t n_layers, n_kv_heads;
+  int32_t n_layers;
+  int32_t n_kv_heads; /* 1..1024 */
   int32_t head_dim;   /* 64 or 128 */
   int32_t page_rows;  /* a multiple of 16, 16..1024 */
   int32_t n_pages;    /* 1..2^20 */
@@ -482,8 +483,8 @@ int dec_kv_read(const dec_kv_cache* c, int layer, void* k, void* v, int type, in
  * to 2^-20 of scale * sum |q| * 8 * (its K scale).  The same call gives the
  * same bits.  A visible row
  * without a valid page is left out and sets DEC_KV_BAD_INDEX.  q, o and their
- * strides are multiples of 16 bytes; o must not overlap q.  n * n_q_heads is
- * at most 2^24.
+ * strides are multiples of 16 bytes; o must not overlap q.  n and n_q_heads are
+ * at most 65536 each, and their product 2^24.
  * workspace: device memory of dec_kv_attention_workspace bytes, 16-byte
  * aligned, for this call alone (its content does not matter before or after,
  * and calls that may overlap need one each). */

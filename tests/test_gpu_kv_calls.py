@@ -107,6 +107,28 @@ def test_pages_of_threads_on_one_stream(fmt):
     c.sync_status()
 
 
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("fmt,room", [("bf16", 16), ("q4", 16), ("bf16", 4096), ("q4", 4096)])
+def test_the_most_queries(fmt, room, listed):
+    """65536 sequences at once, short of rows or not (kernels that count, and that do not): the rows are pages
+    that all share, so the results come in kinds."""
+    n, hd, R = 65536, 64, 16
+    c = kv.KVCache(n_layers=1, n_kv_heads=1, head_dim=hd, page_rows=R, fmt=fmt, n_pages=3, n_seqs=n, max_pages=room // R)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(3 * R, 1, hd, device="cuda", generator=gen) for _ in range(2))
+    c.lens[:3] = R
+    c.table[:3, 0] = ints([0, 1, 2])
+    c.append(0, k, v, seqs=ints(np.repeat(range(3), R)), positions=ints(np.tile(range(R), 3)))
+    kind = torch.arange(n, device="cuda") % 48
+    c.table[:, 0] = (kind % 3).int()
+    c.lens[:] = (kind // 3).int()                       # 0 to 15 rows
+    q = torch.randn(48, 2, hd, device="cuda", generator=gen)
+    want = c.attention(0, q)
+    got = c.attention(0, q[kind], seqs=torch.arange(n, dtype=torch.int32, device="cuda") if listed else None)
+    c.sync_status()
+    assert torch.equal(got, want[kind])
+
+
 # ---- the status ---------------------------------------------------------------------
 
 def test_status_of_other_streams_calls_is_not_lost():

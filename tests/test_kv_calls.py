@@ -5,7 +5,10 @@ import time
 
 import pytest
 
-from transformer_layer_decode_gb300 import kv
+from transformer_layer_decode_gb300 import build as tld_build
+from transformer_layer_decode_gb300 import dec, kv
+
+MEM = 1 << 20  # an aligned address that no call here gets to use
 
 
 @pytest.fixture
@@ -40,3 +43,27 @@ def test_calls_of_two_threads_do_not_interleave(cache):
     for t in threads:
         t.join()
     assert len(seen) == 30 and all(len(s) == 1 for s in seen)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    tld_build.build()
+    return dec.load_library()
+
+
+@pytest.mark.parametrize("n,heads,code", [
+    (65536, 1, dec.DEC_ERR_CUDA), (65536, 256, dec.DEC_ERR_CUDA), (256, 65536, dec.DEC_ERR_CUDA),
+    (65537, 1, dec.DEC_ERR_ARG), (65536, 257, dec.DEC_ERR_SHAPE), (1, 65537, dec.DEC_ERR_SHAPE)])
+def test_the_most_queries_and_heads(lib, n, heads, code):
+    """What the header allows gets as far as the device, which is not there; one more does not."""
+    # a workspace at no multiple of 16: refused after the sizes, should there be a device
+    c = kv.KVCacheDesc(n_layers=1, n_kv_heads=1, head_dim=64, page_rows=16, n_pages=32, n_seqs=65536, max_pages=1, format=0,
+                       pool=MEM, table=MEM, lens=MEM, refs=MEM, status=MEM, scratch=MEM)
+    width = 64 * heads
+    for seqs in (None, MEM):
+        rc = lib.dec_kv_attention(ctypes.byref(c), 0, MEM, 1 << 50, 0, width, width, seqs, n, heads, 0, 0, 0.0, MEM + 4,
+                                  1 << 40, None)
+        if code == dec.DEC_ERR_CUDA and rc == dec.DEC_ERR_ARG:
+            assert "workspace" in dec.load_library().dec_last_error(None).decode()
+        else:
+            assert rc == code

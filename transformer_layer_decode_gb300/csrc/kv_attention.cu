@@ -32,7 +32,7 @@ constexpr int kTileRows = 16;
 constexpr int kWarps = 4;
 constexpr int kThreadsA = kWarps * 32;
 constexpr int kHeadBlock = 8;      // query heads of a unit: the n of the tensor-core products
-constexpr int kMaxQueries = 65535;
+constexpr int kMaxQueries = 65536;
 constexpr int kChunkRows = 128;    // queries whose tiles one warp counts at a time
 constexpr int kMaxChunks = (kMaxQueries + kChunkRows - 1) / kChunkRows;
 // A reference moves only when a score passes it by this (log2 units).
