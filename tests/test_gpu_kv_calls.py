@@ -107,6 +107,25 @@ def test_pages_of_threads_on_one_stream(fmt):
     c.sync_status()
 
 
+@pytest.mark.parametrize("fmt,room", [("bf16", 64), ("q4", 64), ("bf16", 4096), ("q4", 4096)])
+def test_skipped_rows_of_a_result_made_here_are_zero(fmt, room):
+    """A length out of range skips its sequence, in a list or not: zeros, whatever the memory held before."""
+    c = filled(fmt, 2, 64, 16, [30, 40, 50], room=room)
+    q = torch.randn(3, 4, 64, device="cuda")
+    want = c.attention(0, q)
+    c.lens[1] = room + 1
+    c.lens[2] = -1
+    want[1:] = 0
+    for seqs in (None, ints([0, 1, 2])):
+        torch.cuda.synchronize()
+        junk = [torch.full_like(q, float("nan")) for _ in range(64)]   # what the allocator hands out next
+        del junk
+        got = c.attention(0, q, seqs=seqs)
+        with pytest.raises(dec.DecError, match="index"):
+            c.sync_status()
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("listed", [False, True])
 @pytest.mark.parametrize("fmt,room", [("bf16", 16), ("q4", 16), ("bf16", 4096), ("q4", 4096)])
 def test_the_most_queries(fmt, room, listed):

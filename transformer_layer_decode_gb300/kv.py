@@ -211,7 +211,7 @@ class KVCache:
         n, heads = q.shape[0], q.shape[1]
         sp, _ = self._ints("seqs", seqs, n)
         if out is None:
-            out = self._new(torch.empty if seqs is None else torch.zeros, q.shape, q.dtype, stream)
+            out = self._new(torch.zeros, q.shape, q.dtype, stream)  # (a length out of range skips any of them)
         op, ot, os_ = self._rows("out", out, heads)
         if ot != qt or out.shape[0] != n:
             raise ValueError("out: the type and rows of q are wanted")
