@@ -1,5 +1,6 @@
 """Calls of the paged cache in the circumstances that its documentation allows: host threads, streams, captures
 that others begin, the largest sizes, pages and lengths out of range."""
+import ctypes
 import threading
 
 import numpy as np
@@ -146,6 +147,73 @@ def test_the_most_queries(fmt, room, listed):
     got = c.attention(0, q[kind], seqs=torch.arange(n, dtype=torch.int32, device="cuda") if listed else None)
     c.sync_status()
     assert torch.equal(got, want[kind])
+
+
+class Runtime:
+    """Captures that torch knows nothing of, through the CUDA runtime that it has loaded."""
+
+    def __init__(self):
+        with open("/proc/self/maps") as f:
+            paths = {line.split()[-1] for line in f if "libcudart.so" in line}
+        if not paths:
+            pytest.skip("no shared CUDA runtime")
+        self.lib = ctypes.CDLL(sorted(paths)[0])
+
+    def call(self, name, *args):
+        assert getattr(self.lib, name)(*args) == 0, name
+
+    def capture(self, stream, work):
+        s, graph, run = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p(), ctypes.c_void_p()
+        with torch.cuda.stream(stream):
+            self.call("cudaStreamBeginCapture", s, 2)   # (relaxed: allocations are allowed)
+            try:
+                work()
+            finally:
+                self.call("cudaStreamEndCapture", s, ctypes.byref(graph))
+        self.call("cudaGraphInstantiate", ctypes.byref(run), graph, ctypes.c_ulonglong(0))
+        self.call("cudaGraphDestroy", graph)
+        return run
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4"])
+def test_captures_that_torch_did_not_begin(fmt):
+    """Their calls' workspaces stay: memory that is handed out afterwards is not written by a replay."""
+    runtime = Runtime()
+    c = filled(fmt, 2, 64, 16, [3000, 2500])
+    size = c.workspace().numel()
+    qs = [torch.randn(2, 4, 64, device="cuda") for _ in range(2)]
+    want = [c.attention(0, q).clone() for q in qs]
+    outs = [torch.empty_like(q) for q in qs]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def work():
+        for q, o in zip(qs, outs):
+            c.attention(0, q, out=o)
+
+    run = runtime.capture(side, work)
+    with torch.cuda.stream(side):
+        later = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(6)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        runtime.call("cudaGraphLaunch", run, ctypes.c_void_p(side.cuda_stream))
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        assert all(bool((x == 7).all()) for x in later)
+    runtime.call("cudaGraphExecDestroy", run)
+    c.sync_status()
+    # torch's own captures keep theirs in the graph's pool: nothing more is held here
+    held = len(c._captured_workspaces)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        work()
+    g.replay()
+    torch.cuda.synchronize()
+    assert held == 2 and len(c._captured_workspaces) == held
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
 # ---- the status ---------------------------------------------------------------------

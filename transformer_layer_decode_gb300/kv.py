@@ -100,6 +100,7 @@ class KVCache:
             setattr(self.desc, name, getattr(self, name).data_ptr())
         self._lock = threading.Lock()  # of the launches of a call, which hand a workspace or the scratch on
         self._workspaces: dict = {}  # of a stream's attention calls, which run one after another
+        self._captured_workspaces: list = []  # of captures that keep no memory themselves
 
     # ---- marshalling ----------------------------------------------------------
 
@@ -139,6 +140,16 @@ class KVCache:
             return _capturing()
         with torch.cuda.device(self.device):
             return _capturing()
+
+    def _in_private_pool(self, t):
+        """Whether t's memory is from a pool that is no one else's, as in a capture of torch.cuda.graph."""
+        try:
+            segments = torch.cuda.memory_snapshot()
+        except RuntimeError:  # an allocator that does not say
+            return False
+        at = t.data_ptr()
+        return any(s["device"] == self._index and s["address"] <= at < s["address"] + s["total_size"]
+                   and tuple(s["segment_pool_id"]) != (0, 0) for s in segments)
 
     def _new(self, make, shape, dtype, stream):
         """make(shape) for a call on `stream`: its memory, and what fills it, belong to that stream."""
@@ -206,7 +217,8 @@ class KVCache:
         """softmax(scale q K^T) V of one query per entry of seqs over its sequence's visible rows: the last
         `window` ones (0: all) and the first `sinks` ones.  q and out: [n, n_q_heads, head_dim].  Rows of
         skipped entries keep what out holds (zeros where it is made here).  Without a workspace the calls of
-        the current stream share one, and a captured call gets its own; `stream` needs one to be given."""
+        the current stream share one, and a captured call gets its own, which the graph's memory pool keeps or,
+        where the capture was not begun by torch.cuda.graph, this cache; `stream` needs one to be given."""
         qp, qt, qs = self._rows("q", q)
         n, heads = q.shape[0], q.shape[1]
         sp, _ = self._ints("seqs", seqs, n)
@@ -221,6 +233,8 @@ class KVCache:
             if self._captured():  # a graph keeps its own: it may be replayed beside other calls
                 workspace = self.workspace()
                 ws = workspace.data_ptr(), workspace.numel()
+                if not self._in_private_pool(workspace):
+                    self._captured_workspaces.append(workspace)
             else:
                 ws = self._workspaces.get(_raw_stream(self._index))
                 if ws is None:
