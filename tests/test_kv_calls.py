@@ -4,6 +4,7 @@ import threading
 import time
 
 import pytest
+import torch
 
 from transformer_layer_decode_gb300 import build as tld_build
 from transformer_layer_decode_gb300 import dec, kv
@@ -67,3 +68,43 @@ def test_the_most_queries_and_heads(lib, n, heads, code):
             assert "workspace" in dec.load_library().dec_last_error(None).decode()
         else:
             assert rc == code
+
+
+@pytest.mark.parametrize("kw", [
+    {"n_layers": 2**32 + 1}, {"n_kv_heads": 2**32 + 2}, {"head_dim": 2**32 + 64}, {"page_rows": 2**32 + 16},
+    {"n_pages": 2**32 + 4}, {"n_seqs": -2**32 + 2}, {"max_pages": 2**32 + 1}])
+def test_shapes_past_32_bits_are_refused(kw):
+    """Not cut off to a shape that is allowed."""
+    shape = dict(n_layers=1, n_kv_heads=2, head_dim=64, page_rows=16, n_pages=4, n_seqs=2, max_pages=1)
+    shape.update(kw)
+    with pytest.raises(ValueError, match=next(iter(kw))):
+        kv.KVCache(**shape)
+
+
+def test_arguments_past_32_bits_are_refused(cache, monkeypatch):
+    monkeypatch.setattr(kv, "_capturing", lambda: False)
+    cache.device, cache._d, cache.lib = torch.device("cpu"), 64, dec.load_library()
+    cache.desc.n_kv_heads, cache.desc.n_layers, cache.desc.n_seqs = 2, 3, 2
+    called = []
+    monkeypatch.setattr(kv.KVCache, "_call", lambda self, fn, *args, stream=None: called.append(args))
+    x, ws, list_ = torch.zeros(2, 2, 64), torch.zeros(64), torch.zeros(2, dtype=torch.int32)
+
+    def attend(**kw):
+        cache.attention(kw.pop("layer", 1), x, out=torch.zeros(2, 2, 64), workspace=ws, **kw)
+
+    for big in (2**32, 2**32 + 1, 2**31, -2**31 - 1, -2**32):
+        for name in ("layer", "window", "sinks"):
+            with pytest.raises(ValueError, match=name):
+                attend(**{name: big})
+        with pytest.raises(ValueError, match="layer"):
+            cache.append(big, x, x)
+        with pytest.raises(ValueError, match="layer"):
+            cache.read(big, list_, k_out=x, v_out=x)
+        for name in ("window", "sinks"):
+            with pytest.raises(ValueError, match=name):
+                cache.release(**{name: big})
+    assert not called
+    attend(window=2**31 - 1, sinks=2**31 - 1)
+    attend(window=-1)                    # (the library's to refuse)
+    cache.release(window=5, sinks=-2)
+    assert len(called) == 3

@@ -38,6 +38,13 @@ class KVCacheDesc(ctypes.Structure):
                 ("refs", ctypes.c_void_p), ("status", ctypes.c_void_p), ("scratch", ctypes.c_void_p)]
 
 
+def _int32(**numbers):
+    """Refuses what ctypes would cut off to 32 bits: a window of 2^32 + 5 rows is not one of 5."""
+    for name, x in numbers.items():
+        if not -1 << 31 <= x < 1 << 31:
+            raise ValueError(f"{name} {x}: 32 bits are wanted")
+
+
 def default_page_rows(head_dim: int) -> int:
     """Rows of a page unless asked otherwise: those of one attention chunk of the decoder."""
     return 64 if head_dim == 128 else 128
@@ -72,6 +79,8 @@ class KVCache:
         elif None in (n_pages, n_seqs, max_pages):
             raise ValueError("n_pages, n_seqs and max_pages are needed to make a cache")
         page_rows = default_page_rows(head_dim) if page_rows is None else page_rows
+        _int32(n_layers=n_layers, n_kv_heads=n_kv_heads, head_dim=head_dim, page_rows=page_rows, n_pages=n_pages,
+               n_seqs=n_seqs, max_pages=max_pages)
         self.desc = KVCacheDesc(n_layers, n_kv_heads, head_dim, page_rows, n_pages, n_seqs, max_pages,
                                 FORMATS[fmt])
         self._ref = ctypes.byref(self.desc)
@@ -177,6 +186,7 @@ class KVCache:
     def append(self, layer: int, k, v, *, seqs=None, positions=None, stream=None):
         """Writes row t of k and v ([n, n_kv_heads, head_dim], keys already rotated) as row positions[t]
         of sequence seqs[t]; without positions, as the sequence's last row; without seqs, of sequence t."""
+        _int32(layer=layer)
         kp, kt, ks = self._rows("k", k, self.desc.n_kv_heads)
         vp, vt, vs = self._rows("v", v, self.desc.n_kv_heads)
         if k.shape[0] != v.shape[0] or kt != vt or ks != vs:
@@ -189,6 +199,7 @@ class KVCache:
     def read(self, layer: int, seqs, positions=None, *, k_out=None, v_out=None, dtype=torch.float32, stream=None):
         """Rows positions[t] of sequences seqs[t] as values: (k, v), each [n, n_kv_heads, head_dim].
         Rows of skipped entries keep what k_out and v_out hold (zeros where these are made here)."""
+        _int32(layer=layer)
         sp, n = self._ints("seqs", seqs)
         pp, _ = self._ints("positions", positions, n)
         shape = (n, self.desc.n_kv_heads, self.desc.head_dim)
@@ -219,6 +230,8 @@ class KVCache:
         skipped entries keep what out holds (zeros where it is made here).  Without a workspace the calls of
         the current stream share one, and a captured call gets its own, which the graph's memory pool keeps or,
         where the capture was not begun by torch.cuda.graph, this cache; `stream` needs one to be given."""
+        if not (0 <= layer < self.desc.n_layers and 0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+            _int32(layer=layer, window=window, sinks=sinks)
         qp, qt, qs = self._rows("q", q)
         n, heads = q.shape[0], q.shape[1]
         sp, _ = self._ints("seqs", seqs, n)
@@ -269,6 +282,7 @@ class KVCache:
     def release(self, seqs=None, *, window: int = 0, sinks: int = 0, stream=None):
         """Empties sequences and frees their pages; with a window, frees only the pages that a query
         with this window and these sinks no longer sees."""
+        _int32(window=window, sinks=sinks)
         sp, n = self._ints("seqs", seqs)
         self._call(self.lib.dec_kv_release, sp, self.desc.n_seqs if seqs is None else n, window, sinks,
                    stream=stream)
