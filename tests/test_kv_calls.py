@@ -108,3 +108,17 @@ def test_arguments_past_32_bits_are_refused(cache, monkeypatch):
     attend(window=-1)                    # (the library's to refuse)
     cache.release(window=5, sinks=-2)
     assert len(called) == 3
+
+
+def test_scales_past_fp32_are_refused(lib):
+    """The kernels take the scale times log2(e)."""
+    c = kv.KVCacheDesc(n_layers=1, n_kv_heads=1, head_dim=64, page_rows=16, n_pages=32, n_seqs=8, max_pages=1, format=0,
+                       pool=MEM, table=MEM, lens=MEM, refs=MEM, status=MEM, scratch=MEM)
+
+    def rc(scale, n=0):
+        return lib.dec_kv_attention(ctypes.byref(c), 0, MEM, 2 * MEM, 0, 64, 64, None, n, 1, 0, 0, scale, MEM, 1 << 40, None)
+
+    for scale in (3e38, -2.4e38, float("inf"), float("-inf"), float("nan"), 1e300):
+        assert rc(scale) == rc(scale, 1) == dec.DEC_ERR_ARG
+    for scale in (0.0, -0.0, 2.3e38, -1.0, 1e-45):
+        assert rc(scale) == dec.DEC_OK

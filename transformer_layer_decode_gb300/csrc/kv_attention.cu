@@ -1451,7 +1451,10 @@ extern "C" int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q,
   if (layer < 0 || layer >= c->n_layers) return fail_no_handle(DEC_ERR_ARG, "layer %d out of range", layer);
   if (type != DEC_IO_F32 && type != DEC_IO_BF16) return fail_no_handle(DEC_ERR_ARG, "unknown type %d", type);
   if (window < 0 || sinks < 0) return fail_no_handle(DEC_ERR_ARG, "window %d, sinks %d", window, sinks);
-  if (!std::isfinite(scale)) return fail_no_handle(DEC_ERR_ARG, "the scale is not finite");
+  // (in log2 units, as the kernels take it: past fp32 it would make scores of 0 NaN)
+  const float scale2 =
+      (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)c->head_dim)) * 1.4426950408889634);
+  if (!std::isfinite(scale2)) return fail_no_handle(DEC_ERR_ARG, "the scale %g is not finite, or too large", scale);
   if (!seqs && n > c->n_seqs) return fail_no_handle(DEC_ERR_ARG, "%d queries of %d sequences", n, c->n_seqs);
   if (n == 0) return DEC_OK;
   if (!q || !o) return fail_no_handle(DEC_ERR_ARG, "q or o is NULL");
@@ -1484,7 +1487,7 @@ extern "C" int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q,
   p.sinks = sinks;
   p.group = n_q_heads / c->n_kv_heads;
   p.head_blocks = (p.group + kHeadBlock - 1) / kHeadBlock;
-  p.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)c->head_dim)) * 1.4426950408889634);
+  p.scale = scale2;
   p.rec = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.rec);
   p.ref = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + ws.ref);
   p.cut = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + ws.cut);
