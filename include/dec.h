@@ -459,8 +459,8 @@ int dec_kv_append(const dec_kv_cache* c, int layer, const void* k, const void* v
                   dec_stream_t stream);
 
 /* The reverse: rows positions[t] of sequences seqs[t] of one layer, as values
- * of `type` (4-bit: code * scale, exact in fp32), into rows of k and v.  Rows
- * that are skipped are left as they were. */
+ * of `type` (4-bit: code * scale, exact in fp32), into rows of k and v, which
+ * must not overlap.  Rows that are skipped are left as they were. */
 int dec_kv_read(const dec_kv_cache* c, int layer, void* k, void* v, int type, int64_t row_stride,
                 const int32_t* seqs, const int32_t* positions, int n, dec_stream_t stream);
 

@@ -289,3 +289,19 @@ def test_fork_of_a_windowed_parent():
     assert list(a >= 0) == list(b >= 0) == [True, False, False, False, False, True, True, False]
     assert list(a == b) == [True, True, True, True, True, True, False, True]
     assert c.refs.cpu().numpy()[a[[0, 5]]].tolist() == [2, 2] and c.refs.cpu().numpy()[[a[6], b[6]]].tolist() == [1, 1]
+
+
+def test_reads_into_one_tensor_side_by_side():
+    """K's rows and V's in turn, or halves of wider rows: taken; the same rows for both: refused."""
+    c = filled("q4", 2, 64, 16, [37])
+    seqs, pos = ints([0] * 37), ints(range(37))
+    want = c.read(0, seqs, pos)
+    both = torch.zeros(37, 2, 2, 64, device="cuda")
+    c.read(0, seqs, pos, k_out=both[:, 0], v_out=both[:, 1])
+    assert torch.equal(both[:, 0], want[0]) and torch.equal(both[:, 1], want[1])
+    halves = torch.zeros(2, 37, 2, 64, device="cuda")
+    c.read(0, seqs, pos, k_out=halves[1], v_out=halves[0])
+    assert torch.equal(halves[1], want[0]) and torch.equal(halves[0], want[1])
+    c.sync_status()
+    with pytest.raises(dec.DecError, match="overlaps"):
+        c.read(0, seqs, pos, k_out=halves[0], v_out=halves[0])

@@ -122,3 +122,19 @@ def test_scales_past_fp32_are_refused(lib):
         assert rc(scale) == rc(scale, 1) == dec.DEC_ERR_ARG
     for scale in (0.0, -0.0, 2.3e38, -1.0, 1e-45):
         assert rc(scale) == dec.DEC_OK
+
+
+def test_reads_into_rows_that_overlap_are_refused(lib):
+    """K's rows and V's, of 512 bytes here, would be written in any order."""
+    c = kv.KVCacheDesc(n_layers=1, n_kv_heads=2, head_dim=64, page_rows=16, n_pages=32, n_seqs=8, max_pages=1, format=0,
+                       pool=MEM, table=MEM, lens=MEM, refs=MEM, status=MEM, scratch=MEM)
+
+    def rc(v, stride, n):
+        lib.dec_kv_sizes(None, None, None)   # (some other message)
+        rc = lib.dec_kv_read(ctypes.byref(c), 0, MEM, v, 0, stride, MEM, None, n, None)
+        return rc, "overlaps" in lib.dec_last_error(None).decode()
+
+    for v, stride, n in ((MEM, 128, 1), (MEM + 496, 128, 1), (MEM + 512, 128, 2), (MEM + 256, 256, 2), (MEM - 16, 256, 2),
+                         (MEM + 1024, 128, 100), (MEM + 3 * 1024 + 400, 256, 9)):
+        assert rc(v, stride, n) == (dec.DEC_ERR_ARG, True), (v - MEM, stride, n)
+        assert rc(v, stride, 0) == (dec.DEC_OK, False)

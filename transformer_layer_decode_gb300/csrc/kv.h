@@ -47,4 +47,13 @@ __host__ __device__ inline int64_t kv_scratch_ints(int64_t n_pages, int64_t n_se
 int kv_check(const dec_kv_cache* c, bool memory);
 KvView kv_view(const dec_kv_cache& c, int layer);
 
+// Whether rows of `width` bytes at a + i * sa and at b + i * sb (i < n) share a byte
+// (where sa and sb differ: whether what they span does).
+inline bool kv_rows_overlap(uintptr_t a, int64_t sa, uintptr_t b, int64_t sb, int64_t width, int n) {
+  if (a + (n - 1) * sa + width <= b || b + (n - 1) * sb + width <= a) return false;
+  if (sa != sb) return true;
+  const int64_t d = (int64_t)(a > b ? a - b : b - a) % sa;
+  return d < width || d > sa - width;
+}
+
 }  // namespace tld

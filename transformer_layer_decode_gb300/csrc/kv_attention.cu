@@ -1424,14 +1424,6 @@ int check_attention(const dec_kv_cache* c, int n, int n_q_heads) {
   return DEC_OK;
 }
 
-// Whether rows of `width` bytes at a + i * sa and at b + i * sb (i < n) share a byte.
-bool rows_overlap(uintptr_t a, int64_t sa, uintptr_t b, int64_t sb, int64_t width, int n) {
-  if (a + (n - 1) * sa + width <= b || b + (n - 1) * sb + width <= a) return false;
-  if (sa != sb) return true;
-  const int64_t d = (int64_t)(a > b ? a - b : b - a) % sa;
-  return d < width || d > sa - width;
-}
-
 }  // namespace
 
 extern "C" int dec_kv_attention_workspace(const dec_kv_cache* c, size_t* bytes) {
@@ -1464,8 +1456,8 @@ extern "C" int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q,
   if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o)) & 15) || (q_stride * size) % 16 ||
       (o_stride * size) % 16)
     return fail_no_handle(DEC_ERR_ARG, "q, o and their rows must be 16-byte aligned");
-  if (rows_overlap(reinterpret_cast<uintptr_t>(q), q_stride * size, reinterpret_cast<uintptr_t>(o), o_stride * size,
-                   width * size, n))
+  if (kv_rows_overlap(reinterpret_cast<uintptr_t>(q), q_stride * size, reinterpret_cast<uintptr_t>(o), o_stride * size,
+                      width * size, n))
     return fail_no_handle(DEC_ERR_ARG, "o overlaps q");
   int dev = 0, sms = 0;
   if (int rc = device_sms(&dev, &sms)) return rc;

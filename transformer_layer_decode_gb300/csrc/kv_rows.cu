@@ -362,6 +362,9 @@ int rows_call(const dec_kv_cache* c, int layer, void* k, void* v, int type, int6
     return fail_no_handle(DEC_ERR_ARG, "k, v and their rows must be 16-byte aligned");
   if ((int64_t)n * c->n_kv_heads > (int64_t)1 << 30)
     return fail_no_handle(DEC_ERR_SHAPE, "%d rows of %d heads (at most 2^30 in all)", n, c->n_kv_heads);
+  if (READ && kv_rows_overlap(reinterpret_cast<uintptr_t>(k), row_stride * size, reinterpret_cast<uintptr_t>(v),
+                              row_stride * size, width * size, n))
+    return fail_no_handle(DEC_ERR_ARG, "k overlaps v");
   const KvView view = kv_view(*c, layer);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
