@@ -418,8 +418,10 @@ enum dec_kv_bits {
                            fork: nothing done) */
   DEC_KV_NO_PAGES = 2,  /* extend or fork: not enough free pages, or a sequence longer than its
                            table: nothing done */
-  DEC_KV_BAD_LIST = 4   /* extend: a sequence twice; fork: a child twice, not empty, or also a
+  DEC_KV_BAD_LIST = 4,  /* extend: a sequence twice; fork: a child twice, not empty, or also a
                            parent: nothing done */
+  DEC_KV_BAD_BOUNDS = 8 /* debug build of the library (TLD_DEBUG_CHECKS): an index check in a kernel
+                           failed and the access was skipped; the message has its source line */
 };
 
 typedef struct dec_kv_cache {

@@ -34,7 +34,9 @@ __host__ __device__ inline int kv_row_bytes(int head_dim, bool q4) {
 // of pages (compact) or the free pages found (extend, fork), the page copies
 // (source, destination), and where each list entry's pages start.
 constexpr int kKvScratchHead = 32;
-constexpr int kKvScratchStatus = kKvScratchHead - 1;  // of the head's words: the status as dec_kv_status found it
+// Of the head's words: the source line of a check that failed (debug build), and
+// beside it the status as dec_kv_status found it.
+constexpr int kKvScratchLine = kKvScratchHead - 2, kKvScratchStatus = kKvScratchHead - 1;
 __host__ __device__ inline int64_t kv_scratch_moves(int64_t n_pages) { return kKvScratchHead + n_pages; }
 __host__ __device__ inline int64_t kv_scratch_offsets(int64_t n_pages, int64_t n_seqs) {
   return kv_scratch_moves(n_pages) + n_pages + 2 * n_seqs;
@@ -42,6 +44,20 @@ __host__ __device__ inline int64_t kv_scratch_offsets(int64_t n_pages, int64_t n
 __host__ __device__ inline int64_t kv_scratch_ints(int64_t n_pages, int64_t n_seqs) {
   return kv_scratch_offsets(n_pages, n_seqs) + n_seqs + 1;
 }
+
+// Index checks of the debug build (TLD_DEBUG_CHECKS): one that fails sets
+// DEC_KV_BAD_BOUNDS, notes its source line and is false, and the caller skips the
+// access.  Release builds compile every check to true.
+#ifdef TLD_DEBUG_CHECKS
+__device__ __noinline__ inline bool kv_bounds_failed(const KvView& c, int line) {
+  atomicExch(c.scratch + kKvScratchLine, line);
+  atomicOr(c.status, DEC_KV_BAD_BOUNDS);
+  return false;
+}
+#define KV_IN_BOUNDS(c, cond) ((cond) ? true : ::tld::kv_bounds_failed((c), __LINE__))
+#else
+#define KV_IN_BOUNDS(c, cond) true
+#endif
 
 // Checks a cache (its pointers too, with `memory`); DEC_OK or the error, recorded.
 int kv_check(const dec_kv_cache* c, bool memory);

@@ -896,6 +896,7 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
   bool doubt = false;  // a tile had no page
   auto tile_no = [&](int i) { return t0 + warp * L::kStep + i / L::kStep * kRound + i % L::kStep; };
   auto page_of = [&](int row) {
+    if (!KV_IN_BOUNDS(c, row >= 0 && row < c.max_pages * c.page_rows)) return -1;
     const int page = table[row / c.page_rows];
     return page >= 0 && page < c.n_pages ? page : -1;
   };
@@ -905,7 +906,7 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
     nxt_scales = -1;
     if (i < nt) {
       const int at = tile_row(v, tile_no(i)), page = page_of(at), row = at % c.page_rows;
-      if (page >= 0) {
+      if (page >= 0 && KV_IN_BOUNDS(c, row + kTileRows <= c.page_rows && head < c.nkv)) {
         nxt_src = reinterpret_cast<unsigned long long>(c.pool + page * c.page_bytes + head * c.head_bytes +
                                                        row * L::kRowBytes);
         nxt_scales = (c.page_rows - row) * L::kRowBytes + row * 2 * L::NB;
@@ -922,7 +923,7 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
       fetch(j * L::kStep + 32);
       doubt = __any_sync(0xffffffffu, doubt);
     }
-    if (j * L::kStep < nt) {
+    if (j * L::kStep < nt && KV_IN_BOUNDS(c, dst >= smem_u32(smem) && dst + L::kSlot <= smem_u32(smem) + L::kRing)) {
 #pragma unroll
       for (int k = 0; k < L::kStep; ++k) {
         const int i = (j * L::kStep + k) & 31;
@@ -940,10 +941,10 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
   const int plain0 = full0 > n0 ? (full0 - n0 + kRound - 1) / kRound : 0;
   const int plain_n =
       min(nt / L::kStep, full1 - L::kStep >= n0 ? (full1 - L::kStep - n0) / kRound + 1 : 0) - plain0;
+  const bool asks = g < n_heads && KV_IN_BOUNDS(c, r >= 0 && r < p.n && (int64_t)head * p.group + h0 + g < p.nq);
   float x[L::NB][8];  // q, read while the page numbers are, and made operands while the first tiles are under way
   load_query<L::NB>(
-      static_cast<const T*>(p.q) + r * p.q_stride + ((int64_t)head * p.group + h0 + min(g, n_heads - 1)) * D, g < n_heads,
-      t, x);
+      static_cast<const T*>(p.q) + r * p.q_stride + ((int64_t)head * p.group + h0 + min(g, n_heads - 1)) * D, asks, t, x);
   fetch(0);
 #pragma unroll 1
   for (int j = 0; j < ST; ++j) issue(j, ring + j * L::kSlot);
@@ -1021,6 +1022,7 @@ template <int D, class T>
 __device__ __forceinline__ void write_unit(const KvAttnParams& p, int r, int u, UnitSums<D>& o) {
   const int head = u / p.head_blocks, h = (u % p.head_blocks) * kHeadBlock + threadIdx.x / 16;
   if (h >= p.group) return;
+  if (!KV_IN_BOUNDS(p.c, r >= 0 && r < p.n && head < p.c.nkv)) return;
   const float k = over(o.l);
 #pragma unroll
   for (int i = 0; i < o.N; ++i) o.x[i] *= k;
@@ -1073,7 +1075,8 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
   Rows v{-1, 0, 0, 0, 0, 0, 0};
   auto hidden = [&](int r, const Rows& rows) {  // a query that sees no row, or is skipped
     if (p.cut_by_unit)
-      for (int u = tid; u < units; u += kThreadsA) p.cut[r * units + u] = make_int4(0, 0, 0, 0);
+      for (int u = tid; u < units; u += kThreadsA)
+        if (KV_IN_BOUNDS(c, r * units + u < p.ctas)) p.cut[r * units + u] = make_int4(0, 0, 0, 0);
     if (rows.seq < 0) return;
     T* out = static_cast<T*>(p.o) + r * p.o_stride;
     for (int64_t e = tid; e < (int64_t)p.nq * D; e += kThreadsA) out[e] = 0;
@@ -1127,7 +1130,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
     } else {
       for (int k = warp; k < chunks; k += kWarps) {
         const int64_t sum = count(k);
-        if (lane == 0) chunk_sum[k] = sum;
+        if (lane == 0 && KV_IN_BOUNDS(c, k < kMaxChunks)) chunk_sum[k] = sum;
       }
       __syncthreads();
       for (int k = 0; k < chunks; ++k) add(chunk_sum[k]);
@@ -1229,8 +1232,10 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
       write_unit<D, T>(p, share.r, share.u, o);
     } else {  // a part: slot 1 where the unit begins here, slot 0 where it began before
       const int64_t slot = (2 * (int64_t)blockIdx.x + begins) * kHeadBlock + tid / 16;
-      store_out(p.rec + slot * D + (tid % 16) * o.N, o.x);
-      if (tid % 16 == 0) p.ref[slot] = make_float2(o.m, o.l);
+      if (KV_IN_BOUNDS(c, slot >= 0 && slot < 2 * (int64_t)p.ctas * kHeadBlock)) {
+        store_out(p.rec + slot * D + (tid % 16) * o.N, o.x);
+        if (tid % 16 == 0) p.ref[slot] = make_float2(o.m, o.l);
+      }
     }
     if (begins && tid == 0) {
       int more = ends ? 0 : share.more;  // borders within the unit
@@ -1239,7 +1244,10 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
         auto owner = [&](int64_t x) { return ((x + 1) * share.parts - 1) / share.total; };
         more = (int)(owner(first + v.tiles + unit - kLeast) - owner(first + unit + kLeast - 1));
       }
-      if (p.cut_by_unit) p.cut[share.r * units + share.u] = make_int4(share.r, share.u, blockIdx.x, more);
+      const bool there = KV_IN_BOUNDS(c, share.r >= 0 && share.r < p.n && share.u < units &&
+                                             (!p.cut_by_unit || share.r * units + share.u < p.ctas));
+      if (!there) more = 0;
+      else if (p.cut_by_unit) p.cut[share.r * units + share.u] = make_int4(share.r, share.u, blockIdx.x, more);
       else if (more) p.cut[blockIdx.x] = make_int4(share.r, share.u, blockIdx.x, more);
       share.cut |= more;
     }
@@ -1276,6 +1284,7 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
   const int h = WARPS == 1 ? warp : blockIdx.y, first = WARPS == 1 ? 0 : warp;
   const int head = cut.y / p.head_blocks, h0 = (cut.y % p.head_blocks) * kHeadBlock;
   if (h0 + h >= p.group) return;
+  if (!KV_IN_BOUNDS(p.c, cut.x >= 0 && cut.y >= 0 && cut.z >= 0 && head < p.c.nkv)) return;
   auto slot = [&](int i) { return (2 * (int64_t)(cut.z + i) + (i == 0)) * kHeadBlock + h; };
   float m = -3e38f;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, p.ref[slot(i)].x);

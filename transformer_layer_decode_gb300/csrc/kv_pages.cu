@@ -89,7 +89,7 @@ __device__ bool find_free(const KvView& c, int need) {
   int32_t* list = c.scratch + kKvScratchHead;
   return rank_pages(c.n_pages, need, [&](int p) { return c.refs[p] <= 0 ? 1 : 0; },
                     [&](int p, int kind, int rank) {
-                      if (kind && rank < need) list[rank] = p;
+                      if (kind && rank < need && KV_IN_BOUNDS(c, rank >= 0 && rank < c.n_pages)) list[rank] = p;
                     }).x >= need;
 }
 
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_alloc(KvView c, const in
       const int at = offsets[i];
       if (offsets[i + 1] > at) {
         const int s = a[i];
+        if (!KV_IN_BOUNDS(c, at >= 0 && at < c.n_seqs && at < total && c.lens[s] / c.page_rows < c.max_pages)) continue;
         moves[2 * at] = c.table[(int64_t)s * c.max_pages + c.lens[s] / c.page_rows];
         moves[2 * at + 1] = list[at];
       }
@@ -196,7 +197,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_alloc(KvView c, const in
         else hi = mid;
       }
       const int s = a ? a[lo] : lo;
-      c.table[(int64_t)s * c.max_pages + div_up(c.lens[s], c.page_rows) + k - offsets[lo]] = list[k];
+      const int place = div_up(c.lens[s], c.page_rows) + k - offsets[lo];
+      if (!KV_IN_BOUNDS(c, k < c.n_pages && s >= 0 && s < c.n_seqs && place >= 0 && place < c.max_pages &&
+                               list[k] >= 0 && list[k] < c.n_pages))
+        continue;
+      c.table[(int64_t)s * c.max_pages + place] = list[k];
       c.refs[list[k]] = 1;
     }
     __syncthreads();
@@ -227,11 +232,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_compact(KvView c) {
         return p < live ? (used ? 0 : 1) : (used ? 2 : 0);
       },
       [&](int p, int kind, int rank) {
-        if (kind) moves[2 * rank + (kind == 1)] = p;
+        if (kind && KV_IN_BOUNDS(c, rank >= 0 && 2 * rank + 1 < c.n_pages + 2 * c.n_seqs))
+          moves[2 * rank + (kind == 1)] = p;
         name[p] = kind == 0 && p < live ? p : -1;  // (those that move get theirs below)
       }).y;
   for (int k = tid; k < movers; k += kPlanThreads) {
     const int from = moves[2 * k], to = moves[2 * k + 1];
+    if (!KV_IN_BOUNDS(c, from >= live && from < c.n_pages && to >= 0 && to < live)) continue;
     c.refs[to] = c.refs[from];
     c.refs[from] = 0;
     name[from] = to;
@@ -264,6 +271,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_apply(KvView c, const int32_t
       int page = c.table[(int64_t)p * c.max_pages + at];
       if (len % c.page_rows && at == len / c.page_rows) {
         page = list[offsets[i]];
+        if (!KV_IN_BOUNDS(c, page >= 0 && page < c.n_pages)) continue;
         c.refs[page] = 1;
       } else if (page >= 0 && page < c.n_pages) {
         atomicAdd(c.refs + page, 1);
@@ -291,6 +299,9 @@ __global__ void __launch_bounds__(kCopyThreads) kv_apply(KvView c, const int32_t
     const uint32_t piece = (uint32_t)(e % pieces);
     const int64_t rest = e / pieces;
     const int layer = (int)(rest % n_layers), m = (int)(rest / n_layers);
+    if (!KV_IN_BOUNDS(c, moves[2 * m] >= 0 && moves[2 * m] < c.n_pages && moves[2 * m + 1] >= 0 &&
+                             moves[2 * m + 1] < c.n_pages && layer < n_layers))
+      continue;
     uint8_t* pages = c.pool + (int64_t)layer * c.n_pages * c.page_bytes;
     const int64_t at = (int64_t)piece * kCopyPiece + 16 * threadIdx.x;
     const uint8_t* from = pages + moves[2 * m] * c.page_bytes + at;

@@ -256,6 +256,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
     uint8_t* base = token_page[token];
     if (!base) continue;
     const int row = token_row[token], page_rows = c.page_rows, nkv = c.nkv;
+    if (!KV_IN_BOUNDS(c, token < kMaxTokens && t0 + token < n && part >= 0 && row >= 0 && row < page_rows &&
+                             base >= c.pool && base + c.page_bytes <= c.pool + c.n_pages * c.page_bytes &&
+                             2 * nkv * c.head_bytes == c.page_bytes))
+      continue;
     const uint32_t head_bytes = (uint32_t)c.head_bytes;
     const int first = part * (ROUNDS * RPR) + lane / LANES;
     // (lanes past the last row take it once more: the same bytes to the same place)
@@ -409,16 +413,21 @@ extern "C" int dec_kv_status(const dec_kv_cache* c, int* bits, dec_stream_t stre
   if (bits) *bits = 0;
   if (int rc = kv_check(c, true)) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int flag = 0;
+  int word[2] = {0, 0};
+  static_assert(kKvScratchStatus == kKvScratchLine + 1, "copied together");
   int32_t* taken = c->scratch + kKvScratchStatus;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = cfg.blockDim = dim3(1);
   cfg.stream = s;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_take_status, c->status, taken);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&flag, taken, sizeof flag, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(word, taken - 1, sizeof word, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return fail_no_handle(DEC_ERR_CUDA, "reading the cache's status: %s", cudaGetErrorString(e));
+  const int flag = word[1];
   if (bits) *bits = flag;
+  if (flag & DEC_KV_BAD_BOUNDS)
+    return fail_no_handle(DEC_ERR_DEVICE, "an index check of the cache's kernels failed at line %d (bits 0x%x)", word[0],
+                          flag);
   if (flag)
     return fail_no_handle(DEC_ERR_DEVICE, "the cache's kernels refused something (bits 0x%x:%s%s%s)", flag,
                           flag & DEC_KV_BAD_INDEX ? " index out of range" : "",

@@ -17,7 +17,7 @@ from . import dec
 
 DEC_KV_BF16, DEC_KV_Q4B32 = 0, 1
 DEC_IO_F32, DEC_IO_BF16 = 0, 1
-DEC_KV_BAD_INDEX, DEC_KV_NO_PAGES, DEC_KV_BAD_LIST = 1, 2, 4
+DEC_KV_BAD_INDEX, DEC_KV_NO_PAGES, DEC_KV_BAD_LIST, DEC_KV_BAD_BOUNDS = 1, 2, 4, 8
 
 FORMATS = {"bf16": DEC_KV_BF16, "q4": DEC_KV_Q4B32}
 _TYPES = {torch.float32: DEC_IO_F32, torch.bfloat16: DEC_IO_BF16}
