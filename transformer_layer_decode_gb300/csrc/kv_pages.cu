@@ -151,16 +151,17 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_alloc(KvView c, const in
   if (FORK) {
     // A parent that is also a child would be copied before or after it changes, and
     // pages that are none would be copied into the child's table: a warp per entry, or
-    // several (64 forks of 1024 pages each take 3 us more for it).
+    // 2^more of them where there are few entries.
     constexpr int kWarps = kPlanThreads / 32;
-    const int parts = max(kWarps / n, 1);
-    for (int unit = tid >> 5; unit < n * parts; unit += kWarps) {
-      const int i = unit / parts, s = a[i], x = b[i];
+    const int more = max(__clz(n - 1) - __clz(kWarps - 1), 0);
+    for (int unit = tid >> 5; unit >> more < n; unit += kWarps) {
+      const int i = unit >> more, s = a[i], x = b[i];
       if (s < 0 || s >= c.n_seqs || x < 0) continue;
       const int32_t* row = c.table + (int64_t)s * c.max_pages;
       int most = -1;
-#pragma unroll 8
-      for (int at = unit % parts * 32 + (tid & 31); at < c.max_pages; at += 32 * parts) most = max(most, row[at]);
+#pragma unroll 16
+      for (int at = (unit & ((1 << more) - 1)) * 32 + (tid & 31); at < c.max_pages; at += 32 << more)
+        most = max(most, row[at]);
       const int bad = (seen[s >> 5] >> (s & 31) & 1 ? DEC_KV_BAD_LIST : 0) | (most >= c.n_pages ? DEC_KV_BAD_INDEX : 0);
       if (bad) atomicOr(&bad_bits, bad);
     }
