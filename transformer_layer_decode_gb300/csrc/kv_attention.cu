@@ -712,7 +712,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       for (int i = 4; i < 4 * kTiles; i += 2) mx0 = fmaxf(mx0, s[i]), mx1 = fmaxf(mx1, s[i + 1]);
       if (__any_sync(0xffffffffu,
                      mx0 > this->ref[0] + (kLift + kSlack) || mx1 > this->ref[1] + (kLift + kSlack) || over)) {
-        make_room(most0, most1);
+        if (__any_sync(0xffffffffu, over)) make_room(most0, most1);
         this->raise(mx0, mx1, kLift);
       }
 #pragma unroll
@@ -725,7 +725,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 #pragma unroll
       for (int i = 1; i < 4 * kTiles; ++i) mx = fmaxf(mx, s[i]);
       if (__any_sync(0xffffffffu, mx > this->ref + (kLift + kSlack) || over)) {
-        make_room(most0, most1);
+        if (__any_sync(0xffffffffu, over)) make_room(most0, most1);
         this->raise(mx, kLift);
       }
       float sum = 0.f;
