@@ -38,10 +38,14 @@ class KVCacheDesc(ctypes.Structure):
                 ("refs", ctypes.c_void_p), ("status", ctypes.c_void_p), ("scratch", ctypes.c_void_p)]
 
 
+_LARGE = 1 << 31
+
+
 def _int32(**numbers):
-    """Refuses what ctypes would cut off to 32 bits: a window of 2^32 + 5 rows is not one of 5."""
+    """Refuses what ctypes would cut off to 32 bits: a window of 2^32 + 5 rows is not one of 5.  (Calls of a
+    decode step look themselves first, which takes less than this call.)"""
     for name, x in numbers.items():
-        if not -1 << 31 <= x < 1 << 31:
+        if not -_LARGE <= x < _LARGE:
             raise ValueError(f"{name} {x}: 32 bits are wanted")
 
 
@@ -186,7 +190,8 @@ class KVCache:
     def append(self, layer: int, k, v, *, seqs=None, positions=None, stream=None):
         """Writes row t of k and v ([n, n_kv_heads, head_dim], keys already rotated) as row positions[t]
         of sequence seqs[t]; without positions, as the sequence's last row; without seqs, of sequence t."""
-        _int32(layer=layer)
+        if not 0 <= layer < _LARGE:
+            _int32(layer=layer)
         kp, kt, ks = self._rows("k", k, self.desc.n_kv_heads)
         vp, vt, vs = self._rows("v", v, self.desc.n_kv_heads)
         if k.shape[0] != v.shape[0] or kt != vt or ks != vs:
@@ -199,7 +204,8 @@ class KVCache:
     def read(self, layer: int, seqs, positions=None, *, k_out=None, v_out=None, dtype=torch.float32, stream=None):
         """Rows positions[t] of sequences seqs[t] as values: (k, v), each [n, n_kv_heads, head_dim].
         Rows of skipped entries keep what k_out and v_out hold (zeros where these are made here)."""
-        _int32(layer=layer)
+        if not 0 <= layer < _LARGE:
+            _int32(layer=layer)
         sp, n = self._ints("seqs", seqs)
         pp, _ = self._ints("positions", positions, n)
         shape = (n, self.desc.n_kv_heads, self.desc.head_dim)
@@ -230,7 +236,7 @@ class KVCache:
         skipped entries keep what out holds (zeros where it is made here).  Without a workspace the calls of
         the current stream share one, and a captured call gets its own, which the graph's memory pool keeps or,
         where the capture was not begun by torch.cuda.graph, this cache; `stream` needs one to be given."""
-        if not (0 <= layer < self.desc.n_layers and 0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+        if not (0 <= layer < _LARGE and 0 <= window < _LARGE and 0 <= sinks < _LARGE):
             _int32(layer=layer, window=window, sinks=sinks)
         qp, qt, qs = self._rows("q", q)
         n, heads = q.shape[0], q.shape[1]
