@@ -475,18 +475,19 @@ int dec_kv_read(const dec_kv_cache* c, int layer, void* k, void* v, int type, in
  * n_q_heads), n_q_heads any multiple of n_kv_heads; scale 0 means
  * 1 / sqrt(head_dim).  No visible row: o = 0.  Rows not visible are not looked
  * at (whatever they hold); those visible must hold finite values, or the
- * outputs are NaN.  Scores and sums are fp32.  Weights keep 24 bits (16 for
- * bf16 results).  Over 4-bit pages a weight times its V scale keeps 22 bits (11
- * for bf16 results) down to a step of its block of 32 dimensions: with M = 7
- * times the block's largest visible V scale (at least 2^-12), each visible row
- * is off by at most 2^-43 M (2^-29 M, and all together by 2^-23 M more, for
- * bf16 results), whatever the other blocks hold.  For bf16 results over 4-bit
- * pages the tensor cores' sums are cut off, not rounded: a score is off by up
- * to 2^-20 of scale * sum |q| * 8 * (its K scale).  The same call gives the
- * same bits.  A visible row
- * without a valid page is left out and sets DEC_KV_BAD_INDEX.  q, o and their
- * strides are multiples of 16 bytes; o must not overlap q.  n and n_q_heads are
- * at most 65536 each, and their product 2^24.
+ * outputs are NaN, and the sums of their values times weights of up to 2^5 must
+ * stay below fp32's largest number.  A visible row without a valid page is left
+ * out and sets DEC_KV_BAD_INDEX.  The same call gives the same bits.
+ * Scores and sums are fp32.  Weights keep 24 bits (16 for bf16 results).  Over
+ * 4-bit pages a weight times its V scale keeps 22 bits (11 for bf16 results),
+ * down to a step of its block of 32 dimensions: with M = 7 times the block's
+ * largest visible V scale (at least 2^-12), each visible row is off by at most
+ * 2^-43 M (2^-29 M, and all together by 2^-23 M more, for bf16 results), whatever
+ * the other blocks hold.  For bf16 results the sums stay in the tensor cores,
+ * which cut them off, not round: about 2^-23 of a sum for each 16 rows, and over
+ * 4-bit pages up to 2^-20 of scale * sum |q| * 8 * (its K scale) of a score.
+ * q, o and their strides are multiples of 16 bytes; o must not overlap q.  n and
+ * n_q_heads are at most 65536 each, and their product 2^24.
  * workspace: device memory of dec_kv_attention_workspace bytes, 16-byte
  * aligned, for this call alone (its content does not matter before or after,
  * and calls that may overlap need one each). */

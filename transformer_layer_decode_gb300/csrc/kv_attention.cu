@@ -24,10 +24,16 @@ namespace {
 // leaves most SMs idle.)
 //
 // What bounds it: bf16 pages, HBM: 46 windowed queries of 32 heads of 128, 1.46
-// GB, take 221 us, 0.99 of the copy rate.  4-bit pages, instructions, see
-// WarpQ4: 24 queries of up to 24 001 rows, 1.54 GB, 316 us, 0.73.  A short call,
-// a chain of loads: one query of 127 rows 4.7 us, of 8196 rows cut into 344
-// parts 12.9 us, of which joining them takes 3.
+// GB, take 222 us, 0.98 of the copy rate (7 queries of up to 24 001 rows, 1.15 GB:
+// 175 us, 0.98; fp32 results 186, 0.92; head_dim 64 0.89).  4-bit pages, the
+// latency of dependent steps, see WarpQ4: 24 queries of up to 24 001 rows, 1.54 GB,
+// 315 us, 0.73; fp32 results 506, 0.45; head_dim 64 0.58 and 0.42.  A smaller batch,
+// besides, the search for shares, a chain of loads and a merge per unit, and the
+// joining launch, 10 to 20 us: 8 queries of up to 4096 rows 65 us for 366 MB of bf16
+// pages, 35 us for 103 MB of 4-bit ones.  A short call, a chain of loads: one query of
+// 127 rows 4.7 us where no sequence can be long, 6.9 in a table with room for 4096
+// rows (counted, and a joining launch that finds nothing); of 8196 rows cut into 344
+// parts 12.8 us, of which joining them takes 3.
 constexpr int kTileRows = 16;
 constexpr int kWarps = 4;
 constexpr int kThreadsA = kWarps * 32;
@@ -214,7 +220,8 @@ struct WarpSums {
   // values with a mean an accumulator there would fall short by up to 2^-24 a
   // product (1.2e-5 of the result for 24 sequences of 24000 rows).  For fp32 results
   // a tile's products are summed apart, and added here, rounded to the nearest: 8 % of
-  // the time over 4-bit pages (374 -> 405 us), 2 % of a short call, none of HBM's.
+  // the time over 4-bit pages (374 and 405 us where nothing else differed), 2 % of a
+  // short call.
   __device__ __forceinline__ void add_tile(float (&to)[4], const float (&o)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) to[i] += o[i];
@@ -432,8 +439,8 @@ struct WarpBf16 : WarpHead<D> {
   }
 };
 
-// 4-bit pages.  What bounds it is the number of instructions, not HBM: a row of
-// 128 dimensions is 144 bytes for K and V, 1/3.6 of the bf16 row with the same
+// 4-bit pages.  What bounds it is the work on a row, not HBM: a row of 128
+// dimensions is 144 bytes for K and V, 1/3.6 of the bf16 row with the same
 // number of values.  So the codes enter the products with as little unpacking
 // as can be exact.
 //  - K, bf16 results: a nibble n where it lies in a 16-bit word is the fp16 number
@@ -443,7 +450,7 @@ struct WarpBf16 : WarpHead<D> {
 //    such small numbers by fp16's smallest exponent and cut off what is then below
 //    the sum's last bit: scores are off by 4e-7 of themselves.
 //  - V, and K for fp32 results: 1024 + n or 1024 + 16 n by an OR, and n - 8 by one
-//    addition or FMA.
+//    addition or FMA (K's as subnormals took 7 % less time: 405 and 431 us).
 //  - K's block scales multiply the fp32 sums over a block, V's the weights.
 // q is scaled by a power of two and taken in two fp16 pieces (22 bits; bf16 q
 // needs one), and so is weight * scale for fp32 results; for bf16 results it
@@ -451,8 +458,13 @@ struct WarpBf16 : WarpHead<D> {
 // each, the scores are computed the other way round, S^T = K q^T, 16 rows at a
 // time, which takes half the products and block scales, and the weights, packed
 // in pairs of heads, are turned by movmatrix.  Per tile of 16 rows of 128
-// dimensions this takes 345 instructions, 171 of them on the integer pipe (two
-// cycles each); the tile's bytes take 101 cycles of the SM's share of HBM.
+// dimensions this takes 345 instructions, 170 of them on the integer pipe (two
+// cycles each), and 155 cycles of an SM, whose share of HBM would take 101 for the
+// tile's bytes.  No pipe is full in them: issue is active in 56 %, the integer pipe
+// in 55.  Three warps a scheduler (168 registers) each go through scores, maximum,
+// exponentials and V's products one after another, and wait for each.  fp32 results
+// take 614 instructions and 245 cycles, with issue active in 63 %: two sets of
+// products, K's codes made normal numbers, the second pieces and their 2^kLow (8 %).
 // Two tiles a step: one takes 12 % longer (its loop and its checks), four win
 // 5 % on long sequences and lose 40 % on batches of short ones.
 template <int D, class T>

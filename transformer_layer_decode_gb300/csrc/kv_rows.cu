@@ -140,7 +140,7 @@ struct Eight<uint16_t> {
 };
 // wide: p is a multiple of 32 bytes, which one store then writes whole; two
 // stores of half a sector each take longer (8185 rows of 32 heads of 128 read
-// from 4-bit pages: 81 us, against 53).
+// from 4-bit pages: 81 us, against 51).
 __device__ __forceinline__ void store8(float* p, const float (&x)[8], bool wide) {
   if (wide) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
@@ -214,9 +214,11 @@ constexpr int kMaxTokens = 32;  // of a CTA
 // 2 j + 1, two whole 16-bit words of the row's codes.
 //
 // What bounds it: 8185 rows of 32 heads of 128 in bf16, 172 MB with their 4-bit
-// rows, are written in 37 us (instructions: amax, scale, quotients, digits) and
-// read in 33 (instructions, and a CTA's look-up), where the bytes take 26; in fp32, 306
-// MB, in 51 and 51 (46); from and to bf16 pages, 268 MB, in 43 (40).  Four rounds:
+// rows, are written in 37 us and read in 33, where the bytes take 26: latency (a
+// CTA's look-up and the barrier behind it, then its rows' loads, then amax, scale,
+// quotients and digits; issue is active in 67 and 59 %, the integer pipe in 53 and
+// 57).  In fp32, 306 MB, 51 and 51 us (46); from and to bf16 pages, 268 MB, 43 (40),
+// fp32 and bf16 pages, 402 MB, 61 and 62 (60).  Four rounds:
 // two are 10 % slower, eight 15 % in fp32.
 template <int D, bool Q4, class T, bool READ, int ROUNDS>
 __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
