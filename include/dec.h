@@ -397,7 +397,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  * and each attention has a workspace of its own.
  * Attention, fork and compact are two launches each, of which the second reads
  * what the first left in the workspace or the scratch: host threads that queue
- * calls on one stream must not do so at the same time where these share either.
+ * calls on one stream must not do so at the same time where these share either,
+ * nor may two threads read the status at the same time.
  *
  * Lists of sequences are device int32; a negative entry is padding and is
  * skipped, and what belongs to it is neither read nor written.  A list given

@@ -18,7 +18,7 @@ def cache(monkeypatch):
     monkeypatch.setattr(kv, "_current_device", lambda: 0)
     monkeypatch.setattr(kv, "_raw_stream", lambda index: 7)
     c = object.__new__(kv.KVCache)
-    c._index, c._lock, c.desc = 0, threading.Lock(), kv.KVCacheDesc()
+    c._index, c._lock, c._status_lock, c.desc = 0, threading.Lock(), threading.Lock(), kv.KVCacheDesc()
     c._ref = ctypes.byref(c.desc)
     return c
 
@@ -44,6 +44,34 @@ def test_calls_of_two_threads_do_not_interleave(cache):
     for t in threads:
         t.join()
     assert len(seen) == 30 and all(len(s) == 1 for s in seen)
+
+
+def test_a_reading_of_the_status_holds_no_other_call_up(cache):
+    """It waits for its stream: what other threads queue meanwhile goes ahead, but for other readings."""
+    go, order = threading.Event(), []
+
+    class Lib:
+        @staticmethod
+        def dec_kv_status(ref, bits, stream):
+            order.append("waits")
+            assert go.wait(20)
+            order.append("has waited")
+            return 0
+
+    cache.lib = Lib
+    readers = [threading.Thread(target=cache.sync_status) for _ in range(2)]
+    for t in readers:
+        t.start()
+    try:
+        other = threading.Thread(target=cache._call, args=(lambda ref, stream: 0,))
+        other.start()
+        other.join(10)
+        assert not other.is_alive() and all(t.is_alive() for t in readers)
+    finally:
+        go.set()
+        for t in readers:
+            t.join()
+    assert order == ["waits", "has waited"] * 2
 
 
 @pytest.fixture(scope="module")

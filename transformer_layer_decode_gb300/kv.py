@@ -112,6 +112,7 @@ class KVCache:
         for name in ("pool", "table", "lens", "refs", "status", "scratch"):
             setattr(self.desc, name, getattr(self, name).data_ptr())
         self._lock = threading.Lock()  # of the launches of a call, which hand a workspace or the scratch on
+        self._status_lock = threading.Lock()  # of a reading of the status, which waits for its stream
         self._workspaces: dict = {}  # of a stream's attention calls, which run one after another
         self._captured_workspaces: list = []  # of captures that keep no memory themselves
 
@@ -173,14 +174,14 @@ class KVCache:
         with torch.cuda.stream(stream):
             return make(shape, dtype=dtype, device=self.device)
 
-    def _call(self, fn, *args, stream=None):
+    def _call(self, fn, *args, stream=None, lock=None):
         handle = _raw_stream(self._index) if stream is None else \
             stream if isinstance(stream, int) else stream.cuda_stream
         if _current_device() == self._index:
-            with self._lock:
+            with lock or self._lock:
                 rc = fn(self._ref, *args, handle)
         else:
-            with torch.cuda.device(self.device), self._lock:
+            with torch.cuda.device(self.device), lock or self._lock:
                 rc = fn(self._ref, *args, handle)
         if rc:
             self._check(rc)
@@ -300,4 +301,4 @@ class KVCache:
     def sync_status(self, stream=None):
         """Waits for the stream and raises DecError if a kernel refused something since the last call."""
         bits = ctypes.c_int()
-        self._call(self.lib.dec_kv_status, ctypes.byref(bits), stream=stream)
+        self._call(self.lib.dec_kv_status, ctypes.byref(bits), stream=stream, lock=self._status_lock)
