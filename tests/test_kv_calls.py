@@ -74,6 +74,38 @@ def test_a_reading_of_the_status_holds_no_other_call_up(cache):
     assert order == ["waits", "has waited"] * 2
 
 
+@pytest.mark.parametrize("handle,shared", [(7, True), (2, False)])
+def test_streams_that_are_each_thread_s_own_share_no_workspace(cache, monkeypatch, handle, shared):
+    """Calls of one stream run one after another and share a workspace; the handle of the per-thread default
+    stream names as many streams as there are threads."""
+    monkeypatch.setattr(kv, "_raw_stream", lambda index: handle)
+    monkeypatch.setattr(kv, "_capturing", lambda: False)
+    cache.device, cache._d, cache._workspaces = torch.device("cpu"), 64, {}
+    cache.lib = type("Lib", (), {"dec_kv_attention": None})
+    monkeypatch.setattr(kv.KVCache, "workspace", lambda self: torch.empty(16, dtype=torch.uint8))
+    used = {}
+    monkeypatch.setattr(kv.KVCache, "_call", lambda self, fn, *args, stream=None: used.setdefault(
+        threading.get_ident(), []).append(args[-2]))
+    both = threading.Barrier(2)
+
+    def work(turn):
+        if turn:
+            both.wait(10)
+        for _ in range(2):
+            cache.attention(0, torch.zeros(1, 2, 64))
+        if not turn:
+            both.wait(10)
+        both.wait(10)               # (both threads live as long as the other's calls)
+
+    threads = [threading.Thread(target=work, args=(turn,)) for turn in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    a, b = used.values()
+    assert a[0] == a[1] and b[0] == b[1] and (a[0] == b[0]) == shared
+
+
 @pytest.fixture(scope="module")
 def lib():
     tld_build.build()

@@ -39,6 +39,7 @@ class KVCacheDesc(ctypes.Structure):
 
 
 _LARGE = 1 << 31
+_PER_THREAD = 2  # the handle that is another stream in every host thread
 
 
 def _int32(**numbers):
@@ -256,11 +257,14 @@ class KVCache:
                 if not self._in_private_pool(workspace):
                     self._captured_workspaces.append(workspace)
             else:
-                ws = self._workspaces.get(_raw_stream(self._index))
+                key = _raw_stream(self._index)
+                if key == _PER_THREAD:
+                    key = key, threading.get_ident()
+                ws = self._workspaces.get(key)
                 if ws is None:
                     workspace = self.workspace()
                     ws = workspace.data_ptr(), workspace.numel(), workspace
-                    self._workspaces[_raw_stream(self._index)] = ws
+                    self._workspaces[key] = ws
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"workspace: contiguous memory on {self.device} is wanted")
         else:
