@@ -381,12 +381,18 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  *           dimensions; dimension 32 b + 4 g + i (block b, 0 <= g < 8,
  *           0 <= i < 4) is nibble (g * B + b) * 4 + i of the row, low nibble of
  *           a byte first, and stands for (nibble - 8) * scale[b].
+ *           DEC_KV_Q8T16: for K, then for V, [n_kv_heads][page_rows][head_dim]
+ *           bytes, then [n_kv_heads][page_rows / 16] fp32 scales, filled up to a
+ *           multiple of 64 bytes.  A byte stands for (byte - 128) * scale, the
+ *           scale that of its block: 16 rows, from a multiple of 16 on, of one
+ *           head.
  *   pool    [n_layers][n_pages][page_bytes] (dec_kv_sizes), 16-byte aligned
  *   table   [n_seqs][max_pages]: page of each run of rows, or -1 (none)
  *   lens    [n_seqs]: rows of each sequence
  *   refs    [n_pages]: how many table entries name the page; 0 = free
  *   status  one word of enum dec_kv_bits, OR-ed by the kernels
- *   scratch dec_kv_sizes ints, used by extend, fork, compact and status within a call
+ *   scratch dec_kv_sizes ints, used by extend, fork, compact and status within a call,
+ *           and by append for 8-bit pages (a part of each layer's own)
  *
  * An empty cache is table = -1 (all bytes 0xFF), lens = refs = status = 0.
  * A caller that takes rows off a sequence's end by itself (lens) must also take
@@ -394,7 +400,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  * Calls on one cache run one after another (one stream, or ordered by the
  * caller); attention, read and append touch no table, length or count, and
  * calls of these may overlap as long as none reads rows that another writes
- * and each attention has a workspace of its own.
+ * and each attention has a workspace of its own (8-bit pages: rows of a block that
+ * another writes).
  * Attention, fork and compact are two launches each, of which the second reads
  * what the first left in the workspace or the scratch: host threads that queue
  * calls on one stream must not do so at the same time where these share either,
@@ -406,7 +413,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  * device: an index out of range is skipped and sets DEC_KV_BAD_INDEX. */
 enum dec_kv_format {
   DEC_KV_BF16 = 0,  /* bf16 rows */
-  DEC_KV_Q4B32 = 1  /* 4-bit codes in blocks of 32 dimensions with an fp16 scale */
+  DEC_KV_Q4B32 = 1, /* 4-bit codes in blocks of 32 dimensions with an fp16 scale */
+  DEC_KV_Q8T16 = 3  /* 8-bit codes in blocks of 16 rows of a head with a power of two as scale */
 };
 
 enum dec_kv_type { /* of the caller's q, o, k, v */
@@ -455,17 +463,93 @@ int dec_kv_sizes(const dec_kv_cache* c, size_t* page_bytes, size_t* scratch_ints
  * per block the scale s = fp16(max |x| / 7) (the quotient in fp32, at most
  * 65504) and the codes nearest to x / s (exactly, ties to even, within
  * [-8, 7]; 0 where s is 0); a block with a NaN or an infinity gets a NaN
- * scale.  k, v and row_stride * size must be multiples of 16 bytes.  A row
+ * scale.  8-bit pages: of each block that the call writes rows of, the rows before
+ * the first of these are kept and those behind it that the call does not write are
+ * given up (they hold nothing).  The block's scale s becomes the least power of
+ * two, 2^-126 to 2^121, with |x| <= 127 s for the rows written and, where rows
+ * are kept, not below what it was; codes are the integers nearest to x / s, ties
+ * to even, within [-127, 127], and where s rises the kept rows' codes are divided
+ * and rounded the same way.  So a value is off by s / 2, or by s at most after any
+ * number of calls.  The rows may be listed in any order.  A NaN or an infinity
+ * makes the block's scale NaN until its first row is written again.
+ * k, v and row_stride * size must be multiples of 16 bytes.  A row
  * must not be named twice in one call, nor lie in a shared page. */
 int dec_kv_append(const dec_kv_cache* c, int layer, const void* k, const void* v, int type,
                   int64_t row_stride, const int32_t* seqs, const int32_t* positions, int n,
                   dec_stream_t stream);
 
 /* The reverse: rows positions[t] of sequences seqs[t] of one layer, as values
- * of `type` (4-bit: code * scale, exact in fp32), into rows of k and v, which
+ * of `type` (4-bit and 8-bit: code * scale, exact in fp32), into rows of k and v, which
  * must not overlap.  Rows that are skipped are left as they were. */
 int dec_kv_read(const dec_kv_cache* c, int layer, void* k, void* v, int type, int64_t row_stride,
                 const int32_t* seqs, const int32_t* positions, int n, dec_stream_t stream);
+
+/* ---- Rotary positions -----------------------------------------------------------
+ *
+ * Source: the decoder's own rotation of q and k ("Decode is where the bubble has
+ * nowhere to go" lists it without a formula), as a call for the rows of many
+ * sequences.  The first rot_dim dimensions of a head are turned in pairs, (i, i +
+ * rot_dim / 2) or (2 i, 2 i + 1): with an angle of position * frequency[i],
+ * (a, b) becomes magnitude * (a cos - b sin, b cos + a sin); the others stay.
+ *
+ * Positions are whole numbers, so a frequency counts in turns, without the whole
+ * ones: steps[i] = frequency[i] / (2 pi) * 2^64, modulo 2^64, and position * steps[i]
+ * modulo 2^64 is the angle, as exact for far positions as for near ones. */
+enum dec_rope_layout {
+  DEC_ROPE_HALF = 0,  /* pairs (i, i + rot_dim / 2) */
+  DEC_ROPE_PAIRS = 1  /* pairs (2 i, 2 i + 1) */
+};
+
+enum dec_rope_scaling {
+  DEC_ROPE_PLAIN = 0,  /* frequency[i] = theta^(-2 i / rot_dim) */
+  DEC_ROPE_LINEAR = 1, /* divided by factor */
+  DEC_ROPE_NTK = 2,    /* theta * factor^(rot_dim / (rot_dim - 2)) in theta's place: the last is divided
+                          by factor, the first kept */
+  DEC_ROPE_YARN = 3    /* those that turn `fast` times or more over `context` positions are kept, those that
+                          turn `slow` times or less divided by factor, between the two in proportion; the
+                          magnitude is 0.1 log(factor) + 1 */
+};
+
+typedef struct dec_rope {
+  int32_t head_dim;      /* a multiple of 8, 8..1024 */
+  int32_t rot_dim;       /* even, 2..head_dim */
+  int32_t layout;        /* enum dec_rope_layout */
+  float magnitude;       /* finite */
+  const uint64_t* steps; /* device: [rot_dim / 2], 8-byte aligned */
+} dec_rope;
+
+/* Source: none on the pages.  frequency[rot_dim / 2] (host) and the magnitude of a
+ * scaling; theta and factor are positive and finite, and context > 0 and fast >
+ * slow >= 0 (looked at for DEC_ROPE_YARN). */
+int dec_rope_frequencies(int rot_dim, double theta, int scaling, double factor, double context,
+                         double slow, double fast, double* frequency, float* magnitude);
+
+/* Source: none on the pages.  The steps (host) of n frequencies in radians per position. */
+int dec_rope_steps(const double* frequency, int n, uint64_t* steps);
+
+/* Source: none on the pages.  Rotates rows: x and out are [n][n_heads][head_dim] of
+ * `type` (fp32 inside, rounded once), rows x_stride and out_stride elements apart,
+ * row t by positions[t] (device; NULL: by t).  A row with a negative position is
+ * skipped: neither read nor written.  backward: by minus the angle, which
+ * is the gradient of a rotation (and, where the magnitude is 1, its inverse).  out
+ * may be x with the same stride; other overlaps are refused.  x, out and their
+ * strides are multiples of 16 bytes, n_heads is 1..65536 and n * n_heads at most
+ * 2^30. */
+int dec_rope_rotate(const dec_rope* r, const void* x, void* out, int type, int64_t x_stride,
+                    int64_t out_stride, const int32_t* positions, int n, int n_heads, int backward,
+                    dec_stream_t stream);
+
+/* Source: none on the pages.  dec_kv_append of keys that are not rotated yet, with
+ * their queries: row t of k, rotated by its position, and of v are written as
+ * dec_kv_append does (k rounded once, from fp32), and row t of q ([n_q_heads][head_dim],
+ * rows q_stride elements apart) is rotated into q_out, in the same launch.  rope's
+ * head_dim is the cache's.  n_q_heads 0: no q.  q_out may be q with the same stride;
+ * it must not overlap q otherwise, nor k or v.  The rows of q_out of entries that are
+ * skipped are left as they were. */
+int dec_kv_append_rotated(const dec_kv_cache* c, int layer, const dec_rope* rope, const void* q,
+                          void* q_out, int64_t q_stride, int64_t q_out_stride, int n_q_heads,
+                          const void* k, const void* v, int type, int64_t row_stride,
+                          const int32_t* seqs, const int32_t* positions, int n, dec_stream_t stream);
 
 /* Attention of one query per entry of seqs over its sequence's rows in one
  * layer.  q and o: [n][n_q_heads][head_dim] of `type`, rows q_stride and
@@ -487,6 +571,9 @@ int dec_kv_read(const dec_kv_cache* c, int layer, void* k, void* v, int type, in
  * the other blocks hold.  For bf16 results the sums stay in the tensor cores,
  * which cut them off, not round: about 2^-23 of a sum for each 16 rows, and over
  * 4-bit pages up to 2^-20 of scale * sum |q| * 8 * (its K scale) of a score.
+ * Over 8-bit pages weights keep 22 bits (11 for bf16 results), down to a step of
+ * 2^-42 (2^-33) of the largest, and a tile's products are added in fp32; a row whose
+ * block's scale is NaN counts as not finite, and so does one that shares its block.
  * q, o and their strides are multiples of 16 bytes; o must not overlap q.  n and
  * n_q_heads are at most 65536 each, and their product 2^24.
  * workspace: device memory of dec_kv_attention_workspace bytes, 16-byte

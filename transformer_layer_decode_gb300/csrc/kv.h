@@ -19,16 +19,22 @@ struct KvView {
   int32_t* refs;
   int32_t* status;
   int32_t* scratch;
+  int32_t* owners;  // 8-bit pages: [n_pages][page_rows] of the layer (kv_write8)
   int64_t page_bytes;
   int64_t half_bytes;  // of K (or V) in a page
-  int64_t head_bytes;  // of K (or V) of one head in a page
+  int64_t head_bytes;  // of K (or V) of one head in a page (8 bits: without the scales)
   int n_pages, n_seqs, max_pages, page_rows, nkv;
 };
 
-// Bytes of one row of K or V of one head, scales included.
-__host__ __device__ inline int kv_row_bytes(int head_dim, bool q4) {
-  return q4 ? head_dim / 2 + head_dim / 16 : 2 * head_dim;
+// The formats as the kernels' template parameter.
+enum KvFormat { KV_BF16 = DEC_KV_BF16, KV_Q4 = DEC_KV_Q4B32, KV_Q8 = DEC_KV_Q8T16 };
+
+// Bytes of one row of K or V of one head, scales included (8 bits: without).
+__host__ __device__ inline int kv_row_bytes(int head_dim, int format) {
+  return format == KV_Q8 ? head_dim : format == KV_Q4 ? head_dim / 2 + head_dim / 16 : 2 * head_dim;
 }
+
+constexpr int kBlockRows = 16;  // rows of a block of 8-bit pages
 
 // The scratch of extend, fork and compact, in ints: a few words, the new names
 // of pages (compact) or the free pages found (extend, fork), the page copies
@@ -59,17 +65,50 @@ __device__ __noinline__ inline bool kv_bounds_failed(const KvView& c, int line) 
 #define KV_IN_BOUNDS(c, cond) true
 #endif
 
+#ifdef __CUDACC__
+// Where row t of a call's lists lies: its page's first byte (null: skipped; noted where
+// an index was bad), its row in it, its sequence and position.
+struct KvPlace {
+  uint8_t* page;
+  int row, seq, pos;
+};
+__device__ __forceinline__ KvPlace kv_place(const KvView& c, const int32_t* seqs, const int32_t* positions, int64_t t, int n) {
+  KvPlace at{nullptr, 0, -1, 0};
+  const int s = t < n ? (seqs ? seqs[t] : (int)t) : -1;
+  if (s < 0) return at;
+  int page = -1;
+  if (s < c.n_seqs) {
+    const int pos = positions ? positions[t] : c.lens[s] - 1;
+    if (pos >= 0 && pos < c.max_pages * c.page_rows) {
+      page = c.table[(int64_t)s * c.max_pages + pos / c.page_rows];
+      at.row = pos % c.page_rows, at.seq = s, at.pos = pos;
+    }
+  }
+  if (page >= 0 && page < c.n_pages) at.page = c.pool + page * c.page_bytes;
+  else atomicOr(c.status, DEC_KV_BAD_INDEX);
+  return at;
+}
+#endif
+
+struct RopeRows;
+// dec_kv_append to 8-bit pages (and dec_kv_append_rotated, with q).
+cudaError_t kv_write8(const KvView& c, int head_dim, bool f32, const void* k, const void* v, int64_t stride,
+                      const int32_t* seqs, const int32_t* positions, int n, const RopeRows* q, cudaStream_t s);
+
 // Checks a cache (its pointers too, with `memory`); DEC_OK or the error, recorded.
 int kv_check(const dec_kv_cache* c, bool memory);
 KvView kv_view(const dec_kv_cache& c, int layer);
 
-// Whether rows of `width` bytes at a + i * sa and at b + i * sb (i < n) share a byte
-// (where sa and sb differ: whether what they span does).
-inline bool kv_rows_overlap(uintptr_t a, int64_t sa, uintptr_t b, int64_t sb, int64_t width, int n) {
-  if (a + (n - 1) * sa + width <= b || b + (n - 1) * sb + width <= a) return false;
+// Whether rows of wa bytes at a + i * sa and of wb bytes at b + i * sb (i < n) share a
+// byte (where sa and sb differ: whether what they span does).
+inline bool kv_rows_overlap(uintptr_t a, int64_t sa, int64_t wa, uintptr_t b, int64_t sb, int64_t wb, int n) {
+  if (a + (n - 1) * sa + wa <= b || b + (n - 1) * sb + wb <= a) return false;
   if (sa != sb) return true;
-  const int64_t d = (int64_t)(a > b ? a - b : b - a) % sa;
-  return d < width || d > sa - width;
+  const int64_t d = (int64_t)(a > b ? a - b : b - a) % sa;  // how far behind the one that begins first the other does
+  return d < (a > b ? wb : wa) || d > sa - (a > b ? wa : wb);
+}
+inline bool kv_rows_overlap(uintptr_t a, int64_t sa, uintptr_t b, int64_t sb, int64_t width, int n) {
+  return kv_rows_overlap(a, sa, width, b, sb, width, n);
 }
 
 }  // namespace tld

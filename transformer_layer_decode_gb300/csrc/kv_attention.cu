@@ -1,5 +1,5 @@
 // dec_kv_attention: attention of one query per sequence over a paged key/value
-// cache, bf16 or in 4-bit blocks, with a sliding window and first rows that
+// cache, bf16 or in 8-bit or 4-bit blocks, with a sliding window and first rows that
 // stay visible.
 #include <atomic>
 #include <algorithm>
@@ -44,14 +44,15 @@ constexpr int kMaxChunks = (kMaxQueries + kChunkRows - 1) / kChunkRows;
 // A reference moves only when a score passes it by this (log2 units).
 constexpr float kSlack = 5.f;
 
-template <int D, bool Q4>
+template <int D, int F>
 struct Tile {
+  static constexpr bool Q4 = F == KV_Q4, Q8 = F == KV_Q8;
   static constexpr int NB = D / 32;                                  // blocks of 32 dimensions
-  static constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;               // codes or values
+  static constexpr int kRowBytes = Q8 ? D : Q4 ? D / 2 : 2 * D;      // codes or values
   static constexpr int kHalf = kTileRows * (kRowBytes + (Q4 ? 2 * NB : 0));  // K or V, scales after the rows
-  static constexpr int kBytes = 2 * kHalf;
-  static constexpr int kStep = Q4 ? 2 : 1;                           // tiles a warp takes at a time
-  static constexpr int kStages = Q4 ? (D == 128 ? 2 : 4) : (D == 128 ? 2 : 4);  // steps in its ring
+  static constexpr int kBytes = 2 * kHalf + (Q8 ? 16 : 0);           // Q8: K's and V's scale
+  static constexpr int kStep = Q4 || Q8 ? 2 : 1;                     // tiles a warp takes at a time
+  static constexpr int kStages = D == 128 ? 2 : 4;                   // steps in its ring
   static constexpr int kSlot = kStep * kBytes;
   static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kMergeRow = D + 8;                            // floats; heads apart by 8 banks
@@ -62,7 +63,7 @@ struct Tile {
   // warps: about 2.5 us), in tiles; the tiles up to which a unit is not cut
   // between CTAs; and those up to which, if none can have more, every unit is
   // left to one CTA and nothing is counted.
-  static constexpr int kUnit = Q4 ? 24 : 12, kShort = Q4 ? 40 : 20, kWhole = Q4 ? 48 : 24;
+  static constexpr int kUnit = F ? 24 : 12, kShort = F ? 40 : 20, kWhole = F ? 48 : 24;
 };
 
 struct KvAttnParams {
@@ -177,12 +178,13 @@ __device__ __forceinline__ void cp_async_wait() {
 // The pieces are placed so that the reads below touch every bank once: the K
 // reads of 8 lanes (rows 2i, 2i + 1, four neighbouring pieces each) and the V
 // reads (rows 0, 2, 4, 6 or 1, 3, 5, 7, the same pieces of each).
-template <int D, bool Q4>
+template <int D, int F>
 __device__ __forceinline__ int staged(int row, int piece) {
+  constexpr int kRow = Tile<D, F>::kRowBytes;
   const int j = row & 7, t = j >> 1;
-  if constexpr (!Q4) {  // rows of 128 or 256 bytes
-    return row * (2 * D) + ((piece ^ ((t ^ ((j & 1) << 1)) << 1)) << 4);
-  } else if constexpr (D == 128) {  // rows of 64 bytes, two to a line of banks
+  if constexpr (kRow >= 128) {
+    return row * kRow + ((piece ^ ((t ^ ((j & 1) << 1)) << 1)) << 4);
+  } else if constexpr (kRow == 64) {  // two to a line of banks
     return (row >> 1) * 128 + (((j & 1) ^ (t & 1)) << 6) + ((piece ^ (t & 2)) << 4);
   } else {  // rows of 32 bytes, four to a line
     return (row >> 3) * 256 + ((j & 1) << 7) + ((t ^ ((j & 1) << 1)) << 5) + (piece << 4);
@@ -225,6 +227,12 @@ struct WarpSums {
   __device__ __forceinline__ void add_tile(float (&to)[4], const float (&o)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) to[i] += o[i];
+  }
+
+  // The same of sums in units of k.
+  __device__ __forceinline__ void add_tile(float (&to)[4], const float (&o)[4], float k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = fmaf(o[i], k, to[i]);
   }
 
   __device__ __forceinline__ void scale_block(int x, float k) {
@@ -315,21 +323,22 @@ __device__ __forceinline__ uint32_t rows_of_lane(uint32_t rows, int t) {
   return (r & 3) | (r >> 6 & 12);
 }
 
-// Eight dimensions 32 b + 8 t .. of a query as fp32.
-template <int NB, class T>
+// Eight dimensions 32 b + 8 t .. of a query as fp32; BY16: 64 (b / 2) + 16 t + 8 (b % 2) ..
+template <int NB, bool BY16, class T>
 __device__ __forceinline__ void load_query(const T* q, bool valid, int t, float (&x)[NB][8]) {
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
+    const int at = BY16 ? 64 * (b >> 1) + 16 * t + 8 * (b & 1) : 32 * b + 8 * t;
     if (!valid) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
     } else if constexpr (sizeof(T) == 4) {
-      const float4* p = reinterpret_cast<const float4*>(q + 32 * b + 8 * t);
+      const float4* p = reinterpret_cast<const float4*>(q + at);
       const float4 u = p[0], w = p[1];
       x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w;
       x[b][4] = w.x, x[b][5] = w.y, x[b][6] = w.z, x[b][7] = w.w;
     } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(q + 32 * b + 8 * t);
+      const uint4 u = *reinterpret_cast<const uint4*>(q + at);
       x[b][0] = bf16lo(u.x), x[b][1] = bf16hi(u.x), x[b][2] = bf16lo(u.y), x[b][3] = bf16hi(u.y);
       x[b][4] = bf16lo(u.z), x[b][5] = bf16hi(u.z), x[b][6] = bf16lo(u.w), x[b][7] = bf16hi(u.w);
     }
@@ -376,7 +385,7 @@ struct WarpBf16 : WarpHead<D> {
   // One staged tile.  EDGE: some row is not visible; rows_seen: a bit for each that is.
   template <bool EDGE>
   __device__ __forceinline__ void step(const uint8_t* st, int lane, uint64_t rows_seen) {
-    using L = Tile<D, false>;
+    using L = Tile<D, KV_BF16>;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t seen = rows_of_lane((uint32_t)rows_seen, t);
     const uint8_t* sv = st + L::kHalf;
@@ -386,7 +395,7 @@ struct WarpBf16 : WarpHead<D> {
       float c[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        const uint4 w = *reinterpret_cast<const uint4*>(st + staged<D, false>(8 * b + g, 4 * j + t));
+        const uint4 w = *reinterpret_cast<const uint4*>(st + staged<D, KV_BF16>(8 * b + g, 4 * j + t));
         mma_bf16(c, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], w.x, w.y);
         if constexpr (!kWhole) mma_bf16(low, a3[2 * j][0], 0, a3[2 * j][1], 0, w.x, w.y);
         mma_bf16(c, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], w.z, w.w);
@@ -414,7 +423,7 @@ struct WarpBf16 : WarpHead<D> {
       uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = *reinterpret_cast<const uint4*>(sv + staged<D, false>((i & 1) + 2 * t + 8 * (i >> 1), 8 * c + g));
+        v[i] = *reinterpret_cast<const uint4*>(sv + staged<D, KV_BF16>((i & 1) + 2 * t + 8 * (i >> 1), 8 * c + g));
         if (EDGE && !(seen >> i & 1)) v[i] = make_uint4(0, 0, 0, 0);  // 0 * NaN would be NaN
       }
 #pragma unroll
@@ -470,7 +479,7 @@ struct WarpBf16 : WarpHead<D> {
 template <int D, class T>
 struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>> {
   using Sums = WarpSums<D>;
-  using L = Tile<D, true>;
+  using L = Tile<D, KV_Q4>;
   static constexpr int NB = Sums::NB, kTiles = L::kStep;
   static constexpr bool kWhole = sizeof(T) == 2;  // q, and the weights, are one piece
   // The largest weight enters its products as 2^9 to 2^(9 + kSlack), so that they,
@@ -636,10 +645,10 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sk + staged<D, true>(8 * b + g, t));
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + staged<D, KV_Q4>(8 * b + g, t));
           w[b][0] = u.x, w[b][1] = u.y, w[b][2] = u.z, w[b][3] = u.w;
         } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(sk + staged<D, true>(8 * b + g, t >> 1) + 8 * (t & 1));
+          const uint2 u = *reinterpret_cast<const uint2*>(sk + staged<D, KV_Q4>(8 * b + g, t >> 1) + 8 * (t & 1));
           w[b][0] = u.x, w[b][1] = u.y;
         }
       }
@@ -782,10 +791,10 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
       for (int i = 0; i < 4; ++i) {
         const int row = (i & 1) + 2 * t + 8 * (i >> 1);
         if constexpr (D == 128) {
-          const uint2 u = *reinterpret_cast<const uint2*>(sv + staged<D, true>(row, g >> 1) + 8 * (g & 1));
+          const uint2 u = *reinterpret_cast<const uint2*>(sv + staged<D, KV_Q4>(row, g >> 1) + 8 * (g & 1));
           v[i][0] = u.x, v[i][1] = u.y;
         } else {
-          v[i][0] = *reinterpret_cast<const uint32_t*>(sv + staged<D, true>(row, g >> 2) + 4 * (g & 3));
+          v[i][0] = *reinterpret_cast<const uint32_t*>(sv + staged<D, KV_Q4>(row, g >> 2) + 4 * (g & 3));
         }
       }
       uint32_t ph[2];
@@ -838,22 +847,223 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   }
 };
 
-// Fills a stage with a tile: K's rows (Q4: codes) begin at `src`, their scales
+// 8-bit pages.  A tile is a block: one scale for its K and one for its V.  K's multiplies
+// the scores and V's the tile's sums, which are added to the running ones by the FMA
+// pipe, in fp32; nothing of a scale enters an operand, whose range is that of
+// the codes and of q or the weights alone.  A code b stands as the fp16 number 1024 + b
+// behind a byte permutation, b - 128 behind one addition.  q is scaled by a power of two
+// and taken in two fp16 pieces (22 bits; bf16 q needs one), and so are the weights for
+// fp32 results; for bf16 results they are one (11 bits).  With one piece each the scores
+// are computed as S^T = K q^T, 16 rows at a time, and the weights turned by movmatrix.
+template <int D, class T>
+struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>> {
+  using Sums = WarpSums<D>;
+  using L = Tile<D, KV_Q8>;
+  static constexpr int NB = Sums::NB, kTiles = L::kStep, kSteps = D / 16;
+  static constexpr bool kWhole = sizeof(T) == 2;  // q, and the weights, are one piece
+  // The largest weight enters its products as 2^9 to 2^(9 + kSlack), the others so far
+  // above fp16's smallest step; kWhole has these 9 in the exponential, fp32 results
+  // in what they multiply (see WarpQ4).  The second piece enters times 2^kLow.
+  static constexpr int kRoom = 9, kLow = 11;
+  static constexpr float kLift = kWhole ? kRoom : 0;
+  uint32_t a[kSteps][kWhole ? 2 : 4];  // q: dimensions 64 (k / 4) + 16 t + 4 (k % 4) .. of step k
+  float f, f1;                         // score = f * K's scale * product; kWhole: f of head 2t, f1 of the next
+
+  __device__ static int out_dim(int x, int y, int g) { return (D / 8) * g + 4 * x + 2 * y; }
+  __device__ __forceinline__ float out_unit(int) const { return kWhole ? 1.f : 1.f / (1 << kRoom); }
+
+  // x: dimensions 64 (b / 2) + 16 t + 8 (b % 2) ..
+  __device__ __forceinline__ void set_q(float (&x)[NB][8], int t, float scale) {
+    float mx = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[b][i]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const int e = (int)(__float_as_uint(mx) >> 23) - 126;  // mx < 2^e
+    const int sh = max(min(14 - e, 120), -120);            // q to below 2^14
+    const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
+    f = scale * __uint_as_float((uint32_t)(127 - sh) << 23);
+    if (!(mx < INFINITY)) f = __uint_as_float(0x7fffffffu);  // an infinity in q: NaN
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float y0 = x[k / 2][4 * (k % 2) + 2 * h] * up, y1 = x[k / 2][4 * (k % 2) + 2 * h + 1] * up;
+        const uint32_t hi = take_f16(y0, y1);
+        if constexpr (kWhole) {
+          a[k][h] = hi;
+        } else {
+          a[k][2 * h] = hi;
+          a[k][2 * h + 1] = pack_f16(y0, y1);
+        }
+      }
+    if constexpr (kWhole) {
+      f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+      f = __shfl_sync(0xffffffffu, f, 8 * t);
+    }
+    this->clear();
+  }
+
+  // Two codes of a word, the lower or the upper two bytes.
+  __device__ static __forceinline__ uint32_t codes(uint32_t w, uint32_t which) {
+    const uint32_t u = __byte_perm(w, 0x64646464u, which);  // 1024 + b
+    const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&u), __float2half2_rn(-1152.f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static constexpr uint32_t kLower = 0x4140, kUpper = 0x4342;
+
+  // kTiles staged tiles.  EDGE: some row is not visible; rows_seen: a bit for each that is.
+  template <bool EDGE>
+  __device__ __forceinline__ void step(const uint8_t* st, int lane, uint64_t rows_seen) {
+    const int g = lane >> 2, t = lane & 3;
+    // scores: of head g, rows 2t, 2t + 1 of each half; kWhole: of heads 2t, 2t + 1, rows g and g + 8
+    float s[4 * kTiles], v_scale[kTiles];
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+      const uint8_t* sk = st + k * L::kBytes;
+      float2 scales = *reinterpret_cast<const float2*>(sk + 2 * L::kHalf);
+      if (EDGE && !(rows_seen >> (16 * k) & 0xffff)) scales = make_float2(0.f, 0.f);  // (there may be no tile)
+      v_scale[k] = scales.y;
+      uint4 w[2][D / 64];  // rows g, g + 8
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+          w[b][j] = *reinterpret_cast<const uint4*>(sk + staged<D, KV_Q8>(8 * b + g, 4 * j + t));
+      auto word = [&](int b, int i) {
+        const uint4& u = w[b][i / 4];
+        return i % 4 == 0 ? u.x : i % 4 == 1 ? u.y : i % 4 == 2 ? u.z : u.w;
+      };
+      if constexpr (kWhole) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const uint32_t u0 = word(0, i), u1 = word(1, i);
+          mma_f16(c, codes(u0, kLower), codes(u1, kLower), codes(u0, kUpper), codes(u1, kUpper), a[i][0], a[i][1]);
+        }
+        const float k0 = f * scales.x, k1 = f1 * scales.x;
+        s[4 * k] = c[0] * k0, s[4 * k + 1] = c[1] * k1, s[4 * k + 2] = c[2] * k0, s[4 * k + 3] = c[3] * k1;
+        if (EDGE) {
+          if (!(rows_seen >> (16 * k + g) & 1)) s[4 * k] = s[4 * k + 1] = -INFINITY;
+          if (!(rows_seen >> (16 * k + 8 + g) & 1)) s[4 * k + 2] = s[4 * k + 3] = -INFINITY;
+        }
+      } else {
+        const float k0 = f * scales.x;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const uint32_t u = word(b, i);
+            mma_f16(c, a[i][0], a[i][1], a[i][2], a[i][3], codes(u, kLower), codes(u, kUpper));
+          }
+          s[4 * k + 2 * b] = (c[0] + c[2]) * k0;
+          s[4 * k + 2 * b + 1] = (c[1] + c[3]) * k0;
+        }
+        if (EDGE) {
+          const uint32_t seen = rows_of_lane((uint32_t)(rows_seen >> (16 * k)) & 0xffff, t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(seen >> i & 1)) s[4 * k + i] = -INFINITY;
+        }
+      }
+    }
+    float w[4 * kTiles];
+    if constexpr (kWhole) {
+      float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+#pragma unroll
+      for (int i = 4; i < 4 * kTiles; i += 2) mx0 = fmaxf(mx0, s[i]), mx1 = fmaxf(mx1, s[i + 1]);
+      if (__any_sync(0xffffffffu, mx0 > this->ref[0] + (kLift + kSlack) || mx1 > this->ref[1] + (kLift + kSlack)))
+        this->raise(mx0, mx1, kLift);
+#pragma unroll
+      for (int i = 0; i < 4 * kTiles; ++i) {
+        w[i] = exp2_approx(s[i] - this->ref[i & 1]);
+        this->l[i & 1] += w[i];
+      }
+    } else {
+      float mx = s[0];
+#pragma unroll
+      for (int i = 1; i < 4 * kTiles; ++i) mx = fmaxf(mx, s[i]);
+      if (__any_sync(0xffffffffu, mx > this->ref + kSlack)) this->raise(mx, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * kTiles; ++i) {
+        w[i] = exp2_approx(s[i] - this->ref);
+        sum += w[i];
+      }
+      this->l += sum;
+    }
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+      const uint8_t* sv = st + k * L::kBytes + L::kHalf;
+      uint32_t v[4][D / 32];  // 16 dimensions (of 64: 8) of the lane's rows
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = (i & 1) + 2 * t + 8 * (i >> 1);
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sv + staged<D, KV_Q8>(row, g));
+          v[i][0] = u.x, v[i][1] = u.y, v[i][NB - 2] = u.z, v[i][NB - 1] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(sv + staged<D, KV_Q8>(row, g >> 1) + 8 * (g & 1));
+          v[i][0] = u.x, v[i][1] = u.y;
+        }
+      }
+      constexpr int kPieces = kWhole ? 1 : 2;
+      uint32_t pw[kPieces][2];  // weights: rows 2t, 2t + 1 of each half, of head g
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if constexpr (kWhole) {
+          const uint32_t rows = pack_f16(w[4 * k + 2 * b], w[4 * k + 2 * b + 1]);
+          asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pw[0][b]) : "r"(rows));
+        } else {
+          float y0 = w[4 * k + 2 * b] * (1 << kRoom), y1 = w[4 * k + 2 * b + 1] * (1 << kRoom);
+          pw[0][b] = take_f16(y0, y1);
+          pw[kPieces - 1][b] = pack_f16(y0 * (1 << kLow), y1 * (1 << kLow));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          // dimensions 4 j + 2 y and the next, of two rows each
+          const uint32_t z0 = __byte_perm(v[0][j], v[1][j], y ? 0x7362 : 0x5140);
+          const uint32_t z1 = __byte_perm(v[2][j], v[3][j], y ? 0x7362 : 0x5140);
+          const uint32_t a0 = codes(z0, kLower), a1 = codes(z0, kUpper), a2 = codes(z1, kLower), a3 = codes(z1, kUpper);
+          float o[4] = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (!kWhole) {
+            mma_f16(o, a0, a1, a2, a3, pw[kPieces - 1][0], pw[kPieces - 1][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= 1.f / (1 << kLow);
+          }
+          mma_f16(o, a0, a1, a2, a3, pw[0][0], pw[0][1]);
+          this->add_tile(this->acc[j][y], o, v_scale[k]);
+        }
+    }
+  }
+};
+
+// Fills a stage with a tile: K's rows (or codes) begin at `src`, their scales (Q8: scale)
 // `scales` bytes behind, V's half_bytes behind K's; not `there`: with zeros.
-template <int D, bool Q4>
+template <int D, int F>
 __device__ __forceinline__ void stage_tile(uint32_t dst, const uint8_t* src, int scales, int64_t half_bytes, int lane,
                                            bool there) {
-  using L = Tile<D, Q4>;
+  using L = Tile<D, F>;
   constexpr int PPR = L::kRowBytes / 16, N = kTileRows * PPR / 32;
   const uint8_t* k = src + 16 * lane;
   const uint8_t* v = src + (half_bytes + 16 * lane);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int at = i * 32 + lane, to = staged<D, Q4>(at / PPR, at % PPR);
+    const int at = i * 32 + lane, to = staged<D, F>(at / PPR, at % PPR);
     cp_async<16>(dst + to, k + 512 * i, there ? 16 : 0);
     cp_async<16>(dst + L::kHalf + to, v + 512 * i, there ? 16 : 0);
   }
-  if constexpr (Q4) {  // half the lanes K's scales, half V's
+  if constexpr (F == KV_Q8) {
+    if (lane < 2)
+      cp_async<4>(dst + 2 * L::kHalf + 4 * lane, src + (lane ? half_bytes : 0) + scales, there ? 4 : 0);
+  }
+  if constexpr (F == KV_Q4) {  // half the lanes K's scales, half V's
     constexpr int kPart = L::NB * 2;
     const int64_t from = (lane < 16 ? 0 : half_bytes) + (lane & 15) * kPart;
     const int to = kTileRows * L::kRowBytes + (lane < 16 ? 0 : L::kHalf) + (lane & 15) * kPart;
@@ -885,11 +1095,11 @@ struct UnitSums {
 };
 
 // The CTA's sums over tiles t0 .. t1 - 1 of unit u of query r.
-template <int D, bool Q4, class T>
+template <int D, int F, class T>
 __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Rows& v, int r, int u, int t0, int t1,
                                                  uint8_t* smem) {
-  using L = Tile<D, Q4>;
-  using W = std::conditional_t<Q4, WarpQ4<D, T>, WarpBf16<D, T>>;
+  using L = Tile<D, F>;
+  using W = std::conditional_t<F == KV_Q4, WarpQ4<D, T>, std::conditional_t<F == KV_Q8, WarpQ8<D, T>, WarpBf16<D, T>>>;
   constexpr int ST = L::kStages, kRound = kWarps * L::kStep;
   __shared__ float2 warp_ref[kWarps][kHeadBlock];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -921,7 +1131,9 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
       if (page >= 0 && KV_IN_BOUNDS(c, row + kTileRows <= c.page_rows && head < c.nkv)) {
         nxt_src = reinterpret_cast<unsigned long long>(c.pool + page * c.page_bytes + head * c.head_bytes +
                                                        row * L::kRowBytes);
-        nxt_scales = (c.page_rows - row) * L::kRowBytes + row * 2 * L::NB;
+        if constexpr (F == KV_Q8)
+          nxt_scales = (int)((c.nkv - head) * c.head_bytes) - row * D + 4 * (head * (c.page_rows / kBlockRows) + row / kBlockRows);
+        else nxt_scales = (c.page_rows - row) * L::kRowBytes + row * 2 * L::NB;
       } else {
         atomicOr(c.status, DEC_KV_BAD_INDEX);
         doubt = true;
@@ -941,7 +1153,7 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
         const int i = (j * L::kStep + k) & 31;
         const unsigned long long src = __shfl_sync(0xffffffffu, cur_src, i);
         const int scales = __shfl_sync(0xffffffffu, cur_scales, i);
-        stage_tile<D, Q4>(dst + k * L::kBytes, reinterpret_cast<const uint8_t*>(src), max(scales, 0), c.half_bytes, lane,
+        stage_tile<D, F>(dst + k * L::kBytes, reinterpret_cast<const uint8_t*>(src), max(scales, 0), c.half_bytes, lane,
                           scales >= 0);
       }
     }
@@ -955,7 +1167,7 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
       min(nt / L::kStep, full1 - L::kStep >= n0 ? (full1 - L::kStep - n0) / kRound + 1 : 0) - plain0;
   const bool asks = g < n_heads && KV_IN_BOUNDS(c, r >= 0 && r < p.n && (int64_t)head * p.group + h0 + g < p.nq);
   float x[L::NB][8];  // q, read while the page numbers are, and made operands while the first tiles are under way
-  load_query<L::NB>(
+  load_query<L::NB, F == KV_Q8>(
       static_cast<const T*>(p.q) + r * p.q_stride + ((int64_t)head * p.group + h0 + min(g, n_heads - 1)) * D, asks, t, x);
   fetch(0);
 #pragma unroll 1
@@ -1042,8 +1254,8 @@ __device__ __forceinline__ void write_unit(const KvAttnParams& p, int r, int u, 
 }
 
 // Units that are all short: a CTA takes whole units in turn.
-template <int D, bool Q4, class T>
-__global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm)
+template <int D, int F, class T>
+__global__ void __launch_bounds__(kThreadsA, Tile<D, F>::kCtasPerSm)
     kv_attn_whole(const __grid_constant__ KvAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int units = p.c.nkv * p.head_blocks;
@@ -1053,7 +1265,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm)
     const Rows v = query_rows(p, r, &bad);
     if (bad && threadIdx.x == 0) atomicOr(p.c.status, DEC_KV_BAD_INDEX);
     if (v.seq < 0) continue;
-    UnitSums<D> o = unit_sums<D, Q4, T>(p, v, r, u, 0, v.tiles, smem);
+    UnitSums<D> o = unit_sums<D, F, T>(p, v, r, u, 0, v.tiles, smem);
     write_unit<D, T>(p, r, u, o);
   }
 }
@@ -1069,9 +1281,9 @@ struct Share {
   int more;              // CTAs that the unit which begins here goes on for; -1: to be worked out
 };
 
-template <int D, bool Q4, class T>
-__global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(const __grid_constant__ KvAttnParams p) {
-  using L = Tile<D, Q4>;
+template <int D, int F, class T>
+__global__ void __launch_bounds__(kThreadsA, Tile<D, F>::kCtasPerSm) kv_attn(const __grid_constant__ KvAttnParams p) {
+  using L = Tile<D, F>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t chunk_sum[kMaxChunks];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1238,7 +1450,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, Q4>::kCtasPerSm) kv_attn(co
     const int t0 = max(in - unit, 0);
     const int t1 = max((int)min((int64_t)len, in + (share.end - share.pos)) - unit, t0);
     if (tid == 0) share.u = u, share.t0 = t0, share.t1 = t1;  // (read after the barriers within unit_sums)
-    UnitSums<D> o = unit_sums<D, Q4, T>(p, v, share.r, u, t0, t1, smem);
+    UnitSums<D> o = unit_sums<D, F, T>(p, v, share.r, u, t0, t1, smem);
     const bool begins = share.t0 == 0, ends = share.t1 == v.tiles;
     if (begins && ends) {
       write_unit<D, T>(p, share.r, share.u, o);
@@ -1373,9 +1585,11 @@ int device_sms(int* dev, int* sms) {
 
 // CTAs of a launch: one round of what fits on the GPU.
 int attn_ctas(const dec_kv_cache& c, int sms) {
-  const bool q4 = c.format == DEC_KV_Q4B32;
-  if (c.head_dim == 128) return sms * (q4 ? Tile<128, true>::kCtasPerSm : Tile<128, false>::kCtasPerSm);
-  return sms * (q4 ? Tile<64, true>::kCtasPerSm : Tile<64, false>::kCtasPerSm);
+  auto fits = [&](auto bf16, auto q4, auto q8) {
+    return c.format == DEC_KV_Q8T16 ? q8.kCtasPerSm : c.format == DEC_KV_Q4B32 ? q4.kCtasPerSm : bf16.kCtasPerSm;
+  };
+  if (c.head_dim == 128) return sms * fits(Tile<128, KV_BF16>(), Tile<128, KV_Q4>(), Tile<128, KV_Q8>());
+  return sms * fits(Tile<64, KV_BF16>(), Tile<64, KV_Q4>(), Tile<64, KV_Q8>());
 }
 
 struct Workspace {
@@ -1396,29 +1610,29 @@ int64_t longest_unit(const KvAttnParams& p) {
   return p.window ? std::min(rows, (int64_t)p.window + p.sinks) / kTileRows + 3 : (rows + kTileRows - 1) / kTileRows;
 }
 
-template <int D, bool Q4, class T>
+template <int D, int F, class T>
 cudaError_t launch_attn_kv(KvAttnParams p, int dev, int ctas, cudaStream_t s) {
   static std::atomic<bool> ready[kMaxDevices];  // the kernels' shared-memory limits have been set on the device
   if (!ready[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(kv_attn<D, Q4, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Tile<D, Q4>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kv_attn<D, F, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Tile<D, F>::kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kv_attn_whole<D, Q4, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               Tile<D, Q4>::kSmem);
+      e = cudaFuncSetAttribute(kv_attn_whole<D, F, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Tile<D, F>::kSmem);
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
   const int64_t units = (int64_t)p.n * p.c.nkv * p.head_blocks;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreadsA);
-  cfg.dynamicSmemBytes = Tile<D, Q4>::kSmem;
+  cfg.dynamicSmemBytes = Tile<D, F>::kSmem;
   cfg.stream = s;
-  if (longest_unit(p) <= Tile<D, Q4>::kWhole) {
+  if (longest_unit(p) <= Tile<D, F>::kWhole) {
     cfg.gridDim = dim3((unsigned)std::min(units, (int64_t)ctas));
-    return cudaLaunchKernelEx(&cfg, kv_attn_whole<D, Q4, T>, p);
+    return cudaLaunchKernelEx(&cfg, kv_attn_whole<D, F, T>, p);
   }
   cfg.gridDim = dim3(ctas);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn<D, Q4, T>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn<D, F, T>, p);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute pdl = {};
   pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1508,17 +1722,16 @@ extern "C" int dec_kv_attention(const dec_kv_cache* c, int layer, const void* q,
   p.cut_by_unit = (int64_t)n * c->n_kv_heads * p.head_blocks <= ctas;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  const bool q4 = c->format == DEC_KV_Q4B32, f32 = type == DEC_IO_F32;
-#define TLD_ATTN(D, Q)                                       \
-  e = f32 ? launch_attn_kv<D, Q, float>(p, dev, ctas, s)     \
-          : launch_attn_kv<D, Q, uint16_t>(p, dev, ctas, s)
-  if (c->head_dim == 128) {
-    if (q4) TLD_ATTN(128, true);
-    else TLD_ATTN(128, false);
-  } else {
-    if (q4) TLD_ATTN(64, true);
-    else TLD_ATTN(64, false);
-  }
+  const bool f32 = type == DEC_IO_F32;
+#define TLD_ATTN(D)                                                                                              \
+  e = c->format == DEC_KV_Q8T16   ? f32 ? launch_attn_kv<D, KV_Q8, float>(p, dev, ctas, s)                       \
+                                        : launch_attn_kv<D, KV_Q8, uint16_t>(p, dev, ctas, s)                    \
+      : c->format == DEC_KV_Q4B32 ? f32 ? launch_attn_kv<D, KV_Q4, float>(p, dev, ctas, s)                       \
+                                        : launch_attn_kv<D, KV_Q4, uint16_t>(p, dev, ctas, s)                    \
+      : f32                       ? launch_attn_kv<D, KV_BF16, float>(p, dev, ctas, s)                           \
+                                  : launch_attn_kv<D, KV_BF16, uint16_t>(p, dev, ctas, s)
+  if (c->head_dim == 128) TLD_ATTN(128);
+  else TLD_ATTN(64);
 #undef TLD_ATTN
   if (e != cudaSuccess) return fail_no_handle(DEC_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
   return DEC_OK;

@@ -1,12 +1,14 @@
 // dec_kv_append and dec_kv_read: rows of a paged key/value cache from and to
-// plain tensors, bf16 or in 4-bit blocks.  Also the checks shared by the
-// dec_kv_ calls.
+// plain tensors, bf16 or in 4-bit blocks (and 8-bit rows read; kv_write8.cu writes
+// them), and dec_kv_append_rotated.  Also the checks shared by the dec_kv_ calls.
 #include <algorithm>
 #include <cstdio>
 #include <type_traits>
 
 #include "common.cuh"
 #include "kv.h"
+#include "rope.cuh"
+#include "rows.cuh"
 
 using namespace tld;
 
@@ -24,7 +26,7 @@ int kv_check(const dec_kv_cache* c, bool memory) {
     return fail_no_handle(DEC_ERR_SHAPE, "%d pages, %d sequences (at most 2^20 and 65536)", c->n_pages, c->n_seqs);
   if (c->max_pages < 1 || (int64_t)c->max_pages * c->page_rows > (1 << 30))
     return fail_no_handle(DEC_ERR_SHAPE, "max_pages %d of %d rows (at most 2^30 rows)", c->max_pages, c->page_rows);
-  if (c->format != DEC_KV_BF16 && c->format != DEC_KV_Q4B32)
+  if (c->format != DEC_KV_BF16 && c->format != DEC_KV_Q4B32 && c->format != DEC_KV_Q8T16)
     return fail_no_handle(DEC_ERR_ARG, "unknown cache format %d", c->format);
   if (memory) {
     if (!c->pool || !c->table || !c->lens || !c->refs || !c->status || !c->scratch)
@@ -40,8 +42,10 @@ int kv_check(const dec_kv_cache* c, bool memory) {
 
 KvView kv_view(const dec_kv_cache& c, int layer) {
   KvView v;
-  v.head_bytes = (int64_t)c.page_rows * kv_row_bytes(c.head_dim, c.format == DEC_KV_Q4B32);
+  v.head_bytes = (int64_t)c.page_rows * kv_row_bytes(c.head_dim, c.format);
   v.half_bytes = v.head_bytes * c.n_kv_heads;
+  if (c.format == DEC_KV_Q8T16)
+    v.half_bytes = (v.half_bytes + (int64_t)(c.page_rows / kBlockRows) * 4 * c.n_kv_heads + 63) / 64 * 64;
   v.page_bytes = 2 * v.half_bytes;
   v.pool = static_cast<uint8_t*>(c.pool) + (int64_t)layer * c.n_pages * v.page_bytes;
   v.table = c.table;
@@ -49,6 +53,7 @@ KvView kv_view(const dec_kv_cache& c, int layer) {
   v.refs = c.refs;
   v.status = c.status;
   v.scratch = c.scratch;
+  v.owners = c.scratch ? c.scratch + kv_scratch_ints(c.n_pages, c.n_seqs) + (int64_t)layer * c.n_pages * c.page_rows : nullptr;
   v.n_pages = c.n_pages;
   v.n_seqs = c.n_seqs;
   v.max_pages = c.max_pages;
@@ -69,98 +74,6 @@ constexpr int kFewRounds = 8192;  // (about a GPU full of warps)
 // CTAs beyond which they take more tokens each (half or 1.5 times as many: up to
 // 6 % slower).
 constexpr int kManyCtas = 2400;
-
-// The largest of three magnitudes; NaN if one is.
-__device__ __forceinline__ float largest(float a, float b, float c) {
-  float y;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-// The larger magnitudes of two bf16 pairs (with some sign); NaN if either is.
-__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
-
-// Two fp32 numbers handled by one instruction.
-struct Two {
-  uint64_t w;
-  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
-  __device__ __forceinline__ float2 get() const {
-    float2 y;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(w));
-    return y;
-  }
-};
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.w) : "l"(b.w), "l"(c.w));
-  return a;
-}
-__device__ __forceinline__ Two add2(Two a, Two b) {
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.w) : "l"(b.w));
-  return a;
-}
-
-// Eight values of the caller's type as they are loaded, their fp32 values, and
-// the largest magnitude among them and those of four neighbouring lanes (NaN if
-// one of them is).
-template <class T>
-struct Eight;
-template <>
-struct Eight<float> {
-  float4 u, w;
-  __device__ __forceinline__ void load(const float* p) {
-    u = reinterpret_cast<const float4*>(p)[0], w = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
-    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
-  }
-  __device__ __forceinline__ float top() const {
-    float y = largest(largest(largest(u.x, u.y, u.z), u.w, w.x), w.y, w.z);
-    y = largest(y, w.w, __shfl_xor_sync(0xffffffffu, largest(y, w.w, 0.f), 1));
-    return largest(y, __shfl_xor_sync(0xffffffffu, y, 2), 0.f);
-  }
-};
-template <>
-struct Eight<uint16_t> {
-  uint4 u;
-  __device__ __forceinline__ void load(const uint16_t* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
-    x[0] = bf16lo(u.x), x[1] = bf16hi(u.x), x[2] = bf16lo(u.y), x[3] = bf16hi(u.y);
-    x[4] = bf16lo(u.z), x[5] = bf16hi(u.z), x[6] = bf16lo(u.w), x[7] = bf16hi(u.w);
-  }
-  __device__ __forceinline__ float top() const {
-    uint32_t y = larger2(larger2(u.x, u.y), larger2(u.z, u.w));
-    y = larger2(y, __shfl_xor_sync(0xffffffffu, y, 1));
-    y = larger2(y, __shfl_xor_sync(0xffffffffu, y, 2));
-    return largest(bf16lo(y), bf16hi(y), 0.f);
-  }
-};
-// wide: p is a multiple of 32 bytes, which one store then writes whole; two
-// stores of half a sector each take longer (8185 rows of 32 heads of 128 read
-// from 4-bit pages: 81 us, against 51).
-__device__ __forceinline__ void store8(float* p, const float (&x)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
-                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
-}
-__device__ __forceinline__ uint32_t pair(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8], bool) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pair(x[0], x[1]), pair(x[2], x[3]), pair(x[4], x[5]), pair(x[6], x[7]));
-}
-
-constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
 
 // 1 / s to a few 2^-24 of itself.
 __device__ __forceinline__ float reciprocal(float s) {
@@ -220,32 +133,36 @@ constexpr int kMaxTokens = 32;  // of a CTA
 // 57).  In fp32, 306 MB, 51 and 51 us (46); from and to bf16 pages, 268 MB, 43 (40),
 // fp32 and bf16 pages, 402 MB, 61 and 62 (60).  Four rounds:
 // two are 10 % slower, eight 15 % in fp32.
-template <int D, bool Q4, class T, bool READ, int ROUNDS>
-__global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
-                                                          const int32_t* seqs, const int32_t* positions,
-                                                          int n, int tokens, int items_per_token, bool wide) {
+//
+// ROPE: keys are rotated by their positions on the way, in fp32; the angles of the
+// CTA's tokens are worked out once, into shared memory.
+template <int D, int F, class T, bool READ, int ROUNDS, bool ROPE>
+__device__ __forceinline__ void move_rows(const KvView& c, T* k, T* v, int64_t stride, const int32_t* seqs,
+                                          const int32_t* positions, int n, int tokens, int items_per_token, bool wide,
+                                          int block, const RopeView& rope) {
   constexpr int LANES = D / 8, NB = D / 32, RPR = 32 / LANES;  // rows of a round
   __shared__ uint8_t* token_page[kMaxTokens];
   __shared__ int token_row[kMaxTokens];
+  __shared__ int token_pos[ROPE ? kMaxTokens : 1];
+  __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? kMaxTokens * (D / 2) : 1];  // cosines, sines
   const int lane = threadIdx.x & 31, l = lane % LANES, b = l / 4, j = l % 4;
-  const int64_t t0 = (int64_t)blockIdx.x * tokens;
+  const int64_t t0 = (int64_t)block * tokens;
   if (threadIdx.x < tokens) {
     const int64_t t = t0 + threadIdx.x;
-    uint8_t* at = nullptr;
-    const int s = t < n ? (seqs ? seqs[t] : (int)t) : -1;
-    if (s >= 0) {
-      int page = -1;
-      if (s < c.n_seqs) {
-        const int pos = positions ? positions[t] : c.lens[s] - 1;
-        if (pos >= 0 && pos < c.max_pages * c.page_rows) {
-          page = c.table[(int64_t)s * c.max_pages + pos / c.page_rows];
-          token_row[threadIdx.x] = pos % c.page_rows;
-        }
-      }
-      if (page >= 0 && page < c.n_pages) at = c.pool + page * c.page_bytes;
-      else atomicOr(c.status, DEC_KV_BAD_INDEX);
+    const KvPlace at = kv_place(c, seqs, positions, t, n);
+    token_row[threadIdx.x] = at.row;
+    token_page[threadIdx.x] = at.page;
+    if (ROPE) token_pos[threadIdx.x] = at.pos;
+  }
+  if constexpr (ROPE) {
+    __syncthreads();
+    const int half = rope.rot / 2;
+    for (int e = threadIdx.x; e < tokens * half; e += kRowWarps * 32) {
+      const int t = e / half, i = e - t * half;
+      if (!token_page[t]) continue;
+      const float2 y = rope_angle(rope, token_pos[t], i);
+      angles[0][t * (D / 2) + i] = y.x, angles[1][t * (D / 2) + i] = y.y;
     }
-    token_page[threadIdx.x] = at;
   }
   __syncthreads();
   const int last = 2 * c.nkv - 1;
@@ -260,7 +177,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
     const int row = token_row[token], page_rows = c.page_rows, nkv = c.nkv;
     if (!KV_IN_BOUNDS(c, token < kMaxTokens && t0 + token < n && part >= 0 && row >= 0 && row < page_rows &&
                              base >= c.pool && base + c.page_bytes <= c.pool + c.n_pages * c.page_bytes &&
-                             2 * nkv * c.head_bytes == c.page_bytes))
+                             (F == KV_Q8 || 2 * nkv * c.head_bytes == c.page_bytes)))
       continue;
     const uint32_t head_bytes = (uint32_t)c.head_bytes;
     const int first = part * (ROUNDS * RPR) + lane / LANES;
@@ -271,10 +188,30 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
     auto mine = [&](int at) { return (at < nkv ? k_at : v_at) + at * D; };  // the caller's
     // in the page: bf16 values, or two words of codes, 2 NB bytes apart, and a scale
     auto head = [&](int at) { return (uint64_t)(uint32_t)at * head_bytes; };
-    uint8_t* values = base + row * kv_row_bytes(D, false) + 16 * l;
+    uint8_t* values = base + row * kv_row_bytes(D, KV_BF16) + 16 * l;
     uint8_t* words = base + row * (D / 2) + 4 * j * NB + 2 * b;
     uint8_t* scales = base + page_rows * (D / 2) + (row * NB + b) * 2;
-    if constexpr (!READ || !Q4) {
+    if constexpr (READ && F == KV_Q8) {
+      uint2 codes[ROUNDS];
+      float scale[ROUNDS];
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int at = round(i), h = at < nkv ? at : at - nkv;
+        const uint8_t* half = base + (at < nkv ? 0 : c.half_bytes);
+        codes[i] = *reinterpret_cast<const uint2*>(half + (uint64_t)(uint32_t)h * head_bytes + row * D + 8 * l);
+        scale[i] = *reinterpret_cast<const float*>(half + (uint64_t)(uint32_t)nkv * head_bytes +
+                                                   4 * ((int64_t)h * (page_rows / kBlockRows) + row / kBlockRows));
+      }
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        float x[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m)  // 2^23 + byte, less 2^23 + 128
+          x[m] = (__uint_as_float(__byte_perm(m < 4 ? codes[i].x : codes[i].y, 0x4b000000u, 0x7440 | (m & 3))) - 8388736.f) *
+                 scale[i];
+        store8(mine(round(i)), x, wide);
+      }
+    } else if constexpr (!READ || F == KV_BF16) {
       Eight<std::conditional_t<READ, uint16_t, T>> in[ROUNDS];
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
@@ -287,12 +224,23 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
         const int at = round(i);
         float x[8];
         in[i].values(x);
+        if constexpr (ROPE) {
+          const float* cs = angles[0] + token * (D / 2);
+          rope_eight<LANES>(rope, x, l, cs, cs + kMaxTokens * (D / 2), mine(at) - 8 * l, at < nkv);
+        }
         if constexpr (READ) {
           store8(mine(at), x, wide);
-        } else if constexpr (!Q4) {
+        } else if constexpr (F == KV_BF16) {
           store8(reinterpret_cast<uint16_t*>(values + head(at)), x, false);
         } else {
-          const float top = in[i].top();  // the block's largest magnitude
+          float top;  // the block's largest magnitude
+          if constexpr (ROPE) {
+            Eight<float> turned;
+            turned.set(x);
+            top = turned.top();
+          } else {
+            top = in[i].top();
+          }
           const bool finite = top < INFINITY;
           const __half s16 = finite ? __float2half_rn(fminf(seventh(top), 65504.f)) : __ushort_as_half(0x7fff);
           const float f = __half2float(s16);
@@ -327,13 +275,41 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, 
   }
 }
 
+template <int D, int F, class T, bool READ, int ROUNDS>
+__global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
+                                                          const int32_t* seqs, const int32_t* positions,
+                                                          int n, int tokens, int items_per_token, bool wide) {
+  move_rows<D, F, T, READ, ROUNDS, false>(c, k, v, stride, seqs, positions, n, tokens, items_per_token, wide, blockIdx.x,
+                                          RopeView{});
+}
+
+// The rows of a step: the first `blocks` CTAs rotate and write keys and write values,
+// the others rotate queries.
+template <int D, int F, class T, int ROUNDS>
+__global__ void __launch_bounds__(kRowWarps * 32) kv_rows_rotated(const __grid_constant__ KvView c, const T* k, const T* v,
+                                                                  int64_t stride, const int32_t* seqs,
+                                                                  const int32_t* positions, int n, int tokens,
+                                                                  int items_per_token, int blocks,
+                                                                  const __grid_constant__ RopeRows q) {
+  extern __shared__ __align__(16) float q_angles[];
+  if ((int)blockIdx.x >= blocks) {
+    rope_rows<T>(q, blockIdx.x - blocks, q_angles, [&](int64_t t) {
+      const KvPlace at = kv_place(c, seqs, positions, t, n);
+      return at.page ? at.pos : -1;
+    });
+  } else {
+    move_rows<D, F, T, false, ROUNDS, true>(c, const_cast<T*>(k), const_cast<T*>(v), stride, seqs, positions, n, tokens,
+                                            items_per_token, false, blockIdx.x, q.r);
+  }
+}
+
 // Reads and clears the status in one step: bits that calls on other streams set in
 // the meantime are in this answer or in the next.
 __global__ void kv_take_status(int32_t* status, int32_t* taken) { *taken = atomicExch(status, 0); }
 
-template <int D, bool Q4, class T, bool READ>
+template <int D, int F, class T, bool READ>
 cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const int32_t* seqs,
-                        const int32_t* positions, int n, cudaStream_t s) {
+                        const int32_t* positions, int n, const RopeRows* q, cudaStream_t s) {
   constexpr int kPerRound = 256 / D;
   const bool few = (int64_t)n * 2 * c.nkv / kPerRound < kFewRounds;
   const int per_item = kPerRound * (few ? 1 : kRowRounds);
@@ -342,23 +318,40 @@ cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const
   // enough tokens for every warp of a CTA, or a multiple where there are CTAs enough
   const int least = (kRowWarps + items - 1) / items;
   const int tokens = std::min(std::max((n / kManyCtas + least - 1) / least, 1) * least, kMaxTokens);
+  const int blocks = (n + tokens - 1) / tokens;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((n + tokens - 1) / tokens));
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kRowWarps * 32);
   cfg.stream = s;
-  return cudaLaunchKernelEx(&cfg, few ? kv_rows<D, Q4, T, READ, 1> : kv_rows<D, Q4, T, READ, kRowRounds>, c,
+  if constexpr (!READ) {
+    if (q) {
+      RopeRows rows = *q;
+      if (rows.n) {
+        cfg.gridDim.x += (unsigned)rope_cut(rows);
+        cfg.dynamicSmemBytes = rope_smem(rows);
+      }
+      return cudaLaunchKernelEx(&cfg, few ? kv_rows_rotated<D, F, T, 1> : kv_rows_rotated<D, F, T, kRowRounds>, c,
+                                static_cast<const T*>(k), static_cast<const T*>(v), stride, seqs, positions, n, tokens,
+                                items, blocks, rows);
+    }
+  }
+  return cudaLaunchKernelEx(&cfg, few ? kv_rows<D, F, T, READ, 1> : kv_rows<D, F, T, READ, kRowRounds>, c,
                             static_cast<T*>(k), static_cast<T*>(v), stride, seqs, positions, n, tokens, items, wide);
 }
 
+template <int D, class T, bool READ>
+cudaError_t launch_format(int format, const KvView& c, void* k, void* v, int64_t stride, const int32_t* seqs,
+                          const int32_t* positions, int n, const RopeRows* q, cudaStream_t s) {
+  if (format == KV_Q4) return launch_rows<D, KV_Q4, T, READ>(c, k, v, stride, seqs, positions, n, q, s);
+  if (format == KV_BF16) return launch_rows<D, KV_BF16, T, READ>(c, k, v, stride, seqs, positions, n, q, s);
+  if constexpr (READ) return launch_rows<D, KV_Q8, T, true>(c, k, v, stride, seqs, positions, n, q, s);
+  else return kv_write8(c, D, sizeof(T) == 4, k, v, stride, seqs, positions, n, q, s);
+}
+
+// q: the queries that an append rotates, and its rotation (of no queries: n = 0).
 template <bool READ>
 int rows_call(const dec_kv_cache* c, int layer, void* k, void* v, int type, int64_t row_stride,
-              const int32_t* seqs, const int32_t* positions, int n, dec_stream_t stream) {
-  if (int rc = kv_check(c, true)) return rc;
-  if (layer < 0 || layer >= c->n_layers) return fail_no_handle(DEC_ERR_ARG, "layer %d out of range", layer);
-  if (type != DEC_IO_F32 && type != DEC_IO_BF16) return fail_no_handle(DEC_ERR_ARG, "unknown type %d", type);
-  if (n < 0 || (!seqs && n > c->n_seqs))
-    return fail_no_handle(DEC_ERR_ARG, "%d rows (without a list, one per sequence at most)", n);
-  if (n == 0) return DEC_OK;
+              const int32_t* seqs, const int32_t* positions, int n, const RopeRows* q, dec_stream_t stream) {
   if (!k || !v) return fail_no_handle(DEC_ERR_ARG, "k or v is NULL");
   const int64_t size = type == DEC_IO_F32 ? 4 : 2, width = (int64_t)c->n_kv_heads * c->head_dim;
   if (row_stride < width || row_stride > (int64_t)1 << 40)
@@ -371,22 +364,34 @@ int rows_call(const dec_kv_cache* c, int layer, void* k, void* v, int type, int6
   if (READ && kv_rows_overlap(reinterpret_cast<uintptr_t>(k), row_stride * size, reinterpret_cast<uintptr_t>(v),
                               row_stride * size, width * size, n))
     return fail_no_handle(DEC_ERR_ARG, "k overlaps v");
+  if (q && q->n) {
+    const uintptr_t out = reinterpret_cast<uintptr_t>(q->out);
+    for (const void* x : {k, v})
+      if (kv_rows_overlap(out, q->out_stride * size, (int64_t)q->heads * q->d * size, reinterpret_cast<uintptr_t>(x),
+                          row_stride * size, width * size, n))
+        return fail_no_handle(DEC_ERR_ARG, "q_out overlaps k or v");
+  }
   const KvView view = kv_view(*c, layer);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool f32 = type == DEC_IO_F32;
   cudaError_t e;
-  const bool q4 = c->format == DEC_KV_Q4B32, f32 = type == DEC_IO_F32;
-#define TLD_ROWS(D, Q)                                                                                  \
-  e = f32 ? launch_rows<D, Q, float, READ>(view, k, v, row_stride, seqs, positions, n, s)               \
-          : launch_rows<D, Q, uint16_t, READ>(view, k, v, row_stride, seqs, positions, n, s)
-  if (c->head_dim == 128) {
-    if (q4) TLD_ROWS(128, true);
-    else TLD_ROWS(128, false);
-  } else {
-    if (q4) TLD_ROWS(64, true);
-    else TLD_ROWS(64, false);
-  }
+#define TLD_ROWS(D)                                                                                               \
+  e = f32 ? launch_format<D, float, READ>(c->format, view, k, v, row_stride, seqs, positions, n, q, s)            \
+          : launch_format<D, uint16_t, READ>(c->format, view, k, v, row_stride, seqs, positions, n, q, s)
+  if (c->head_dim == 128) TLD_ROWS(128);
+  else TLD_ROWS(64);
 #undef TLD_ROWS
   if (e != cudaSuccess) return fail_no_handle(DEC_ERR_CUDA, "row kernel launch: %s", cudaGetErrorString(e));
+  return DEC_OK;
+}
+
+// What every call on rows checks first.
+int rows_check(const dec_kv_cache* c, int layer, int type, const int32_t* seqs, int n) {
+  if (int rc = kv_check(c, true)) return rc;
+  if (layer < 0 || layer >= c->n_layers) return fail_no_handle(DEC_ERR_ARG, "layer %d out of range", layer);
+  if (type != DEC_IO_F32 && type != DEC_IO_BF16) return fail_no_handle(DEC_ERR_ARG, "unknown type %d", type);
+  if (n < 0 || (!seqs && n > c->n_seqs))
+    return fail_no_handle(DEC_ERR_ARG, "%d rows (without a list, one per sequence at most)", n);
   return DEC_OK;
 }
 
@@ -395,20 +400,47 @@ int rows_call(const dec_kv_cache* c, int layer, void* k, void* v, int type, int6
 extern "C" int dec_kv_sizes(const dec_kv_cache* c, size_t* page_bytes, size_t* scratch_ints) {
   if (int rc = kv_check(c, false)) return rc;
   if (page_bytes) *page_bytes = (size_t)kv_view(*c, 0).page_bytes;
-  if (scratch_ints) *scratch_ints = (size_t)kv_scratch_ints(c->n_pages, c->n_seqs);
+  if (scratch_ints) {
+    *scratch_ints = (size_t)kv_scratch_ints(c->n_pages, c->n_seqs);
+    if (c->format == DEC_KV_Q8T16) *scratch_ints += (size_t)c->n_layers * c->n_pages * c->page_rows;
+  }
   return DEC_OK;
 }
 
 extern "C" int dec_kv_append(const dec_kv_cache* c, int layer, const void* k, const void* v, int type,
                              int64_t row_stride, const int32_t* seqs, const int32_t* positions, int n,
                              dec_stream_t stream) {
+  if (int rc = rows_check(c, layer, type, seqs, n)) return rc;
+  if (n == 0) return DEC_OK;
   return rows_call<false>(c, layer, const_cast<void*>(k), const_cast<void*>(v), type, row_stride, seqs, positions, n,
-                          stream);
+                          nullptr, stream);
 }
 
 extern "C" int dec_kv_read(const dec_kv_cache* c, int layer, void* k, void* v, int type, int64_t row_stride,
                            const int32_t* seqs, const int32_t* positions, int n, dec_stream_t stream) {
-  return rows_call<true>(c, layer, k, v, type, row_stride, seqs, positions, n, stream);
+  if (int rc = rows_check(c, layer, type, seqs, n)) return rc;
+  if (n == 0) return DEC_OK;
+  return rows_call<true>(c, layer, k, v, type, row_stride, seqs, positions, n, nullptr, stream);
+}
+
+extern "C" int dec_kv_append_rotated(const dec_kv_cache* c, int layer, const dec_rope* rope, const void* q, void* q_out,
+                                     int64_t q_stride, int64_t q_out_stride, int n_q_heads, const void* k, const void* v,
+                                     int type, int64_t row_stride, const int32_t* seqs, const int32_t* positions, int n,
+                                     dec_stream_t stream) {
+  if (int rc = rows_check(c, layer, type, seqs, n)) return rc;
+  if (int rc = rope_check(rope)) return rc;
+  if (rope->head_dim != c->head_dim)
+    return fail_no_handle(DEC_ERR_SHAPE, "a rotation of head_dim %d for a cache of %d", rope->head_dim, c->head_dim);
+  if (n_q_heads < 0 || n_q_heads > 65536 || (int64_t)n * n_q_heads > (int64_t)1 << 30)
+    return fail_no_handle(DEC_ERR_SHAPE, "%d rows of %d query heads (0..65536, and at most 2^30 in all)", n, n_q_heads);
+  if (n == 0) return DEC_OK;
+  RopeRows rows{};
+  rows.r = rope_view(*rope, false);
+  if (n_q_heads) {
+    if (int rc = rope_rows_check(rope, q, q_out, type, q_stride, q_out_stride, n, n_q_heads, false, &rows)) return rc;
+  }
+  return rows_call<false>(c, layer, const_cast<void*>(k), const_cast<void*>(v), type, row_stride, seqs, positions, n,
+                          &rows, stream);
 }
 
 extern "C" int dec_kv_status(const dec_kv_cache* c, int* bits, dec_stream_t stream) {

@@ -1,0 +1,190 @@
+// Rotary positions: the angles of a row and its rotation, for the kernels that
+// rotate rows and those that write rotated keys into a paged cache.
+#pragma once
+#include <stdint.h>
+
+#include "../../include/dec.h"
+#include "rows.cuh"
+
+namespace tld {
+
+// A rotation, as a kernel argument.
+struct RopeView {
+  const uint64_t* steps;  // [rot / 2], turns per position in 2^-64
+  int rot;                // dimensions turned
+  int pairs;              // pairs (2 i, 2 i + 1), else (i, i + rot / 2)
+  float magnitude;
+  float sign;             // of the sine: -1 backward
+};
+
+// cos and sin of pair i at a position, times the magnitude.  position * step modulo
+// 2^64 is the angle in turns, exactly; its upper half is a signed number of half turns
+// in [-1, 1), which sincospi takes without a reduction.  What its rounding to fp32
+// leaves, an angle e of 2^-25 of half a turn at most, comes on by cos(x + e) = cos x - e
+// sin x and sin(x + e) = sin x + e cos x (to e^2 / 2 < 2^-47): without it the results
+// of rotations are 1.6 times as far off.
+__device__ __forceinline__ float2 rope_angle(const RopeView& r, int position, int i) {
+  const int turn = (int)((uint64_t)(uint32_t)position * r.steps[i] >> 32);
+  const float x = (float)turn;
+  const float e = (float)(turn - __float2int_rz(x)) * 1.4629180792671596e-9f * r.magnitude;  // (2 pi / 2^32)
+  float s, c;
+  sincospif(x * 4.656612873077393e-10f, &s, &c);
+  return make_float2(fmaf(c, r.magnitude, -s * e), fmaf(s, r.magnitude, c * e) * r.sign);
+}
+
+// (a, b) turned.
+__device__ __forceinline__ void rope_turn(float& a, float& b, float c, float s) {
+  const float x = a;
+  a = fmaf(x, c, -b * s);
+  b = fmaf(b, c, x * s);
+}
+
+// Rows to be rotated, [n][heads][d] of T.  A CTA takes `tokens` rows and, of these,
+// `heads_per` heads.
+struct RopeRows {
+  RopeView r;
+  const void* x;
+  void* out;
+  int64_t x_stride, out_stride;
+  int n, heads, d;
+  int tokens, heads_per, splits;  // splits: CTAs that share the heads of a row
+  int in_place;                   // the dimensions that stay need not be copied
+};
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 32;           // of a CTA, at most
+constexpr int kRopeSmem = 32 * 1024;      // its cosines and sines, at most
+
+constexpr int max_int(int a, int b) { return a > b ? a : b; }
+
+// How a launch cuts the rows; the CTAs that it takes.
+inline int rope_cut(RopeRows& p) {
+  const int items = max_int(1, p.heads * p.d / 16);  // (about: of 16 values)
+  p.tokens = 1;
+  while (p.tokens < kRopeTokens && 2 * p.tokens * items <= kRopeThreads && p.tokens * p.r.rot * 8 <= kRopeSmem) p.tokens *= 2;
+  p.splits = p.tokens == 1 ? (items + 2 * kRopeThreads - 1) / (2 * kRopeThreads) : 1;
+  p.heads_per = (p.heads + p.splits - 1) / p.splits;
+  p.splits = (p.heads + p.heads_per - 1) / p.heads_per;
+  return (p.n + p.tokens - 1) / p.tokens * p.splits;
+}
+inline size_t rope_smem(const RopeRows& p) { return (size_t)p.tokens * p.r.rot * sizeof(float); }
+
+// Block `block` of rope_cut's.  position(t): of row t, negative to skip it.  smem:
+// rope_smem bytes.
+template <class T, class Position>
+__device__ __forceinline__ void rope_rows(const RopeRows& p, int block, float* smem, Position position) {
+  __shared__ int at[kRopeTokens];
+  const int tid = threadIdx.x, half = p.r.rot / 2;
+  const int64_t t0 = (int64_t)(block / p.splits) * p.tokens;
+  const int h0 = block % p.splits * p.heads_per, heads = min(p.heads_per, p.heads - h0);
+  if (tid < p.tokens) at[tid] = t0 + tid < p.n ? position(t0 + tid) : -1;
+  __syncthreads();
+  float* sines = smem + p.tokens * half;
+  for (int e = tid; e < p.tokens * half; e += kRopeThreads) {
+    const int t = e / half;
+    if (at[t] < 0) continue;
+    const float2 y = rope_angle(p.r, at[t], e - t * half);
+    smem[e] = y.x, sines[e] = y.y;
+  }
+  __syncthreads();
+  const T* x = static_cast<const T*>(p.x) + h0 * (int64_t)p.d;
+  T* out = static_cast<T*>(p.out) + h0 * (int64_t)p.d;
+  const bool wide = ((reinterpret_cast<uintptr_t>(out) | p.out_stride * sizeof(T)) & 31) == 0 && p.d % 8 == 0;
+  if (p.r.pairs || p.r.rot % 16 == 0) {
+    // eight values of a lane, and their partners (or the next eight)
+    const int stay = p.in_place ? 0 : p.d - p.r.rot;
+    const int turned = p.r.pairs ? (p.r.rot + 7) / 8 : p.r.rot / 16;
+    const int per_head = p.r.pairs ? (p.in_place ? turned : p.d / 8) : turned + stay / 8;
+    for (int e = tid; e < p.tokens * heads * per_head; e += kRopeThreads) {
+      const int row = e / per_head, c = e - row * per_head, t = row / heads, h = row - t * heads;
+      if (at[t] < 0) continue;
+      const T* from = x + (t0 + t) * p.x_stride + h * p.d;
+      T* to = out + (t0 + t) * p.out_stride + h * p.d;
+      const float *cs = smem + t * half, *sn = sines + t * half;
+      Eight<T> in;
+      float a[8];
+      if (p.r.pairs) {
+        in.load(from + 8 * c);
+        in.values(a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * c + i < half) rope_turn(a[2 * i], a[2 * i + 1], cs[4 * c + i], sn[4 * c + i]);
+        store8(to + 8 * c, a, wide);
+      } else if (c < turned) {
+        Eight<T> partner;
+        float b[8];
+        in.load(from + 8 * c);
+        partner.load(from + half + 8 * c);
+        in.values(a);
+        partner.values(b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rope_turn(a[i], b[i], cs[8 * c + i], sn[8 * c + i]);
+        store8(to + 8 * c, a, wide);
+        store8(to + half + 8 * c, b, wide);
+      } else {
+        const int e0 = p.r.rot + 8 * (c - turned);
+        in.load(from + e0);
+        in.values(a);
+        store8(to + e0, a, wide);
+      }
+    }
+  } else {  // partners that lie in no eight of their own: a pair, or a value that stays, each
+    const int per_head = half + (p.in_place ? 0 : p.d - p.r.rot);
+    for (int e = tid; e < p.tokens * heads * per_head; e += kRopeThreads) {
+      const int row = e / per_head, i = e - row * per_head, t = row / heads, h = row - t * heads;
+      if (at[t] < 0) continue;
+      const T* from = x + (t0 + t) * p.x_stride + h * p.d;
+      T* to = out + (t0 + t) * p.out_stride + h * p.d;
+      if (i < half) {
+        float a = value_of(from[i]), b = value_of(from[i + half]);
+        rope_turn(a, b, smem[t * half + i], sines[t * half + i]);
+        put(to[i], a), put(to[i + half], b);
+      } else {
+        to[i + half] = from[i + half];
+      }
+    }
+  }
+}
+
+// Eight dimensions 8 l .. of a key, which the lanes of a row hold, turned; `cs` and `sn`
+// are of its position, `row` where the key was read from.  Every lane of the warp takes part;
+// lanes that do not `turn` keep what they have.
+template <int LANES, class T>
+__device__ __forceinline__ void rope_eight(const RopeView& r, float (&x)[8], int l, const float* cs, const float* sn,
+                                           const T* row, bool turn) {
+  const int half = r.rot / 2;
+  if (r.pairs) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (turn && 4 * l + i < half) rope_turn(x[2 * i], x[2 * i + 1], cs[4 * l + i], sn[4 * l + i]);
+  } else if (half % 8 == 0) {
+    const int far = half / 8;
+    const bool low = l < far, in = turn && l < 2 * far;
+    const int lane = threadIdx.x & 31, from = low ? lane + far : l < 2 * far ? lane - far : lane;
+    const int at = 8 * (low ? l : l - far);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_sync(0xffffffffu, x[i], from);
+      if (in) {
+        const float c = cs[at + i], s = low ? -sn[at + i] : sn[at + i];
+        x[i] = fmaf(x[i], c, other * s);
+      }
+    }
+  } else if (turn) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = 8 * l + i;
+      if (e < half) x[i] = fmaf(x[i], cs[e], -value_of(row[e + half]) * sn[e]);
+      else if (e < r.rot) x[i] = fmaf(x[i], cs[e - half], value_of(row[e - half]) * sn[e - half]);
+    }
+  }
+}
+
+// Checks a rotation; DEC_OK or the error, recorded.
+int rope_check(const dec_rope* r) noexcept;
+RopeView rope_view(const dec_rope& r, bool backward);
+// Checks rows to be rotated and fills in *p.
+int rope_rows_check(const dec_rope* r, const void* x, void* out, int type, int64_t x_stride, int64_t out_stride, int n,
+                    int n_heads, bool backward, RopeRows* p) noexcept;
+
+}  // namespace tld

@@ -43,7 +43,8 @@ EXPORTED = ("dec_create", "dec_load_weights", "dec_load_kv", "dec_read_kv", "dec
             "dec_destroy", "dec_last_error", "dec_attention_noalloc",
             "dec_kv_sizes", "dec_kv_append", "dec_kv_read", "dec_kv_attention",
             "dec_kv_attention_workspace", "dec_kv_extend", "dec_kv_fork", "dec_kv_release",
-            "dec_kv_compact", "dec_kv_status")
+            "dec_kv_compact", "dec_kv_status",
+            "dec_rope_frequencies", "dec_rope_steps", "dec_rope_rotate", "dec_kv_append_rotated")
 
 
 class DecError(RuntimeError):
@@ -83,7 +84,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "(run transformer_layer_decode_gb300.build.build())")
     L = ctypes.CDLL(path)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-    i64, f32 = ctypes.c_int64, ctypes.c_float
+    i64, f32, f64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
     sig = {
         "dec_create": [ctypes.POINTER(ModelDesc), ctypes.POINTER(vp)],
         "dec_load_weights": [vp, i32, i32, vp, sz],
@@ -114,6 +115,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dec_kv_release": [vp, vp, i32, i32, i32, vp],
         "dec_kv_compact": [vp, vp],
         "dec_kv_status": [vp, vp, vp],
+        # rotary positions (bound in rope.py and kv.py)
+        "dec_rope_frequencies": [i32, f64, i32, f64, f64, f64, f64, vp, vp],
+        "dec_rope_steps": [vp, i32, vp],
+        "dec_rope_rotate": [vp, vp, vp, i32, i64, i64, vp, i32, i32, i32, vp],
+        "dec_kv_append_rotated": [vp, i32, vp, vp, vp, i64, i64, i32, vp, vp, i32, i64, vp, vp, i32, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)

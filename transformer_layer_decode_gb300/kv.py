@@ -1,9 +1,9 @@
 """A paged key/value cache of many sequences (the dec_kv_ calls of include/dec.h).
 
 :class:`KVCache` holds the tensors of one cache and marshals the calls: rows
-written and read (bf16 or 4-bit blocks), attention of one query per sequence
-with a sliding window and first rows that stay visible, and pages allocated,
-shared, freed and made dense.  Every call is queued on a stream and waits for
+written and read (bf16, 8-bit or 4-bit blocks; keys rotated on the way), attention
+of one query per sequence with a sliding window and first rows that stay visible,
+and pages allocated, shared, freed and made dense.  Every call is queued on a stream and waits for
 nothing; :meth:`KVCache.sync_status` reports what the kernels refused.
 """
 from __future__ import annotations
@@ -15,11 +15,11 @@ import torch
 
 from . import dec
 
-DEC_KV_BF16, DEC_KV_Q4B32 = 0, 1
+DEC_KV_BF16, DEC_KV_Q4B32, DEC_KV_Q8T16 = 0, 1, 3
 DEC_IO_F32, DEC_IO_BF16 = 0, 1
 DEC_KV_BAD_INDEX, DEC_KV_NO_PAGES, DEC_KV_BAD_LIST, DEC_KV_BAD_BOUNDS = 1, 2, 4, 8
 
-FORMATS = {"bf16": DEC_KV_BF16, "q4": DEC_KV_Q4B32}
+FORMATS = {"bf16": DEC_KV_BF16, "q4": DEC_KV_Q4B32, "q8": DEC_KV_Q8T16}
 _TYPES = {torch.float32: DEC_IO_F32, torch.bfloat16: DEC_IO_BF16}
 
 # what torch.cuda.current_stream(), current_device() and is_current_stream_capturing() ask, without their
@@ -59,7 +59,7 @@ class KVCache:
     """One cache: a pool of pages for every layer, and the tables of its sequences.
 
     n_layers, n_kv_heads, head_dim (64 or 128), page_rows (a multiple of 16)
-    and fmt ("bf16" or "q4") fix the shape of a page.  The tensors are made
+    and fmt ("bf16", "q8" or "q4") fix the shape of a page.  The tensors are made
     empty here from n_pages, n_seqs and max_pages (pages of one sequence), or
     taken as they are: pool uint8 [n_layers, n_pages, page_bytes], table int32
     [n_seqs, max_pages], lens int32 [n_seqs], refs int32 [n_pages].
@@ -191,7 +191,8 @@ class KVCache:
 
     def append(self, layer: int, k, v, *, seqs=None, positions=None, stream=None):
         """Writes row t of k and v ([n, n_kv_heads, head_dim], keys already rotated) as row positions[t]
-        of sequence seqs[t]; without positions, as the sequence's last row; without seqs, of sequence t."""
+        of sequence seqs[t]; without positions, as the sequence's last row; without seqs, of sequence t.
+        8-bit pages: rows of a block of 16 behind the first that is written, and not written, are given up."""
         if not 0 <= layer < _LARGE:
             _int32(layer=layer)
         kp, kt, ks = self._rows("k", k, self.desc.n_kv_heads)
@@ -221,6 +222,36 @@ class KVCache:
             raise ValueError(f"k_out and v_out: the same type and row stride and {n} rows are wanted")
         self._call(self.lib.dec_kv_read, layer, kp, vp, kt, ks, sp, pp, n, stream=stream)
         return k_out, v_out
+
+    def append_rotated(self, layer: int, rotary, q, k, v, *, seqs=None, positions=None, q_out=None, stream=None):
+        """append() of keys that `rotary` (rope.Rotary) has yet to rotate, each by its position, and row t of
+        q ([n, n_q_heads, head_dim]; None: no queries) rotated the same way: returns q_out, which may be q.
+        Rows of skipped entries keep what q_out holds (zeros where it is made here)."""
+        if not 0 <= layer < _LARGE:
+            _int32(layer=layer)
+        if rotary.device != self.device:
+            raise ValueError(f"rotary: a rotation on {self.device} is wanted, not on {rotary.device}")
+        kp, kt, ks = self._rows("k", k, self.desc.n_kv_heads)
+        vp, vt, vs = self._rows("v", v, self.desc.n_kv_heads)
+        if k.shape[0] != v.shape[0] or kt != vt or ks != vs:
+            raise ValueError("k and v: the same type, rows and row stride are wanted")
+        n = k.shape[0]
+        qp, op, qs, os_, heads = None, None, 0, 0, 0
+        if q is not None:
+            qp, qt, qs = self._rows("q", q)
+            heads = q.shape[1]
+            if q_out is None:
+                q_out = self._new(torch.zeros, q.shape, q.dtype, stream)
+            op, ot, os_ = self._rows("q_out", q_out, heads)
+            if qt != kt or ot != kt or q.shape[0] != n or q_out.shape[0] != n:
+                raise ValueError("q and q_out: the type and rows of k are wanted")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        sp, _ = self._ints("seqs", seqs, n)
+        pp, _ = self._ints("positions", positions, n)
+        self._call(self.lib.dec_kv_append_rotated, layer, rotary._ref, qp, op, qs, os_, heads, kp, vp, kt, ks, sp, pp, n,
+                   stream=stream)
+        return q_out
 
     # ---- attention ------------------------------------------------------------
 
