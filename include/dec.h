@@ -530,7 +530,7 @@ int dec_rope_steps(const double* frequency, int n, uint64_t* steps);
 /* Source: none on the pages.  Rotates rows: x and out are [n][n_heads][head_dim] of
  * `type` (fp32 inside, rounded once), rows x_stride and out_stride elements apart,
  * row t by positions[t] (device; NULL: by t).  A row with a negative position is
- * skipped: neither read nor written.  backward: by minus the angle, which
+ * skipped: its result is left as it was.  backward: by minus the angle, which
  * is the gradient of a rotation (and, where the magnitude is 1, its inverse).  out
  * may be x with the same stride; other overlaps are refused.  x, out and their
  * strides are multiples of 16 bytes, n_heads is 1..65536 and n * n_heads at most

@@ -1,6 +1,7 @@
 // Rows written into 8-bit pages: dec_kv_append and dec_kv_append_rotated of caches
 // whose blocks of 16 rows of a head share a scale.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv.h"
@@ -11,20 +12,18 @@ using namespace tld;
 
 namespace {
 
-constexpr int kWarps8 = 8;
-constexpr int kThreads8 = kWarps8 * 32;
-constexpr int kTokens8 = 16;     // list entries of a CTA, at most
+constexpr int kThreads8 = 256;
+constexpr int kTokens8 = 16;     // list entries of a CTA of write_blocks, at most
 static_assert(kTokens8 * kBlockRows == kThreads8, "a thread for each row of each entry's block");
 constexpr int kListed = 512;     // lists up to this length are looked through by every CTA
+constexpr int kBlockCtas = 1216;  // of write_blocks, where the heads are enough for them
 constexpr uint32_t kLeastScale = 1u << 23, kMostScale = 248u << 23;  // 2^-126, 2^121
 
-// How a CTA finds which list entries write rows of one block.
-enum Find { FIND_ALONE, FIND_LIST, FIND_OWNERS };
-
-// The entry that writes each row: owners[page][row], for kv_write8's CTAs.  (What
+// The entry that writes each row: owners[page][row], for write_blocks' CTAs.  (What
 // other calls left there is told apart by looking the entry up in the list.)
 __global__ void __launch_bounds__(256) kv_owners(const __grid_constant__ KvView c, const int32_t* seqs,
                                                  const int32_t* positions, int n) {
+  pdl_trigger();
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const KvPlace at = kv_place(c, seqs, positions, t, n);
   if (at.page) c.owners[(at.page - c.pool) / c.page_bytes * c.page_rows + at.row] = (int)t;
@@ -47,207 +46,493 @@ __device__ __forceinline__ uint32_t four_bytes(float m0, float m1, float m2, flo
                      __byte_perm(__float_as_uint(m2), __float_as_uint(m3), 0x0040), 0x5410);
 }
 
-// A warp's block: rows `of` (list entries, or -1) of one head of K or V, the first of
-// them `first`.
-template <int D, class T, bool TURN>
-__device__ __forceinline__ void write_block(const KvView& c, const T* x, int64_t stride, int64_t head_at, const int* of,
-                                            int first, uint8_t* codes, uint32_t* scale_at, const RopeView& rope,
-                                            const float* cs, const float* sn) {
-  constexpr int LANES = D / 8, RPR = 32 / LANES, ROUNDS = kBlockRows / RPR;
-  const int lane = threadIdx.x & 31, l = lane % LANES, r0 = lane / LANES;
-  using In = std::conditional_t<TURN, float, T>;
-  Eight<In> in[ROUNDS];
-  uint32_t live = 0;  // rounds that have a row
-  const uint32_t was = first ? *scale_at & 0x7f800000u : 0;
-#pragma unroll
-  for (int i = 0; i < ROUNDS; ++i) {
-    const int t = of[i * RPR + r0];
-    if (!__any_sync(0xffffffffu, t >= 0)) continue;
-    live |= 1u << i;
-    const T* row = x + max(t, 0) * stride + head_at;
-    Eight<T> y{};
-    if (t >= 0) y.load(row + 8 * l);
+// Eight values of a row, at dimension 8 l of a head: as loaded, with (TURN) those that
+// they are turned with, if these are an aligned eight too.
+template <class T, bool TURN>
+struct Piece {
+  Eight<T> own, partner;
+  __device__ __forceinline__ void load(const T* row, int l, const RopeView& r) {
+    own.load(row + 8 * l);
     if constexpr (TURN) {
-      float v[8];
-      y.values(v);
-      const int at = (i * RPR + r0) * (D / 2);
-      rope_eight<LANES>(rope, v, l, cs + at, sn + at, row, t >= 0);
-      in[i].set(v);
-    } else {
-      in[i] = y;
+      const int half = r.rot / 2;
+      if (!r.pairs && half % 8 == 0 && 8 * l < r.rot) partner.load(row + (8 * l < half ? 8 * l + half : 8 * l - half));
     }
   }
-  float top = 0.f;
+};
+
+// Eight values at dimension 8 l, turned by the angles of their row (see rope.cuh), where
+// their partners are among them or lie in no aligned eight of `row`.
+template <class T>
+__device__ __forceinline__ void turn_alone(float (&x)[8], const T* row, int l, const RopeView& r, const float* cs,
+                                           const float* sn) {
+  const int half = r.rot / 2;
 #pragma unroll
-  for (int i = 0; i < ROUNDS; ++i)
-    if (live >> i & 1) top = largest(top, in[i].top_here(), 0.f);
-  uint32_t s = scale_for(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-  if (first) s = max(s, was == 0x7f800000u ? 0x7fffffffu : was);
-  const Two inv(inverse(s)), magic(kMagic + 128.f);
-  if (first && s != was && s < 0x7f800000u) {  // the kept rows, to the new steps
-    constexpr int PER_ROW = D / 16, AT_ONCE = 32 / PER_ROW;
-    const float ratio = __uint_as_float(was) * inverse(s);
+  for (int i = 0; i < 4; ++i)
+    if (r.pairs && 4 * l + i < half) rope_turn(x[2 * i], x[2 * i + 1], cs[4 * l + i], sn[4 * l + i]);
+  if (r.pairs) return;
 #pragma unroll
-    for (int i = 0; i < kBlockRows / AT_ONCE; ++i) {
-      const int r = i * AT_ONCE + lane / PER_ROW;
-      if (r >= first) continue;
-      uint4* at = reinterpret_cast<uint4*>(codes + r * D) + lane % PER_ROW;
-      const uint4 old = *at;
-      auto fewer = [&](uint32_t w) {
-        float m[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          m[k] = fmaf((float)((int)(w >> (8 * k) & 255) - 128), ratio, kMagic + 128.f);
-        return four_bytes(m[0], m[1], m[2], m[3]);
-      };
-      *at = make_uint4(fewer(old.x), fewer(old.y), fewer(old.z), fewer(old.w));
-    }
+  for (int i = 0; i < 8; ++i) {
+    const int e = 8 * l + i;
+    if (e < half) x[i] = fmaf(x[i], cs[e], -value_of(row[e + half]) * sn[e]);
+    else if (e < r.rot) x[i] = fmaf(x[i], cs[e - half], value_of(row[e - half]) * sn[e - half]);
   }
-#pragma unroll
-  for (int i = 0; i < ROUNDS; ++i) {
-    if (!(live >> i & 1)) continue;
-    float v[8];
-    in[i].values(v);
-    if (s == kMostScale) {  // (which may be too small)
-      const float most = 127.f * __uint_as_float(kMostScale);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = fminf(fmaxf(v[k], -most), most);
-    }
-    float2 m[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) m[k] = fma2(Two(v[2 * k], v[2 * k + 1]), inv, magic).get();
-    const int r = i * RPR + r0;
-    if (of[r] >= 0)
-      reinterpret_cast<uint2*>(codes + r * D)[l] =
-          make_uint2(four_bytes(m[0].x, m[0].y, m[1].x, m[1].y), four_bytes(m[2].x, m[2].y, m[3].x, m[3].y));
-  }
-  if (lane == 0) *scale_at = s;
 }
 
-// A CTA takes `tokens` list entries and finds, for each, the entries that write rows of
-// the same block; the entry of a block's lowest row has the block written, its heads of
-// K and V a warp each.  `splits` CTAs share the heads.  ROPE: keys are rotated on the
-// way, in fp32, and the CTAs from `blocks` on rotate queries.
+// A piece's fp32 values, turned.
+template <class T>
+__device__ __forceinline__ void turned(const Piece<T, true>& p, float (&x)[8], const T* row, int l, const RopeView& r,
+                                       const float* cs, const float* sn) {
+  const int half = r.rot / 2;
+  p.own.values(x);
+  if (r.pairs || half % 8) {
+    turn_alone(x, row, l, r, cs, sn);
+  } else if (8 * l < r.rot) {
+    const bool low = 8 * l < half;
+    const int at = low ? 8 * l : 8 * l - half;
+    float y[8];
+    p.partner.values(y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[at + i], y[i] * (low ? -sn[at + i] : sn[at + i]));
+  }
+}
+
+// For the largest scale, which may be too small.
+__device__ __forceinline__ void clamp8(float (&x)[8], uint32_t s) {
+  if (s != kMostScale) return;
+  const float most = 127.f * __uint_as_float(kMostScale);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = fminf(fmaxf(x[k], -most), most);
+}
+
+// The codes of eight values for the scale s.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], uint32_t s) {
+  const Two inv(inverse(s)), magic(kMagic + 128.f);
+  float2 m[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m[k] = fma2(Two(x[2 * k], x[2 * k + 1]), inv, magic).get();
+  return make_uint2(four_bytes(m[0].x, m[0].y, m[1].x, m[1].y), four_bytes(m[2].x, m[2].y, m[3].x, m[3].y));
+}
+
+// Eight kept codes, whose scale becomes 1 / ratio of what it was.
+__device__ __forceinline__ uint2 fewer8(uint2 w, float ratio) {
+  auto four = [&](uint32_t u) {
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmaf((float)((int)(u >> (8 * k) & 255) - 128), ratio, kMagic + 128.f);
+    return four_bytes(m[0], m[1], m[2], m[3]);
+  };
+  return make_uint2(four(w.x), four(w.y));
+}
+
+// A block's new scale from the largest magnitude written and, where rows are kept, what
+// it was; a NaN stays.
+__device__ __forceinline__ uint32_t new_scale(uint32_t top, uint32_t was, bool keeps) {
+  const uint32_t s = scale_for(top);
+  return keeps ? max(s, was == 0x7f800000u ? 0x7fffffffu : was) : s;
+}
+
+// The place of a block's scale in its page, and of its codes.
+struct Block8 {
+  uint8_t* codes;
+  uint32_t* scale;
+};
+template <int D>
+__device__ __forceinline__ Block8 block_at(const KvView& c, uint8_t* page, int item, int row0) {
+  const int which = item >= c.nkv, head = item - which * c.nkv;
+  uint8_t* half = page + which * c.half_bytes;
+  return Block8{half + head * c.head_bytes + row0 * D,
+                reinterpret_cast<uint32_t*>(half + c.nkv * c.head_bytes) + head * (c.page_rows / kBlockRows) +
+                    row0 / kBlockRows};
+}
+__device__ __forceinline__ bool block_fits(const KvView& c, const uint8_t* page, int row0) {
+  return KV_IN_BOUNDS(c, page >= c.pool && page + c.page_bytes <= c.pool + c.n_pages * c.page_bytes && row0 >= 0 &&
+                             row0 % kBlockRows == 0 && row0 + kBlockRows <= c.page_rows &&
+                             c.nkv * c.head_bytes < c.half_bytes);
+}
+
+// What both kernels are given.
+template <class T>
+struct Write8 {
+  KvView c;
+  const T *k, *v;
+  int64_t stride;
+  const int32_t *seqs, *positions;
+  int n;
+  int blocks;  // CTAs that write; those from there on rotate queries
+  RopeRows q;  // and the rotation of keys
+};
+
+// A row of its own block for each list entry (a decode step): D / 8 lanes take a row of a
+// head, of K or V.
 template <int D, class T, bool ROPE>
-__global__ void __launch_bounds__(kThreads8) write8(const __grid_constant__ KvView c, const T* k, const T* v, int64_t stride,
-                                                    const int32_t* seqs, const int32_t* positions, int n, int tokens,
-                                                    int splits, Find find, int blocks, const __grid_constant__ RopeRows q) {
+__global__ void __launch_bounds__(kThreads8) write_rows(const __grid_constant__ Write8<T> p) {
+  constexpr int LANES = D / 8, ITEMS = kThreads8 / LANES;
   extern __shared__ __align__(16) float q_angles[];
-  __shared__ KvPlace place[kTokens8];
-  __shared__ int of[kTokens8][kBlockRows];
-  __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? kBlockRows * (D / 2) : 1];
+  __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? (ITEMS / 2 + 1) * (D / 2) : 1];
+  const KvView& c = p.c;
   if constexpr (ROPE) {
-    if ((int)blockIdx.x >= blocks) {
-      rope_rows<T>(q, blockIdx.x - blocks, q_angles, [&](int64_t t) {
-        const KvPlace at = kv_place(c, seqs, positions, t, n);
+    if ((int)blockIdx.x >= p.blocks) {
+      rope_rows<T>(p.q, blockIdx.x - p.blocks, q_angles, [&](int64_t t) {
+        const KvPlace at = kv_place(c, p.seqs, p.positions, t, p.n);
         return at.page ? at.pos : -1;
       });
       return;
     }
   }
-  const int tid = threadIdx.x, warp = tid >> 5, split = blockIdx.x % splits;
-  const int64_t t0 = (int64_t)(blockIdx.x / splits) * tokens;
-  if (tid < tokens) place[tid] = kv_place(c, seqs, positions, t0 + tid, n);
-  of[tid / kBlockRows][tid % kBlockRows] = -1;
-  if (find == FIND_OWNERS) pdl_wait();
-  __syncthreads();
-  if (find == FIND_ALONE) {
-    if (tid < tokens) of[tid][place[tid].row % kBlockRows] = (int)(t0 + tid);
-  } else if (find == FIND_LIST) {
-    for (int e = tid; e < n; e += kThreads8) {
-      const int s = seqs[e], pos = positions[e];
-      for (int a = 0; a < tokens; ++a)
-        if (place[a].page && place[a].seq == s && pos >= 0 && place[a].pos / kBlockRows == pos / kBlockRows)
-          atomicMax(&of[a][pos % kBlockRows], e);
+  const int tid = threadIdx.x, l = tid % LANES, items = 2 * c.nkv;
+  const int64_t id0 = (int64_t)blockIdx.x * ITEMS, id = id0 + tid / LANES, t = id / items;
+  const int item = (int)(id - t * items);
+  const bool is_key = item < c.nkv, real = t < p.n;
+  Piece<T, ROPE> in{};
+  const T* row = is_key ? p.k + t * p.stride + item * D : p.v + t * p.stride + (item - c.nkv) * D;
+  if (real) {
+    if (ROPE && is_key) in.load(row, l, p.q.r);
+    else in.own.load(row + 8 * l);
+  }
+  const KvPlace at = kv_place(c, p.seqs, p.positions, t, p.n);
+  const int r = at.row % kBlockRows, row0 = at.row - r;
+  const bool ok = at.page && block_fits(c, at.page, row0);
+  const Block8 b = block_at<D>(c, ok ? at.page : c.pool, item, ok ? row0 : 0);
+  const uint32_t was = ok && r ? *b.scale & 0x7f800000u : 0;
+  float x[8];
+  if constexpr (ROPE) {
+    const int half = p.q.r.rot / 2;
+    const int64_t first = id0 / items;
+    const int tokens = (int)min((id0 + ITEMS - 1) / items, (int64_t)p.n - 1) - (int)first + 1;
+    for (int e = tid; e < tokens * half; e += kThreads8) {
+      const int a = e / half, i = e - a * half;
+      const KvPlace of = kv_place(c, p.seqs, p.positions, first + a, p.n);
+      if (!of.page) continue;
+      const float2 y = rope_angle(p.q.r, of.pos, i);
+      angles[0][a * (D / 2) + i] = y.x, angles[1][a * (D / 2) + i] = y.y;
     }
+    __syncthreads();
+    const float* cs = angles[0] + (t - first) * (D / 2);
+    if (is_key && ok) turned<T>(in, x, row, l, p.q.r, cs, cs + (angles[1] - angles[0]));
+    else in.own.values(x);
   } else {
-    const int a = tid / kBlockRows, r = tid % kBlockRows;
-    if (a < tokens && place[a].page) {
-      const int at = place[a].row / kBlockRows * kBlockRows + r;
-      const int e = c.owners[(place[a].page - c.pool) / c.page_bytes * c.page_rows + at];
-      if (e >= 0 && e < n && seqs[e] == place[a].seq && positions[e] == place[a].pos / kBlockRows * kBlockRows + r)
-        of[a][r] = e;
+    in.own.values(x);
+  }
+  Eight<float> all;
+  all.set(x);
+  uint32_t top = __float_as_uint(all.top_here());
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (!ok) return;
+  const uint32_t s = new_scale(top, was, r != 0);
+  if (r && s != was && s < 0x7f800000u) {  // the kept rows, to the new steps
+    const float ratio = __uint_as_float(was) * inverse(s);
+#pragma unroll 5
+    for (int i = 0; i < kBlockRows - 1; ++i) {
+      if (i >= r) break;
+      uint2* old = reinterpret_cast<uint2*>(b.codes + i * D) + l;
+      *old = fewer8(*old, ratio);
     }
   }
+  clamp8(x, s);
+  reinterpret_cast<uint2*>(b.codes + r * D)[l] = codes8(x, s);
+  if (l == 0) *b.scale = s;
+}
+
+// How a row is turned: not at all; dimensions whose partners are an aligned eight of their
+// own; neighbours; dimensions whose partners lie anywhere.
+enum Turn { TURN_NONE, TURN_EIGHTS, TURN_PAIRS, TURN_ODD };
+
+// Where a lane's two eights of a row lie, of D / 16 lanes: 8 c and D / 2 + 8 c, or those
+// that turn with each other.
+template <int D, int TURN>
+struct Eights {
+  int at[2];
+  bool turns;  // with each other
+  __device__ __forceinline__ Eights(int c, const RopeView& r) {
+    at[0] = 8 * c, at[1] = D / 2 + 8 * c, turns = false;
+    const int half = r.rot / 2;
+    if (TURN != TURN_EIGHTS) return;
+    turns = 8 * c < half;
+    at[0] = turns ? 8 * c : r.rot + 16 * (c - half / 8);
+    at[1] = turns ? half + 8 * c : at[0] + 8;
+  }
+};
+
+// Four angles' cosines or sines, from pair i (a multiple of 4) of row r on, in tables
+// where the lanes of a row read whole lines: D / 16 lanes the first four of their eight,
+// then the second four.
+template <int D>
+__device__ __forceinline__ int angle_at(int r, int i) {
+  return r * (D / 2) + ((i >> 2 & 1) * (D / 16) + (i >> 3)) * 4 + (i & 3);
+}
+
+// One head's block, by a warp: rows `of` (list entries, or -1; smem), the first of them
+// `first`.  D / 16 lanes have a row, 512 / D rows at a time; lanes whose row is not
+// written load the first one, which leaves the largest magnitude what it is.
+template <int D, class T, int TURN>
+__device__ __forceinline__ void write_block(const T* x, int64_t stride, const int* of, int first,
+                                            const Block8& b, const RopeView& rope, const float* cs, const float* sn) {
+  constexpr int LANES = D / 16, RPR = 32 / LANES, ROUNDS = kBlockRows / RPR;
+  const int lane = threadIdx.x & 31, ci = lane % LANES, r0 = lane / LANES;
+  const Eights<D, TURN> e(ci, rope);
+  Eight<T> in[ROUNDS][2];
+  uint32_t written = 0;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int t = of[i * RPR + r0];
+    written |= (uint32_t)(t >= 0) << i;
+    const T* row = x + (t >= 0 ? t : of[first]) * stride;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) in[i][k].load(row + e.at[k]);
+  }
+  const uint32_t was = first ? *b.scale & 0x7f800000u : 0;
+  // Row i's two eights, turned.
+  auto values = [&](int i, float (&y)[2][8]) {
+    in[i][0].values(y[0]);
+    in[i][1].values(y[1]);
+    const int r = written >> i & 1 ? i * RPR + r0 : first;
+    if constexpr (TURN == TURN_EIGHTS) {
+      if (e.turns) {
+#pragma unroll
+        for (int q = 0; q < 8; q += 4) {
+          const float4 co = *reinterpret_cast<const float4*>(cs + angle_at<D>(r, 8 * ci + q));
+          const float4 si = *reinterpret_cast<const float4*>(sn + angle_at<D>(r, 8 * ci + q));
+          rope_turn(y[0][q], y[1][q], co.x, si.x);
+          rope_turn(y[0][q + 1], y[1][q + 1], co.y, si.y);
+          rope_turn(y[0][q + 2], y[1][q + 2], co.z, si.z);
+          rope_turn(y[0][q + 3], y[1][q + 3], co.w, si.w);
+        }
+      }
+    } else if constexpr (TURN == TURN_PAIRS) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+          const float4 co = *reinterpret_cast<const float4*>(cs + angle_at<D>(r, e.at[k] / 2));
+          const float4 si = *reinterpret_cast<const float4*>(sn + angle_at<D>(r, e.at[k] / 2));
+          if (e.at[k] < rope.rot) rope_turn(y[k][0], y[k][1], co.x, si.x);
+          if (e.at[k] + 2 < rope.rot) rope_turn(y[k][2], y[k][3], co.y, si.y);
+          if (e.at[k] + 4 < rope.rot) rope_turn(y[k][4], y[k][5], co.z, si.z);
+          if (e.at[k] + 6 < rope.rot) rope_turn(y[k][6], y[k][7], co.w, si.w);
+        }
+    } else if constexpr (TURN == TURN_ODD) {
+      const T* row = x + of[r] * stride;
+      const int half = rope.rot / 2;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int d = e.at[k] + j;
+          if (d >= rope.rot) continue;
+          const int pair = d < half ? d : d - half, at = angle_at<D>(r, pair & ~3) + (pair & 3);
+          const float other = value_of(row[d < half ? d + half : d - half]);
+          y[k][j] = fmaf(y[k][j], cs[at], d < half ? -other * sn[at] : other * sn[at]);
+        }
+    }
+  };
+  // (Turned for the scale and again for the codes, from half the registers, took longer:
+  // 4093 rows of 8 heads 17.3 us against 16.2.)
+  Eight<std::conditional_t<TURN != TURN_NONE, float, T>> have[ROUNDS][2];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    float y[2][8];
+    if constexpr (TURN != TURN_NONE) values(i, y);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (TURN != TURN_NONE) have[i][k].set(y[k]);
+      else have[i][k] = in[i][k];
+      top = largest(top, have[i][k].top_here(), 0.f);
+    }
+  }
+  const uint32_t s = new_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(top)), was, first != 0);
+  if (first && s != was && s < 0x7f800000u) {  // the kept rows, to the new steps
+    const float ratio = __uint_as_float(was) * inverse(s);
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      uint4* at = reinterpret_cast<uint4*>(b.codes + (i * RPR + r0) * D) + ci;
+      if (i * RPR + r0 < first) {
+        const uint4 w = *at;
+        const uint2 lo = fewer8(make_uint2(w.x, w.y), ratio), hi = fewer8(make_uint2(w.z, w.w), ratio);
+        *at = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    float y[2][8];
+    have[i][0].values(y[0]), have[i][1].values(y[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      clamp8(y[k], s);
+      if (written >> i & 1) *reinterpret_cast<uint2*>(b.codes + (i * RPR + r0) * D + e.at[k]) = codes8(y[k], s);
+    }
+  }
+  if (lane == 0) *b.scale = s;
+}
+
+// Rows of any list.  For `tokens` list entries a CTA finds the entries that write rows of
+// the same blocks; the entry of a block's lowest row has the block written, its heads of
+// K and V a warp each.  `splits` CTAs share the heads.
+template <int D, class T, bool ROPE>
+__global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
+    write_blocks(const __grid_constant__ Write8<T> p, int tokens, int splits, int per_split, bool listed) {
+  extern __shared__ __align__(16) float q_angles[];
+  __shared__ KvPlace place[kTokens8];
+  __shared__ int of[kTokens8][kBlockRows];
+  __shared__ int first_row[kTokens8];  // of a block that this entry has written, else -1
+  __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? kBlockRows * (D / 2) : 1];
+  const KvView& c = p.c;
+  pdl_trigger();
+  if constexpr (ROPE) {
+    if ((int)blockIdx.x >= p.blocks) {
+      rope_rows<T>(p.q, blockIdx.x - p.blocks, q_angles, [&](int64_t t) {
+        const KvPlace at = kv_place(c, p.seqs, p.positions, t, p.n);
+        return at.page ? at.pos : -1;
+      });
+      return;
+    }
+  }
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int chunk = blockIdx.x / splits, begin = (blockIdx.x - chunk * splits) * per_split;
+  const int end = min(begin + per_split, 2 * c.nkv);
+  const int64_t t0 = (int64_t)chunk * tokens;
+  const int a = tid / kBlockRows, ar = tid % kBlockRows;
+  if (tid < tokens) place[tid] = kv_place(c, p.seqs, p.positions, t0 + tid, p.n);
+  of[a][ar] = -1;
+  if (!listed) pdl_wait();
   __syncthreads();
-  const int items = 2 * c.nkv;
-  for (int a = 0; a < tokens; ++a) {
-    uint8_t* page = place[a].page;
-    if (!page) continue;
-    int first = 0;
-    while (first < kBlockRows - 1 && of[a][first] < 0) ++first;
-    if (of[a][first] != t0 + a) continue;  // another entry has this block written
-    const int row0 = place[a].row / kBlockRows * kBlockRows;
-    if (!KV_IN_BOUNDS(c, page >= c.pool && page + c.page_bytes <= c.pool + c.n_pages * c.page_bytes && row0 >= 0 &&
-                             row0 + kBlockRows <= c.page_rows && c.nkv * c.head_bytes < c.half_bytes))
-      continue;
-    if constexpr (ROPE) {
+  if (listed) {
+    for (int e = tid; e < p.n; e += kThreads8) {
+      const int s = p.seqs[e], pos = p.positions[e];
+      for (int i = 0; i < tokens; ++i)
+        if (place[i].page && place[i].seq == s && pos >= 0 && place[i].pos / kBlockRows == pos / kBlockRows)
+          atomicMax(&of[i][pos % kBlockRows], e);
+    }
+    __syncthreads();
+  } else if (a < tokens && place[a].page) {
+    const int at = place[a].row / kBlockRows * kBlockRows + ar;
+    const int e = c.owners[(place[a].page - c.pool) / c.page_bytes * c.page_rows + at];
+    if (e >= 0 && e < p.n && p.seqs[e] == place[a].seq && p.positions[e] == place[a].pos / kBlockRows * kBlockRows + ar)
+      of[a][ar] = e;
+  }
+  __syncwarp();
+  const uint32_t written = __ballot_sync(0xffffffffu, of[a][ar] >= 0) >> (tid & 16) & 0xffff;
+  const int lowest = __ffs(written) - 1;
+  if (ar == 0) first_row[a] = a < tokens && place[a].page && written && of[a][lowest] == t0 + a ? lowest : -1;
+  __syncthreads();
+  for (int i = 0; i < tokens; ++i) {
+    const int first = first_row[i];
+    if (first < 0) continue;  // another entry has this one's block written
+    const int row0 = place[i].row / kBlockRows * kBlockRows;
+    if (!block_fits(c, place[i].page, row0)) continue;
+    if (ROPE && begin < c.nkv) {
       __syncthreads();  // the block before has been read
-      const int half = q.r.rot / 2, pos0 = place[a].pos / kBlockRows * kBlockRows;
+      const int half = p.q.r.rot / 2, pos0 = place[i].pos / kBlockRows * kBlockRows;
       for (int e = tid; e < kBlockRows * half; e += kThreads8) {
-        const int r = e / half, i = e - r * half;
-        if (of[a][r] < 0) continue;
-        const float2 y = rope_angle(q.r, pos0 + r, i);
-        angles[0][r * (D / 2) + i] = y.x, angles[1][r * (D / 2) + i] = y.y;
+        const int ra = e / half, j = e - ra * half;
+        if (of[i][ra] < 0) continue;
+        const float2 y = rope_angle(p.q.r, pos0 + ra, j);
+        const int at = angle_at<D>(ra, j & ~3) + (j & 3);
+        angles[0][at] = y.x, angles[ROPE][at] = y.y;
       }
       __syncthreads();
     }
-    for (int item = split * kWarps8 + warp; item < items; item += splits * kWarps8) {
-      const int which = item >= c.nkv, head = item - which * c.nkv;
-      uint8_t* half = page + which * c.half_bytes;
-      uint8_t* codes = half + head * c.head_bytes + row0 * D;
-      uint32_t* scale_at = reinterpret_cast<uint32_t*>(half + c.nkv * c.head_bytes) + head * (c.page_rows / kBlockRows) +
-                           row0 / kBlockRows;
-      if (which) write_block<D, T, false>(c, v, stride, head * D, of[a], first, codes, scale_at, q.r, nullptr, nullptr);
-      else write_block<D, T, ROPE>(c, k, stride, head * D, of[a], first, codes, scale_at, q.r, angles[0], angles[1]);
+    for (int item = begin + warp; item < end; item += kThreads8 / 32) {
+      const Block8 b = block_at<D>(c, place[i].page, item, row0);
+      const T* from = (item < c.nkv ? p.k : p.v - c.nkv * D) + item * D;
+      const RopeView& rope = p.q.r;
+      if (!ROPE || item >= c.nkv)
+        write_block<D, T, TURN_NONE>(from, p.stride, of[i], first, b, rope, nullptr, nullptr);
+      else if (rope.pairs)
+        write_block<D, T, ROPE ? TURN_PAIRS : 0>(from, p.stride, of[i], first, b, rope, angles[0], angles[ROPE]);
+      else if (rope.rot % 16 == 0)
+        write_block<D, T, ROPE ? TURN_EIGHTS : 0>(from, p.stride, of[i], first, b, rope, angles[0], angles[ROPE]);
+      else
+        write_block<D, T, ROPE ? TURN_ODD : 0>(from, p.stride, of[i], first, b, rope, angles[0], angles[ROPE]);
     }
   }
 }
 
-template <int D, class T>
-cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t stride, const int32_t* seqs,
-                    const int32_t* positions, int n, const RopeRows* q, cudaStream_t s) {
-  // Without positions a sequence has one row, without a list every entry is a sequence of its own.
-  const Find find = !positions || !seqs ? FIND_ALONE : n <= kListed ? FIND_LIST : FIND_OWNERS;
+// The queries of a call, rotated by where their keys go.  Begins beside the rows' writing,
+// and ends behind it.
+template <class T>
+__global__ void __launch_bounds__(kRopeThreads) placed_rope(const __grid_constant__ Write8<T> p) {
+  extern __shared__ __align__(16) float q_angles[];
+  rope_rows<T>(p.q, blockIdx.x, q_angles, [&](int64_t t) {
+    const KvPlace at = kv_place(p.c, p.seqs, p.positions, t, p.n);
+    return at.page ? at.pos : -1;
+  });
+  pdl_wait();
+}
+template <class T>
+cudaError_t launch_placed_rope(Write8<T> p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rope_cut(p.q));
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.dynamicSmemBytes = rope_smem(p.q);
   cfg.stream = s;
   cudaLaunchAttribute pdl = {};
-  if (find == FIND_OWNERS) {
-    cfg.gridDim = dim3((unsigned)((n + 255) / 256));
-    cfg.blockDim = dim3(256);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kv_owners, c, seqs, positions, n);
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, placed_rope<T>, p);
+}
+
+template <int D, class T, bool ROPE>
+cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t stride, const int32_t* seqs,
+                    const int32_t* positions, int n, const RopeRows* q, cudaStream_t s) {
+  Write8<T> p{c, static_cast<const T*>(k), static_cast<const T*>(v), stride, seqs, positions, n, 0, RopeRows{}};
+  if (q) p.q = *q;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads8);
+  cfg.stream = s;
+  auto grid = [&](int64_t blocks, bool queries) {
+    p.blocks = (int)blocks;
+    cfg.gridDim = dim3((unsigned)blocks);
+    if (ROPE && queries && p.q.n) {
+      cfg.gridDim.x += (unsigned)rope_cut(p.q);
+      cfg.dynamicSmemBytes = rope_smem(p.q);
+    }
+  };
+  const int items = 2 * c.nkv;
+  // Without positions a sequence has one row, without a list every entry is a sequence of its own.
+  if (!positions || !seqs) {
+    constexpr int ITEMS = kThreads8 / (D / 8);
+    grid(((int64_t)n * items + ITEMS - 1) / ITEMS, true);
+    return cudaLaunchKernelEx(&cfg, write_rows<D, T, ROPE>, p);
+  }
+  const bool listed = n <= kListed;
+  cudaLaunchAttribute pdl = {};
+  if (!listed) {
+    cudaLaunchConfig_t first = cfg;
+    first.gridDim = dim3((unsigned)((n + 255) / 256));
+    cudaError_t e = cudaLaunchKernelEx(&first, kv_owners, c, seqs, positions, n);
     if (e != cudaSuccess) return e;
     pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &pdl;
     cfg.numAttrs = 1;
   }
-  const int tokens = std::min(std::max(n / 512, 1), kTokens8);
-  const int per_block = (2 * c.nkv + kWarps8 - 1) / kWarps8;  // CTAs that give a warp each of a block's heads
+  const int tokens = std::min(std::max(n / 256, 1), kTokens8);
   const int64_t chunks = (n + tokens - 1) / tokens;
-  const int splits = (int)std::min((int64_t)per_block, std::max((int64_t)1, 2048 / chunks));
-  const int blocks = (int)chunks * splits;
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kThreads8);
-  RopeRows rows{};
-  if (q) {
-    rows = *q;
-    if (rows.n) {
-      cfg.gridDim.x += (unsigned)rope_cut(rows);
-      cfg.dynamicSmemBytes = rope_smem(rows);
-    }
-  }
-  return cudaLaunchKernelEx(&cfg, q ? write8<D, T, true> : write8<D, T, false>, c, static_cast<const T*>(k),
-                            static_cast<const T*>(v), stride, seqs, positions, n, tokens, splits, find, blocks, rows);
+  const int steps = (items + kThreads8 / 32 - 1) / (kThreads8 / 32);  // a head of K or V for each warp
+  const int want = (int)std::min((int64_t)steps, std::max((int64_t)1, kBlockCtas / chunks));
+  const int per_split = (steps + want - 1) / want * (kThreads8 / 32), splits = (items + per_split - 1) / per_split;
+  grid(chunks * splits, listed);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, write_blocks<D, T, ROPE>, p, tokens, splits, per_split, listed);
+  // Many queries have a launch of their own, which fits more CTAs on an SM.
+  if (e == cudaSuccess && ROPE && !listed && p.q.n) e = launch_placed_rope<T>(p, s);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t tld::kv_write8(const KvView& c, int head_dim, bool f32, const void* k, const void* v, int64_t stride,
                            const int32_t* seqs, const int32_t* positions, int n, const RopeRows* q, cudaStream_t s) {
-  if (head_dim == 128)
-    return f32 ? launch8<128, float>(c, k, v, stride, seqs, positions, n, q, s)
-               : launch8<128, uint16_t>(c, k, v, stride, seqs, positions, n, q, s);
-  return f32 ? launch8<64, float>(c, k, v, stride, seqs, positions, n, q, s)
-             : launch8<64, uint16_t>(c, k, v, stride, seqs, positions, n, q, s);
+#define TLD_WRITE8(D, T)                                                         \
+  return q ? launch8<D, T, true>(c, k, v, stride, seqs, positions, n, q, s)      \
+           : launch8<D, T, false>(c, k, v, stride, seqs, positions, n, q, s)
+  if (head_dim == 128) {
+    if (f32) TLD_WRITE8(128, float);
+    TLD_WRITE8(128, uint16_t);
+  }
+  if (f32) TLD_WRITE8(64, float);
+  TLD_WRITE8(64, uint16_t);
+#undef TLD_WRITE8
 }

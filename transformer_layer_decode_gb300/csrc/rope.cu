@@ -41,7 +41,7 @@ int rope_rows_check(const dec_rope* r, const void* x, void* out, int type, int64
   const bool same = a == b && (x_stride == out_stride || n == 1);
   if (!same && kv_rows_overlap(a, x_stride * size, b, out_stride * size, width * size, n))
     return fail_no_handle(DEC_ERR_ARG, "the rotated rows overlap the ones to rotate");
-  *p = RopeRows{rope_view(*r, backward), x, out, x_stride, out_stride, n, n_heads, r->head_dim, 0, 0, 0, same};
+  *p = RopeRows{rope_view(*r, backward), x, out, x_stride, out_stride, n, n_heads, r->head_dim, 0, 0, 0, same, 0, 0, 0, 0};
   return DEC_OK;
 }
 

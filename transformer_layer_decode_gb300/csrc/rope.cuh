@@ -47,24 +47,46 @@ struct RopeRows {
   void* out;
   int64_t x_stride, out_stride;
   int n, heads, d;
-  int tokens, heads_per, splits;  // splits: CTAs that share the heads of a row
+  int tokens, heads_per, splits;  // splits: CTAs that share the heads of its rows
   int in_place;                   // the dimensions that stay need not be copied
+  int turned, per_head;           // lanes of a row that turn pairs; all of them
+  uint32_t by_heads, by_lanes;    // rope_over's for heads_per and per_head
 };
+
+// e / d for d given as rope_by(d), exact while e * d < 2^32.
+inline uint32_t rope_by(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
+__device__ __forceinline__ int rope_over(int e, uint32_t by) { return by ? (int)__umulhi((uint32_t)e, by) : e; }
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 32;           // of a CTA, at most
 constexpr int kRopeSmem = 32 * 1024;      // its cosines and sines, at most
+constexpr int kRopeCtas = 608;            // that the GPU holds at once
 
 constexpr int max_int(int a, int b) { return a > b ? a : b; }
 
-// How a launch cuts the rows; the CTAs that it takes.
+// How a launch cuts the rows; the CTAs that it takes.  Few rows: a lane's item each,
+// heads dealt out where there are many.  Many: as many rows a CTA as it takes to
+// have all CTAs on the GPU at once, since a CTA begins with a chain of loads and its
+// angles, and only then streams.
 inline int rope_cut(RopeRows& p) {
   const int items = max_int(1, p.heads * p.d / 16);  // (about: of 16 values)
-  p.tokens = 1;
-  while (p.tokens < kRopeTokens && 2 * p.tokens * items <= kRopeThreads && p.tokens * p.r.rot * 8 <= kRopeSmem) p.tokens *= 2;
-  p.splits = p.tokens == 1 ? (items + 2 * kRopeThreads - 1) / (2 * kRopeThreads) : 1;
+  const int most = max_int(1, kRopeSmem / (p.r.rot * 4) < kRopeTokens ? kRopeSmem / (p.r.rot * 4) : kRopeTokens);
+  p.tokens = max_int(kRopeThreads / items, (p.n + kRopeCtas - 1) / kRopeCtas);
+  p.tokens = p.tokens < 1 ? 1 : p.tokens > most ? most : p.tokens;
+  p.splits = p.n < kRopeCtas / 2 ? (items + 2 * kRopeThreads - 1) / (2 * kRopeThreads) : 1;
   p.heads_per = (p.heads + p.splits - 1) / p.splits;
   p.splits = (p.heads + p.heads_per - 1) / p.heads_per;
+  // a lane has eight values and their partners, or the next eight; or else a pair, or a value
+  const int half = p.r.rot / 2, stay = p.in_place ? 0 : p.d - p.r.rot;
+  if (p.r.pairs) {
+    p.turned = (p.r.rot + 7) / 8;
+    p.per_head = p.in_place ? p.turned : p.d / 8;
+  } else {
+    p.turned = half % 8 ? half : half / 8;
+    p.per_head = p.turned + (half % 8 ? stay : stay / 8);
+  }
+  p.by_heads = rope_by(p.heads_per);
+  p.by_lanes = rope_by(p.per_head);
   return (p.n + p.tokens - 1) / p.tokens * p.splits;
 }
 inline size_t rope_smem(const RopeRows& p) { return (size_t)p.tokens * p.r.rot * sizeof(float); }
@@ -75,63 +97,75 @@ template <class T, class Position>
 __device__ __forceinline__ void rope_rows(const RopeRows& p, int block, float* smem, Position position) {
   __shared__ int at[kRopeTokens];
   const int tid = threadIdx.x, half = p.r.rot / 2;
-  const int64_t t0 = (int64_t)(block / p.splits) * p.tokens;
-  const int h0 = block % p.splits * p.heads_per, heads = min(p.heads_per, p.heads - h0);
+  const int64_t t0 = (int64_t)(p.splits > 1 ? block / p.splits : block) * p.tokens;
+  const int h0 = p.splits > 1 ? block % p.splits * p.heads_per : 0, heads = min(p.heads_per, p.heads - h0);
+  const T* x = static_cast<const T*>(p.x) + h0 * (int64_t)p.d;
+  T* out = static_cast<T*>(p.out) + h0 * (int64_t)p.d;
+  const int total = p.tokens * heads * p.per_head;
+  const bool eights = p.r.pairs || half % 8 == 0;
+  struct Lane {
+    int t, h, c;
+    Eight<T> a, b;
+  };
+  // (rows that are skipped are read for nothing: their positions are not known yet)
+  auto fetch = [&](int e) {
+    Lane y{};
+    if (e >= total) return y;
+    const int row = rope_over(e, p.by_lanes);
+    y.c = e - row * p.per_head;
+    y.t = heads == p.heads_per ? rope_over(row, p.by_heads) : row / heads;
+    y.h = row - y.t * heads;
+    if (t0 + y.t < p.n) {
+      const T* from = x + (t0 + y.t) * p.x_stride + y.h * p.d;
+      if (p.r.pairs || y.c < p.turned) y.a.load(from + 8 * y.c);
+      else y.a.load(from + p.r.rot + 8 * (y.c - p.turned));
+      if (!p.r.pairs && y.c < p.turned) y.b.load(from + half + 8 * y.c);
+    }
+    return y;
+  };
+  Lane now{};
+  if (eights) now = fetch(tid);  // under way while the angles are worked out
   if (tid < p.tokens) at[tid] = t0 + tid < p.n ? position(t0 + tid) : -1;
   __syncthreads();
   float* sines = smem + p.tokens * half;
   for (int e = tid; e < p.tokens * half; e += kRopeThreads) {
-    const int t = e / half;
+    const int t = p.tokens > 1 ? e / half : 0;
     if (at[t] < 0) continue;
     const float2 y = rope_angle(p.r, at[t], e - t * half);
     smem[e] = y.x, sines[e] = y.y;
   }
   __syncthreads();
-  const T* x = static_cast<const T*>(p.x) + h0 * (int64_t)p.d;
-  T* out = static_cast<T*>(p.out) + h0 * (int64_t)p.d;
-  const bool wide = ((reinterpret_cast<uintptr_t>(out) | p.out_stride * sizeof(T)) & 31) == 0 && p.d % 8 == 0;
-  if (p.r.pairs || p.r.rot % 16 == 0) {
-    // eight values of a lane, and their partners (or the next eight)
-    const int stay = p.in_place ? 0 : p.d - p.r.rot;
-    const int turned = p.r.pairs ? (p.r.rot + 7) / 8 : p.r.rot / 16;
-    const int per_head = p.r.pairs ? (p.in_place ? turned : p.d / 8) : turned + stay / 8;
-    for (int e = tid; e < p.tokens * heads * per_head; e += kRopeThreads) {
-      const int row = e / per_head, c = e - row * per_head, t = row / heads, h = row - t * heads;
-      if (at[t] < 0) continue;
-      const T* from = x + (t0 + t) * p.x_stride + h * p.d;
-      T* to = out + (t0 + t) * p.out_stride + h * p.d;
-      const float *cs = smem + t * half, *sn = sines + t * half;
-      Eight<T> in;
-      float a[8];
-      if (p.r.pairs) {
-        in.load(from + 8 * c);
-        in.values(a);
+  const bool wide = ((reinterpret_cast<uintptr_t>(out) | p.out_stride * sizeof(T)) & 31) == 0;
+  if (eights) {
+    for (int e = tid; e < total; e += kRopeThreads) {
+      const Lane next = fetch(e + kRopeThreads);
+      if (at[now.t] >= 0) {
+        T* to = out + (t0 + now.t) * p.out_stride + now.h * p.d;
+        const float *cs = smem + now.t * half, *sn = sines + now.t * half;
+        const int c = now.c;
+        float a[8];
+        now.a.values(a);
+        if (p.r.pairs) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * c + i < half) rope_turn(a[2 * i], a[2 * i + 1], cs[4 * c + i], sn[4 * c + i]);
-        store8(to + 8 * c, a, wide);
-      } else if (c < turned) {
-        Eight<T> partner;
-        float b[8];
-        in.load(from + 8 * c);
-        partner.load(from + half + 8 * c);
-        in.values(a);
-        partner.values(b);
+          for (int i = 0; i < 4; ++i)
+            if (4 * c + i < half) rope_turn(a[2 * i], a[2 * i + 1], cs[4 * c + i], sn[4 * c + i]);
+          store8(to + 8 * c, a, wide);
+        } else if (c < p.turned) {
+          float b[8];
+          now.b.values(b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rope_turn(a[i], b[i], cs[8 * c + i], sn[8 * c + i]);
-        store8(to + 8 * c, a, wide);
-        store8(to + half + 8 * c, b, wide);
-      } else {
-        const int e0 = p.r.rot + 8 * (c - turned);
-        in.load(from + e0);
-        in.values(a);
-        store8(to + e0, a, wide);
+          for (int i = 0; i < 8; ++i) rope_turn(a[i], b[i], cs[8 * c + i], sn[8 * c + i]);
+          store8(to + 8 * c, a, wide);
+          store8(to + half + 8 * c, b, wide);
+        } else {
+          store8(to + p.r.rot + 8 * (c - p.turned), a, wide);
+        }
       }
+      now = next;
     }
-  } else {  // partners that lie in no eight of their own: a pair, or a value that stays, each
-    const int per_head = half + (p.in_place ? 0 : p.d - p.r.rot);
-    for (int e = tid; e < p.tokens * heads * per_head; e += kRopeThreads) {
-      const int row = e / per_head, i = e - row * per_head, t = row / heads, h = row - t * heads;
+  } else {  // partners that lie in no eight of their own
+    for (int e = tid; e < total; e += kRopeThreads) {
+      const int row = e / p.per_head, i = e - row * p.per_head, t = row / heads, h = row - t * heads;
       if (at[t] < 0) continue;
       const T* from = x + (t0 + t) * p.x_stride + h * p.d;
       T* to = out + (t0 + t) * p.out_stride + h * p.d;
