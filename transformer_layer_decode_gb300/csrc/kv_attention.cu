@@ -50,10 +50,12 @@ struct Tile {
   static constexpr int NB = D / 32;                                  // blocks of 32 dimensions
   static constexpr int kRowBytes = Q8 ? D : Q4 ? D / 2 : 2 * D;      // codes or values
   static constexpr int kHalf = kTileRows * (kRowBytes + (Q4 ? 2 * NB : 0));  // K or V, scales after the rows
-  static constexpr int kBytes = 2 * kHalf + (Q8 ? 16 : 0);           // Q8: K's and V's scale
+  static constexpr int kBytes = 2 * kHalf;
   static constexpr int kStep = Q4 || Q8 ? 2 : 1;                     // tiles a warp takes at a time
   static constexpr int kStages = D == 128 ? 2 : 4;                   // steps in its ring
-  static constexpr int kSlot = kStep * kBytes;
+  // Q8: K's and V's scales of the step's tiles are behind them.  (Rows of a tile that is not
+  // 128-byte aligned take cp.async 2.7 times as many writes, and sectors a second reading.)
+  static constexpr int kSlot = kStep * kBytes + (Q8 ? 128 : 0);
   static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kMergeRow = D + 8;                            // floats; heads apart by 8 banks
   static constexpr int kMerge = kWarps * kHeadBlock * kMergeRow * 4; // the warps' sums, once the ring is drained
@@ -923,7 +925,7 @@ struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) {
       const uint8_t* sk = st + k * L::kBytes;
-      float2 scales = *reinterpret_cast<const float2*>(sk + 2 * L::kHalf);
+      float2 scales = *reinterpret_cast<const float2*>(st + kTiles * L::kBytes + 8 * k);
       if (EDGE && !(rows_seen >> (16 * k) & 0xffff)) scales = make_float2(0.f, 0.f);  // (there may be no tile)
       v_scale[k] = scales.y;
       uint4 w[2][D / 64];  // rows g, g + 8
@@ -1045,9 +1047,10 @@ struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 };
 
 // Fills a stage with a tile: K's rows (or codes) begin at `src`, their scales (Q8: scale)
-// `scales` bytes behind, V's half_bytes behind K's; not `there`: with zeros.
+// `scales` bytes behind, V's half_bytes behind K's; not `there`: with zeros.  Q8: the scales
+// go to scale_dst.
 template <int D, int F>
-__device__ __forceinline__ void stage_tile(uint32_t dst, const uint8_t* src, int scales, int64_t half_bytes, int lane,
+__device__ __forceinline__ void stage_tile(uint32_t dst, uint32_t scale_dst, const uint8_t* src, int scales, int64_t half_bytes, int lane,
                                            bool there) {
   using L = Tile<D, F>;
   constexpr int PPR = L::kRowBytes / 16, N = kTileRows * PPR / 32;
@@ -1061,7 +1064,7 @@ __device__ __forceinline__ void stage_tile(uint32_t dst, const uint8_t* src, int
   }
   if constexpr (F == KV_Q8) {
     if (lane < 2)
-      cp_async<4>(dst + 2 * L::kHalf + 4 * lane, src + (lane ? half_bytes : 0) + scales, there ? 4 : 0);
+      cp_async<4>(scale_dst + 4 * lane, src + (lane ? half_bytes : 0) + scales, there ? 4 : 0);
   }
   if constexpr (F == KV_Q4) {  // half the lanes K's scales, half V's
     constexpr int kPart = L::NB * 2;
@@ -1153,7 +1156,7 @@ __device__ __forceinline__ UnitSums<D> unit_sums(const KvAttnParams& p, const Ro
         const int i = (j * L::kStep + k) & 31;
         const unsigned long long src = __shfl_sync(0xffffffffu, cur_src, i);
         const int scales = __shfl_sync(0xffffffffu, cur_scales, i);
-        stage_tile<D, F>(dst + k * L::kBytes, reinterpret_cast<const uint8_t*>(src), max(scales, 0), c.half_bytes, lane,
+        stage_tile<D, F>(dst + k * L::kBytes, dst + L::kStep * L::kBytes + 8 * k, reinterpret_cast<const uint8_t*>(src), max(scales, 0), c.half_bytes, lane,
                           scales >= 0);
       }
     }
