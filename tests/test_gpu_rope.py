@@ -106,15 +106,38 @@ def test_rows_that_are_skipped_and_strides(io, hd, rot):
     assert r.rotate(x[:0]).shape == (0, 4, hd)
 
 
-@pytest.mark.parametrize("n,heads", [(8000, 5), (3, 700), (1, 4000)])
-def test_many_rows_and_heads(n, heads):
-    r = rope.Rotary(64, layout="half")
-    x = rows((n, heads, 64), torch.bfloat16)
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,heads,hd,rot", [(8000, 5, 64, 64), (3, 700, 64, 64), (1, 4000, 64, 64), (310, 1300, 64, 64),
+                                            (320, 70, 1024, 512), (20011, 1, 8, 8), (1300, 3, 96, 42)])
+def test_many_rows_and_heads(io, n, heads, hd, rot):
+    """Every way of cutting the rows between CTAs: rows together, heads apart, both."""
+    r = rope.Rotary(hd, rot_dim=rot, layout="half")
+    x = rows((n, heads, hd), io)
     positions = (np.arange(n) * 13) % 5000
     got = r.rotate(x, ints(positions))
-    freq, m = ref.frequencies(64)
+    freq, m = ref.frequencies(rot)
     want = ref.rotate(f64(x), positions, freq, m, "half")
-    assert (np.abs(f64(got) - want) <= limit(f64(x), want, positions, freq, m, "half", torch.bfloat16)).all()
+    assert (np.abs(f64(got) - want) <= limit(f64(x), want, positions, freq, m, "half", io)).all()
+
+
+def test_on_another_stream_and_in_a_graph():
+    r = rope.Rotary(128)
+    x, positions = rows((600, 4, 128), torch.bfloat16), ints(range(600))
+    want = r.rotate(x, positions)
+    side, out = torch.cuda.Stream(), torch.zeros_like(x)
+    side.wait_stream(torch.cuda.current_stream())
+    r.rotate(x, positions, out=out, stream=side)
+    made = r.rotate(x, positions, stream=side)
+    by_handle = r.rotate(x, positions, stream=side.cuda_stream)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want) and torch.equal(made, want) and torch.equal(by_handle, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = r.rotate(x, positions)
+    x.copy_(rows(x.shape, torch.bfloat16, 9))
+    positions.add_(7)
+    graph.replay()
+    assert torch.equal(kept, r.rotate(x, positions))
 
 
 @pytest.mark.parametrize("layout,rot", [("half", 64), ("interleaved", 64), ("half", 20)])

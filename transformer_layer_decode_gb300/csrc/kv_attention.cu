@@ -51,8 +51,8 @@ struct Tile {
   static constexpr int kRowBytes = Q8 ? D : Q4 ? D / 2 : 2 * D;      // codes or values
   static constexpr int kHalf = kTileRows * (kRowBytes + (Q4 ? 2 * NB : 0));  // K or V, scales after the rows
   static constexpr int kBytes = 2 * kHalf;
-  static constexpr int kStep = Q4 || Q8 ? 2 : 1;                     // tiles a warp takes at a time
-  static constexpr int kStages = D == 128 ? 2 : 4;                   // steps in its ring
+  static constexpr int kStep = F ? 2 : 1;                            // tiles a warp takes at a time
+  static constexpr int kStages = D == 128 ? 2 : Q8 ? 3 : 4;          // steps in its ring
   // Q8: K's and V's scales of the step's tiles are behind them.  (Rows of a tile that is not
   // 128-byte aligned take cp.async 2.7 times as many writes, and sectors a second reading.)
   static constexpr int kSlot = kStep * kBytes + (Q8 ? 128 : 0);
@@ -865,8 +865,8 @@ struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   static constexpr bool kWhole = sizeof(T) == 2;  // q, and the weights, are one piece
   // The largest weight enters its products as 2^9 to 2^(9 + kSlack), the others so far
   // above fp16's smallest step; kWhole has these 9 in the exponential, fp32 results
-  // in what they multiply (see WarpQ4).  The second piece enters times 2^kLow.
-  static constexpr int kRoom = 9, kLow = 11;
+  // in what they multiply (see WarpQ4).
+  static constexpr int kRoom = 9;
   static constexpr float kLift = kWhole ? kRoom : 0;
   uint32_t a[kSteps][kWhole ? 2 : 4];  // q: dimensions 64 (k / 4) + 16 t + 4 (k % 4) .. of step k
   float f, f1;                         // score = f * K's scale * product; kWhole: f of head 2t, f1 of the next
@@ -1022,7 +1022,7 @@ struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
         } else {
           float y0 = w[4 * k + 2 * b] * (1 << kRoom), y1 = w[4 * k + 2 * b + 1] * (1 << kRoom);
           pw[0][b] = take_f16(y0, y1);
-          pw[kPieces - 1][b] = pack_f16(y0 * (1 << kLow), y1 * (1 << kLow));
+          pw[kPieces - 1][b] = pack_f16(y0, y1);
         }
       }
 #pragma unroll
@@ -1034,11 +1034,7 @@ struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
           const uint32_t z1 = __byte_perm(v[2][j], v[3][j], y ? 0x7362 : 0x5140);
           const uint32_t a0 = codes(z0, kLower), a1 = codes(z0, kUpper), a2 = codes(z1, kLower), a3 = codes(z1, kUpper);
           float o[4] = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (!kWhole) {
-            mma_f16(o, a0, a1, a2, a3, pw[kPieces - 1][0], pw[kPieces - 1][1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] *= 1.f / (1 << kLow);
-          }
+          if constexpr (!kWhole) mma_f16(o, a0, a1, a2, a3, pw[kPieces - 1][0], pw[kPieces - 1][1]);
           mma_f16(o, a0, a1, a2, a3, pw[0][0], pw[0][1]);
           this->add_tile(this->acc[j][y], o, v_scale[k]);
         }

@@ -73,7 +73,8 @@ inline int rope_cut(RopeRows& p) {
   const int most = max_int(1, kRopeSmem / (p.r.rot * 4) < kRopeTokens ? kRopeSmem / (p.r.rot * 4) : kRopeTokens);
   p.tokens = max_int(kRopeThreads / items, (p.n + kRopeCtas - 1) / kRopeCtas);
   p.tokens = p.tokens < 1 ? 1 : p.tokens > most ? most : p.tokens;
-  p.splits = p.n < kRopeCtas / 2 ? (items + 2 * kRopeThreads - 1) / (2 * kRopeThreads) : 1;
+  // (of many rows, too, no more heads than rope_over counts)
+  p.splits = p.n < kRopeCtas / 2 ? (items + 2 * kRopeThreads - 1) / (2 * kRopeThreads) : (items + 4095) / 4096;
   p.heads_per = (p.heads + p.splits - 1) / p.splits;
   p.splits = (p.heads + p.heads_per - 1) / p.heads_per;
   // a lane has eight values and their partners, or the next eight; or else a pair, or a value
