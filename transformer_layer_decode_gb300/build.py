@@ -1,4 +1,5 @@
-"""Builds libtld_gb300.so from csrc/ with nvcc for sm_103a (in-tree, _build/)."""
+"""Builds libtld_gb300.so from csrc/ with nvcc for sm_103a, and with g++ the Python module that marshals
+its short calls (in-tree, _build/)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -13,6 +14,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtld_gb300.so")
 # debug build: the kernels' index checks compiled in (TLD_DEBUG_CHECKS)
 DEBUG_LIB = os.path.join(BUILD, "libtld_gb300_debug.so")
+# marshalling of a decode step's calls, a Python module
+CALLS = os.path.join(BUILD, "tld_calls.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -43,12 +46,38 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_calls(force: bool = False) -> str:
+    """Compiles csrc/py_calls.cpp against this Python and this torch."""
+    src = os.path.join(CSRC, "py_calls.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "dec.h")))
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return CALLS
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    libs = os.path.join(root, "lib")
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), "-I", INCLUDE, src, "-o", tmp,
+           "-L", libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
           debug: bool = False) -> str:
     """Compile every .cu in csrc/ in parallel and link the shared library (with
     debug=True: the debug build, index checks compiled in, in its own objects)."""
     lib = DEBUG_LIB if debug else LIB
     if not force and not ptxas_info and up_to_date(lib):
+        build_calls()
         return lib
     objdir = os.path.join(BUILD, "debug") if debug else BUILD
     os.makedirs(objdir, exist_ok=True)
@@ -67,8 +96,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(build_calls, force)
         objs = list(ex.map(compile_one, sources()))
+        calls.result()
     tmp = lib + f".{os.getpid()}.tmp"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

@@ -16,6 +16,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libtld_gb300.so")
 # the same library with the kernels' index checks compiled in (TLD_DEBUG_CHECKS)
 DEBUG_LIB_PATH = os.path.join(_HERE, "_build", "libtld_gb300_debug.so")
+# the Python module that marshals a decode step's calls (csrc/py_calls.cpp)
+CALLS_PATH = os.path.join(_HERE, "_build", "tld_calls.so")
 
 # enum values of dec.h
 DEC_OK, DEC_ERR_ARG, DEC_ERR_SHAPE, DEC_ERR_STATE = 0, -1, -2, -3
@@ -129,6 +131,31 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.dec_last_error.restype = ctypes.c_char_p
     _libs[path] = L
     return L
+
+
+_calls = None
+
+
+def load_calls():
+    """The module that marshals a decode step's calls (built by ``build.build()``); raise if it is missing."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries are the module's)
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"not built: {CALLS_PATH} is missing (run transformer_layer_decode_gb300.build.build())")
+        loader = importlib.machinery.ExtensionFileLoader("tld_calls", CALLS_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("tld_calls", loader))
+        loader.exec_module(module)
+        _calls = module
+    return _calls
+
+
+def address_of(fn) -> int:
+    """Where a function of the library is."""
+    return ctypes.cast(fn, ctypes.c_void_p).value
 
 
 def _ptr(x) -> int | None:

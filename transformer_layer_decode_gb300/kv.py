@@ -66,7 +66,12 @@ class KVCache:
 
     Host threads may share a cache: a call's launches are queued without another's
     between them.  On the GPU the calls keep the order that include/dec.h asks for.
+
+    The calls of a decode step are marshalled by the module of dec.load_calls() where their arguments are
+    plainly right, and here where they are not, or have a stream of their own.
     """
+
+    _context = None  # what that module knows of a cache
 
     def __init__(self, *, n_layers: int, n_kv_heads: int, head_dim: int, page_rows: int | None = None,
                  fmt: str = "bf16", n_pages: int | None = None, n_seqs: int | None = None,
@@ -116,6 +121,10 @@ class KVCache:
         self._status_lock = threading.Lock()  # of a reading of the status, which waits for its stream
         self._workspaces: dict = {}  # of a stream's attention calls, which run one after another
         self._captured_workspaces: list = []  # of captures that keep no memory themselves
+        self._fast = dec.load_calls()
+        self._context = self._fast.context(ctypes.addressof(self.desc), self._index, n_kv_heads, head_dim, *(
+            dec.address_of(f) for f in (self.lib.dec_kv_append, self.lib.dec_kv_read, self.lib.dec_kv_attention,
+                                        self.lib.dec_kv_append_rotated)))
 
     # ---- marshalling ----------------------------------------------------------
 
@@ -193,6 +202,11 @@ class KVCache:
         """Writes row t of k and v ([n, n_kv_heads, head_dim], keys already rotated) as row positions[t]
         of sequence seqs[t]; without positions, as the sequence's last row; without seqs, of sequence t.
         8-bit pages: rows of a block of 16 behind the first that is written, and not written, are given up."""
+        if stream is None and self._context is not None:
+            with self._lock:
+                rc = self._fast.append(self._context, layer, k, v, seqs, positions)
+            if rc is not None:
+                return self._check(rc) if rc else None
         if not 0 <= layer < _LARGE:
             _int32(layer=layer)
         kp, kt, ks = self._rows("k", k, self.desc.n_kv_heads)
@@ -207,6 +221,13 @@ class KVCache:
     def read(self, layer: int, seqs, positions=None, *, k_out=None, v_out=None, dtype=torch.float32, stream=None):
         """Rows positions[t] of sequences seqs[t] as values: (k, v), each [n, n_kv_heads, head_dim].
         Rows of skipped entries keep what k_out and v_out hold (zeros where these are made here)."""
+        if stream is None and self._context is not None and k_out is not None and v_out is not None:
+            with self._lock:
+                rc = self._fast.read(self._context, layer, k_out, v_out, seqs, positions)
+            if rc is not None:
+                if rc:
+                    self._check(rc)
+                return k_out, v_out
         if not 0 <= layer < _LARGE:
             _int32(layer=layer)
         sp, n = self._ints("seqs", seqs)
@@ -227,6 +248,13 @@ class KVCache:
         """append() of keys that `rotary` (rope.Rotary) has yet to rotate, each by its position, and row t of
         q ([n, n_q_heads, head_dim]; None: no queries) rotated the same way: returns q_out, which may be q.
         Rows of skipped entries keep what q_out holds (zeros where it is made here)."""
+        if stream is None and self._context is not None and (q is None) == (q_out is None):
+            with self._lock:
+                rc = self._fast.append_rotated(self._context, layer, k, v, seqs, positions, rotary._context, q, q_out)
+            if rc is not None:
+                if rc:
+                    self._check(rc)
+                return q_out
         if not 0 <= layer < _LARGE:
             _int32(layer=layer)
         if rotary.device != self.device:
@@ -271,6 +299,16 @@ class KVCache:
         where the capture was not begun by torch.cuda.graph, this cache; `stream` needs one to be given."""
         if not (0 <= layer < _LARGE and 0 <= window < _LARGE and 0 <= sinks < _LARGE):
             _int32(layer=layer, window=window, sinks=sinks)
+        if out is not None and stream is None and self._context is not None:
+            ws = self._workspace(workspace, None)
+            with self._lock:
+                rc = self._fast.attention(self._context, layer, q, out, seqs, window, sinks, scale, ws[0], ws[1])
+            if rc is not None:
+                if rc:
+                    self._check(rc)
+                return out
+        else:
+            ws = None
         qp, qt, qs = self._rows("q", q)
         n, heads = q.shape[0], q.shape[1]
         sp, _ = self._ints("seqs", seqs, n)
@@ -279,30 +317,34 @@ class KVCache:
         op, ot, os_ = self._rows("out", out, heads)
         if ot != qt or out.shape[0] != n:
             raise ValueError("out: the type and rows of q are wanted")
+        if ws is None:
+            ws = self._workspace(workspace, stream)
+        self._call(self.lib.dec_kv_attention, layer, qp, op, qt, qs, os_, sp, n, heads, window, sinks, scale,
+                   ws[0], ws[1], stream=stream)
+        return out
+
+    def _workspace(self, workspace, stream):
+        """(address, bytes, what holds it) of an attention call's workspace: the one given, the stream's or the graph's."""
         if workspace is None:
             if stream is not None:
                 raise ValueError("a call with a stream of its own needs a workspace of its own")
             if self._captured():  # a graph keeps its own: it may be replayed beside other calls
                 workspace = self.workspace()
-                ws = workspace.data_ptr(), workspace.numel()
                 if not self._in_private_pool(workspace):
                     self._captured_workspaces.append(workspace)
-            else:
-                key = _raw_stream(self._index)
-                if key == _PER_THREAD:
-                    key = key, threading.get_ident()
-                ws = self._workspaces.get(key)
-                if ws is None:
-                    workspace = self.workspace()
-                    ws = workspace.data_ptr(), workspace.numel(), workspace
-                    self._workspaces[key] = ws
-        elif workspace.device != self.device or not workspace.is_contiguous():
+                return workspace.data_ptr(), workspace.numel(), workspace
+            key = _raw_stream(self._index)
+            if key == _PER_THREAD:
+                key = key, threading.get_ident()
+            ws = self._workspaces.get(key)
+            if ws is None:
+                workspace = self.workspace()
+                ws = workspace.data_ptr(), workspace.numel(), workspace
+                self._workspaces[key] = ws
+            return ws
+        if workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"workspace: contiguous memory on {self.device} is wanted")
-        else:
-            ws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        self._call(self.lib.dec_kv_attention, layer, qp, op, qt, qs, os_, sp, n, heads, window, sinks, scale,
-                   ws[0], ws[1], stream=stream)
-        return out
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
     # ---- pages ----------------------------------------------------------------
 

@@ -39,6 +39,7 @@ class Rotary:
     stays; "yarn" keeps those that turn `fast` times or more over `context` positions, divides those that
     turn `slow` times or less, and multiplies the rotated values by 0.1 log(factor) + 1.  Or they are given,
     `frequencies` [rot_dim / 2], and `magnitude`, which otherwise overrides the scaling's, with them.
+    A captured graph needs the rotation alive, as it does a cache.
     """
 
     def __init__(self, head_dim: int, *, rot_dim: int | None = None, layout: str = "half", theta: float = 1e4,
@@ -79,6 +80,9 @@ class Rotary:
         self.device, self._index = self.steps.device, self.steps.device.index
         self.desc = RopeDesc(head_dim, rot_dim, LAYOUTS[layout], magnitude, self.steps.data_ptr())
         self._ref = ctypes.byref(self.desc)
+        self._fast = dec.load_calls()
+        self._context = self._fast.context(ctypes.addressof(self.desc), self._index, 0, head_dim,
+                                           dec.address_of(self.lib.dec_rope_rotate))
 
     def _check(self, rc: int):
         if rc != dec.DEC_OK:
@@ -98,6 +102,12 @@ class Rotary:
         """Row t of x ([n, heads, head_dim]) rotated by positions[t] (int32; without them, by t).  A row with a
         negative position is skipped, and keeps what `out` holds (zeros where that is made here).  `out` may be
         x.  backward: by the negative angles, the gradient of a rotation."""
+        if stream is None and out is not None:  # (marshalled where plainly right, as KVCache's calls are)
+            rc = self._fast.rotate(self._context, x, positions, out, bool(backward))
+            if rc is not None:
+                if rc:
+                    self._check(rc)
+                return out
         xp, xt, xs = self._rows("x", x)
         n, heads = x.shape[0], x.shape[1]
         if positions is not None and (positions.dtype != torch.int32 or positions.shape != (n,)
