@@ -90,6 +90,20 @@ __device__ __forceinline__ KvPlace kv_place(const KvView& c, const int32_t* seqs
 }
 #endif
 
+// A launch that is set up while the kernel before it runs (one that calls pdl_trigger) or
+// ends: each of its threads begins with pdl_wait, behind which it is as any other (a
+// kernel of which a block left without waiting could be over before the one before it).
+struct BehindLast {
+  cudaLaunchAttribute pdl = {};
+  explicit BehindLast(cudaLaunchConfig_t* cfg) {
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = &pdl;
+    cfg->numAttrs = 1;
+  }
+  BehindLast(const BehindLast&) = delete;
+};
+
 struct RopeRows;
 // dec_kv_append to 8-bit pages (and dec_kv_append_rotated, with q).
 cudaError_t kv_write8(const KvView& c, int head_dim, bool f32, const void* k, const void* v, int64_t stride,

@@ -1257,6 +1257,8 @@ template <int D, int F, class T>
 __global__ void __launch_bounds__(kThreadsA, Tile<D, F>::kCtasPerSm)
     kv_attn_whole(const __grid_constant__ KvAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
+  pdl_wait();
+  pdl_trigger();
   const int units = p.c.nkv * p.head_blocks;
   for (int id = blockIdx.x; id < p.n * units; id += gridDim.x) {
     const int r = id / units, u = id % units;
@@ -1287,6 +1289,7 @@ __global__ void __launch_bounds__(kThreadsA, Tile<D, F>::kCtasPerSm) kv_attn(con
   __shared__ int64_t chunk_sum[kMaxChunks];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvView& c = p.c;
+  pdl_wait();
   pdl_trigger();
 
   // ---- this CTA's share of the line
@@ -1626,6 +1629,7 @@ cudaError_t launch_attn_kv(KvAttnParams p, int dev, int ctas, cudaStream_t s) {
   cfg.blockDim = dim3(kThreadsA);
   cfg.dynamicSmemBytes = Tile<D, F>::kSmem;
   cfg.stream = s;
+  const BehindLast behind(&cfg);
   if (longest_unit(p) <= Tile<D, F>::kWhole) {
     cfg.gridDim = dim3((unsigned)std::min(units, (int64_t)ctas));
     return cudaLaunchKernelEx(&cfg, kv_attn_whole<D, F, T>, p);
@@ -1633,13 +1637,8 @@ cudaError_t launch_attn_kv(KvAttnParams p, int dev, int ctas, cudaStream_t s) {
   cfg.gridDim = dim3(ctas);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attn<D, F, T>, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute pdl = {};
-  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl.val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  cfg.attrs = &pdl;
-  cfg.numAttrs = 1;
   if (!p.cut_by_unit) return cudaLaunchKernelEx(&cfg, kv_attn_join<D, T, 1>, p);
   if (units > ctas / kHeadBlock) {
     cfg.gridDim = dim3((unsigned)units);

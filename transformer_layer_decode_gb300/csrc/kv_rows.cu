@@ -279,6 +279,8 @@ template <int D, int F, class T, bool READ, int ROUNDS>
 __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
                                                           const int32_t* seqs, const int32_t* positions,
                                                           int n, int tokens, int items_per_token, bool wide) {
+  pdl_wait();
+  pdl_trigger();
   move_rows<D, F, T, READ, ROUNDS, false>(c, k, v, stride, seqs, positions, n, tokens, items_per_token, wide, blockIdx.x,
                                           RopeView{});
 }
@@ -292,6 +294,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows_rotated(const __grid_c
                                                                   int items_per_token, int blocks,
                                                                   const __grid_constant__ RopeRows q) {
   extern __shared__ __align__(16) float q_angles[];
+  pdl_wait();
+  pdl_trigger();
   if ((int)blockIdx.x >= blocks) {
     rope_rows<T>(q, blockIdx.x - blocks, q_angles, [&](int64_t t) {
       const KvPlace at = kv_place(c, seqs, positions, t, n);
@@ -323,6 +327,7 @@ cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kRowWarps * 32);
   cfg.stream = s;
+  const BehindLast behind(&cfg);
   if constexpr (!READ) {
     if (q) {
       RopeRows rows = *q;

@@ -23,6 +23,7 @@ constexpr uint32_t kLeastScale = 1u << 23, kMostScale = 248u << 23;  // 2^-126, 
 // other calls left there is told apart by looking the entry up in the list.)
 __global__ void __launch_bounds__(256) kv_owners(const __grid_constant__ KvView c, const int32_t* seqs,
                                                  const int32_t* positions, int n) {
+  pdl_wait();
   pdl_trigger();
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const KvPlace at = kv_place(c, seqs, positions, t, n);
@@ -170,6 +171,8 @@ __global__ void __launch_bounds__(kThreads8) write_rows(const __grid_constant__ 
   extern __shared__ __align__(16) float q_angles[];
   __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? (ITEMS / 2 + 1) * (D / 2) : 1];
   const KvView& c = p.c;
+  pdl_wait();
+  pdl_trigger();
   if constexpr (ROPE) {
     if ((int)blockIdx.x >= p.blocks) {
       rope_rows<T>(p.q, blockIdx.x - p.blocks, q_angles, [&](int64_t t) {
@@ -377,6 +380,7 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
   __shared__ int first_row[kTokens8];  // of a block that this entry has written, else -1
   __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? kBlockRows * (D / 2) : 1];
   const KvView& c = p.c;
+  if (listed) pdl_wait();
   pdl_trigger();
   if constexpr (ROPE) {
     if ((int)blockIdx.x >= p.blocks) {
@@ -466,11 +470,7 @@ cudaError_t launch_placed_rope(Write8<T> p, cudaStream_t s) {
   cfg.blockDim = dim3(kRopeThreads);
   cfg.dynamicSmemBytes = rope_smem(p.q);
   cfg.stream = s;
-  cudaLaunchAttribute pdl = {};
-  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &pdl;
-  cfg.numAttrs = 1;
+  const BehindLast behind(&cfg);
   return cudaLaunchKernelEx(&cfg, placed_rope<T>, p);
 }
 
@@ -482,6 +482,7 @@ cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t strid
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads8);
   cfg.stream = s;
+  const BehindLast behind(&cfg);
   auto grid = [&](int64_t blocks, bool queries) {
     p.blocks = (int)blocks;
     cfg.gridDim = dim3((unsigned)blocks);
@@ -498,16 +499,11 @@ cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t strid
     return cudaLaunchKernelEx(&cfg, write_rows<D, T, ROPE>, p);
   }
   const bool listed = n <= kListed;
-  cudaLaunchAttribute pdl = {};
   if (!listed) {
     cudaLaunchConfig_t first = cfg;
     first.gridDim = dim3((unsigned)((n + 255) / 256));
     cudaError_t e = cudaLaunchKernelEx(&first, kv_owners, c, seqs, positions, n);
     if (e != cudaSuccess) return e;
-    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &pdl;
-    cfg.numAttrs = 1;
   }
   const int tokens = std::min(std::max(n / 256, 1), kTokens8);
   const int64_t chunks = (n + tokens - 1) / tokens;

@@ -52,6 +52,8 @@ namespace {
 template <class T>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeRows p, const int32_t* positions) {
   extern __shared__ __align__(16) float angles[];
+  pdl_wait();
+  pdl_trigger();
   rope_rows<T>(p, blockIdx.x, angles, [&](int64_t t) { return positions ? positions[t] : (int)t; });
 }
 
@@ -116,6 +118,7 @@ extern "C" int dec_rope_rotate(const dec_rope* r, const void* x, void* out, int 
   cfg.blockDim = dim3(kRopeThreads);
   cfg.dynamicSmemBytes = rope_smem(p);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  const BehindLast behind(&cfg);
   const cudaError_t e = type == DEC_IO_F32 ? cudaLaunchKernelEx(&cfg, rope_kernel<float>, p, positions)
                                            : cudaLaunchKernelEx(&cfg, rope_kernel<uint16_t>, p, positions);
   if (e != cudaSuccess) return fail_no_handle(DEC_ERR_CUDA, "rotation launch: %s", cudaGetErrorString(e));
