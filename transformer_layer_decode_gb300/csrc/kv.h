@@ -108,6 +108,9 @@ struct RopeRows;
 // dec_kv_append to 8-bit pages (and dec_kv_append_rotated, with q).
 cudaError_t kv_write8(const KvView& c, int head_dim, bool f32, const void* k, const void* v, int64_t stride,
                       const int32_t* seqs, const int32_t* positions, int n, const RopeRows* q, cudaStream_t s);
+// Behind a launch on the same stream that triggers once it has waited for what is before it.
+cudaError_t kv_rotate_queries(const KvView& c, bool f32, const int32_t* seqs, const int32_t* positions, int n, RopeRows q,
+                              cudaStream_t s);
 
 // Checks a cache (its pointers too, with `memory`); DEC_OK or the error, recorded.
 int kv_check(const dec_kv_cache* c, bool memory);

@@ -70,10 +70,13 @@ constexpr int kRowWarps = 8;  // warps of a CTA of the row kernels
 // Rounds of a warp, rows whose loads are under way together, where there are
 // enough warps to fill the GPU; one otherwise.
 constexpr int kRowRounds = 4;
+constexpr int kTurnedRounds = 2;  // of rows of which keys are rotated, whose partners are loaded too
 constexpr int kFewRounds = 8192;  // (about a GPU full of warps)
 // CTAs beyond which they take more tokens each (half or 1.5 times as many: up to
 // 6 % slower).
 constexpr int kManyCtas = 2400;
+// Rotated rows: CTAs that the GPU holds at once, and rounds of a CTA's warps at most.
+constexpr int kTurnedCtas = 456, kTurnedTurns = 6;
 
 // 1 / s to a few 2^-24 of itself.
 __device__ __forceinline__ float reciprocal(float s) {
@@ -117,6 +120,21 @@ __device__ __forceinline__ float seventh(float x) {
   return fmaf(fmaf(-7.f, q, x), y, q);
 }
 
+// Eight values of a block of 32 whose largest magnitude is `top`: their codes to two words
+// of the row, 2 NB bytes apart, and (leads) the block's scale.
+template <int NB>
+__device__ __forceinline__ void put_q4(float (&x)[8], float top, uint8_t* words, uint8_t* scale, bool leads) {
+  const bool finite = top < INFINITY;
+  const __half s16 = finite ? __float2half_rn(fminf(seventh(top), 65504.f)) : __ushort_as_half(0x7fff);
+  const float f = __half2float(s16);
+  // (where f is 0 every |x| is far below 1/2)
+  const uint32_t codes = q4_codes(x, f > 0.f ? f : 1.f), w = finite ? codes : 0x88888888u;
+  uint16_t* to = reinterpret_cast<uint16_t*>(words);
+  to[0] = (uint16_t)w;
+  to[NB] = (uint16_t)(w >> 16);
+  if (leads) *reinterpret_cast<__half*>(scale) = s16;
+}
+
 constexpr int kMaxTokens = 32;  // of a CTA
 
 // A CTA takes `tokens` tokens, looks up where each goes (a thread per token),
@@ -133,36 +151,22 @@ constexpr int kMaxTokens = 32;  // of a CTA
 // 57).  In fp32, 306 MB, 51 and 51 us (46); from and to bf16 pages, 268 MB, 43 (40),
 // fp32 and bf16 pages, 402 MB, 61 and 62 (60).  Four rounds:
 // two are 10 % slower, eight 15 % in fp32.
-//
-// ROPE: keys are rotated by their positions on the way, in fp32; the angles of the
-// CTA's tokens are worked out once, into shared memory.
-template <int D, int F, class T, bool READ, int ROUNDS, bool ROPE>
-__device__ __forceinline__ void move_rows(const KvView& c, T* k, T* v, int64_t stride, const int32_t* seqs,
-                                          const int32_t* positions, int n, int tokens, int items_per_token, bool wide,
-                                          int block, const RopeView& rope) {
+template <int D, int F, class T, bool READ, int ROUNDS>
+__global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
+                                                          const int32_t* seqs, const int32_t* positions,
+                                                          int n, int tokens, int items_per_token, bool wide) {
   constexpr int LANES = D / 8, NB = D / 32, RPR = 32 / LANES;  // rows of a round
   __shared__ uint8_t* token_page[kMaxTokens];
   __shared__ int token_row[kMaxTokens];
-  __shared__ int token_pos[ROPE ? kMaxTokens : 1];
-  __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? kMaxTokens * (D / 2) : 1];  // cosines, sines
+  pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31, l = lane % LANES, b = l / 4, j = l % 4;
-  const int64_t t0 = (int64_t)block * tokens;
+  const int64_t t0 = (int64_t)blockIdx.x * tokens;
   if (threadIdx.x < tokens) {
     const int64_t t = t0 + threadIdx.x;
     const KvPlace at = kv_place(c, seqs, positions, t, n);
     token_row[threadIdx.x] = at.row;
     token_page[threadIdx.x] = at.page;
-    if (ROPE) token_pos[threadIdx.x] = at.pos;
-  }
-  if constexpr (ROPE) {
-    __syncthreads();
-    const int half = rope.rot / 2;
-    for (int e = threadIdx.x; e < tokens * half; e += kRowWarps * 32) {
-      const int t = e / half, i = e - t * half;
-      if (!token_page[t]) continue;
-      const float2 y = rope_angle(rope, token_pos[t], i);
-      angles[0][t * (D / 2) + i] = y.x, angles[1][t * (D / 2) + i] = y.y;
-    }
   }
   __syncthreads();
   const int last = 2 * c.nkv - 1;
@@ -224,32 +228,12 @@ __device__ __forceinline__ void move_rows(const KvView& c, T* k, T* v, int64_t s
         const int at = round(i);
         float x[8];
         in[i].values(x);
-        if constexpr (ROPE) {
-          const float* cs = angles[0] + token * (D / 2);
-          rope_eight<LANES>(rope, x, l, cs, cs + kMaxTokens * (D / 2), mine(at) - 8 * l, at < nkv);
-        }
         if constexpr (READ) {
           store8(mine(at), x, wide);
         } else if constexpr (F == KV_BF16) {
           store8(reinterpret_cast<uint16_t*>(values + head(at)), x, false);
         } else {
-          float top;  // the block's largest magnitude
-          if constexpr (ROPE) {
-            Eight<float> turned;
-            turned.set(x);
-            top = turned.top();
-          } else {
-            top = in[i].top();
-          }
-          const bool finite = top < INFINITY;
-          const __half s16 = finite ? __float2half_rn(fminf(seventh(top), 65504.f)) : __ushort_as_half(0x7fff);
-          const float f = __half2float(s16);
-          // (where f is 0 every |x| is far below 1/2)
-          const uint32_t codes = q4_codes(x, f > 0.f ? f : 1.f), w = finite ? codes : 0x88888888u;
-          uint16_t* to = reinterpret_cast<uint16_t*>(words + head(at));
-          to[0] = (uint16_t)w;
-          to[NB] = (uint16_t)(w >> 16);
-          if (j == 0) *reinterpret_cast<__half*>(scales + head(at)) = s16;
+          put_q4<NB>(x, in[i].top(), words + head(at), scales + head(at), j == 0);
         }
       }
     } else {
@@ -275,25 +259,21 @@ __device__ __forceinline__ void move_rows(const KvView& c, T* k, T* v, int64_t s
   }
 }
 
-template <int D, int F, class T, bool READ, int ROUNDS>
-__global__ void __launch_bounds__(kRowWarps * 32) kv_rows(KvView c, T* k, T* v, int64_t stride,
-                                                          const int32_t* seqs, const int32_t* positions,
-                                                          int n, int tokens, int items_per_token, bool wide) {
-  pdl_wait();
-  pdl_trigger();
-  move_rows<D, F, T, READ, ROUNDS, false>(c, k, v, stride, seqs, positions, n, tokens, items_per_token, wide, blockIdx.x,
-                                          RopeView{});
-}
-
-// The rows of a step: the first `blocks` CTAs rotate and write keys and write values,
-// the others rotate queries.
+// The rows of a step, as kv_rows writes them: the first `blocks` CTAs rotate and write keys
+// and write values, the others rotate queries.  Many rows are loaded before it is known
+// where they go and how they turn (8185 rows of 32 heads of fp32 to bf16 pages 79 -> 72 us),
+// those of bf16 also the next ones before these are coded (4093 rows of 8 heads 15.0 -> 11.7;
+// of fp32 that takes the registers of a third CTA an SM: 88).
 template <int D, int F, class T, int ROUNDS>
-__global__ void __launch_bounds__(kRowWarps * 32) kv_rows_rotated(const __grid_constant__ KvView c, const T* k, const T* v,
-                                                                  int64_t stride, const int32_t* seqs,
-                                                                  const int32_t* positions, int n, int tokens,
-                                                                  int items_per_token, int blocks,
-                                                                  const __grid_constant__ RopeRows q) {
+__global__ void __launch_bounds__(kRowWarps * 32, sizeof(T) == 4 || ROUNDS > 1 ? 3 : 4)
+    kv_rows_rotated(const __grid_constant__ KvView c, const T* k, const T* v, int64_t stride, const int32_t* seqs,
+                    const int32_t* positions, int n, int tokens, int items_per_token, int blocks,
+                    const __grid_constant__ RopeRows q) {
+  constexpr int LANES = D / 8, NB = D / 32, RPR = 32 / LANES;
+  constexpr bool FIRST = ROUNDS > 1, AHEAD = FIRST && sizeof(T) == 2;
   extern __shared__ __align__(16) float q_angles[];
+  __shared__ KvPlace place[kMaxTokens];
+  __shared__ __align__(16) float angles[2][kMaxTokens * (D / 2)];  // cosines, sines
   pdl_wait();
   pdl_trigger();
   if ((int)blockIdx.x >= blocks) {
@@ -301,9 +281,74 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows_rotated(const __grid_c
       const KvPlace at = kv_place(c, seqs, positions, t, n);
       return at.page ? at.pos : -1;
     });
-  } else {
-    move_rows<D, F, T, false, ROUNDS, true>(c, const_cast<T*>(k), const_cast<T*>(v), stride, seqs, positions, n, tokens,
-                                            items_per_token, false, blockIdx.x, q.r);
+    return;
+  }
+  const int lane = threadIdx.x & 31, l = lane % LANES, b = l / 4, j = l % 4, nkv = c.nkv, last = 2 * nkv - 1;
+  const int64_t t0 = (int64_t)blockIdx.x * tokens;
+  struct Item {  // a warp's: ROUNDS rounds of rows of a token
+    int token, part;
+    Piece<T, true> in[ROUNDS];
+  };
+  // (lanes past the last row take it once more: the same bytes to the same place)
+  auto round = [&](const Item& y, int i) { return min((y.part * ROUNDS + i) * RPR + lane / LANES, last); };
+  auto row_of = [&](const Item& y, int at) {
+    return (at < nkv ? k + at * D : v + (at - nkv) * D) + (t0 + y.token) * stride;
+  };
+  auto fetch = [&](int item) {
+    Item y;
+    y.token = item / items_per_token, y.part = item % items_per_token;
+    if (y.token < tokens && t0 + y.token < n) {
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int at = round(y, i);
+        if (at < nkv) y.in[i].load(row_of(y, at), l, q.r);
+        else y.in[i].own.load(row_of(y, at) + 8 * l);
+      }
+    }
+    return y;
+  };
+  Item now;
+  if (FIRST) now = fetch(threadIdx.x >> 5);
+  if (threadIdx.x < tokens) place[threadIdx.x] = kv_place(c, seqs, positions, t0 + threadIdx.x, n);
+  __syncthreads();
+  const int half = q.r.rot / 2;
+  for (int e = threadIdx.x; e < tokens * half; e += kRowWarps * 32) {
+    const int t = e / half, i = e - t * half;
+    if (!place[t].page) continue;
+    const float2 y = rope_angle(q.r, place[t].pos, i);
+    const int at = angle_at<D>(t, i);
+    angles[0][at] = y.x, angles[1][at] = y.y;
+  }
+  __syncthreads();
+  for (int item = threadIdx.x >> 5; item < tokens * items_per_token; item += kRowWarps) {
+    Item next;
+    if (AHEAD) next = fetch(item + kRowWarps);
+    else if (!FIRST) now = fetch(item);
+    const KvPlace at_token = place[now.token];
+    if (at_token.page && KV_IN_BOUNDS(c, now.token < kMaxTokens && t0 + now.token < n && at_token.row >= 0 &&
+                                             at_token.row < c.page_rows && at_token.page >= c.pool &&
+                                             at_token.page + c.page_bytes <= c.pool + c.n_pages * c.page_bytes &&
+                                             2 * nkv * c.head_bytes == c.page_bytes)) {
+      const float* cs = angles[0] + now.token * (D / 2);
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int at = round(now, i);
+        uint8_t* head = at_token.page + (uint64_t)(uint32_t)at * (uint32_t)c.head_bytes;
+        float x[8];
+        if (at < nkv) turned<D>(now.in[i], x, row_of(now, at), l, q.r, cs, cs + kMaxTokens * (D / 2));
+        else now.in[i].own.values(x);
+        if constexpr (F == KV_BF16) {
+          store8(reinterpret_cast<uint16_t*>(head + at_token.row * (2 * D) + 16 * l), x, false);
+        } else {
+          Eight<float> all;
+          all.set(x);
+          put_q4<NB>(x, all.top(), head + at_token.row * (D / 2) + 4 * j * NB + 2 * b,
+                     head + c.page_rows * (D / 2) + (at_token.row * NB + b) * 2, j == 0);
+        }
+      }
+    }
+    if (AHEAD) now = next;
+    else if (FIRST) now = fetch(item + kRowWarps);
   }
 }
 
@@ -311,17 +356,35 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows_rotated(const __grid_c
 // the meantime are in this answer or in the next.
 __global__ void kv_take_status(int32_t* status, int32_t* taken) { *taken = atomicExch(status, 0); }
 
+// Tokens of a CTA that rotates many rows, a multiple of `least`.  Its beginning, with the
+// angles of its tokens, takes as long as two of its warps' turns, and the last CTAs to begin
+// should have others beside them: so the least of waves times their length (8 heads of
+// fp32, 4093 rows: 12 tokens 13.2 us, 8 17.3, 2 18.1; 2500 rows: 6 tokens 7.6, 12 10.5).  More
+// than 6 turns no longer help (8185 rows of 32 heads of bf16: 3 tokens 55 us, 13 60).
+inline int turned_tokens(int n, int least, int items) {
+  int best = least;
+  int64_t cost = INT64_MAX;
+  for (int tokens = least; tokens <= kMaxTokens; tokens += least) {
+    const int turns = (tokens * items + kRowWarps - 1) / kRowWarps;
+    if (turns > kTurnedTurns && tokens > least) break;
+    const int64_t ctas = (n + (int64_t)tokens - 1) / tokens, waves = (ctas + kTurnedCtas - 1) / kTurnedCtas;
+    if (waves * (turns + 2) < cost) cost = waves * (turns + 2), best = tokens;
+  }
+  return best;
+}
+
 template <int D, int F, class T, bool READ>
 cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const int32_t* seqs,
                         const int32_t* positions, int n, const RopeRows* q, cudaStream_t s) {
   constexpr int kPerRound = 256 / D;
   const bool few = (int64_t)n * 2 * c.nkv / kPerRound < kFewRounds;
-  const int per_item = kPerRound * (few ? 1 : kRowRounds);
+  const int per_item = kPerRound * (few ? 1 : q ? kTurnedRounds : kRowRounds);
   const int items = (2 * c.nkv + per_item - 1) / per_item;
   const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | stride * sizeof(T)) & 31) == 0;
   // enough tokens for every warp of a CTA, or a multiple where there are CTAs enough
   const int least = (kRowWarps + items - 1) / items;
-  const int tokens = std::min(std::max((n / kManyCtas + least - 1) / least, 1) * least, kMaxTokens);
+  int tokens = std::min(std::max((n / kManyCtas + least - 1) / least, 1) * least, kMaxTokens);
+  if (q && !few) tokens = turned_tokens(n, least, items);
   const int blocks = (n + tokens - 1) / tokens;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -331,13 +394,15 @@ cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const
   if constexpr (!READ) {
     if (q) {
       RopeRows rows = *q;
-      if (rows.n) {
+      const bool apart = rope_many(rows);
+      if (rows.n && !apart) {
         cfg.gridDim.x += (unsigned)rope_cut(rows);
         cfg.dynamicSmemBytes = rope_smem(rows);
       }
-      return cudaLaunchKernelEx(&cfg, few ? kv_rows_rotated<D, F, T, 1> : kv_rows_rotated<D, F, T, kRowRounds>, c,
-                                static_cast<const T*>(k), static_cast<const T*>(v), stride, seqs, positions, n, tokens,
-                                items, blocks, rows);
+      const cudaError_t e = cudaLaunchKernelEx(&cfg, few ? kv_rows_rotated<D, F, T, 1> : kv_rows_rotated<D, F, T, kTurnedRounds>,
+                                               c, static_cast<const T*>(k), static_cast<const T*>(v), stride, seqs, positions,
+                                               n, tokens, items, blocks, rows);
+      return e == cudaSuccess && apart ? kv_rotate_queries(c, sizeof(T) == 4, seqs, positions, n, rows, s) : e;
     }
   }
   return cudaLaunchKernelEx(&cfg, few ? kv_rows<D, F, T, READ, 1> : kv_rows<D, F, T, READ, kRowRounds>, c,

@@ -17,6 +17,7 @@ constexpr int kTokens8 = 16;     // list entries of a CTA of write_blocks, at mo
 static_assert(kTokens8 * kBlockRows == kThreads8, "a thread for each row of each entry's block");
 constexpr int kListed = 512;     // lists up to this length are looked through by every CTA
 constexpr int kBlockCtas = 1216;  // of write_blocks, where the heads are enough for them
+constexpr int kTurnedCtas = 456;  // (each begins with the angles of its blocks)
 constexpr uint32_t kLeastScale = 1u << 23, kMostScale = 248u << 23;  // 2^-126, 2^121
 
 // The entry that writes each row: owners[page][row], for write_blocks' CTAs.  (What
@@ -45,56 +46,6 @@ __device__ __forceinline__ float inverse(uint32_t s) { return __uint_as_float(0x
 __device__ __forceinline__ uint32_t four_bytes(float m0, float m1, float m2, float m3) {
   return __byte_perm(__byte_perm(__float_as_uint(m0), __float_as_uint(m1), 0x0040),
                      __byte_perm(__float_as_uint(m2), __float_as_uint(m3), 0x0040), 0x5410);
-}
-
-// Eight values of a row, at dimension 8 l of a head: as loaded, with (TURN) those that
-// they are turned with, if these are an aligned eight too.
-template <class T, bool TURN>
-struct Piece {
-  Eight<T> own, partner;
-  __device__ __forceinline__ void load(const T* row, int l, const RopeView& r) {
-    own.load(row + 8 * l);
-    if constexpr (TURN) {
-      const int half = r.rot / 2;
-      if (!r.pairs && half % 8 == 0 && 8 * l < r.rot) partner.load(row + (8 * l < half ? 8 * l + half : 8 * l - half));
-    }
-  }
-};
-
-// Eight values at dimension 8 l, turned by the angles of their row (see rope.cuh), where
-// their partners are among them or lie in no aligned eight of `row`.
-template <class T>
-__device__ __forceinline__ void turn_alone(float (&x)[8], const T* row, int l, const RopeView& r, const float* cs,
-                                           const float* sn) {
-  const int half = r.rot / 2;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (r.pairs && 4 * l + i < half) rope_turn(x[2 * i], x[2 * i + 1], cs[4 * l + i], sn[4 * l + i]);
-  if (r.pairs) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = 8 * l + i;
-    if (e < half) x[i] = fmaf(x[i], cs[e], -value_of(row[e + half]) * sn[e]);
-    else if (e < r.rot) x[i] = fmaf(x[i], cs[e - half], value_of(row[e - half]) * sn[e - half]);
-  }
-}
-
-// A piece's fp32 values, turned.
-template <class T>
-__device__ __forceinline__ void turned(const Piece<T, true>& p, float (&x)[8], const T* row, int l, const RopeView& r,
-                                       const float* cs, const float* sn) {
-  const int half = r.rot / 2;
-  p.own.values(x);
-  if (r.pairs || half % 8) {
-    turn_alone(x, row, l, r, cs, sn);
-  } else if (8 * l < r.rot) {
-    const bool low = 8 * l < half;
-    const int at = low ? 8 * l : 8 * l - half;
-    float y[8];
-    p.partner.values(y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[at + i], y[i] * (low ? -sn[at + i] : sn[at + i]));
-  }
 }
 
 // For the largest scale, which may be too small.
@@ -207,11 +158,12 @@ __global__ void __launch_bounds__(kThreads8) write_rows(const __grid_constant__ 
       const KvPlace of = kv_place(c, p.seqs, p.positions, first + a, p.n);
       if (!of.page) continue;
       const float2 y = rope_angle(p.q.r, of.pos, i);
-      angles[0][a * (D / 2) + i] = y.x, angles[1][a * (D / 2) + i] = y.y;
+      const int at = angle_at<D>(a, i);
+      angles[0][at] = y.x, angles[1][at] = y.y;
     }
     __syncthreads();
     const float* cs = angles[0] + (t - first) * (D / 2);
-    if (is_key && ok) turned<T>(in, x, row, l, p.q.r, cs, cs + (angles[1] - angles[0]));
+    if (is_key && ok) turned<D>(in, x, row, l, p.q.r, cs, cs + (angles[1] - angles[0]));
     else in.own.values(x);
   } else {
     in.own.values(x);
@@ -256,14 +208,6 @@ struct Eights {
     at[1] = turns ? half + 8 * c : at[0] + 8;
   }
 };
-
-// Four angles' cosines or sines, from pair i (a multiple of 4) of row r on, in tables
-// where the lanes of a row read whole lines: D / 16 lanes the first four of their eight,
-// then the second four.
-template <int D>
-__device__ __forceinline__ int angle_at(int r, int i) {
-  return r * (D / 2) + ((i >> 2 & 1) * (D / 16) + (i >> 3)) * 4 + (i & 3);
-}
 
 // One head's block, by a warp: rows `of` (list entries, or -1; smem), the first of them
 // `first`.  D / 16 lanes have a row, 512 / D rows at a time; lanes whose row is not
@@ -321,7 +265,7 @@ __device__ __forceinline__ void write_block(const T* x, int64_t stride, const in
         for (int j = 0; j < 8; ++j) {
           const int d = e.at[k] + j;
           if (d >= rope.rot) continue;
-          const int pair = d < half ? d : d - half, at = angle_at<D>(r, pair & ~3) + (pair & 3);
+          const int pair = d < half ? d : d - half, at = angle_at<D>(r, pair);
           const float other = value_of(row[d < half ? d + half : d - half]);
           y[k][j] = fmaf(y[k][j], cs[at], d < half ? -other * sn[at] : other * sn[at]);
         }
@@ -396,10 +340,18 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
   const int end = min(begin + per_split, 2 * c.nkv);
   const int64_t t0 = (int64_t)chunk * tokens;
   const int a = tid / kBlockRows, ar = tid % kBlockRows;
-  if (tid < tokens) place[tid] = kv_place(c, p.seqs, p.positions, t0 + tid, p.n);
+  bool may = false;  // have a block written: not behind an entry that writes a lower row of it
+  if (tid < tokens) {
+    const int64_t t = t0 + tid;
+    const bool second = t > 0 && t < p.n && p.seqs[t - 1] == p.seqs[t] && p.positions[t - 1] < p.positions[t] &&
+                        p.positions[t - 1] >= 0 && p.positions[t - 1] / kBlockRows == p.positions[t] / kBlockRows;
+    place[tid] = kv_place(c, p.seqs, p.positions, t, p.n);
+    if (second) place[tid].page = nullptr;
+    may = place[tid].page;
+  }
   of[a][ar] = -1;
   if (!listed) pdl_wait();
-  __syncthreads();
+  if (!__syncthreads_or(may)) return;
   if (listed) {
     for (int e = tid; e < p.n; e += kThreads8) {
       const int s = p.seqs[e], pos = p.positions[e];
@@ -431,7 +383,7 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
         const int ra = e / half, j = e - ra * half;
         if (of[i][ra] < 0) continue;
         const float2 y = rope_angle(p.q.r, pos0 + ra, j);
-        const int at = angle_at<D>(ra, j & ~3) + (j & 3);
+        const int at = angle_at<D>(ra, j);
         angles[0][at] = y.x, angles[ROPE][at] = y.y;
       }
       __syncthreads();
@@ -450,28 +402,6 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
         write_block<D, T, ROPE ? TURN_ODD : 0>(from, p.stride, of[i], first, b, rope, angles[0], angles[ROPE]);
     }
   }
-}
-
-// The queries of a call, rotated by where their keys go.  Begins beside the rows' writing,
-// and ends behind it.
-template <class T>
-__global__ void __launch_bounds__(kRopeThreads) placed_rope(const __grid_constant__ Write8<T> p) {
-  extern __shared__ __align__(16) float q_angles[];
-  rope_rows<T>(p.q, blockIdx.x, q_angles, [&](int64_t t) {
-    const KvPlace at = kv_place(p.c, p.seqs, p.positions, t, p.n);
-    return at.page ? at.pos : -1;
-  });
-  pdl_wait();
-}
-template <class T>
-cudaError_t launch_placed_rope(Write8<T> p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rope_cut(p.q));
-  cfg.blockDim = dim3(kRopeThreads);
-  cfg.dynamicSmemBytes = rope_smem(p.q);
-  cfg.stream = s;
-  const BehindLast behind(&cfg);
-  return cudaLaunchKernelEx(&cfg, placed_rope<T>, p);
 }
 
 template <int D, class T, bool ROPE>
@@ -495,8 +425,11 @@ cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t strid
   // Without positions a sequence has one row, without a list every entry is a sequence of its own.
   if (!positions || !seqs) {
     constexpr int ITEMS = kThreads8 / (D / 8);
-    grid(((int64_t)n * items + ITEMS - 1) / ITEMS, true);
-    return cudaLaunchKernelEx(&cfg, write_rows<D, T, ROPE>, p);
+    const bool apart = ROPE && rope_many(p.q);
+    grid(((int64_t)n * items + ITEMS - 1) / ITEMS, !apart);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, write_rows<D, T, ROPE>, p);
+    if (e == cudaSuccess && apart) e = kv_rotate_queries(c, sizeof(T) == 4, seqs, positions, n, p.q, s);
+    return e;
   }
   const bool listed = n <= kListed;
   if (!listed) {
@@ -508,12 +441,12 @@ cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t strid
   const int tokens = std::min(std::max(n / 256, 1), kTokens8);
   const int64_t chunks = (n + tokens - 1) / tokens;
   const int steps = (items + kThreads8 / 32 - 1) / (kThreads8 / 32);  // a head of K or V for each warp
-  const int want = (int)std::min((int64_t)steps, std::max((int64_t)1, kBlockCtas / chunks));
+  const int want = (int)std::min((int64_t)steps, std::max((int64_t)1, (ROPE ? kTurnedCtas : kBlockCtas) / chunks));
   const int per_split = (steps + want - 1) / want * (kThreads8 / 32), splits = (items + per_split - 1) / per_split;
-  grid(chunks * splits, listed);
+  const bool apart = ROPE && rope_many(p.q);
+  grid(chunks * splits, !apart);
   cudaError_t e = cudaLaunchKernelEx(&cfg, write_blocks<D, T, ROPE>, p, tokens, splits, per_split, listed);
-  // Many queries have a launch of their own, which fits more CTAs on an SM.
-  if (e == cudaSuccess && ROPE && !listed && p.q.n) e = launch_placed_rope<T>(p, s);
+  if (e == cudaSuccess && apart) e = kv_rotate_queries(c, sizeof(T) == 4, seqs, positions, n, p.q, s);
   return e;
 }
 

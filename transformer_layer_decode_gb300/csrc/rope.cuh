@@ -181,36 +181,68 @@ __device__ __forceinline__ void rope_rows(const RopeRows& p, int block, float* s
   }
 }
 
-// Eight dimensions 8 l .. of a key, which the lanes of a row hold, turned; `cs` and `sn`
-// are of its position, `row` where the key was read from.  Every lane of the warp takes part;
-// lanes that do not `turn` keep what they have.
-template <int LANES, class T>
-__device__ __forceinline__ void rope_eight(const RopeView& r, float (&x)[8], int l, const float* cs, const float* sn,
-                                           const T* row, bool turn) {
-  const int half = r.rot / 2;
-  if (r.pairs) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (turn && 4 * l + i < half) rope_turn(x[2 * i], x[2 * i + 1], cs[4 * l + i], sn[4 * l + i]);
-  } else if (half % 8 == 0) {
-    const int far = half / 8;
-    const bool low = l < far, in = turn && l < 2 * far;
-    const int lane = threadIdx.x & 31, from = low ? lane + far : l < 2 * far ? lane - far : lane;
-    const int at = 8 * (low ? l : l - far);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_sync(0xffffffffu, x[i], from);
-      if (in) {
-        const float c = cs[at + i], s = low ? -sn[at + i] : sn[at + i];
-        x[i] = fmaf(x[i], c, other * s);
-      }
+// Whether rows are so many that they are rotated by a launch of their own, which fits
+// more CTAs on an SM than one that also writes rows.
+inline bool rope_many(const RopeRows& p) { return (int64_t)p.n * p.heads * p.d >= 1 << 23; }
+
+// Where pair i's cosine (or sine) of row r lies in a table of D / 2 of each, so that lanes
+// which have eight pairs each read whole lines: the first four of each eight, then the
+// second four.
+template <int D>
+__device__ __forceinline__ int angle_at(int r, int i) {
+  return r * (D / 2) + ((i >> 2 & 1) * (D / 16) + (i >> 3)) * 4 + (i & 3);
+}
+
+// Eight values of a row, at dimension 8 l of a head: as loaded, with (TURN) those that
+// they are turned with, if these are an aligned eight too.
+template <class T, bool TURN>
+struct Piece {
+  Eight<T> own, partner;
+  __device__ __forceinline__ void load(const T* row, int l, const RopeView& r) {
+    own.load(row + 8 * l);
+    if constexpr (TURN) {
+      const int half = r.rot / 2;
+      if (!r.pairs && half % 8 == 0 && 8 * l < r.rot) partner.load(row + (8 * l < half ? 8 * l + half : 8 * l - half));
     }
-  } else if (turn) {
+  }
+};
+
+// A piece's fp32 values, turned by its row's angles.
+template <int D, class T>
+__device__ __forceinline__ void turned(const Piece<T, true>& p, float (&x)[8], const T* row, int l, const RopeView& r,
+                                       const float* cs, const float* sn) {
+  const int half = r.rot / 2;
+  p.own.values(x);
+  if (r.pairs) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + angle_at<D>(0, 4 * l));
+    const float4 s = *reinterpret_cast<const float4*>(sn + angle_at<D>(0, 4 * l));
+    if (4 * l < half) rope_turn(x[0], x[1], c.x, s.x);
+    if (4 * l + 1 < half) rope_turn(x[2], x[3], c.y, s.y);
+    if (4 * l + 2 < half) rope_turn(x[4], x[5], c.z, s.z);
+    if (4 * l + 3 < half) rope_turn(x[6], x[7], c.w, s.w);
+  } else if (half % 8 == 0) {
+    if (8 * l >= r.rot) return;
+    const float sign = 8 * l < half ? -1.f : 1.f;
+    const int first = 8 * l < half ? 8 * l : 8 * l - half;
+    float y[8];
+    p.partner.values(y);
+#pragma unroll
+    for (int q = 0; q < 8; q += 4) {
+      const float4 c = *reinterpret_cast<const float4*>(cs + angle_at<D>(0, first + q));
+      const float4 s = *reinterpret_cast<const float4*>(sn + angle_at<D>(0, first + q));
+      x[q] = fmaf(x[q], c.x, sign * (y[q] * s.x));
+      x[q + 1] = fmaf(x[q + 1], c.y, sign * (y[q + 1] * s.y));
+      x[q + 2] = fmaf(x[q + 2], c.z, sign * (y[q + 2] * s.z));
+      x[q + 3] = fmaf(x[q + 3], c.w, sign * (y[q + 3] * s.w));
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = 8 * l + i;
-      if (e < half) x[i] = fmaf(x[i], cs[e], -value_of(row[e + half]) * sn[e]);
-      else if (e < r.rot) x[i] = fmaf(x[i], cs[e - half], value_of(row[e - half]) * sn[e - half]);
+      if (e >= r.rot) continue;
+      const int at = angle_at<D>(0, e < half ? e : e - half);
+      const float other = value_of(row[e < half ? e + half : e - half]);
+      x[i] = fmaf(x[i], cs[at], e < half ? -other * sn[at] : other * sn[at]);
     }
   }
 }
