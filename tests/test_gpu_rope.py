@@ -236,6 +236,70 @@ def test_append_rotated(io, fmt, layout, rot, hd, nkv, heads, R, n):
     assert torch.equal(a.append_rotated(1, r, q, k, v, seqs=seqs, positions=positions)[live], want[live])
 
 
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt", ["bf16", "q4", "q8"])
+@pytest.mark.parametrize("layout,rot,hd,nkv,heads,R,n", [
+    ("half", 128, 128, 8, 32, 64, 2100), ("interleaved", 64, 64, 5, 40, 16, 3301), ("half", 20, 128, 3, 1, 48, 2750),
+    ("half", 32, 64, 17, 2, 32, 1201), ("interleaved", 128, 128, 8, 2, 16, 4111)])
+def test_append_many_rotated(io, fmt, layout, rot, hd, nkv, heads, R, n):
+    """Rows enough for several turns of a CTA, and queries enough for a launch of their own or not."""
+    test_append_rotated(io, fmt, layout, rot, hd, nkv, heads, R, n)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q4", "q8"])
+@pytest.mark.parametrize("listed", [False, True])
+def test_steps_of_many_sequences_in_a_graph(fmt, listed):
+    """Many queries, of one row each and of a list, whose lists, rows and pages the kernels just before change."""
+    n, heads, nkv, hd, R, steps = 2100, 32, 2, 128, 16, 3
+    r = rope.Rotary(hd)
+
+    def make():
+        c = kv.KVCache(n_layers=1, n_kv_heads=nkv, head_dim=hd, page_rows=R, fmt=fmt, n_pages=2 * n, n_seqs=n, max_pages=2)
+        c.pool.zero_()
+        c.extend(n_new=ints([14 + i % 3 for i in range(n)]))
+        return c
+
+    a, b = make(), make()
+    seqs, pos = ints(range(n)), ints([0] * n)
+    q, k, v = (rows((n, h, hd), torch.bfloat16, h) for h in (heads, nkv, nkv + 1))
+    v = v[:, :nkv].contiguous()
+    out = torch.empty_like(q)
+
+    def step():
+        q.add_(0.25), k.mul_(1.5), v.mul_(-1.25)
+        a.extend()
+        torch.sub(a.lens, 1, out=pos)
+        if listed:
+            seqs.copy_(seqs.flip(0))
+            pos.copy_(pos[seqs])
+            a.append_rotated(0, r, q, k, v, seqs=seqs, positions=pos, q_out=out)
+        else:
+            a.append_rotated(0, r, q, k, v, q_out=out)
+
+    def same():
+        b.extend()
+        torch.cuda.synchronize()
+        b.append_rotated(0, r, None, k, v, seqs=seqs, positions=pos if listed else b.lens - 1)
+        torch.cuda.synchronize()
+        assert torch.equal(a.pool, b.pool)
+        assert torch.equal(out, r.rotate(q, pos))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(steps):
+        graph.replay()
+        same()
+    a.sync_status()
+    b.sync_status()
+
+
 def test_one_projection_s_rows_in_place():
     """q, k and v as slices of one tensor, q rotated where it lies; and keys alone."""
     r = rope.Rotary(64)

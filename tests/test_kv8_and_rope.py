@@ -184,7 +184,7 @@ def test_steps(lib):
 
 
 def test_python_refuses_before_it_calls():
-    for kw, word in (({"layout": "neox"}, "layout"), ({"scaling": "dynamic"}, "scaling"), ({"rot_dim": 130}, "rot_dim"),
+    for kw, word in (({"layout": "halves"}, "layout"), ({"scaling": "cubic"}, "scaling"), ({"rot_dim": 130}, "rot_dim"),
                      ({"rot_dim": 3}, "rot_dim"), ({"rot_dim": 1 << 33}, "rot_dim"), ({"frequencies": [1.0]}, "frequencies"),
                      ({"frequencies": np.ones(64), "scaling": "linear"}, "not scaled"), ({"magnitude": math.nan}, "magnitude"),
                      ({"device": "cpu"}, "CUDA")):

@@ -88,6 +88,10 @@ __device__ __forceinline__ KvPlace kv_place(const KvView& c, const int32_t* seqs
   else atomicOr(c.status, DEC_KV_BAD_INDEX);
   return at;
 }
+
+// The beginning of a kernel that runs beside the one before it, which has waited and
+// triggered: what launches before that one wrote is complete, and no line of an L1 is older.
+__device__ __forceinline__ void pdl_join() { __threadfence(); }
 #endif
 
 // A launch that is set up while the kernel before it runs (one that calls pdl_trigger) or

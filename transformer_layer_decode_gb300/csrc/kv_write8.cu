@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
   __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? kBlockRows * (D / 2) : 1];
   const KvView& c = p.c;
   if (listed) pdl_wait();
+  else if (threadIdx.x < 32) pdl_join();  // (those that read before they wait)
   pdl_trigger();
   if constexpr (ROPE) {
     if ((int)blockIdx.x >= p.blocks) {
