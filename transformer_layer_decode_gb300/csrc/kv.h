@@ -67,20 +67,24 @@ __device__ __noinline__ inline bool kv_bounds_failed(const KvView& c, int line) 
 
 #ifdef __CUDACC__
 // Where row t of a call's lists lies: its page's first byte (null: skipped; noted where
-// an index was bad), its row in it, its sequence and position.
+// an index was bad), its row in it, its sequence and position.  L2: read past the L1s, for
+// kernels that run beside the one before them, which has waited and triggered: what the
+// launches before that one wrote is complete then, but a line of an L1 may be older.
 struct KvPlace {
   uint8_t* page;
   int row, seq, pos;
 };
+template <bool L2 = false>
 __device__ __forceinline__ KvPlace kv_place(const KvView& c, const int32_t* seqs, const int32_t* positions, int64_t t, int n) {
+  auto look = [](const int32_t* p) { return L2 ? __ldcg(p) : *p; };
   KvPlace at{nullptr, 0, -1, 0};
-  const int s = t < n ? (seqs ? seqs[t] : (int)t) : -1;
+  const int s = t < n ? (seqs ? look(seqs + t) : (int)t) : -1;
   if (s < 0) return at;
   int page = -1;
   if (s < c.n_seqs) {
-    const int pos = positions ? positions[t] : c.lens[s] - 1;
+    const int pos = positions ? look(positions + t) : look(c.lens + s) - 1;
     if (pos >= 0 && pos < c.max_pages * c.page_rows) {
-      page = c.table[(int64_t)s * c.max_pages + pos / c.page_rows];
+      page = look(c.table + (int64_t)s * c.max_pages + pos / c.page_rows);
       at.row = pos % c.page_rows, at.seq = s, at.pos = pos;
     }
   }
@@ -89,9 +93,6 @@ __device__ __forceinline__ KvPlace kv_place(const KvView& c, const int32_t* seqs
   return at;
 }
 
-// The beginning of a kernel that runs beside the one before it, which has waited and
-// triggered: what launches before that one wrote is complete, and no line of an L1 is older.
-__device__ __forceinline__ void pdl_join() { __threadfence(); }
 #endif
 
 // A launch that is set up while the kernel before it runs (one that calls pdl_trigger) or

@@ -494,7 +494,7 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   // the first one's rounding, 2^-11 of it, and would lose its bits to fp16's smallest
   // step where the product is below 2^-3.
   static constexpr int kRoom = 9, kLow = 11;
-  static constexpr float kLift = kWhole ? kRoom : 0;
+  [[maybe_unused]] static constexpr float kLift = kWhole ? kRoom : 0;
   uint32_t a[2 * NB][kWhole ? 2 : 4];  // q
   uint32_t bias[kWhole ? 2 : 1];       // kWhole: -8 sum of q per block, in three pieces: operand of one product
   float f, f1;                         // score = f * product, in log2 units; kWhole: f of head 2t, f1 of the next
@@ -867,7 +867,7 @@ struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
   // above fp16's smallest step; kWhole has these 9 in the exponential, fp32 results
   // in what they multiply (see WarpQ4).
   static constexpr int kRoom = 9;
-  static constexpr float kLift = kWhole ? kRoom : 0;
+  [[maybe_unused]] static constexpr float kLift = kWhole ? kRoom : 0;
   uint32_t a[kSteps][kWhole ? 2 : 4];  // q: dimensions 64 (k / 4) + 16 t + 4 (k % 4) .. of step k
   float f, f1;                         // score = f * K's scale * product; kWhole: f of head 2t, f1 of the next
 

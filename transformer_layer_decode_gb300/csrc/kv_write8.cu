@@ -324,11 +324,12 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
   __shared__ int first_row[kTokens8];  // of a block that this entry has written, else -1
   __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? kBlockRows * (D / 2) : 1];
   const KvView& c = p.c;
+  // (behind kv_owners, its CTAs look up their own entries' places beside it)
   if (listed) pdl_wait();
-  else if (threadIdx.x < 32) pdl_join();  // (those that read before they wait)
   pdl_trigger();
   if constexpr (ROPE) {
     if ((int)blockIdx.x >= p.blocks) {
+      if (!listed) pdl_wait();
       rope_rows<T>(p.q, blockIdx.x - p.blocks, q_angles, [&](int64_t t) {
         const KvPlace at = kv_place(c, p.seqs, p.positions, t, p.n);
         return at.page ? at.pos : -1;
@@ -344,9 +345,12 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
   bool may = false;  // have a block written: not behind an entry that writes a lower row of it
   if (tid < tokens) {
     const int64_t t = t0 + tid;
-    const bool second = t > 0 && t < p.n && p.seqs[t - 1] == p.seqs[t] && p.positions[t - 1] < p.positions[t] &&
-                        p.positions[t - 1] >= 0 && p.positions[t - 1] / kBlockRows == p.positions[t] / kBlockRows;
-    place[tid] = kv_place(c, p.seqs, p.positions, t, p.n);
+    bool second = false;
+    if (t > 0 && t < p.n) {
+      const int was = __ldcg(p.positions + t - 1), now = __ldcg(p.positions + t);
+      second = __ldcg(p.seqs + t - 1) == __ldcg(p.seqs + t) && was < now && was >= 0 && was / kBlockRows == now / kBlockRows;
+    }
+    place[tid] = kv_place<true>(c, p.seqs, p.positions, t, p.n);
     if (second) place[tid].page = nullptr;
     may = place[tid].page;
   }
