@@ -402,9 +402,10 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  * calls of these may overlap as long as none reads rows that another writes
  * and each attention has a workspace of its own (8-bit pages: rows of a block that
  * another writes).
- * Attention, fork and compact are two launches each, of which the second reads
- * what the first left in the workspace or the scratch: host threads that queue
- * calls on one stream must not do so at the same time where these share either,
+ * Attention, fork, compact and append (long lists, 8-bit pages) are two launches
+ * or more, of which one reads what another left in the workspace or the scratch:
+ * host threads that queue calls on one stream must not do so at the same time
+ * where these share either (of the scratch, appends share nothing with appends),
  * nor may two threads read the status at the same time.
  *
  * Lists of sequences are device int32; a negative entry is padding and is
@@ -542,7 +543,7 @@ int dec_rope_rotate(const dec_rope* r, const void* x, void* out, int type, int64
 /* Source: none on the pages.  dec_kv_append of keys that are not rotated yet, with
  * their queries: row t of k, rotated by its position, and of v are written as
  * dec_kv_append does (k rounded once, from fp32), and row t of q ([n_q_heads][head_dim],
- * rows q_stride elements apart) is rotated into q_out, in the same launch.  rope's
+ * rows q_stride elements apart) is rotated into q_out, in the same call.  rope's
  * head_dim is the cache's.  n_q_heads 0: no q.  q_out may be q with the same stride;
  * it must not overlap q otherwise, nor k or v.  The rows of q_out of entries that are
  * skipped are left as they were. */
