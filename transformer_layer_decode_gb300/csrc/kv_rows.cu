@@ -151,12 +151,14 @@ constexpr int kMaxTokens = 32;  // of a CTA
 // 57).  In fp32, 306 MB, 51 and 51 us (46); from and to bf16 pages, 268 MB, 43 (40),
 // fp32 and bf16 pages, 402 MB, 61 and 62 (60).  Four rounds:
 // two are 10 % slower, eight 15 % in fp32.  (The view as a grid constant: 48 registers and a
-// fifth CTA an SM; a copy of it, 52, and rows written to 4-bit pages 41 us for 38.)
+// fifth CTA an SM; a copy of it, 52, and rows written to 4-bit pages 41 us for 38.  8-bit
+// pages are read from a copy: 34.4 us for 35.5.)
 template <int D, int F, class T, bool READ, int ROUNDS>
-__global__ void __launch_bounds__(kRowWarps * 32) kv_rows(const __grid_constant__ KvView c, T* k, T* v,
+__global__ void __launch_bounds__(kRowWarps * 32) kv_rows(const __grid_constant__ KvView view, T* k, T* v,
                                                           int64_t stride, const int32_t* seqs,
                                                           const int32_t* positions, int n, int tokens,
                                                           int items_per_token, bool wide) {
+  std::conditional_t<F == KV_Q8, const KvView, const KvView&> c = view;
   constexpr int LANES = D / 8, NB = D / 32, RPR = 32 / LANES;  // rows of a round
   __shared__ uint8_t* token_page[kMaxTokens];
   __shared__ int token_row[kMaxTokens];
