@@ -572,8 +572,8 @@ int dec_kv_append_rotated(const dec_kv_cache* c, int layer, const dec_rope* rope
  * the other blocks hold.  For bf16 results the sums stay in the tensor cores,
  * which cut them off, not round: about 2^-23 of a sum for each 16 rows, and over
  * 4-bit pages up to 2^-20 of scale * sum |q| * 8 * (its K scale) of a score.
- * Over 8-bit pages weights keep 22 bits (11 for bf16 results), down to a step of
- * 2^-33 where the largest counts 1 or more, and a tile's products are added in fp32
+ * Over 8-bit pages weights keep 22 bits, down to a step of 2^-33 where the largest
+ * counts 1 or more, and a tile's products are added in fp32
  * (sums of values times weights of up to 2^14); a row whose block's scale is NaN
  * counts as not finite, and so does one that shares its block.
  * q, o and their strides are multiples of 16 bytes; o must not overlap q.  n and

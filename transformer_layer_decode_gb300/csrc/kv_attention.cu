@@ -854,15 +854,17 @@ struct WarpQ4 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
 // pipe, in fp32; nothing of a scale enters an operand, whose range is that of
 // the codes and of q or the weights alone.  A code b stands as the fp16 number 1024 + b
 // behind a byte permutation, b - 128 behind one addition.  q is scaled by a power of two
-// and taken in two fp16 pieces (22 bits; bf16 q needs one), and so are the weights for
-// fp32 results; for bf16 results they are one (11 bits).  With one piece each the scores
-// are computed as S^T = K q^T, 16 rows at a time, and the weights turned by movmatrix.
+// and taken in two fp16 pieces (22 bits; bf16 q needs one), and so are the weights.  (With
+// one of 11 bits for bf16 results, 9 % of these were not the nearest bf16 numbers, and are
+// 0.03 to 0.05 % with two; 24 long sequences 378 -> 382 us, a batch with a window 122 -> 126.)
+// With one piece of q the scores are computed as S^T = K q^T, 16 rows at a time, and the
+// weights turned by movmatrix.
 template <int D, class T>
 struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>> {
   using Sums = WarpSums<D>;
   using L = Tile<D, KV_Q8>;
   static constexpr int NB = Sums::NB, kTiles = L::kStep, kSteps = D / 16;
-  static constexpr bool kWhole = sizeof(T) == 2;  // q, and the weights, are one piece
+  static constexpr bool kWhole = sizeof(T) == 2;  // q is one piece
   // The largest weight enters its products as 2^9 to 2^(9 + kSlack), the others so far
   // above fp16's smallest step; kWhole has these 9 in the exponential, fp32 results
   // in what they multiply (see WarpQ4).
@@ -1012,17 +1014,17 @@ struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
           v[i][0] = u.x, v[i][1] = u.y;
         }
       }
-      constexpr int kPieces = kWhole ? 1 : 2;
-      uint32_t pw[kPieces][2];  // weights: rows 2t, 2t + 1 of each half, of head g
+      uint32_t pw[2][2];  // weights, in two pieces: rows 2t, 2t + 1 of each half, of head g
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
+        constexpr float kUp = kWhole ? 1 : 1 << kRoom;
+        float y0 = w[4 * k + 2 * b] * kUp, y1 = w[4 * k + 2 * b + 1] * kUp;
+        pw[0][b] = take_f16(y0, y1);
+        pw[1][b] = pack_f16(y0, y1);
         if constexpr (kWhole) {
-          const uint32_t rows = pack_f16(w[4 * k + 2 * b], w[4 * k + 2 * b + 1]);
-          asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pw[0][b]) : "r"(rows));
-        } else {
-          float y0 = w[4 * k + 2 * b] * (1 << kRoom), y1 = w[4 * k + 2 * b + 1] * (1 << kRoom);
-          pw[0][b] = take_f16(y0, y1);
-          pw[kPieces - 1][b] = pack_f16(y0, y1);
+#pragma unroll
+          for (uint32_t* x : {&pw[0][b], &pw[1][b]})
+            asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(*x) : "r"(*x));
         }
       }
 #pragma unroll
@@ -1034,7 +1036,7 @@ struct WarpQ8 : std::conditional_t<sizeof(T) == 2, WarpHeadPair<D>, WarpHead<D>>
           const uint32_t z1 = __byte_perm(v[2][j], v[3][j], y ? 0x7362 : 0x5140);
           const uint32_t a0 = codes(z0, kLower), a1 = codes(z0, kUpper), a2 = codes(z1, kLower), a3 = codes(z1, kUpper);
           float o[4] = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (!kWhole) mma_f16(o, a0, a1, a2, a3, pw[kPieces - 1][0], pw[kPieces - 1][1]);
+          mma_f16(o, a0, a1, a2, a3, pw[1][0], pw[1][1]);
           mma_f16(o, a0, a1, a2, a3, pw[0][0], pw[0][1]);
           this->add_tile(this->acc[j][y], o, v_scale[k]);
         }
