@@ -395,6 +395,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  *           and by append for 8-bit pages (a part of each layer's own)
  *
  * An empty cache is table = -1 (all bytes 0xFF), lens = refs = status = 0.
+ * Of 8-bit pages that a caller puts into the table by itself the scales must be 0, or
+ * those of rows that it wants kept: dec_kv_append looks at what a scale was.
  * A caller that takes rows off a sequence's end by itself (lens) must also take
  * the pages that are then past it out of table and refs.
  * Calls on one cache run one after another (one stream, or ordered by the
@@ -402,8 +404,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  * calls of these may overlap as long as none reads rows that another writes
  * and each attention has a workspace of its own (8-bit pages: rows of a block that
  * another writes).
- * Attention, fork, compact and append (long lists, 8-bit pages) are two launches
- * or more, of which one reads what another left in the workspace or the scratch:
+ * Attention, fork, compact, and for 8-bit pages extend and append (long lists) are two
+ * launches or more, of which one reads what another left in the workspace or the scratch:
  * host threads that queue calls on one stream must not do so at the same time
  * where these share either (of the scratch, appends share nothing with appends),
  * nor may two threads read the status at the same time.
@@ -593,7 +595,8 @@ int dec_kv_attention_workspace(const dec_kv_cache* c, size_t* bytes);
 /* Makes each listed sequence n_new[i] rows longer (NULL: one), and gives it
  * the pages that the new rows need: in list order, the free pages from the
  * lowest number up.  All or nothing: on an error bit no sequence changes.
- * n <= n_seqs.  The new rows hold nothing until dec_kv_append writes them. */
+ * n <= n_seqs.  The new rows hold nothing until dec_kv_append writes them; the scales
+ * of new 8-bit pages are 0. */
 int dec_kv_extend(const dec_kv_cache* c, const int32_t* seqs, const int32_t* n_new, int n,
                   dec_stream_t stream);
 

@@ -4,6 +4,7 @@
 // Each call that allocates or moves pages plans in one CTA (its work is a scan
 // over refs, a few ints per page), which checks everything and changes nothing
 // on an error, and carries the plan out in a second launch over the whole GPU.
+// (extend has a second one for 8-bit pages, whose scales it clears.)
 // All choices are by rank (the k-th page needed gets the k-th lowest free one),
 // so results do not depend on the order in which threads run.
 #include "common.cuh"
@@ -98,7 +99,7 @@ template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_alloc(KvView c, const int32_t* a, const int32_t* b, int n) {
   __shared__ uint32_t seen[65536 / 32];
   __shared__ int bad_bits;
-  if (FORK) pdl_trigger();
+  pdl_trigger();  // (nothing before the launch behind it waits for the end of this one)
   const int tid = threadIdx.x;
   int32_t* offsets = c.scratch + kv_scratch_offsets(c.n_pages, c.n_seqs);
   int32_t* moves = c.scratch + kv_scratch_moves(c.n_pages);
@@ -251,6 +252,24 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_compact(KvView c) {
   }
 }
 
+// 8-bit pages that a sequence has been given: scales of 0 in every layer.  A block that is
+// not begun at its first row keeps its old scale where it is the larger one, and that of
+// a page's last owner, or of memory that no one wrote, is none of its own.
+__global__ void __launch_bounds__(kCopyThreads) kv_fresh(KvView c, int n_layers) {
+  pdl_wait();
+  const int32_t* list = c.scratch + kKvScratchHead;
+  const uint32_t scales = (uint32_t)c.nkv * (c.page_rows / kBlockRows);  // of a page's K, or V
+  const int64_t total = (int64_t)c.scratch[SC_MOVES] * n_layers * 2 * scales;
+  for (int64_t e = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; e < total; e += (int64_t)gridDim.x * kCopyThreads) {
+    const uint32_t i = (uint32_t)(e % scales);
+    const int64_t rest = e / scales, page = rest / 2 / n_layers;
+    const int layer = (int)(rest / 2 % n_layers), at = list[page];
+    if (!KV_IN_BOUNDS(c, page < c.n_pages && at >= 0 && at < c.n_pages)) continue;
+    uint8_t* half = c.pool + ((int64_t)layer * c.n_pages + at) * c.page_bytes + rest % 2 * c.half_bytes;
+    reinterpret_cast<float*>(half + c.nkv * c.head_bytes)[i] = 0.f;
+  }
+}
+
 // Carries out a plan: copies the listed pages in every layer; FORK: writes the
 // children's table rows and counts; otherwise (compact) renames the pages in
 // every table.
@@ -386,8 +405,14 @@ extern "C" int dec_kv_extend(const dec_kv_cache* c, const int32_t* seqs, const i
                              dec_stream_t stream) {
   if (int rc = check_list(c, n)) return rc;
   if (n == 0) return DEC_OK;
-  const cudaLaunchConfig_t cfg = config(1, kPlanThreads, stream);
-  return launched(cudaLaunchKernelEx(&cfg, kv_plan_alloc<false>, kv_view(*c, 0), seqs, n_new, n));
+  const bool blocks = c->format == DEC_KV_Q8T16;
+  int sms = 0;
+  if (blocks)
+    if (int rc = sm_count(&sms)) return rc;
+  const KvView v = kv_view(*c, 0);
+  const cudaLaunchConfig_t plan = config(1, kPlanThreads, stream);
+  const int rc = launched(cudaLaunchKernelEx(&plan, kv_plan_alloc<false>, v, seqs, n_new, n));
+  return rc || !blocks ? rc : launched(launch_after(kv_fresh, 2 * sms, stream, v, (int)c->n_layers));
 }
 
 extern "C" int dec_kv_fork(const dec_kv_cache* c, const int32_t* parents, const int32_t* children, int n,

@@ -105,6 +105,8 @@ class KVCache:
         else:
             device = torch.device("cuda") if device is None else torch.device(device)
             pool = torch.empty(n_layers, n_pages, self.page_bytes, dtype=torch.uint8, device=device)
+            if fmt == "q8":  # (what a block's scale was counts where it is not begun at its first row)
+                pool.view(n_layers, n_pages, 2, -1)[..., n_kv_heads * page_rows * head_dim:] = 0
             table = torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device)
             lens = torch.zeros(n_seqs, dtype=torch.int32, device=device)
             refs = torch.zeros(n_pages, dtype=torch.int32, device=device)
