@@ -95,8 +95,8 @@ def test_a_page_s_next_owner():
 def test_a_new_cache_without_extend():
     """Pages that the caller puts into the table of a cache made here, on memory that held something."""
     p = ref.Pages8(2, 64, 32)
-    junk = torch.full((64, 1 << 20), 0x7E, dtype=torch.uint8, device="cuda")
-    del junk
+    junk = torch.full((2, 64, p.page_bytes), 0x7E, dtype=torch.uint8, device="cuda")
+    del junk  # (the allocator hands it out again)
     c = kv.KVCache(n_layers=2, n_kv_heads=2, head_dim=64, page_rows=32, fmt="q8", n_pages=64, n_seqs=2, max_pages=3)
     c.table.copy_(ints([[5, 0, 63], [7, 8, 9]]))
     c.lens.fill_(80)
