@@ -67,24 +67,20 @@ __device__ __noinline__ inline bool kv_bounds_failed(const KvView& c, int line) 
 
 #ifdef __CUDACC__
 // Where row t of a call's lists lies: its page's first byte (null: skipped; noted where
-// an index was bad), its row in it, its sequence and position.  L2: read past the L1s, for
-// kernels that run beside the one before them, which has waited and triggered: what the
-// launches before that one wrote is complete then, but a line of an L1 may be older.
+// an index was bad), its row in it, its sequence and position.
 struct KvPlace {
   uint8_t* page;
   int row, seq, pos;
 };
-template <bool L2 = false>
 __device__ __forceinline__ KvPlace kv_place(const KvView& c, const int32_t* seqs, const int32_t* positions, int64_t t, int n) {
-  auto look = [](const int32_t* p) { return L2 ? __ldcg(p) : *p; };
   KvPlace at{nullptr, 0, -1, 0};
-  const int s = t < n ? (seqs ? look(seqs + t) : (int)t) : -1;
+  const int s = t < n ? (seqs ? seqs[t] : (int)t) : -1;
   if (s < 0) return at;
   int page = -1;
   if (s < c.n_seqs) {
-    const int pos = positions ? look(positions + t) : look(c.lens + s) - 1;
+    const int pos = positions ? positions[t] : c.lens[s] - 1;
     if (pos >= 0 && pos < c.max_pages * c.page_rows) {
-      page = look(c.table + (int64_t)s * c.max_pages + pos / c.page_rows);
+      page = c.table[(int64_t)s * c.max_pages + pos / c.page_rows];
       at.row = pos % c.page_rows, at.seq = s, at.pos = pos;
     }
   }
@@ -96,8 +92,9 @@ __device__ __forceinline__ KvPlace kv_place(const KvView& c, const int32_t* seqs
 #endif
 
 // A launch that is set up while the kernel before it runs (one that calls pdl_trigger) or
-// ends: each of its threads begins with pdl_wait, behind which it is as any other (a
-// kernel of which a block left without waiting could be over before the one before it).
+// ends.  Each of its threads calls pdl_wait before its first access to global memory:
+// only behind it is what earlier kernels wrote there to be seen, and a kernel of which a
+// block left without waiting could be over before the one before it.
 struct BehindLast {
   cudaLaunchAttribute pdl = {};
   explicit BehindLast(cudaLaunchConfig_t* cfg) {
@@ -113,9 +110,6 @@ struct RopeRows;
 // dec_kv_append to 8-bit pages (and dec_kv_append_rotated, with q).
 cudaError_t kv_write8(const KvView& c, int head_dim, bool f32, const void* k, const void* v, int64_t stride,
                       const int32_t* seqs, const int32_t* positions, int n, const RopeRows* q, cudaStream_t s);
-// Behind a launch on the same stream that triggers once it has waited for what is before it.
-cudaError_t kv_rotate_queries(const KvView& c, bool f32, const int32_t* seqs, const int32_t* positions, int n, RopeRows q,
-                              cudaStream_t s);
 
 // Checks a cache (its pointers too, with `memory`); DEC_OK or the error, recorded.
 int kv_check(const dec_kv_cache* c, bool memory);

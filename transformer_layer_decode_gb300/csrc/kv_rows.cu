@@ -75,8 +75,8 @@ constexpr int kFewRounds = 8192;  // (about a GPU full of warps)
 // CTAs beyond which they take more tokens each (half or 1.5 times as many: up to
 // 6 % slower).
 constexpr int kManyCtas = 2400;
-// Rotated rows: CTAs that the GPU holds at once, and rounds of a CTA's warps at most.
-constexpr int kTurnedCtas = 456, kTurnedTurns = 6;
+// Rotated rows: rounds of a CTA's warps at most.
+constexpr int kTurnedTurns = 6;
 
 // 1 / s to a few 2^-24 of itself.
 __device__ __forceinline__ float reciprocal(float s) {
@@ -145,7 +145,7 @@ constexpr int kMaxTokens = 32;  // of a CTA
 // 2 j + 1, two whole 16-bit words of the row's codes.
 //
 // What bounds it: 8185 rows of 32 heads of 128 in bf16, 172 MB with their 4-bit
-// rows, are written in 37 us and read in 33, where the bytes take 26: latency (a
+// rows, are written in 38 us and read in 33, where the bytes take 26: latency (a
 // CTA's look-up and the barrier behind it, then its rows' loads, then amax, scale,
 // quotients and digits; issue is active in 67 and 59 %, the integer pipe in 53 and
 // 57).  In fp32, 306 MB, 51 and 51 us (46); from and to bf16 pages, 268 MB, 43 (40),
@@ -267,9 +267,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_rows(const __grid_constant_
 // and write values, the others rotate queries.  Many rows are loaded before it is known
 // where they go and how they turn (8185 rows of 32 heads of fp32 to bf16 pages 79 -> 72 us),
 // those of bf16 also the next ones before these are coded (4093 rows of 8 heads 15.0 -> 11.7;
-// of fp32 that takes the registers of a third CTA an SM: 88).
-template <int D, int F, class T, int ROUNDS>
-__global__ void __launch_bounds__(kRowWarps * 32, sizeof(T) == 4 || ROUNDS > 1 ? 3 : 4)
+// of fp32 that takes the registers of a third CTA an SM: 88).  CTAs: of an SM; of many rows of
+// bf16 three, which leaves them the registers for that (8185 rows of 32 heads to bf16 pages
+// 56 us, four 64), but four beside queries, whose CTAs have to fit as well (4093 rows of 8
+// heads and 32 of queries 23 us, three 26); of fp32 four (8185 rows 68 us, three 72).
+template <int D, int F, class T, int ROUNDS, int CTAS>
+__global__ void __launch_bounds__(kRowWarps * 32, CTAS)
     kv_rows_rotated(const __grid_constant__ KvView c, const T* k, const T* v, int64_t stride, const int32_t* seqs,
                     const int32_t* positions, int n, int tokens, int items_per_token, int blocks,
                     const __grid_constant__ RopeRows q) {
@@ -363,15 +366,15 @@ __global__ void kv_take_status(int32_t* status, int32_t* taken) { *taken = atomi
 // Tokens of a CTA that rotates many rows, a multiple of `least`.  Its beginning, with the
 // angles of its tokens, takes as long as two of its warps' turns, and the last CTAs to begin
 // should have others beside them: so the least of waves times their length (8 heads of
-// fp32, 4093 rows: 12 tokens 13.2 us, 8 17.3, 2 18.1; 2500 rows: 6 tokens 7.6, 12 10.5).  More
-// than 6 turns no longer help (8185 rows of 32 heads of bf16: 3 tokens 55 us, 13 60).
-inline int turned_tokens(int n, int least, int items) {
+// fp32, 4093 rows: 8 tokens 12.9 us, 12 15.6, 2 16.2; 2500 rows: 6 tokens 8.9, 12 11.3).  More
+// than 6 turns seldom help (8185 rows of 32 heads of bf16: 3 tokens 55 us, 6 52, 12 57, 16 68).
+inline int turned_tokens(int n, int least, int items, int resident) {
   int best = least;
   int64_t cost = INT64_MAX;
   for (int tokens = least; tokens <= kMaxTokens; tokens += least) {
     const int turns = (tokens * items + kRowWarps - 1) / kRowWarps;
     if (turns > kTurnedTurns && tokens > least) break;
-    const int64_t ctas = (n + (int64_t)tokens - 1) / tokens, waves = (ctas + kTurnedCtas - 1) / kTurnedCtas;
+    const int64_t ctas = (n + (int64_t)tokens - 1) / tokens, waves = (ctas + resident - 1) / resident;
     if (waves * (turns + 2) < cost) cost = waves * (turns + 2), best = tokens;
   }
   return best;
@@ -388,7 +391,8 @@ cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const
   // enough tokens for every warp of a CTA, or a multiple where there are CTAs enough
   const int least = (kRowWarps + items - 1) / items;
   int tokens = std::min(std::max((n / kManyCtas + least - 1) / least, 1) * least, kMaxTokens);
-  if (q && !few) tokens = turned_tokens(n, least, items);
+  const int turned_ctas = sizeof(T) == 2 && q && !q->n ? 3 : 4;
+  if (q && !few) tokens = turned_tokens(n, least, items, turned_ctas * kSms);
   const int blocks = (n + tokens - 1) / tokens;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -398,15 +402,16 @@ cudaError_t launch_rows(const KvView& c, void* k, void* v, int64_t stride, const
   if constexpr (!READ) {
     if (q) {
       RopeRows rows = *q;
-      const bool apart = rope_many(rows);
-      if (rows.n && !apart) {
+      if (rows.n) {
         cfg.gridDim.x += (unsigned)rope_cut(rows);
         cfg.dynamicSmemBytes = rope_smem(rows);
       }
-      const cudaError_t e = cudaLaunchKernelEx(&cfg, few ? kv_rows_rotated<D, F, T, 1> : kv_rows_rotated<D, F, T, kTurnedRounds>,
-                                               c, static_cast<const T*>(k), static_cast<const T*>(v), stride, seqs, positions,
-                                               n, tokens, items, blocks, rows);
-      return e == cudaSuccess && apart ? kv_rotate_queries(c, sizeof(T) == 4, seqs, positions, n, rows, s) : e;
+      auto kernel = kv_rows_rotated<D, F, T, 1, 4>;
+      if (!few) kernel = kv_rows_rotated<D, F, T, kTurnedRounds, 4>;
+      if constexpr (sizeof(T) == 2)
+        if (!few && turned_ctas == 3) kernel = kv_rows_rotated<D, F, T, kTurnedRounds, 3>;
+      return cudaLaunchKernelEx(&cfg, kernel, c, static_cast<const T*>(k), static_cast<const T*>(v), stride, seqs,
+                                positions, n, tokens, items, blocks, rows);
     }
   }
   return cudaLaunchKernelEx(&cfg, few ? kv_rows<D, F, T, READ, 1> : kv_rows<D, F, T, READ, kRowRounds>, c,

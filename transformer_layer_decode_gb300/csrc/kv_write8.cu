@@ -15,9 +15,17 @@ namespace {
 constexpr int kThreads8 = 256;
 constexpr int kTokens8 = 16;     // list entries of a CTA of write_blocks, at most
 static_assert(kTokens8 * kBlockRows == kThreads8, "a thread for each row of each entry's block");
-constexpr int kListed = 512;     // lists up to this length are looked through by every CTA
-constexpr int kBlockCtas = 1216;  // of write_blocks, where the heads are enough for them
-constexpr int kTurnedCtas = 456;  // (each begins with the angles of its blocks)
+// Lists up to this length are looked through by every CTA; of longer ones a launch before
+// notes who writes which row (512 rows of 8 heads: 4.8 us, noted 6.0; 1024: 6.3 and 7.4;
+// 2048: 10.0 and 7.7.  Of 2 heads 4.1 and 5.7, 5.2 and 5.7, 8.1 and 6.1).
+constexpr int kListed = 1024;
+// CTAs of write_blocks, where the heads are enough for them (1000 rows of 32 heads of
+// bf16: 912 CTAs 13.0 us, 1216 11.8, 1824 11.0; 8185 rows: 43.5, 40.2, 39.2, but 2432 41.1).
+constexpr int kBlockCtas = 8 * kSms;
+// With keys that turn each begins with the angles of its blocks (4093 rows of 8 heads and 32
+// of queries: 24.4 us, 1216 CTAs 27.2; the other way round where a block has many heads:
+// 1000 rows of 32 and 128 heads 36.9, and 25.6).
+constexpr int kTurnedCtas = 3 * kSms;
 constexpr uint32_t kLeastScale = 1u << 23, kMostScale = 248u << 23;  // 2^-126, 2^121
 
 // The entry that writes each row: owners[page][row], for write_blocks' CTAs.  (What
@@ -324,12 +332,10 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
   __shared__ int first_row[kTokens8];  // of a block that this entry has written, else -1
   __shared__ __align__(16) float angles[ROPE ? 2 : 1][ROPE ? kBlockRows * (D / 2) : 1];
   const KvView& c = p.c;
-  // (behind kv_owners, its CTAs look up their own entries' places beside it)
-  if (listed) pdl_wait();
+  pdl_wait();
   pdl_trigger();
   if constexpr (ROPE) {
     if ((int)blockIdx.x >= p.blocks) {
-      if (!listed) pdl_wait();
       rope_rows<T>(p.q, blockIdx.x - p.blocks, q_angles, [&](int64_t t) {
         const KvPlace at = kv_place(c, p.seqs, p.positions, t, p.n);
         return at.page ? at.pos : -1;
@@ -347,15 +353,14 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 4 ? 2 : ROPE ? 3 : 4)
     const int64_t t = t0 + tid;
     bool second = false;
     if (t > 0 && t < p.n) {
-      const int was = __ldcg(p.positions + t - 1), now = __ldcg(p.positions + t);
-      second = __ldcg(p.seqs + t - 1) == __ldcg(p.seqs + t) && was < now && was >= 0 && was / kBlockRows == now / kBlockRows;
+      const int was = p.positions[t - 1], now = p.positions[t];
+      second = p.seqs[t - 1] == p.seqs[t] && was < now && was >= 0 && was / kBlockRows == now / kBlockRows;
     }
-    place[tid] = kv_place<true>(c, p.seqs, p.positions, t, p.n);
+    place[tid] = kv_place(c, p.seqs, p.positions, t, p.n);
     if (second) place[tid].page = nullptr;
     may = place[tid].page;
   }
   of[a][ar] = -1;
-  if (!listed) pdl_wait();
   if (!__syncthreads_or(may)) return;
   if (listed) {
     for (int e = tid; e < p.n; e += kThreads8) {
@@ -418,10 +423,10 @@ cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t strid
   cfg.blockDim = dim3(kThreads8);
   cfg.stream = s;
   const BehindLast behind(&cfg);
-  auto grid = [&](int64_t blocks, bool queries) {
+  auto grid = [&](int64_t blocks) {
     p.blocks = (int)blocks;
     cfg.gridDim = dim3((unsigned)blocks);
-    if (ROPE && queries && p.q.n) {
+    if (ROPE && p.q.n) {
       cfg.gridDim.x += (unsigned)rope_cut(p.q);
       cfg.dynamicSmemBytes = rope_smem(p.q);
     }
@@ -430,11 +435,8 @@ cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t strid
   // Without positions a sequence has one row, without a list every entry is a sequence of its own.
   if (!positions || !seqs) {
     constexpr int ITEMS = kThreads8 / (D / 8);
-    const bool apart = ROPE && rope_many(p.q);
-    grid(((int64_t)n * items + ITEMS - 1) / ITEMS, !apart);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, write_rows<D, T, ROPE>, p);
-    if (e == cudaSuccess && apart) e = kv_rotate_queries(c, sizeof(T) == 4, seqs, positions, n, p.q, s);
-    return e;
+    grid(((int64_t)n * items + ITEMS - 1) / ITEMS);
+    return cudaLaunchKernelEx(&cfg, write_rows<D, T, ROPE>, p);
   }
   const bool listed = n <= kListed;
   if (!listed) {
@@ -448,11 +450,8 @@ cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t strid
   const int steps = (items + kThreads8 / 32 - 1) / (kThreads8 / 32);  // a head of K or V for each warp
   const int want = (int)std::min((int64_t)steps, std::max((int64_t)1, (ROPE ? kTurnedCtas : kBlockCtas) / chunks));
   const int per_split = (steps + want - 1) / want * (kThreads8 / 32), splits = (items + per_split - 1) / per_split;
-  const bool apart = ROPE && rope_many(p.q);
-  grid(chunks * splits, !apart);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, write_blocks<D, T, ROPE>, p, tokens, splits, per_split, listed);
-  if (e == cudaSuccess && apart) e = kv_rotate_queries(c, sizeof(T) == 4, seqs, positions, n, p.q, s);
-  return e;
+  grid(chunks * splits);
+  return cudaLaunchKernelEx(&cfg, write_blocks<D, T, ROPE>, p, tokens, splits, per_split, listed);
 }
 
 }  // namespace

@@ -57,32 +57,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   rope_rows<T>(p, blockIdx.x, angles, [&](int64_t t) { return positions ? positions[t] : (int)t; });
 }
 
-// The queries of an append, rotated by where their keys go.  Begins beside the rows'
-// writing, and ends behind it.
-template <class T>
-__global__ void __launch_bounds__(kRopeThreads) placed_rope(const __grid_constant__ RopeRows p, const __grid_constant__ KvView c,
-                                                            const int32_t* seqs, const int32_t* positions, int n) {
-  extern __shared__ __align__(16) float angles[];
-  __threadfence();  // (no line of an L1 is older than the launches before; loads past the L1s take 3 us of 8185 rows)
-  rope_rows<T>(p, blockIdx.x, angles, [&](int64_t t) {
-    const KvPlace at = kv_place(c, seqs, positions, t, n);
-    return at.page ? at.pos : -1;
-  });
-  pdl_wait();
-}
-
 }  // namespace
-
-cudaError_t tld::kv_rotate_queries(const KvView& c, bool f32, const int32_t* seqs, const int32_t* positions, int n,
-                                   RopeRows q, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rope_cut(q));
-  cfg.blockDim = dim3(kRopeThreads);
-  cfg.dynamicSmemBytes = rope_smem(q);
-  cfg.stream = s;
-  const BehindLast behind(&cfg);
-  return cudaLaunchKernelEx(&cfg, f32 ? placed_rope<float> : placed_rope<uint16_t>, q, c, seqs, positions, n);
-}
 
 extern "C" int dec_rope_frequencies(int rot_dim, double theta, int scaling, double factor, double context, double slow,
                                     double fast, double* frequency, float* magnitude) {

@@ -60,7 +60,7 @@ __device__ __forceinline__ int rope_over(int e, uint32_t by) { return by ? (int)
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 32;           // of a CTA, at most
 constexpr int kRopeSmem = 32 * 1024;      // its cosines and sines, at most
-constexpr int kRopeCtas = 608;            // that the GPU holds at once
+constexpr int kRopeCtas = 4 * kSms;       // that the GPU holds at once
 
 constexpr int max_int(int a, int b) { return a > b ? a : b; }
 
@@ -180,10 +180,6 @@ __device__ __forceinline__ void rope_rows(const RopeRows& p, int block, float* s
     }
   }
 }
-
-// Whether rows are so many that they are rotated by a launch of their own, which fits
-// more CTAs on an SM than one that also writes rows.
-inline bool rope_many(const RopeRows& p) { return (int64_t)p.n * p.heads * p.d >= 1 << 23; }
 
 // Where pair i's cosine (or sine) of row r lies in a table of D / 2 of each, so that lanes
 // which have eight pairs each read whole lines: the first four of each eight, then the

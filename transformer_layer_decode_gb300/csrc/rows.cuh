@@ -115,6 +115,8 @@ __device__ __forceinline__ float value_of(uint16_t x) { return __uint_as_float((
 __device__ __forceinline__ void put(float& to, float x) { to = x; }
 __device__ __forceinline__ void put(uint16_t& to, float x) { to = f32_to_bf16_bits(x); }
 
+constexpr int kSms = 152;  // of a GB300
+
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
 
 }  // namespace tld
