@@ -508,9 +508,14 @@ enum dec_rope_scaling {
   DEC_ROPE_LINEAR = 1, /* divided by factor */
   DEC_ROPE_NTK = 2,    /* theta * factor^(rot_dim / (rot_dim - 2)) in theta's place: the last is divided
                           by factor, the first kept */
-  DEC_ROPE_YARN = 3    /* those that turn `fast` times or more over `context` positions are kept, those that
-                          turn `slow` times or less divided by factor, between the two in proportion; the
-                          magnitude is 0.1 log(factor) + 1 */
+  DEC_ROPE_YARN = 3,   /* those that turn `fast` times or more over `context` positions are kept, those that
+                          turn `slow` times or less divided by factor, between the two in proportion to
+                          the turns, as its paper has it; the magnitude is 0.1 log(factor) + 1 */
+  DEC_ROPE_YARN_INDEX = 4 /* the same but for what lies between: in proportion to the pair's number i, from
+                          the pair that turns `fast` times (rounded down, at least 0) to the one that turns
+                          `slow` times (rounded up, at most rot_dim - 1).  Models that are published
+                          with this scaling were trained with these: of 64 pairs two dozen turn
+                          otherwise than DEC_ROPE_YARN has them, up to twice as fast.  theta > 1 */
 };
 
 typedef struct dec_rope {
@@ -523,7 +528,7 @@ typedef struct dec_rope {
 
 /* Source: none on the pages.  frequency[rot_dim / 2] (host) and the magnitude of a
  * scaling; theta and factor are positive and finite, and context > 0 and fast >
- * slow >= 0 (looked at for DEC_ROPE_YARN). */
+ * slow >= 0 (looked at for DEC_ROPE_YARN and DEC_ROPE_YARN_INDEX). */
 int dec_rope_frequencies(int rot_dim, double theta, int scaling, double factor, double context,
                          double slow, double fast, double* frequency, float* magnitude);
 

@@ -63,25 +63,38 @@ extern "C" int dec_rope_frequencies(int rot_dim, double theta, int scaling, doub
                                     double fast, double* frequency, float* magnitude) {
   if (rot_dim < 2 || rot_dim % 2 || rot_dim > 1024) return fail_no_handle(DEC_ERR_SHAPE, "rot_dim %d: even, 2..1024", rot_dim);
   if (!frequency) return fail_no_handle(DEC_ERR_ARG, "frequency is NULL");
-  if (scaling < DEC_ROPE_PLAIN || scaling > DEC_ROPE_YARN) return fail_no_handle(DEC_ERR_ARG, "unknown scaling %d", scaling);
+  if (scaling < DEC_ROPE_PLAIN || scaling > DEC_ROPE_YARN_INDEX) return fail_no_handle(DEC_ERR_ARG, "unknown scaling %d", scaling);
   if (!(theta > 0) || !std::isfinite(theta)) return fail_no_handle(DEC_ERR_ARG, "theta %g: positive and finite", theta);
   if (scaling != DEC_ROPE_PLAIN && (!(factor > 0) || !std::isfinite(factor)))
     return fail_no_handle(DEC_ERR_ARG, "factor %g: positive and finite", factor);
-  if (scaling == DEC_ROPE_YARN && !(context > 0 && std::isfinite(context) && slow >= 0 && fast > slow && std::isfinite(fast)))
+  const bool yarn = scaling == DEC_ROPE_YARN || scaling == DEC_ROPE_YARN_INDEX;
+  if (yarn && !(context > 0 && std::isfinite(context) && slow >= 0 && fast > slow && std::isfinite(fast)))
     return fail_no_handle(DEC_ERR_ARG, "context %g, slow %g, fast %g: context > 0 and fast > slow >= 0", context, slow, fast);
   if (scaling == DEC_ROPE_NTK && rot_dim < 4) return fail_no_handle(DEC_ERR_SHAPE, "rot_dim %d: 4 or more to scale theta", rot_dim);
+  if (scaling == DEC_ROPE_YARN_INDEX && !(theta > 1))
+    return fail_no_handle(DEC_ERR_ARG, "theta %g: above 1 for pairs that turn ever more slowly", theta);
   const double base = scaling == DEC_ROPE_NTK ? theta * std::pow(factor, (double)rot_dim / (rot_dim - 2)) : theta;
   constexpr double kTurn = 6.283185307179586;
+  // The pair that turns r times over the context, were there one for every number.
+  auto pair_of = [&](double r) { return rot_dim * std::log(context / (kTurn * r)) / (2 * std::log(theta)); };
+  double first = 0, last = 0;  // DEC_ROPE_YARN_INDEX: the last pair kept, the first one divided
+  if (scaling == DEC_ROPE_YARN_INDEX) {
+    first = std::fmax(std::floor(pair_of(fast)), 0.0);
+    last = std::fmax(std::fmin(std::ceil(pair_of(slow)), rot_dim - 1.0), first);
+  }
   for (int i = 0; i < rot_dim / 2; ++i) {
     double w = std::pow(base, -2.0 * i / rot_dim);
     if (scaling == DEC_ROPE_LINEAR) w /= factor;
-    if (scaling == DEC_ROPE_YARN) {
-      const double keep = std::fmin(std::fmax((context * w / kTurn - slow) / (fast - slow), 0.0), 1.0);
+    if (yarn) {
+      const double place = scaling == DEC_ROPE_YARN ? (context * w / kTurn - slow) / (fast - slow)
+                           : last > first           ? 1 - (i - first) / (last - first)
+                                                    : (i <= first ? 1.0 : 0.0);
+      const double keep = std::fmin(std::fmax(place, 0.0), 1.0);
       w = w * keep + w / factor * (1 - keep);
     }
     frequency[i] = w;
   }
-  if (magnitude) *magnitude = scaling == DEC_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1) : 1.f;
+  if (magnitude) *magnitude = yarn ? (float)(0.1 * std::log(factor) + 1) : 1.f;
   return DEC_OK;
 }
 

@@ -15,10 +15,11 @@ import torch
 from . import dec
 
 DEC_ROPE_HALF, DEC_ROPE_PAIRS = 0, 1
-DEC_ROPE_PLAIN, DEC_ROPE_LINEAR, DEC_ROPE_NTK, DEC_ROPE_YARN = 0, 1, 2, 3
+DEC_ROPE_PLAIN, DEC_ROPE_LINEAR, DEC_ROPE_NTK, DEC_ROPE_YARN, DEC_ROPE_YARN_INDEX = 0, 1, 2, 3, 4
 
 LAYOUTS = {"half": DEC_ROPE_HALF, "interleaved": DEC_ROPE_PAIRS}
 SCALINGS = {None: DEC_ROPE_PLAIN, "linear": DEC_ROPE_LINEAR, "ntk": DEC_ROPE_NTK, "yarn": DEC_ROPE_YARN}
+RAMPS = {"turns": DEC_ROPE_YARN, "index": DEC_ROPE_YARN_INDEX}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -37,19 +38,25 @@ class Rotary:
     radians per position, are theta^(-2 i / rot_dim), made slower for long contexts by `scaling`: "linear"
     divides them by `factor`; "ntk" enlarges theta so that the slowest is divided by it and the fastest
     stays; "yarn" keeps those that turn `fast` times or more over `context` positions, divides those that
-    turn `slow` times or less, and multiplies the rotated values by 0.1 log(factor) + 1.  Or they are given,
-    `frequencies` [rot_dim / 2], and `magnitude`, which otherwise overrides the scaling's, with them.
+    turn `slow` times or less, and multiplies the rotated values by 0.1 log(factor) + 1.  Between these two `ramp`
+    says how: "turns", in proportion to a frequency's turns, which is the paper's formula, or "index", in
+    proportion to its number, between whole ones.  Models that are published with this scaling were trained with
+    "index": load them with ramp="index", since two dozen of 64 frequencies differ, some by a factor of two.
+    Or the frequencies are given, `frequencies` [rot_dim / 2], and `magnitude`, which otherwise overrides the
+    scaling's, with them.
     A captured graph needs the rotation alive, as it does a cache.
     """
 
     def __init__(self, head_dim: int, *, rot_dim: int | None = None, layout: str = "half", theta: float = 1e4,
                  scaling: str | None = None, factor: float = 1.0, context: float = 0.0, slow: float = 1.0,
-                 fast: float = 32.0, frequencies=None, magnitude: float | None = None, device=None,
+                 fast: float = 32.0, ramp: str = "turns", frequencies=None, magnitude: float | None = None, device=None,
                  lib_path: str | None = None):
         if layout not in LAYOUTS:
             raise ValueError(f"layout {layout!r}: one of {sorted(LAYOUTS)}")
         if scaling not in SCALINGS:
             raise ValueError(f"scaling {scaling!r}: one of {[k for k in SCALINGS if k]} or None")
+        if ramp not in RAMPS or (ramp != "turns" and scaling != "yarn"):
+            raise ValueError(f"ramp {ramp!r}: one of {sorted(RAMPS)}, of scaling 'yarn'")
         rot_dim = head_dim if rot_dim is None else rot_dim
         if not (8 <= head_dim <= 1024 and head_dim % 8 == 0):
             raise ValueError(f"head_dim {head_dim}: a multiple of 8, 8..1024")
@@ -58,7 +65,8 @@ class Rotary:
         self.lib = dec.load_library(lib_path or dec.LIB_PATH)
         if frequencies is None:
             self.frequencies, m = np.empty(rot_dim // 2), ctypes.c_float()
-            self._check(self.lib.dec_rope_frequencies(rot_dim, theta, SCALINGS[scaling], factor, context, slow, fast,
+            kind = RAMPS[ramp] if scaling == "yarn" else SCALINGS[scaling]
+            self._check(self.lib.dec_rope_frequencies(rot_dim, theta, kind, factor, context, slow, fast,
                                                       self.frequencies.ctypes.data, ctypes.byref(m)))
             magnitude = m.value if magnitude is None else magnitude
         else:
