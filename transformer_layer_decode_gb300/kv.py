@@ -64,6 +64,8 @@ class KVCache:
     taken as they are: pool uint8 [n_layers, n_pages, page_bytes], table int32
     [n_seqs, max_pages], lens int32 [n_seqs], refs int32 [n_pages].
 
+    The calls are for serving: autograd does not see them, and results have no gradients.
+
     Host threads may share a cache: a call's launches are queued without another's
     between them.  On the GPU the calls keep the order that include/dec.h asks for.
 

@@ -109,7 +109,8 @@ class Rotary:
     def rotate(self, x, positions=None, *, out=None, backward: bool = False, stream=None):
         """Row t of x ([n, heads, head_dim]) rotated by positions[t] (int32; without them, by t).  A row with a
         negative position is skipped, and keeps what `out` holds (zeros where that is made here).  `out` may be
-        x.  backward: by the negative angles, the gradient of a rotation."""
+        x.  backward: by the negative angles, the gradient of a rotation.  Autograd sees neither: the result of an x
+        that requires a gradient has none, and an autograd function that wants one calls both."""
         if stream is None and out is not None:  # (marshalled where plainly right, as KVCache's calls are)
             rc = self._fast.rotate(self._context, x, positions, out, bool(backward))
             if rc is not None:
