@@ -7,6 +7,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -14,8 +15,6 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtld_gb300.so")
 # debug build: the kernels' index checks compiled in (TLD_DEBUG_CHECKS)
 DEBUG_LIB = os.path.join(BUILD, "libtld_gb300_debug.so")
-# marshalling of a decode step's calls, a Python module
-CALLS = os.path.join(BUILD, "tld_calls.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -46,29 +45,42 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def build_calls(force: bool = False) -> str:
-    """Compiles csrc/py_calls.cpp against this Python and this torch."""
-    src = os.path.join(CSRC, "py_calls.cpp")
-    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "dec.h")))
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
-        return CALLS
+def build_calls(force: bool = False) -> str | None:
+    """Compiles csrc/py_calls.cpp against this Python and this torch; None, with a warning, where their headers are
+    missing: the library does not need it."""
     import sysconfig
 
-    import torch
-    root = os.path.dirname(torch.__file__)
+    try:
+        import torch
+
+        from . import dec
+        out = dec.calls_path()
+        includes = [os.path.join(os.path.dirname(torch.__file__), "include"), sysconfig.get_paths()["include"]]
+        needed = [os.path.join(includes[0], "torch", "csrc", "autograd", "python_variable.h"),
+                  os.path.join(includes[1], "Python.h")]
+        missing = [p for p in needed if not os.path.exists(p)]
+    except ImportError as e:
+        missing = [str(e)]
+    if missing:
+        warnings.warn(f"a decode step's calls will be marshalled in Python: {', '.join(missing)} is missing", RuntimeWarning)
+        return None
+    src = os.path.join(CSRC, "py_calls.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "dec.h")))
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= newest:
+        return out
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     os.makedirs(BUILD, exist_ok=True)
-    tmp = CALLS + f".{os.getpid()}.tmp"
-    libs = os.path.join(root, "lib")
+    tmp = out + f".{os.getpid()}.tmp"
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), "-I", INCLUDE, src, "-o", tmp,
+           *(x for p in includes for x in ("-I", p)), "-I", os.path.join(includes[0], "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", INCLUDE, src, "-o", tmp,
            "-L", libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stderr}")
-    os.replace(tmp, CALLS)
-    return CALLS
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,

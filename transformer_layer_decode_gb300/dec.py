@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from dataclasses import dataclass
 
 import numpy as np
@@ -16,8 +17,6 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libtld_gb300.so")
 # the same library with the kernels' index checks compiled in (TLD_DEBUG_CHECKS)
 DEBUG_LIB_PATH = os.path.join(_HERE, "_build", "libtld_gb300_debug.so")
-# the Python module that marshals a decode step's calls (csrc/py_calls.cpp)
-CALLS_PATH = os.path.join(_HERE, "_build", "tld_calls.so")
 
 # enum values of dec.h
 DEC_OK, DEC_ERR_ARG, DEC_ERR_SHAPE, DEC_ERR_STATE = 0, -1, -2, -3
@@ -133,24 +132,36 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return L
 
 
-_calls = None
+def calls_path() -> str:
+    """The Python module that marshals a decode step's calls (csrc/py_calls.cpp), as built for this Python and this
+    torch: it reads torch's own objects, whose layout another version or ABI need not share."""
+    import sysconfig
+
+    import torch
+    key = f"torch{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(_HERE, "_build", f"tld_calls-{key}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+_calls: dict = {}
 
 
 def load_calls():
-    """The module that marshals a decode step's calls (built by ``build.build()``); raise if it is missing."""
-    global _calls
-    if _calls is None:
+    """The module of :func:`calls_path` (built by ``build.build()``).  None, with a warning, where it is missing: the
+    calls are then marshalled in Python, which takes the host two to three times as long."""
+    path = calls_path()
+    if path not in _calls:
         import importlib.machinery
         import importlib.util
 
-        import torch  # noqa: F401  (its libraries are the module's)
-        if not os.path.exists(CALLS_PATH):
-            raise RuntimeError(f"not built: {CALLS_PATH} is missing (run transformer_layer_decode_gb300.build.build())")
-        loader = importlib.machinery.ExtensionFileLoader("tld_calls", CALLS_PATH)
+        if not os.path.exists(path):
+            warnings.warn(f"not built: {path} is missing (run transformer_layer_decode_gb300.build.build()); the calls of "
+                          "a decode step are marshalled in Python", RuntimeWarning, stacklevel=3)
+            return None
+        loader = importlib.machinery.ExtensionFileLoader("tld_calls", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("tld_calls", loader))
         loader.exec_module(module)
-        _calls = module
-    return _calls
+        _calls[path] = module
+    return _calls[path]
 
 
 def address_of(fn) -> int:

@@ -73,7 +73,7 @@ class KVCache:
     plainly right, and here where they are not, or have a stream of their own.
     """
 
-    _context = None  # what that module knows of a cache
+    _context = None  # what that module knows of a cache, if it is there
 
     def __init__(self, *, n_layers: int, n_kv_heads: int, head_dim: int, page_rows: int | None = None,
                  fmt: str = "bf16", n_pages: int | None = None, n_seqs: int | None = None,
@@ -126,9 +126,10 @@ class KVCache:
         self._workspaces: dict = {}  # of a stream's attention calls, which run one after another
         self._captured_workspaces: list = []  # of captures that keep no memory themselves
         self._fast = dec.load_calls()
-        self._context = self._fast.context(ctypes.addressof(self.desc), self._index, n_kv_heads, head_dim, *(
-            dec.address_of(f) for f in (self.lib.dec_kv_append, self.lib.dec_kv_read, self.lib.dec_kv_attention,
-                                        self.lib.dec_kv_append_rotated)))
+        if self._fast is not None:
+            self._context = self._fast.context(ctypes.addressof(self.desc), self._index, n_kv_heads, head_dim, *(
+                dec.address_of(f) for f in (self.lib.dec_kv_append, self.lib.dec_kv_read, self.lib.dec_kv_attention,
+                                            self.lib.dec_kv_append_rotated)))
 
     # ---- marshalling ----------------------------------------------------------
 

@@ -88,9 +88,10 @@ class Rotary:
         self.device, self._index = self.steps.device, self.steps.device.index
         self.desc = RopeDesc(head_dim, rot_dim, LAYOUTS[layout], magnitude, self.steps.data_ptr())
         self._ref = ctypes.byref(self.desc)
-        self._fast = dec.load_calls()
-        self._context = self._fast.context(ctypes.addressof(self.desc), self._index, 0, head_dim,
-                                           dec.address_of(self.lib.dec_rope_rotate))
+        self._fast, self._context = dec.load_calls(), None
+        if self._fast is not None:
+            self._context = self._fast.context(ctypes.addressof(self.desc), self._index, 0, head_dim,
+                                               dec.address_of(self.lib.dec_rope_rotate))
 
     def _check(self, rc: int):
         if rc != dec.DEC_OK:
@@ -111,7 +112,7 @@ class Rotary:
         negative position is skipped, and keeps what `out` holds (zeros where that is made here).  `out` may be
         x.  backward: by the negative angles, the gradient of a rotation.  Autograd sees neither: the result of an x
         that requires a gradient has none, and an autograd function that wants one calls both."""
-        if stream is None and out is not None:  # (marshalled where plainly right, as KVCache's calls are)
+        if stream is None and out is not None and self._context is not None:  # (marshalled where plainly right, as KVCache's calls are)
             rc = self._fast.rotate(self._context, x, positions, out, bool(backward))
             if rc is not None:
                 if rc:
