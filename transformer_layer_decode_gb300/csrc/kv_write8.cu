@@ -445,6 +445,8 @@ cudaError_t launch8(const KvView& c, const void* k, const void* v, int64_t strid
     cudaError_t e = cudaLaunchKernelEx(&first, kv_owners, c, seqs, positions, n);
     if (e != cudaSuccess) return e;
   }
+  // (n / 128 and n / 512: 1000 rows of 8 heads 7.2 and 7.6 us for 6.6, 4093 rows 9.3 and 10.4 for
+  // 8.9; 1000 of 32 heads 10.2 and 17.1 for 11.6)
   const int tokens = std::min(std::max(n / 256, 1), kTokens8);
   const int64_t chunks = (n + tokens - 1) / tokens;
   const int steps = (items + kThreads8 / 32 - 1) / (kThreads8 / 32);  // a head of K or V for each warp

@@ -60,14 +60,15 @@ __device__ __forceinline__ int rope_over(int e, uint32_t by) { return by ? (int)
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 32;           // of a CTA, at most
 constexpr int kRopeSmem = 32 * 1024;      // its cosines and sines, at most
-constexpr int kRopeCtas = 4 * kSms;       // that the GPU holds at once
+// CTAs that the GPU holds at once (three and six an SM: 8185 rows of 32 heads 27 us each, four 25).
+constexpr int kRopeCtas = 4 * kSms;
 
 constexpr int max_int(int a, int b) { return a > b ? a : b; }
 
 // How a launch cuts the rows; the CTAs that it takes.  Few rows: a lane's item each,
 // heads dealt out where there are many.  Many: as many rows a CTA as it takes to
 // have all CTAs on the GPU at once, since a CTA begins with a chain of loads and its
-// angles, and only then streams.
+// angles, and only then streams.  (Queries beside rows that are written are cut the same way.)
 inline int rope_cut(RopeRows& p) {
   const int items = max_int(1, p.heads * p.d / 16);  // (about: of 16 values)
   const int most = max_int(1, kRopeSmem / (p.r.rot * 4) < kRopeTokens ? kRopeSmem / (p.r.rot * 4) : kRopeTokens);
